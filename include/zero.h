@@ -605,6 +605,144 @@ int zero_dist_update(zero_layout_t* layout, const void* allreduced, void* stream
 int zero_dist_update_buckets(zero_layout_t* layout, const void* allreduced, int first_bucket,
                              int n_buckets, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Operators of a transformer block's forward and backward                    */
+/*                                                                            */
+/* What produces the gradients that the step consumes: RMSNorm with the       */
+/* residual's addition, activations packed to 8 bits and the weight gradient  */
+/* taken from them, and attention's training pair. They need no layout. All   */
+/* buffers are the caller's; calls only enqueue kernels on `stream` (no       */
+/* allocation, no host synchronisation), so they can be captured into a CUDA  */
+/* graph. Results do not depend on timing: no atomic adds of values, every    */
+/* sum has a fixed order for given sizes. Non-finite inputs propagate to the  */
+/* outputs that depend on them, so the step's overflow check sees them.       */
+/* ------------------------------------------------------------------------ */
+
+/* Rows of an RMSNorm call. Strides are in elements between the starts of two
+ * rows (>= cols); elements of a row are contiguous. Outputs have rows of
+ * exactly cols elements. All dtypes are accepted; when cols and the strides
+ * are multiples of 8, rows move as 16-byte vectors.
+ *   dtype         x, residual / dsum, sum_out, y, dy, dx.
+ *   weight_dtype  weight[cols].
+ *   residual_stride  of residual (forward) or dsum (backward). */
+typedef struct {
+  int64_t rows;
+  int64_t cols;          /* 1..65536 */
+  int64_t x_stride;
+  int64_t residual_stride;
+  int64_t dy_stride;     /* backward only */
+  int32_t dtype;
+  int32_t weight_dtype;
+  double eps;            /* >= 0 */
+} zero_rmsnorm_desc;
+
+/* s = RNE(x + residual) (s = x without a residual); rstd = (mean(s^2) +
+ * eps)^(-1/2) in fp32; y = RNE(s * rstd * weight).
+ *   residual   may be NULL; then sum_out must be NULL too.
+ *   sum_out    receives s (required with a residual); may be x or residual
+ *              itself when that one's stride is cols.
+ *   y          may be NULL when only the packed copy is wanted.
+ *   q, scales  both NULL, or a packed activation of rows x cols that receives
+ *              exactly what zero_act_pack makes of y.
+ *   rstd       fp32 [rows]; may be NULL. */
+int zero_rmsnorm_forward(const zero_rmsnorm_desc* desc, const void* x, const void* residual,
+                         const void* weight, void* sum_out, void* y, int8_t* q, uint8_t* scales,
+                         float* rstd, void* stream);
+
+/* Bytes of the scratch that zero_rmsnorm_backward needs (host only). */
+int zero_rmsnorm_backward_workspace(const zero_rmsnorm_desc* desc, int64_t* bytes);
+
+/* With xhat = x * rstd and g = dy * weight:
+ *   dx = RNE(dsum + rstd * (g - xhat * mean(g * xhat))), the gradient of both
+ *   x and the residual; dweight[c] = sum over rows of dy * xhat (fp32 sums),
+ *   stored as dweight_dtype.
+ *   x     the forward's s (sum_out, or x without a residual).
+ *   dsum  the gradient that reaches s by its other use; may be NULL.
+ *   dx    may be dy or dsum itself when that one's stride is cols. */
+int zero_rmsnorm_backward(const zero_rmsnorm_desc* desc, const void* dy, const void* x,
+                          const void* weight, const float* rstd, const void* dsum, void* dx,
+                          void* dweight, int dweight_dtype, void* workspace,
+                          int64_t workspace_bytes, void* stream);
+
+/* Packed activations: 8-bit codes with one power-of-two scale per 32
+ * elements along the row.
+ *   q       int8 [rows, pitch], pitch = cols rounded up to 128; codes of the
+ *           padding are 0.
+ *   scales  uint8 [rows, pitch / 32]: b stands for 2^(b - 127), b = 255 marks
+ *           a group that held an inf or NaN.
+ * pack: b - 127 = floor(log2(largest magnitude of the group)) - 6, at least
+ * -127 (a group of zeros: b = 0); code = x / 2^(b-127) rounded to nearest even
+ * and clamped to +-127. restore: code * 2^(b-127), rounded to the output type
+ * (exact in bf16 and fp32); every element of a marked group is NaN. */
+int zero_act_layout(int64_t rows, int64_t cols, int64_t* pitch, int64_t* q_bytes,
+                    int64_t* scale_bytes);
+int zero_act_pack(const void* x, int64_t x_stride, int64_t rows, int64_t cols, int dtype, int8_t* q,
+                  uint8_t* scales, void* stream);
+int zero_act_unpack(const int8_t* q, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
+                    int64_t out_stride, int dtype, void* stream);
+
+/* Weight gradient of a linear layer y = x W^T from its packed input:
+ * dw[n_out, n_in] = dy^T X, X = the packed activation (tokens x n_in) restored
+ * in dy's type; fp32 sums, rounded once to dw_dtype.
+ *   dy          [tokens, n_out] ZERO_F16 or ZERO_BF16, dy_stride elements
+ *               between rows (a multiple of 8).
+ *   dw_dtype    ZERO_F32 or dy's type.
+ *   accumulate  1: dw += (ZERO_F32 only; fp32 main gradients), 0: dw =.
+ *   workspace   zero_act_weight_grad_workspace bytes (NULL when that is 0). */
+int zero_act_weight_grad_workspace(int64_t tokens, int64_t n_out, int64_t n_in, int64_t* bytes);
+int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const int8_t* q,
+                         const uint8_t* scales, int64_t tokens, int64_t n_out, int64_t n_in,
+                         void* dw, int dw_dtype, int accumulate, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/* Attention over [batch, length, heads, head_dim] tensors.
+ *   dtype       ZERO_F16 or ZERO_BF16, all tensors.
+ *   head_dim    a multiple of 8, up to 128.
+ *   q_heads     a multiple of kv_heads: query head h uses key head
+ *               h / (q_heads / kv_heads).
+ *   Strides     {batch, token, head} in elements, multiples of 8 (a dimension
+ *               of size 1 may have any); elements of a head are contiguous.
+ *               Outputs' elements must not overlap.
+ *   Query i sees key j when j < key_lengths[b] (all k_len keys without
+ *   lengths), j <= i + k_len - q_len with `causal`, and j > i + k_len - q_len -
+ *   window with window > 0. What lies past key_lengths is never used, whatever
+ *   it holds. A query that sees no key has o = 0, lse = -inf and passes no
+ *   gradient.
+ *   scale       of the products q.k; > 0. */
+typedef struct {
+  int64_t batch, q_len, k_len; /* lengths up to 2^28 */
+  int32_t q_heads, kv_heads, head_dim;
+  int32_t dtype;
+  int32_t causal;
+  int32_t reserved;
+  int64_t window;
+  double scale;
+  int64_t q_strides[3], k_strides[3], v_strides[3], o_strides[3];
+  int64_t do_strides[3], dq_strides[3], dk_strides[3], dv_strides[3]; /* backward only */
+} zero_attention_desc;
+
+/* o = softmax(scale q k^T) v over the keys seen; lse = log of the sum of
+ * exp(scale q.k), fp32 [batch, q_heads, q_len].
+ *   key_lengths  device int32 [batch], each 0..k_len, or NULL. */
+int zero_attention_forward(const zero_attention_desc* desc, const void* q, const void* k,
+                           const void* v, const int32_t* key_lengths, void* o, float* lse,
+                           void* stream);
+
+/* The gradients of q, k and v from o's, recomputing the probabilities from
+ * lse. dk and dv are summed over the query heads that share them.
+ *   workspace  zero_attention_backward_workspace bytes. */
+int zero_attention_backward_workspace(const zero_attention_desc* desc, int64_t* bytes);
+int zero_attention_backward(const zero_attention_desc* desc, const void* dout, const void* q,
+                            const void* k, const void* v, const void* o, const float* lse,
+                            const int32_t* key_lengths, void* dq, void* dk, void* dv,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Whether a bounded device wait gave up in one of these operators since the
+ * last call: ZERO_ERR_TIMEOUT if so (the outputs of the calls since then are
+ * not to be used), ZERO_OK otherwise. Clears the mark. Synchronises `stream`;
+ * covers the current device. */
+int zero_operator_status(void* stream);
+
 /* Message for the last failing call on this thread ("" if none). The pointer
  * stays valid until the next failing call on this thread. */
 const char* zero_last_error(void);

@@ -15,6 +15,11 @@ from ._abi import (ZERO_BF16, ZERO_MAX_ELEMS, ZERO_STATE_BLOB_BYTES, zero_accumu
                    zero_scaler_cfg, zero_scaler_state, zero_set_step_events, zero_shard_range, zero_state_bind,
                    zero_state_bind_alternate, zero_step_speculative, zero_step_speculative_tensors,
                    zero_state_export, zero_state_import, zero_state_init, zero_step,
-                   zero_step_host, zero_step_per_tensor_launch, zero_step_tensors, lib)
+                   zero_step_host, zero_step_per_tensor_launch, zero_step_tensors,
+                   zero_rmsnorm_desc, zero_rmsnorm_forward, zero_rmsnorm_backward,
+                   zero_rmsnorm_backward_workspace, zero_act_layout, zero_act_pack, zero_act_unpack,
+                   zero_act_weight_grad, zero_act_weight_grad_workspace, zero_attention_desc,
+                   zero_attention_forward, zero_attention_backward,
+                   zero_attention_backward_workspace, zero_operator_status, lib)
 
 __all__ = [n for n in dir() if n.startswith("zero_") or n.startswith("ZERO_")] + ["ZeroError", "lib"]

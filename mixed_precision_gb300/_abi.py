@@ -65,6 +65,22 @@ class zero_scaler_state(ctypes.Structure):
                 ("state_set", ctypes.c_int32), ("fast_path", ctypes.c_int32)]
 
 
+class zero_rmsnorm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "rows", "cols", "x_stride", "residual_stride", "dy_stride")] + \
+        [("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_double)]
+
+
+class zero_attention_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "q_len", "k_len")] + \
+        [(n, ctypes.c_int32) for n in ("q_heads", "kv_heads", "head_dim", "dtype", "causal",
+                                       "reserved")] + \
+        [("window", ctypes.c_int64), ("scale", ctypes.c_double)] + \
+        [(n, ctypes.c_int64 * 3) for n in (
+            "q_strides", "k_strides", "v_strides", "o_strides", "do_strides", "dq_strides",
+            "dk_strides", "dv_strides")]
+
+
 ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p)
 FREE_FN = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_void_p)
 
@@ -123,6 +139,22 @@ def lib() -> ctypes.CDLL:
             "zero_dist_update": [P, P, P],
             "zero_dist_update_buckets": [P, P, I, I, P],
             "zero_dist_widen": [P, P, P, P],
+            "zero_rmsnorm_forward": [ctypes.POINTER(zero_rmsnorm_desc)] + [P] * 9,
+            "zero_rmsnorm_backward_workspace": [ctypes.POINTER(zero_rmsnorm_desc),
+                                                ctypes.POINTER(I64)],
+            "zero_rmsnorm_backward": [ctypes.POINTER(zero_rmsnorm_desc)] + [P] * 7 +
+                                     [I, P, I64, P],
+            "zero_act_layout": [I64, I64] + [ctypes.POINTER(I64)] * 3,
+            "zero_act_pack": [P, I64, I64, I64, I, P, P, P],
+            "zero_act_unpack": [P, P, I64, I64, P, I64, I, P],
+            "zero_act_weight_grad_workspace": [I64, I64, I64, ctypes.POINTER(I64)],
+            "zero_act_weight_grad": [P, I64, I, P, P, I64, I64, I64, P, I, I, P, I64, P],
+            "zero_attention_forward": [ctypes.POINTER(zero_attention_desc)] + [P] * 7,
+            "zero_attention_backward_workspace": [ctypes.POINTER(zero_attention_desc),
+                                                  ctypes.POINTER(I64)],
+            "zero_attention_backward": [ctypes.POINTER(zero_attention_desc)] + [P] * 11 +
+                                       [I64, P],
+            "zero_operator_status": [P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -343,3 +375,75 @@ def zero_dist_update_buckets(layout: int, allreduced: int, first_bucket: int, n_
 
 def zero_dist_widen(layout: int, grads: int, out: int, stream: int) -> None:
     _check(lib().zero_dist_widen(layout, grads, out, stream or None))
+
+
+def zero_rmsnorm_forward(desc: zero_rmsnorm_desc, x: int, residual: int, weight: int, sum_out: int,
+                         y: int, q: int, scales: int, rstd: int, stream: int) -> None:
+    _check(lib().zero_rmsnorm_forward(desc, x, residual, weight, sum_out, y, q, scales, rstd,
+                                      stream))
+
+
+def zero_rmsnorm_backward_workspace(desc: zero_rmsnorm_desc) -> int:
+    n = ctypes.c_int64()
+    _check(lib().zero_rmsnorm_backward_workspace(desc, n))
+    return n.value
+
+
+def zero_rmsnorm_backward(desc: zero_rmsnorm_desc, dy: int, x: int, weight: int, rstd: int, dsum: int,
+                          dx: int, dweight: int, dweight_dtype: int, workspace: int,
+                          workspace_bytes: int, stream: int) -> None:
+    _check(lib().zero_rmsnorm_backward(desc, dy, x, weight, rstd, dsum, dx, dweight, dweight_dtype,
+                                       workspace, workspace_bytes, stream))
+
+
+def zero_act_layout(rows: int, cols: int):
+    """(pitch, bytes of q, bytes of scales)."""
+    a, b, c = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().zero_act_layout(rows, cols, a, b, c))
+    return a.value, b.value, c.value
+
+
+def zero_act_pack(x: int, x_stride: int, rows: int, cols: int, dtype: int, q: int, scales: int,
+                  stream: int) -> None:
+    _check(lib().zero_act_pack(x, x_stride, rows, cols, dtype, q, scales, stream))
+
+
+def zero_act_unpack(q: int, scales: int, rows: int, cols: int, out: int, out_stride: int, dtype: int,
+                    stream: int) -> None:
+    _check(lib().zero_act_unpack(q, scales, rows, cols, out, out_stride, dtype, stream))
+
+
+def zero_act_weight_grad_workspace(tokens: int, n_out: int, n_in: int) -> int:
+    n = ctypes.c_int64()
+    _check(lib().zero_act_weight_grad_workspace(tokens, n_out, n_in, n))
+    return n.value
+
+
+def zero_act_weight_grad(dy: int, dy_stride: int, dtype: int, q: int, scales: int, tokens: int,
+                         n_out: int, n_in: int, dw: int, dw_dtype: int, accumulate: bool,
+                         workspace: int, workspace_bytes: int, stream: int) -> None:
+    _check(lib().zero_act_weight_grad(dy, dy_stride, dtype, q, scales, tokens, n_out, n_in, dw,
+                                      dw_dtype, accumulate, workspace, workspace_bytes, stream))
+
+
+def zero_attention_forward(desc: zero_attention_desc, q: int, k: int, v: int, key_lengths: int, o: int,
+                           lse: int, stream: int) -> None:
+    _check(lib().zero_attention_forward(desc, q, k, v, key_lengths, o, lse, stream))
+
+
+def zero_attention_backward_workspace(desc: zero_attention_desc) -> int:
+    n = ctypes.c_int64()
+    _check(lib().zero_attention_backward_workspace(desc, n))
+    return n.value
+
+
+def zero_attention_backward(desc: zero_attention_desc, dout: int, q: int, k: int, v: int, o: int,
+                            lse: int, key_lengths: int, dq: int, dk: int, dv: int, workspace: int,
+                            workspace_bytes: int, stream: int) -> None:
+    _check(lib().zero_attention_backward(desc, dout, q, k, v, o, lse, key_lengths, dq, dk, dv,
+                                         workspace, workspace_bytes, stream))
+
+
+def zero_operator_status(stream: int) -> None:
+    """Raises ZeroError(ZERO_ERR_TIMEOUT) if a bounded wait gave up since the last call."""
+    _check(lib().zero_operator_status(stream or None))

@@ -1,0 +1,85 @@
+// Internal interface between the host side of the block operators
+// (block_api.cpp) and their kernels (k_norm.cu, k_act.cu, k_wgrad.cu,
+// k_attention.cu). Not part of the public ABI (include/zero.h is).
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace zg {
+
+constexpr int kActGroup = 32;   // elements of a packed row that share one scale
+constexpr int kActPitch = 128;  // a packed row is padded to a multiple of this
+
+struct NormArgs {
+  int64_t rows;
+  int cols, pitch;  // pitch: of the packed output
+  int64_t x_stride, r_stride, dy_stride;
+  int dtype, weight_dtype, dweight_dtype;
+  float eps;
+  const void *x, *res, *weight, *dy;  // res: residual (forward) or dsum (backward)
+  const float* rstd_in;
+  void *sum, *y, *dx, *dweight;
+  int8_t* q;
+  uint8_t* scales;
+  float* rstd;
+  float* part;  // backward: [parts][cols] partial sums of dweight
+};
+cudaError_t launch_norm_forward(const NormArgs& a, int sms, cudaStream_t s);
+// Rows of partial sums that the backward writes (its workspace is parts x cols floats).
+int norm_backward_parts(int64_t rows, int cols);
+cudaError_t launch_norm_backward(const NormArgs& a, int sms, cudaStream_t s);
+
+struct ActArgs {
+  int64_t rows;
+  int cols, pitch;
+  int64_t stride;  // of x or out
+  int dtype;
+  const void* x;
+  void* out;
+  const int8_t* q_in;
+  const uint8_t* scales_in;
+  int8_t* q;
+  uint8_t* scales;
+};
+cudaError_t launch_act_pack(const ActArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_act_unpack(const ActArgs& a, int sms, cudaStream_t s);
+
+struct WgradArgs {
+  const void* dy;
+  int64_t dy_stride;
+  int dtype;
+  const int8_t* q;
+  const uint8_t* scales;
+  int64_t tokens, n_out;
+  int n_in, pitch;
+  void* dw;
+  int dw_dtype, accumulate;
+};
+cudaError_t launch_wgrad(const WgradArgs& a, int sms, cudaStream_t s);
+
+struct AttnArgs {
+  int64_t batch, q_len, k_len;
+  int q_heads, kv_heads, head_dim, group;  // group = q_heads / kv_heads
+  int dtype, causal;
+  int64_t window;  // 0: none
+  float scale;
+  int64_t qs[3], ks[3], vs[3], os[3], dos[3], dqs[3], dks[3], dvs[3];  // {batch, token, head}
+  const void *q, *k, *v, *dout;
+  const void* o_in;
+  void *o, *dq, *dk, *dv;
+  const int32_t* lengths;
+  float* lse;
+  const float* lse_in;
+  float* delta;  // backward: [batch, q_heads, q_len] row sums of do * o
+};
+cudaError_t launch_attention_forward(const AttnArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s);
+
+// The device's error word of the block operators (bit kErrWaitTimeout).
+cudaError_t block_error_read_clear(unsigned* value, cudaStream_t s);
+
+}  // namespace zg
