@@ -1,78 +1,395 @@
-// Weight gradient from a packed activation: dw = dy^T X, X restored in dy's
-// type. Plain tiled form: 64 x 64 outputs a block, fp32 sums over the tokens.
+// Weight gradient from a packed activation: dw[n_out, n_in] = dy^T X, X the
+// packed activation restored in dy's type.
+//
+// On the tensor cores (tcgen05, fp32 sums in TMEM): both operands have the
+// contraction (tokens) as their outer dimension, so both are MN-major tiles.
+// dy comes by TMA. X goes through registers: eight warps read the codes from
+// global memory one step ahead, turn each into dy's type (an int8 code and a
+// power-of-two scale: exact in bf16) and write the swizzled tile, so the
+// 16-bit activation never exists in global memory.
+//
+// A block makes MT * 128 x BN outputs over a run of tokens. When the outputs
+// alone do not fill the machine, a cluster of S blocks shares a tile, each
+// over its own run of tokens; each block then sends its sums to the block
+// that owns the columns (distributed shared memory), which adds the S parts
+// in order. No atomics, no workspace; the order of every sum is fixed.
+#include <type_traits>
+
 #include "act.cuh"
 #include "block.h"
+#include "tc.cuh"
 #include "vec.cuh"
 
 namespace zg {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16;
+__device__ unsigned g_wgrad_error;
+
+constexpr int kConvWarps = 8;
+constexpr int kWgThreads = (kConvWarps + 2) * 32;  // converters, the TMA warp, the MMA warp
+constexpr int kStep = 64;                          // tokens a step
+constexpr int kChunk = kStep * 128;                // bytes of 64 columns x 64 tokens
+constexpr int kRedRows = 128;
+
+template <int MT, int BN>
+struct Tile {
+  static constexpr int kABytes = MT * 2 * kChunk, kBBytes = BN / 64 * kChunk;
+  static constexpr int kStage = kABytes + kBBytes;
+  static constexpr int kStages = 196608 / kStage < 6 ? 196608 / kStage : 6;
+  static constexpr int kRed = kRedRows * BN * 4;  // a phase of the cluster's sum
+  static constexpr int kSmem = (kStages * kStage > kRed ? kStages * kStage : kRed) + 1024;
+  static constexpr int kCols = MT * BN < 128 ? 128 : MT * BN;  // TMEM columns
+  static_assert((kCols & (kCols - 1)) == 0 && kCols <= 512, "a power of two");
+};
+
+// Two bf16 products of int8 codes (bytes 2p and 2p+1 of w) and a scale pair.
+// 128 + (low seven bits) is a bf16 number made by a byte move; taking away 128
+// or, below zero, 256 leaves the code, all exact.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t w, int p, __nv_bfloat162 s) {
+  const uint32_t sel = p == 0 ? 0x4140 : 0x4342;
+  const uint32_t a = __byte_perm(w & 0x7F7F7F7Fu, 0x43434343u, sel);
+  const uint32_t c = __byte_perm(w & 0x80808080u, 0xC3C3C3C3u, sel);
+  const __nv_bfloat162 v = __hmul2(__hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                           *reinterpret_cast<const __nv_bfloat162*>(&c)),
+                                   s);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 template <typename T>
-__global__ void __launch_bounds__(256) k_wgrad(const WgradArgs a) {
-  __shared__ float sa[kDepth][kTile + 4], sb[kDepth][kTile + 4];
-  const int64_t m0 = (int64_t)blockIdx.y * kTile;
-  const int n0 = blockIdx.x * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const T* dy = static_cast<const T*>(a.dy);
-  float acc[4][4] = {};
-  for (int64_t t0 = 0; t0 < a.tokens; t0 += kDepth) {
-    for (int i = threadIdx.x; i < kDepth * kTile; i += 256) {
-      const int r = i / kTile, c = i % kTile;
-      const int64_t t = t0 + r;
-      const bool live = t < a.tokens;
-      sa[r][c] = live && m0 + c < a.n_out ? DT<T>::to_f32(dy[t * a.dy_stride + m0 + c]) : 0.0f;
-      float x = 0.0f;
-      if (live && n0 + c < a.n_in)
-        x = static_cast<float>(a.q[t * a.pitch + n0 + c]) *
-            act_scale(a.scales[t * (a.pitch / kActGroup) + (n0 + c) / kActGroup]);
-      sb[r][c] = DT<T>::to_f32(DT<T>::from_f32(x));
-    }
-    __syncthreads();
+__device__ __forceinline__ uint4 restore8(uint2 q, uint32_t byte);
+
+template <>
+__device__ __forceinline__ uint4 restore8<__nv_bfloat16>(uint2 q, uint32_t byte) {
+  // the scale as a bf16: its exponent byte; 2^-127 is subnormal, 255 stands for NaN
+  const uint32_t b = byte == 0 ? 0x0040u : byte == 255 ? 0x7FC0u : byte << 7;
+  const uint32_t bb = b | b << 16;
+  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&bb);
+  return make_uint4(codes_bf16(q.x, 0, s), codes_bf16(q.x, 1, s), codes_bf16(q.y, 0, s), codes_bf16(q.y, 1, s));
+}
+
+template <>
+__device__ __forceinline__ uint4 restore8<__half>(uint2 q, uint32_t byte) {
+  // fp16 may not hold the result: one fp32 product (exact), one rounding
+  const float s = act_scale(byte);
+  uint4 r;
+  uint32_t* o = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
-    for (int r = 0; r < kDepth; ++r) {
-      float u[4], v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = sa[r][ty * 4 + i], v[i] = sb[r][tx * 4 + i];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(u[i], v[j], acc[i][j]);
-    }
-    __syncthreads();
+  for (int p = 0; p < 4; ++p) {
+    const uint32_t w = p < 2 ? q.x : q.y;
+    const float lo = static_cast<float>(static_cast<int8_t>(w >> 16 * (p & 1))) * s;
+    const float hi = static_cast<float>(static_cast<int8_t>(w >> (16 * (p & 1) + 8))) * s;
+    const __half2 h = __floats2half2_rn(lo, hi);
+    o[p] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty * 4 + i;
-      const int n = n0 + tx * 4 + j;
-      if (m >= a.n_out || n >= a.n_in) continue;
-      const int64_t at = m * a.n_in + n;
-      if (a.dw_dtype == kF32) {
-        float* dw = static_cast<float*>(a.dw);
-        dw[at] = a.accumulate ? dw[at] + acc[i][j] : acc[i][j];
-      } else {
-        static_cast<T*>(a.dw)[at] = DT<T>::from_f32(acc[i][j]);
+  return r;
+}
+
+// 8 neighbouring outputs of a row, from column n.
+template <typename T>
+__device__ __forceinline__ void store_out(const WgradArgs& a, int64_t m, int n, const float (&v)[8]) {
+  if (m >= a.n_out || n >= a.n_in) return;
+  const int64_t at = m * a.n_in + n;
+  if (a.n_in % 8 == 0) {
+    if (a.dw_dtype == kF32) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at);
+      float4 u = make_float4(v[0], v[1], v[2], v[3]), w = make_float4(v[4], v[5], v[6], v[7]);
+      if (a.accumulate) {
+        const float4 x = p[0], y = p[1];
+        u = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+        w = make_float4(y.x + w.x, y.y + w.y, y.z + w.z, y.w + w.w);
+      }
+      p[0] = u;
+      p[1] = w;
+    } else {
+      store8(static_cast<T*>(a.dw) + at, v);
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (n + j >= a.n_in) break;
+    if (a.dw_dtype == kF32) {
+      float* p = static_cast<float*>(a.dw) + at + j;
+      *p = a.accumulate ? *p + v[j] : v[j];
+    } else {
+      static_cast<T*>(a.dw)[at + j] = DT<T>::from_f32(v[j]);
+    }
+  }
+}
+
+template <typename T, int MT, int BN>
+__global__ void __launch_bounds__(kWgThreads, 1)
+    k_wgrad(const __grid_constant__ CUtensorMap map, const WgradArgs a, int n_tiles, int split, int per_split) {
+  using C = Tile<MT, BN>;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], done;
+  __shared__ uint32_t tmem_slot, abort_word;
+  // the swizzle is a function of address bits: tiles start on 1024 bytes
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const uint32_t base = smem_u32(smem);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
+  const int n0 = tile % n_tiles * BN;
+  const int64_t m0 = (int64_t)(tile / n_tiles) * (MT * 128);
+  const int64_t steps_all = (a.tokens + kStep - 1) / kStep;
+  const int64_t first = (int64_t)rank * per_split;
+  const int steps = (int)max((int64_t)0, min((int64_t)per_split, steps_all - first));
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1 + kConvWarps);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&done, 1);
+    abort_word = 0;
+    mbar_init_fence();
+    tma_prefetch(&map);
+  }
+  if (warp == kConvWarps + 1) tmem_alloc(&tmem_slot, C::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const Waiter wait{&abort_word, &g_wgrad_error};
+
+  if (warp < kConvWarps) {
+    // ---- converters: a warp takes 8 tokens of a step, a lane 8 columns of a row
+    constexpr int kLanes = BN / 8;        // lanes a row
+    constexpr int kRows = 32 / kLanes;    // rows a round
+    constexpr int kRounds = 8 / kRows;
+    const int c = lane % kLanes * 8, r0 = warp * 8 + lane / kLanes;
+    const bool in = n0 + c < a.pitch;
+    uint2 q[kRounds];
+    uint32_t b[kRounds];
+    auto fetch = [&](int step) {
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i) {
+        const int64_t t = (first + step) * kStep + r0 + i * kRows;
+        q[i] = make_uint2(0, 0);
+        b[i] = 0;
+        if (in && step < steps && t < a.tokens) {
+          q[i] = *reinterpret_cast<const uint2*>(a.q + t * a.pitch + n0 + c);
+          b[i] = a.scales[t * (a.pitch / kActGroup) + (n0 + c) / kActGroup];
+        }
+      }
+    };
+    fetch(0);
+    for (int step = 0; step < steps; ++step) {
+      const int s = step % C::kStages;
+      if (step >= C::kStages && !wait(&empty[s], (step / C::kStages - 1) & 1)) break;
+      uint8_t* tile_b = smem + s * C::kStage + C::kABytes + c / 64 * kChunk;
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i) {
+        const int r = r0 + i * kRows;
+        *reinterpret_cast<uint4*>(tile_b + r * 128 + ((c / 8 % 8) ^ (r & 7)) * 16) = restore8<T>(q[i], b[i]);
+      }
+      fetch(step + 1);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[s]);
+    }
+  } else if (warp == kConvWarps) {
+    // ---- dy tiles by TMA
+    if (lane == 0) {
+      int step = 0;
+      for (; step < steps; ++step) {
+        const int s = step % C::kStages;
+        if (step >= C::kStages && !wait(&empty[s], (step / C::kStages - 1) & 1)) break;
+        mbar_arrive_expect_tx(&full[s], C::kABytes);
+#pragma unroll
+        for (int i = 0; i < MT * 2; ++i)
+          tma_load2(base + s * C::kStage + i * kChunk, &map, (int)m0 + i * 64, (int)((first + step) * kStep), &full[s]);
+      }
+      if (step < steps)  // gave up: leave the copies in flight time to land
+        for (int i = max(0, step - C::kStages); i < step; ++i)
+          mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, kSpinLimit >> 10);
+    }
+    __syncwarp();
+  } else {
+    // ---- the tensor cores
+    if (lane == 0) {
+      constexpr uint32_t idesc = mma_desc(!std::is_same<T, __half>::value,
+                                          128, BN, true, true);
+      for (int step = 0; step < steps; ++step) {
+        const int s = step % C::kStages;
+        if (!wait(&full[s], (step / C::kStages) & 1)) break;
+        tc_fence_after();
+        const uint32_t at = base + s * C::kStage;
+#pragma unroll
+        for (int k = 0; k < kStep / 16; ++k)
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            mma_ss(tmem + m * BN, smem_desc(at + m * 2 * kChunk + k * 2048, kChunk, 1024),
+                   smem_desc(at + C::kABytes + k * 2048, kChunk, 1024), idesc, step > 0 || k > 0);
+        mma_commit(&empty[s]);
+      }
+      mma_commit(&done);
+    }
+    __syncwarp();
+  }
+  // Every MMA of the block has finished, and with it every read of the tiles
+  // (and every TMA write: each was waited for before its MMAs).
+  const bool ok = wait(&done, 0);
+  tc_fence_after();
+
+  const int row = (warp & 3) * 32 + lane, half = warp / 4 * (BN / 2);
+  const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's lanes
+  if (split == 1) {
+    if (warp < kConvWarps && ok) {
+#pragma unroll 1
+      for (int m = 0; m < MT; ++m)
+#pragma unroll 1
+        for (int c = 0; c < BN / 2; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(mine + m * BN + half + c, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[g * 8 + j]);
+            store_out<T>(a, m0 + m * 128 + row, n0 + half + c + g * 8, v);
+          }
+        }
+    }
+  } else {
+    // ---- the cluster's sum: 128 rows a phase; part p of the columns belongs to
+    // block p, which receives [source block][column][row] in its shared memory
+    const int part = BN / split;  // columns, 16 at least
+#pragma unroll 1
+    for (int m = 0; m < MT; ++m) {
+      cluster_sync();  // every block's tiles, or last phase's parts, have been read
+      if (warp < kConvWarps) {
+#pragma unroll 1
+        for (int c = half; c < half + BN / 2; c += 16) {
+          uint32_t r[16];
+          if (steps > 0 && ok) {
+            tmem_ld16(mine + m * BN + c, r);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[j] = 0;
+          }
+          const uint32_t to = cluster_map(base + ((rank * part + c % part) * kRedRows + row) * 4, c / part);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) cluster_store(to + j * kRedRows * 4, __uint_as_float(r[j]));
+        }
+      }
+      cluster_sync();
+      if (warp < kConvWarps) {
+        const float* in = reinterpret_cast<const float*>(smem);
+        for (int c = warp / 4 * 8; c < part; c += 16) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = in[(c + j) * kRedRows + row];
+          for (int s = 1; s < split; ++s)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += in[(s * part + c + j) * kRedRows + row];
+          store_out<T>(a, m0 + m * 128 + row, n0 + rank * part + c, v);
+        }
       }
     }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kConvWarps + 1) {
+    tc_fence_after();
+    tmem_free(tmem, C::kCols);
+  }
+}
+
+// dw of no tokens.
+__global__ void __launch_bounds__(256) k_wgrad_zero(const WgradArgs a) {
+  const int64_t n = a.n_out * a.n_in;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+    if (a.dw_dtype == kF32)
+      static_cast<float*>(a.dw)[i] = 0.0f;
+    else
+      static_cast<uint16_t*>(a.dw)[i] = 0;
+  }
+}
+
+struct Plan {
+  int mt, bn, split;
+};
+
+// The tile and split with the least estimated time. A step of MT x BN takes
+// MT * BN * 2 cycles of MMA (128 x 64 tokens at 4096 products a cycle); a
+// block costs a fixed start and its outputs' way out, more through a cluster.
+Plan wgrad_plan(int64_t tokens, int64_t n_out, int64_t n_in, int sms) {
+  const int64_t steps = (tokens + kStep - 1) / kStep;
+  static const int shapes[][2] = {{2, 256}, {1, 256}, {1, 128}};
+  Plan best{1, 128, 1};
+  double least = 1e300;
+  for (const auto& sh : shapes)
+    for (int split = 1; split <= 8; split *= 2) {
+      if (split > 1 && split > steps) break;
+      const double tiles = (double)((n_out + sh[0] * 128 - 1) / (sh[0] * 128)) * ((n_in + sh[1] - 1) / sh[1]);
+      const double waves = (double)(int64_t)((tiles * split + sms - 1) / sms);
+      const double mma = 2.0 * sh[0] * sh[1];
+      const double out = sh[0] * sh[1] * (split > 1 ? 12.0 : 6.0);
+      const double t = waves * (3000.0 + out + mma * (double)((steps + split - 1) / split));
+      if (t < least) {
+        least = t;
+        best = Plan{sh[0], sh[1], split};
+      }
+    }
+  return best;
+}
+
+template <typename T, int MT, int BN>
+cudaError_t run(const WgradArgs& a, int split, cudaStream_t s) {
+  using C = Tile<MT, BN>;
+  CUtensorMap map;
+  const uint64_t extent[2] = {(uint64_t)a.n_out, (uint64_t)a.tokens}, strides[1] = {(uint64_t)a.dy_stride * 2};
+  if (!make_tensor_map(&map, a.dy, a.dtype == kBF16, 2, extent, strides, kStep)) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(k_wgrad<T, MT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  const int n_tiles = (a.n_in + BN - 1) / BN;
+  const int64_t m_tiles = (a.n_out + MT * 128 - 1) / (MT * 128);
+  const int64_t steps = (a.tokens + kStep - 1) / kStep;
+  if (m_tiles * n_tiles * split > 0x7FFFFFFFll || a.tokens > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(m_tiles * n_tiles * split));
+  cfg.blockDim = dim3(kWgThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_wgrad<T, MT, BN>, map, a, n_tiles, split, (int)((steps + split - 1) / split));
+}
+
+template <typename T>
+cudaError_t wgrad_t(const WgradArgs& a, int sms, cudaStream_t s) {
+  const Plan p = wgrad_plan(a.tokens, a.n_out, a.n_in, sms);
+  if (p.mt == 2) return run<T, 2, 256>(a, p.split, s);
+  if (p.bn == 256) return run<T, 1, 256>(a, p.split, s);
+  return run<T, 1, 128>(a, p.split, s);
 }
 
 }  // namespace
 
-// No kernel of the block operators waits on anything yet.
 cudaError_t block_error_read_clear(unsigned* value, cudaStream_t s) {
-  *value = 0;
-  return cudaStreamSynchronize(s);
+  cudaError_t e = cudaMemcpyFromSymbolAsync(value, g_wgrad_error, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+  if (e != cudaSuccess) return e;
+  e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess || *value == 0) return e;
+  const unsigned zero = 0;
+  e = cudaMemcpyToSymbolAsync(g_wgrad_error, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
+  return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
 }
 
 cudaError_t launch_wgrad(const WgradArgs& a, int sms, cudaStream_t s) {
-  (void)sms;
-  const dim3 grid((a.n_in + kTile - 1) / kTile, (unsigned)((a.n_out + kTile - 1) / kTile));
-  if (a.dtype == kF16)
-    k_wgrad<__half><<<grid, 256, 0, s>>>(a);
-  else
-    k_wgrad<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.tokens == 0) {
+    if (a.accumulate) return cudaSuccess;
+    k_wgrad_zero<<<sms * 4, 256, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  return a.dtype == kF16 ? wgrad_t<__half>(a, sms, s) : wgrad_t<__nv_bfloat16>(a, sms, s);
 }
 
 }  // namespace zg
