@@ -3,7 +3,7 @@
 //
 // On the tensor cores (tcgen05, fp32 sums in TMEM): both operands have the
 // contraction (tokens) as their outer dimension, so both are MN-major tiles.
-// dy comes by TMA. X goes through registers: eight warps read the codes from
+// dy comes by TMA. X goes through registers: sixteen warps read the codes from
 // global memory one step ahead, turn each into dy's type (an int8 code and a
 // power-of-two scale: exact in bf16) and write the swizzled tile, so the
 // 16-bit activation never exists in global memory.
@@ -25,20 +25,34 @@ namespace {
 
 __device__ unsigned g_wgrad_error;
 
-constexpr int kConvWarps = 8;
+constexpr int kConvWarps = 16;
+constexpr int kParts = kConvWarps / 4;             // warps that share 32 rows of the outputs
+constexpr int kWarpRows = 64 / kConvWarps;         // tokens of a step that a warp converts
 constexpr int kWgThreads = (kConvWarps + 2) * 32;  // converters, the TMA warp, the MMA warp
 constexpr int kStep = 64;                          // tokens a step
 constexpr int kChunk = kStep * 128;                // bytes of 64 columns x 64 tokens
 constexpr int kRedRows = 128;
 
-template <int MT, int BN>
+// Steps whose sums stay in one accumulator when dw is fp32. The tensor core
+// truncates each addition to the running sum, so its error grows with the
+// number of additions in a row: 6.6e-6 of the result after 512 of them (8192
+// tokens). After 16 steps (64 additions) the sums are moved to a second
+// accumulator with rounded additions, which keeps the error below 1e-6. A
+// 16-bit dw is rounded 1000 times more coarsely and skips this.
+constexpr int kRun = 16;
+
+// ROUND: with the second accumulator, MT x BN columns further.
+template <int MT, int BN, bool ROUND>
 struct Tile {
   static constexpr int kABytes = MT * 2 * kChunk, kBBytes = BN / 64 * kChunk;
   static constexpr int kStage = kABytes + kBBytes;
   static constexpr int kStages = 196608 / kStage < 6 ? 196608 / kStage : 6;
   static constexpr int kRed = kRedRows * BN * 4;  // a phase of the cluster's sum
   static constexpr int kSmem = (kStages * kStage > kRed ? kStages * kStage : kRed) + 1024;
-  static constexpr int kCols = MT * BN < 128 ? 128 : MT * BN;  // TMEM columns
+  static constexpr int kCols = MT * BN * (ROUND ? 2 : 1);  // TMEM columns
+  // Steps that the converters' loads run ahead: about 2000 cycles of MMA, which
+  // covers the memory's latency under load.
+  static constexpr int kAhead = MT * BN == 512 ? 3 : MT * BN == 256 ? 4 : 6;
   static_assert((kCols & (kCols - 1)) == 0 && kCols <= 512, "a power of two");
 };
 
@@ -55,30 +69,42 @@ __device__ __forceinline__ uint32_t codes_bf16(uint32_t w, int p, __nv_bfloat162
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 8 codes restored in T; their group's scale byte is byte `at` of w.
 template <typename T>
-__device__ __forceinline__ uint4 restore8(uint2 q, uint32_t byte);
+__device__ __forceinline__ uint4 restore8(uint2 q, uint32_t w, int at);
 
 template <>
-__device__ __forceinline__ uint4 restore8<__nv_bfloat16>(uint2 q, uint32_t byte) {
-  // the scale as a bf16: its exponent byte; 2^-127 is subnormal, 255 stands for NaN
-  const uint32_t b = byte == 0 ? 0x0040u : byte == 255 ? 0x7FC0u : byte << 7;
-  const uint32_t bb = b | b << 16;
-  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&bb);
+__device__ __forceinline__ uint4 restore8<__nv_bfloat16>(uint2 q, uint32_t w, int at) {
+  // the scale as a bf16 pair: its exponent byte; 0 stands for the subnormal
+  // 2^-127, 255 for NaN
+  uint32_t b = __byte_perm(w, 0, 0x4040 | at | at << 8) << 7;
+  b = max(b, 0x00400040u);
+  if (b >= 0x7F807F80u) b = 0x7FC07FC0u;
+  const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&b);
   return make_uint4(codes_bf16(q.x, 0, s), codes_bf16(q.x, 1, s), codes_bf16(q.y, 0, s), codes_bf16(q.y, 1, s));
 }
 
 template <>
-__device__ __forceinline__ uint4 restore8<__half>(uint2 q, uint32_t byte) {
-  // fp16 may not hold the result: one fp32 product (exact), one rounding
-  const float s = act_scale(byte);
+__device__ __forceinline__ uint4 restore8<__half>(uint2 q, uint32_t scales, int at) {
+  // 1024 + (code + 128) is an fp16 number made by a byte move; taking away 1152
+  // leaves the code. Its product with the scale may leave fp16's range, so the
+  // scale goes in two powers of two of which the first keeps the code exact:
+  // one rounding, as if the product had been rounded at once.
+  const uint32_t byte = scales >> at * 8 & 0xFFu;
+  const int e = static_cast<int>(byte) - 127;
+  const int e1 = max(-14, min(8, e)), e2 = max(-24, min(15, e - e1));
+  const uint32_t s1 = static_cast<uint32_t>(e1 + 15) << 10;
+  const uint32_t s2 = byte == 255 ? 0x7E00u
+                      : e2 >= -14 ? static_cast<uint32_t>(e2 + 15) << 10 : 1u << (e2 + 24);
+  const uint32_t p1 = s1 | s1 << 16, p2 = s2 | s2 << 16, off = 0xE480E480u;  // -1152
+  auto half2_of = [](uint32_t u) { return *reinterpret_cast<const __half2*>(&u); };
   uint4 r;
   uint32_t* o = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    const uint32_t w = p < 2 ? q.x : q.y;
-    const float lo = static_cast<float>(static_cast<int8_t>(w >> 16 * (p & 1))) * s;
-    const float hi = static_cast<float>(static_cast<int8_t>(w >> (16 * (p & 1) + 8))) * s;
-    const __half2 h = __floats2half2_rn(lo, hi);
+    const uint32_t w = (p < 2 ? q.x : q.y) ^ 0x80808080u;
+    const uint32_t m = __byte_perm(w, 0x64646464u, p & 1 ? 0x4342 : 0x4140);
+    const __half2 h = __hmul2(__hmul2(__hadd2(half2_of(m), half2_of(off)), half2_of(p1)), half2_of(p2));
     o[p] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return r;
@@ -117,12 +143,21 @@ __device__ __forceinline__ void store_out(const WgradArgs& a, int64_t m, int n, 
   }
 }
 
-template <typename T, int MT, int BN>
+// r += 32 columns of TMEM.
+__device__ __forceinline__ void add32(uint32_t addr, uint32_t (&r)[32]) {
+  uint32_t t[32];
+  tmem_ld32(addr, t);
+  tmem_wait_ld();
+#pragma unroll
+  for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(t[j]));
+}
+
+template <typename T, int MT, int BN, bool ROUND>
 __global__ void __launch_bounds__(kWgThreads, 1)
     k_wgrad(const __grid_constant__ CUtensorMap map, const WgradArgs a, int n_tiles, int split, int per_split) {
-  using C = Tile<MT, BN>;
+  using C = Tile<MT, BN, ROUND>;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], done;
+  __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], done, moved;
   __shared__ uint32_t tmem_slot, abort_word;
   // the swizzle is a function of address bits: tiles start on 1024 bytes
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -141,6 +176,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       mbar_init(&empty[s], 1);
     }
     mbar_init(&done, 1);
+    mbar_init(&moved, kConvWarps);
     abort_word = 0;
     mbar_init_fence();
     tma_prefetch(&map);
@@ -152,41 +188,102 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   const uint32_t tmem = tmem_slot;
   const Waiter wait{&abort_word, &g_wgrad_error};
 
+  const int row = (warp & 3) * 32 + lane, half = warp / 4 * (BN / kParts);
+  const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's lanes
+  const int runs = ROUND ? (steps + kRun - 1) / kRun : 1;
+
   if (warp < kConvWarps) {
-    // ---- converters: a warp takes 8 tokens of a step, a lane 8 columns of a row
+    // ---- converters: a warp takes 4 tokens of a step, a lane 8 columns of a row
     constexpr int kLanes = BN / 8;        // lanes a row
     constexpr int kRows = 32 / kLanes;    // rows a round
-    constexpr int kRounds = 8 / kRows;
-    const int c = lane % kLanes * 8, r0 = warp * 8 + lane / kLanes;
-    const bool in = n0 + c < a.pitch;
-    uint2 q[kRounds];
-    uint32_t b[kRounds];
-    auto fetch = [&](int step) {
+    constexpr int kRounds = kWarpRows / kRows;
+    constexpr int kAhead = C::kAhead;
+    const int c = lane % kLanes * 8, r0 = warp * kWarpRows + lane / kLanes;
+    // A row's scales are BN / 32 bytes. The warp's rows of them are one word in
+    // each of the first lanes, handed round when used.
+    constexpr int kWords = BN / 128;
+    const int srow = warp * kWarpRows + lane / kWords % kWarpRows, at = lane / 4 & 3;
+    // Columns past the pitch are outputs that nobody stores, tokens past the
+    // last meet zeros of dy: both read what is there instead (the last columns,
+    // the last token), so no load needs a condition. The last token's own NaN
+    // reaches only columns that it makes NaN anyway.
+    const int8_t* qp = a.q + min(n0 + c, a.pitch - 8);
+    const uint8_t* sp = a.scales + min(n0 + lane % kWords * 128, a.pitch - 128) / kActGroup;
+    const int q_row = kRows * a.pitch, s_pitch = a.pitch / kActGroup;
+    uint2 q[kAhead][kRounds];
+    uint32_t b[kAhead];
+    int fetched = 0;  // steps so far; fetch is called for each in turn
+    auto fetch = [&](int slot) {
+      if (fetched >= steps) return;
+      const int64_t t0 = (first + fetched++) * kStep;
+      if (t0 + kStep <= a.tokens) {
+        const int8_t* p = qp + (t0 + r0) * a.pitch;
 #pragma unroll
-      for (int i = 0; i < kRounds; ++i) {
-        const int64_t t = (first + step) * kStep + r0 + i * kRows;
-        q[i] = make_uint2(0, 0);
-        b[i] = 0;
-        if (in && step < steps && t < a.tokens) {
-          q[i] = *reinterpret_cast<const uint2*>(a.q + t * a.pitch + n0 + c);
-          b[i] = a.scales[t * (a.pitch / kActGroup) + (n0 + c) / kActGroup];
-        }
+        for (int i = 0; i < kRounds; ++i) q[slot][i] = *reinterpret_cast<const uint2*>(p + (int64_t)i * q_row);
+        b[slot] = *reinterpret_cast<const uint32_t*>(sp + (t0 + srow) * s_pitch);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i)
+          q[slot][i] = *reinterpret_cast<const uint2*>(qp + min(t0 + r0 + i * kRows, a.tokens - 1) * a.pitch);
+        b[slot] = *reinterpret_cast<const uint32_t*>(sp + min(t0 + srow, a.tokens - 1) * s_pitch);
       }
     };
-    fetch(0);
-    for (int step = 0; step < steps; ++step) {
-      const int s = step % C::kStages;
-      if (step >= C::kStages && !wait(&empty[s], (step / C::kStages - 1) & 1)) break;
-      uint8_t* tile_b = smem + s * C::kStage + C::kABytes + c / 64 * kChunk;
+    int place[kRounds];  // of the lane's 16 bytes in a B tile
 #pragma unroll
-      for (int i = 0; i < kRounds; ++i) {
-        const int r = r0 + i * kRows;
-        *reinterpret_cast<uint4*>(tile_b + r * 128 + ((c / 8 % 8) ^ (r & 7)) * 16) = restore8<T>(q[i], b[i]);
-      }
-      fetch(step + 1);
-      fence_async_smem();
+    for (int k = 0; k < kRounds; ++k) {
+      const int r = r0 + k * kRows;
+      place[k] = C::kABytes + c / 64 * kChunk + r * 128 + ((c / 8 % 8) ^ (r & 7)) * 16;
+    }
+    // Add the first accumulator to the second (run 0: copy), rounded.
+    auto move = [&](int run) {
+      if (!wait(&done, run & 1)) return false;
+      tc_fence_after();
+#pragma unroll 1
+      for (int m = 0; m < MT; ++m)
+#pragma unroll 1
+        for (int k = m * BN + half; k < m * BN + half + BN / kParts; k += 32) {
+          uint32_t r[32];
+          tmem_ld32(mine + k, r);
+          if (run > 0) add32(mine + MT * BN + k, r);
+          tmem_wait_ld();
+          tmem_st32(mine + MT * BN + k, r);
+        }
+      tmem_wait_st();
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&full[s]);
+      if (lane == 0) mbar_arrive(&moved);
+      return true;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(i);
+    bool go = true;
+    int s = 0;
+    uint32_t turn = 1;  // of the stage's barrier: the first round waits for nothing
+    for (int base_step = 0; base_step < steps && go; base_step += kAhead) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int step = base_step + i;
+        if (step >= steps) break;
+        // the stages ahead are filled first: then the finished run is moved
+        if (ROUND && step >= kRun + C::kStages - 1 && (step - C::kStages + 1) % kRun == 0)
+          go = move((step - C::kStages + 1) / kRun - 1);
+        if (!go || !(go = wait(&empty[s], turn))) break;
+        uint8_t* stage = smem + s * C::kStage;
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k) {
+          const uint32_t w = __shfl_sync(0xFFFFFFFFu, b[i], k * 2 + lane / 16);
+          *reinterpret_cast<uint4*>(stage + place[k]) = restore8<T>(q[i][k], w, at);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+        fetch(i);
+        if (++s == C::kStages) s = 0, turn ^= 1;
+      }
+    }
+    if (ROUND) {  // runs that ended within the last stages' reach, but the last
+      const int told = steps >= kRun + C::kStages ? (steps - C::kStages) / kRun : 0;
+      for (int run = told; run + 1 < runs && go; ++run) go = move(run);
     }
   } else if (warp == kConvWarps) {
     // ---- dy tiles by TMA
@@ -220,8 +317,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 #pragma unroll
           for (int m = 0; m < MT; ++m)
             mma_ss(tmem + m * BN, smem_desc(at + m * 2 * kChunk + k * 2048, kChunk, 1024),
-                   smem_desc(at + C::kABytes + k * 2048, kChunk, 1024), idesc, step > 0 || k > 0);
+                   smem_desc(at + C::kABytes + k * 2048, kChunk, 1024), idesc,
+                   (ROUND ? step % kRun : step) > 0 || k > 0);
         mma_commit(&empty[s]);
+        if (ROUND && step % kRun == kRun - 1 && step + 1 < steps) {
+          mma_commit(&done);
+          if (!wait(&moved, (step / kRun) & 1)) break;
+          tc_fence_after();
+        }
       }
       mma_commit(&done);
     }
@@ -229,19 +332,18 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   }
   // Every MMA of the block has finished, and with it every read of the tiles
   // (and every TMA write: each was waited for before its MMAs).
-  const bool ok = wait(&done, 0);
+  const bool ok = wait(&done, steps > 0 ? (runs - 1) & 1 : 0);
   tc_fence_after();
 
-  const int row = (warp & 3) * 32 + lane, half = warp / 4 * (BN / 2);
-  const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's lanes
   if (split == 1) {
     if (warp < kConvWarps && ok) {
 #pragma unroll 1
       for (int m = 0; m < MT; ++m)
 #pragma unroll 1
-        for (int c = 0; c < BN / 2; c += 32) {
+        for (int c = 0; c < BN / kParts; c += 32) {
           uint32_t r[32];
           tmem_ld32(mine + m * BN + half + c, r);
+          if (ROUND && runs > 1) add32(mine + (MT + m) * BN + half + c, r);
           tmem_wait_ld();
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
@@ -261,10 +363,17 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       cluster_sync();  // every block's tiles, or last phase's parts, have been read
       if (warp < kConvWarps) {
 #pragma unroll 1
-        for (int c = half; c < half + BN / 2; c += 16) {
+        for (int c = half; c < half + BN / kParts; c += 16) {
           uint32_t r[16];
           if (steps > 0 && ok) {
             tmem_ld16(mine + m * BN + c, r);
+            if (ROUND && runs > 1) {
+              uint32_t t[16];
+              tmem_ld16(mine + (MT + m) * BN + c, t);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(t[j]));
+            }
             tmem_wait_ld();
           } else {
 #pragma unroll
@@ -278,7 +387,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       cluster_sync();
       if (warp < kConvWarps) {
         const float* in = reinterpret_cast<const float*>(smem);
-        for (int c = warp / 4 * 8; c < part; c += 16) {
+        for (int c = warp / 4 * 8; c < part; c += 8 * kParts) {
           float v[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] = in[(c + j) * kRedRows + row];
@@ -316,14 +425,14 @@ struct Plan {
 // The tile and split with the least estimated time. A step of MT x BN takes
 // MT * BN * 2 cycles of MMA (128 x 64 tokens at 4096 products a cycle); a
 // block costs a fixed start and its outputs' way out, more through a cluster.
-Plan wgrad_plan(int64_t tokens, int64_t n_out, int64_t n_in, int sms) {
+Plan wgrad_plan(int64_t tokens, int64_t n_out, int64_t n_in, bool round, int sms) {
   const int64_t steps = (tokens + kStep - 1) / kStep;
-  static const int shapes[][2] = {{2, 256}, {1, 256}, {1, 128}};
+  static const int shapes[][2] = {{2, 256}, {2, 128}, {1, 128}};
   Plan best{1, 128, 1};
   double least = 1e300;
   for (const auto& sh : shapes)
     for (int split = 1; split <= 8; split *= 2) {
-      if (split > 1 && split > steps) break;
+      if ((split > 1 && split > steps) || (round && sh[1] == 256)) break;
       const double tiles = (double)((n_out + sh[0] * 128 - 1) / (sh[0] * 128)) * ((n_in + sh[1] - 1) / sh[1]);
       const double waves = (double)(int64_t)((tiles * split + sms - 1) / sms);
       const double mma = 2.0 * sh[0] * sh[1];
@@ -337,13 +446,13 @@ Plan wgrad_plan(int64_t tokens, int64_t n_out, int64_t n_in, int sms) {
   return best;
 }
 
-template <typename T, int MT, int BN>
+template <typename T, int MT, int BN, bool ROUND>
 cudaError_t run(const WgradArgs& a, int split, cudaStream_t s) {
-  using C = Tile<MT, BN>;
+  using C = Tile<MT, BN, ROUND>;
   CUtensorMap map;
   const uint64_t extent[2] = {(uint64_t)a.n_out, (uint64_t)a.tokens}, strides[1] = {(uint64_t)a.dy_stride * 2};
   if (!make_tensor_map(&map, a.dy, a.dtype == kBF16, 2, extent, strides, kStep)) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(k_wgrad<T, MT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(k_wgrad<T, MT, BN, ROUND>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   const int n_tiles = (a.n_in + BN - 1) / BN;
   const int64_t m_tiles = (a.n_out + MT * 128 - 1) / (MT * 128);
@@ -360,15 +469,17 @@ cudaError_t run(const WgradArgs& a, int split, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_wgrad<T, MT, BN>, map, a, n_tiles, split, (int)((steps + split - 1) / split));
+  return cudaLaunchKernelEx(&cfg, k_wgrad<T, MT, BN, ROUND>, map, a, n_tiles, split, (int)((steps + split - 1) / split));
 }
 
 template <typename T>
 cudaError_t wgrad_t(const WgradArgs& a, int sms, cudaStream_t s) {
-  const Plan p = wgrad_plan(a.tokens, a.n_out, a.n_in, sms);
-  if (p.mt == 2) return run<T, 2, 256>(a, p.split, s);
-  if (p.bn == 256) return run<T, 1, 256>(a, p.split, s);
-  return run<T, 1, 128>(a, p.split, s);
+  // sums of up to kRun steps stay in one accumulator either way
+  const bool round = a.dw_dtype == kF32 && a.tokens > kRun * kStep;
+  const Plan p = wgrad_plan(a.tokens, a.n_out, a.n_in, round, sms);
+  if (round) return p.mt == 2 ? run<T, 2, 128, true>(a, p.split, s) : run<T, 1, 128, true>(a, p.split, s);
+  if (p.bn == 256) return run<T, 2, 256, false>(a, p.split, s);
+  return p.mt == 2 ? run<T, 2, 128, false>(a, p.split, s) : run<T, 1, 128, false>(a, p.split, s);
 }
 
 }  // namespace
