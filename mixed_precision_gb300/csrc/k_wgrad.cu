@@ -27,7 +27,6 @@ __device__ unsigned g_wgrad_error;
 
 constexpr int kConvWarps = 16;
 constexpr int kParts = kConvWarps / 4;             // warps that share 32 rows of the outputs
-constexpr int kWarpRows = 64 / kConvWarps;         // tokens of a step that a warp converts
 constexpr int kWgThreads = (kConvWarps + 2) * 32;  // converters, the TMA warp, the MMA warp
 constexpr int kStep = 64;                          // tokens a step
 constexpr int kChunk = kStep * 128;                // bytes of 64 columns x 64 tokens
@@ -50,9 +49,14 @@ struct Tile {
   static constexpr int kRed = kRedRows * BN * 4;  // a phase of the cluster's sum
   static constexpr int kSmem = (kStages * kStage > kRed ? kStages * kStage : kRed) + 1024;
   static constexpr int kCols = MT * BN * (ROUND ? 2 : 1);  // TMEM columns
-  // Steps that the converters' loads run ahead: about 2000 cycles of MMA, which
-  // covers the memory's latency under load.
-  static constexpr int kAhead = MT * BN == 512 ? 3 : MT * BN == 256 ? 4 : 6;
+  // The converter warps work in groups on neighbouring steps: a step's chain
+  // (wait, convert, fence, arrive) takes longer than its MMAs do in the smaller
+  // tiles, so more of them overlap there.
+  static constexpr int kGroups = BN == 256 ? 2 : 4;
+  static constexpr int kWarpRows = kStep * kGroups / kConvWarps;  // tokens of a step that a warp converts
+  // Own steps that a warp's loads run ahead: kGroups steps each, which covers
+  // the memory's latency under load.
+  static constexpr int kAhead = 2;
   static_assert((kCols & (kCols - 1)) == 0 && kCols <= 512, "a power of two");
 };
 
@@ -172,7 +176,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1 + kConvWarps);
+      mbar_init(&full[s], 1 + kConvWarps / C::kGroups);
       mbar_init(&empty[s], 1);
     }
     mbar_init(&done, 1);
@@ -193,16 +197,18 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   const int runs = ROUND ? (steps + kRun - 1) / kRun : 1;
 
   if (warp < kConvWarps) {
-    // ---- converters: a warp takes 4 tokens of a step, a lane 8 columns of a row
+    // ---- converters: a warp takes kWarpRows tokens of every kGroups-th step, a lane 8 columns of a row
     constexpr int kLanes = BN / 8;        // lanes a row
     constexpr int kRows = 32 / kLanes;    // rows a round
-    constexpr int kRounds = kWarpRows / kRows;
+    constexpr int kRounds = C::kWarpRows / kRows;
+    constexpr int kTeam = kConvWarps / C::kGroups;
+    const int group = warp / kTeam, member = warp % kTeam;
     constexpr int kAhead = C::kAhead;
-    const int c = lane % kLanes * 8, r0 = warp * kWarpRows + lane / kLanes;
+    const int c = lane % kLanes * 8, r0 = member * C::kWarpRows + lane / kLanes;
     // A row's scales are BN / 32 bytes. The warp's rows of them are one word in
     // each of the first lanes, handed round when used.
     constexpr int kWords = BN / 128;
-    const int srow = warp * kWarpRows + lane / kWords % kWarpRows, at = lane / 4 & 3;
+    const int srow = member * C::kWarpRows + lane / kWords % C::kWarpRows, at = lane / 4 & 3;
     // Columns past the pitch are outputs that nobody stores, tokens past the
     // last meet zeros of dy: both read what is there instead (the last columns,
     // the last token), so no load needs a condition. The last token's own NaN
@@ -212,10 +218,9 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     const int q_row = kRows * a.pitch, s_pitch = a.pitch / kActGroup;
     uint2 q[kAhead][kRounds];
     uint32_t b[kAhead];
-    int fetched = 0;  // steps so far; fetch is called for each in turn
-    auto fetch = [&](int slot) {
-      if (fetched >= steps) return;
-      const int64_t t0 = (first + fetched++) * kStep;
+    auto fetch = [&](int slot, int step) {
+      if (step >= steps) return;
+      const int64_t t0 = (first + step) * kStep;
       if (t0 + kStep <= a.tokens) {
         const int8_t* p = qp + (t0 + r0) * a.pitch;
 #pragma unroll
@@ -255,36 +260,34 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       return true;
     };
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(i);
+    for (int i = 0; i < kAhead; ++i) fetch(i, group + i * C::kGroups);
     bool go = true;
-    int s = 0;
-    uint32_t turn = 1;  // of the stage's barrier: the first round waits for nothing
-    for (int base_step = 0; base_step < steps && go; base_step += kAhead) {
+    int run = 0;  // runs moved
+    for (int base_step = group; base_step < steps && go; base_step += kAhead * C::kGroups) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int step = base_step + i;
+        const int step = base_step + i * C::kGroups;
         if (step >= steps) break;
-        // the stages ahead are filled first: then the finished run is moved
-        if (ROUND && step >= kRun + C::kStages - 1 && (step - C::kStages + 1) % kRun == 0)
-          go = move((step - C::kStages + 1) / kRun - 1);
-        if (!go || !(go = wait(&empty[s], turn))) break;
+        // A stage that comes free only after the next run has begun: the run
+        // before is moved first, and not before the stages ahead are filled.
+        if (ROUND)
+          while (go && run + 1 < runs && step >= (run + 1) * kRun + C::kStages) go = move(run++);
+        const int s = step % C::kStages;
+        if (!go || !(go = wait(&empty[s], (step / C::kStages - 1) & 1))) break;
         uint8_t* stage = smem + s * C::kStage;
 #pragma unroll
         for (int k = 0; k < kRounds; ++k) {
-          const uint32_t w = __shfl_sync(0xFFFFFFFFu, b[i], k * 2 + lane / 16);
+          const uint32_t w = __shfl_sync(0xFFFFFFFFu, b[i], k * kRows * kWords + lane / 16);
           *reinterpret_cast<uint4*>(stage + place[k]) = restore8<T>(q[i][k], w, at);
         }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
-        fetch(i);
-        if (++s == C::kStages) s = 0, turn ^= 1;
+        fetch(i, step + kAhead * C::kGroups);
       }
     }
-    if (ROUND) {  // runs that ended within the last stages' reach, but the last
-      const int told = steps >= kRun + C::kStages ? (steps - C::kStages) / kRun : 0;
-      for (int run = told; run + 1 < runs && go; ++run) go = move(run);
-    }
+    if (ROUND)
+      while (go && run + 1 < runs) go = move(run++);
   } else if (warp == kConvWarps) {
     // ---- dy tiles by TMA
     if (lane == 0) {
