@@ -1,0 +1,112 @@
+// What the attention kernels share: the keys a row sees, packed fp32 pairs,
+// the exponential.
+#pragma once
+
+#include <cstdint>
+
+#include "block.h"
+#include "tc.cuh"
+#include "vec.cuh"
+
+namespace zg {
+
+constexpr int kTile = 128;                  // query rows and keys of a tile
+constexpr int kTileChunk = kTile * 128;     // bytes of 64 head elements x 128 rows
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ int valid_keys(const AttnArgs& a, int64_t b) {
+  const int k_len = static_cast<int>(a.k_len);
+  return a.lengths == nullptr ? k_len : min(max(a.lengths[b], 0), k_len);
+}
+
+// Keys [lo, hi) that query i sees, of `keys` valid ones. (Lengths are at most
+// 2^28 and a window at most their sum, so int holds every sum here.)
+__device__ __forceinline__ void key_range(const AttnArgs& a, int keys, int i, int& lo, int& hi) {
+  const int d = i + static_cast<int>(a.k_len) - static_cast<int>(a.q_len);
+  hi = a.causal ? min(keys, d + 1) : keys;
+  lo = a.window > 0 ? max(0, d - static_cast<int>(a.window) + 1) : 0;
+}
+
+// 2^x; 0 for -inf, about 2^-22 relative error.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Two values rounded to T, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t round2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t round2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t round2<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The 64-wide chunks of a [rows <= 128] x head tile, by one thread.
+template <int DP>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int token, int head, int batch,
+                                          uint64_t* bar) {
+#pragma unroll
+  for (int i = 0; i < DP / 64; ++i) tma_load4(dst + i * kTileChunk, map, i * 64, token, head, batch, bar);
+}
+
+// d = a b^T over the head: both tiles K-major, DP elements.
+template <int DP>
+__device__ __forceinline__ void mma_head(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+#pragma unroll
+  for (int k = 0; k < DP / 16; ++k) {
+    const uint32_t off = k / 4 * kTileChunk + k % 4 * 32;
+    mma_ss(d, smem_desc(a + off, 0, 1024), smem_desc(b + off, 0, 1024), idesc, k > 0);
+  }
+}
+
+// d [+]= a b over 128 rows: a in TMEM, b a tile read with its rows as the
+// contraction (MN-major).
+template <int DP>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+#pragma unroll
+  for (int k = 0; k < kTile / 16; ++k)
+    mma_ts(d, a + k * 8, smem_desc(b + k * 2048, kTileChunk, 1024), idesc, add || k > 0);
+}
+
+// Maps of a [batch, token, head, dim] tensor for tiles of 128 tokens x 64.
+inline bool attn_map(CUtensorMap* map, const void* base, int dtype, const int64_t s[3], int64_t batch, int64_t len,
+                     int heads, int dim) {
+  const uint64_t n[4] = {(uint64_t)dim, (uint64_t)len, (uint64_t)heads, (uint64_t)batch};
+  const uint64_t b[3] = {(uint64_t)s[1] * 2, (uint64_t)s[2] * 2, (uint64_t)s[0] * 2};
+  return make_tensor_map(map, base, dtype == kBF16, 4, n, b, kTile);
+}
+
+}  // namespace zg

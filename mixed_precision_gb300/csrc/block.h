@@ -79,7 +79,9 @@ struct AttnArgs {
 cudaError_t launch_attention_forward(const AttnArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s);
 
-// The device's error word of the block operators (bit kErrWaitTimeout).
-cudaError_t block_error_read_clear(unsigned* value, cudaStream_t s);
+// The kernels' error words on the current device (bit kErrWaitTimeout): *value
+// |= the word, which is cleared. Each synchronises the stream.
+cudaError_t wgrad_error(unsigned* value, cudaStream_t s);
+cudaError_t attn_fwd_error(unsigned* value, cudaStream_t s);
 
 }  // namespace zg

@@ -75,8 +75,8 @@ int device_sms(int* sms) {
   return ZERO_OK;
 }
 
-constexpr int64_t kMaxRows = int64_t(1) << 40;
-constexpr int64_t kMaxStride = int64_t(1) << 40;  // rows x stride stays far inside 64 bits
+constexpr int64_t kMaxRows = int64_t(1) << 31;
+constexpr int64_t kMaxStride = int64_t(1) << 38;  // in bytes below the tensor maps' 2^40
 constexpr int kMaxNormCols = 65536;
 constexpr int64_t kMaxLen = int64_t(1) << 28;
 
@@ -515,8 +515,11 @@ int zero_attention_backward(const zero_attention_desc* desc, const void* dout, c
 int zero_operator_status(void* stream) {
   Range r("zero_operator_status");
   unsigned error = 0;
-  cudaError_t e = block_error_read_clear(&error, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "operator status");
+  cudaError_t (*const words[])(unsigned*, cudaStream_t) = {wgrad_error, attn_fwd_error};
+  for (auto word : words) {
+    cudaError_t e = word(&error, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "operator status");
+  }
   if (error != 0)
     return fail(ZERO_ERR_TIMEOUT, "a bounded wait gave up in a block operator");
   return ZERO_OK;

@@ -1,6 +1,6 @@
-// Attention's training pair, plain form: a warp per row, each lane holding
+// Attention's backward pass, plain form: a warp per row, each lane holding
 // four neighbouring elements of the head, one dot product (five shuffles) per
-// query-key pair, running maximum and sum.
+// query-key pair.
 #include "block.h"
 #include "vec.cuh"
 
@@ -41,36 +41,6 @@ __device__ __forceinline__ void key_range(const AttnArgs& a, int64_t b, int64_t 
   hi = valid_keys(a, b);
   if (a.causal) hi = min(hi, d + 1);
   lo = a.window > 0 ? max((int64_t)0, d - a.window + 1) : 0;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) k_attn_forward(const AttnArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-  if (row >= a.batch * a.q_heads * a.q_len) return;
-  const int d = (threadIdx.x & 31) * 4;
-  const int64_t i = row % a.q_len, h = row / a.q_len % a.q_heads, b = row / a.q_len / a.q_heads;
-  const int64_t c = h / a.group;
-  float q[4], o[4] = {};
-  load4(static_cast<const T*>(a.q) + b * a.qs[0] + i * a.qs[1] + h * a.qs[2], d, a.head_dim, q);
-  int64_t lo, hi;
-  key_range(a, b, i, lo, hi);
-  float top = -INFINITY, total = 0.0f;
-  for (int64_t j = lo; j < hi; ++j) {
-    float k[4], v[4];
-    load4(static_cast<const T*>(a.k) + b * a.ks[0] + j * a.ks[1] + c * a.ks[2], d, a.head_dim, k);
-    load4(static_cast<const T*>(a.v) + b * a.vs[0] + j * a.vs[1] + c * a.vs[2], d, a.head_dim, v);
-    const float s = warp_sum(dot4(q, k)) * a.scale;
-    const float up = fmaxf(top, s), keep = expf(top - up), p = expf(s - up);
-    total = fmaf(total, keep, p);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = fmaf(o[e], keep, p * v[e]);
-    top = up;
-  }
-  const float inv = hi > lo ? 1.0f / total : 0.0f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] *= inv;
-  save4(static_cast<T*>(a.o) + b * a.os[0] + i * a.os[1] + h * a.os[2], d, a.head_dim, o);
-  if ((threadIdx.x & 31) == 0) a.lse[row] = hi > lo ? top + logf(total) : -INFINITY;
 }
 
 template <typename T>
@@ -147,16 +117,6 @@ cudaError_t backward_t(const AttnArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
-
-cudaError_t launch_attention_forward(const AttnArgs& a, int sms, cudaStream_t s) {
-  (void)sms;
-  const int64_t rows = a.batch * a.q_heads * a.q_len;
-  if (a.dtype == kF16)
-    k_attn_forward<__half><<<blocks(rows), kWarps * 32, 0, s>>>(a);
-  else
-    k_attn_forward<__nv_bfloat16><<<blocks(rows), kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s) {
   (void)sms;

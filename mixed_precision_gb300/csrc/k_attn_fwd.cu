@@ -1,0 +1,314 @@
+// Attention forward: o = softmax(scale q k^T) v and the rows' log-sum-exp.
+//
+// A block takes two tiles of 128 query rows that share their keys: tiles of
+// the query heads of one key head, counted tile by tile and head by head, so
+// with two heads a group both tiles are the same rows of two heads. Keys and
+// values pass once through shared memory (TMA) in tiles of 128.
+//   S_t = Q_t K^T      tcgen05, S in TMEM (fp32)
+//   P_t = 2^(c S_t - c m)   a thread per row; P_t (16 bits) over S_t in TMEM
+//   O_t += P_t V       tcgen05, P from TMEM, O in TMEM
+// The two tiles alternate: while four warps turn S_0 into P_0 the tensor core
+// works for tile 1, and the other way round. The row's maximum m is kept as
+// it was until it grows by more than 8 in the exponent of two: P stays
+// below 2^8, sums and O are fp32, and O is rescaled rarely (once or twice a
+// row on ordinary data) instead of in every tile.
+//
+// Keys past a batch entry's length: their S is replaced by -inf, and their
+// rows of V (whatever they hold) by zeros in shared memory.
+#include <type_traits>
+
+#include "attn.cuh"
+
+namespace zg {
+namespace {
+
+__device__ unsigned g_attn_fwd_error;
+
+constexpr int kFwdThreads = 10 * 32;  // two softmax groups of four warps, the TMA warp, the MMA warp
+constexpr float kStale = 8.0f;        // how far the maximum may lag, as an exponent of two
+
+template <int DP>
+struct Fwd {
+  static constexpr int kTileBytes = DP / 64 * kTileChunk;
+  static constexpr int kSlots = DP == 128 ? 4 : 8;  // keys and values in turn
+  static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024;
+  static constexpr uint32_t kO = 256;  // TMEM: S_0, S_1 at 0, 128; O_0, O_1 from here, DP columns each
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    k_attn_fwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+               const __grid_constant__ CUtensorMap map_v, const AttnArgs a, int q_tiles, int pairs) {
+  using C = Fwd<DP>;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t q_full, kv_full[C::kSlots], kv_empty[C::kSlots], s_full[2], p_full[2], o_full;
+  __shared__ uint32_t tmem_slot, abort_word;
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const uint32_t base = smem_u32(smem), ring = base + 2 * C::kTileBytes;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+  // blocks of the last query rows (most keys under a causal mask) come first
+  const int bh = blockIdx.x % (int)(a.batch * a.kv_heads), p = pairs - 1 - blockIdx.x / (int)(a.batch * a.kv_heads);
+  const int c = bh % a.kv_heads, b = bh / a.kv_heads;
+  const int units = q_tiles * a.group;
+  const bool two = 2 * p + 1 < units;
+  const int keys = valid_keys(a, b);
+  int first = 0x7FFFFFFF, last = 0;  // key tiles [first, last) that either tile sees
+  for (int t = 0; t < (two ? 2 : 1); ++t) {
+    const int row0 = (2 * p + t) / a.group * kTile, row1 = min(row0 + kTile, (int)a.q_len) - 1;
+    int lo, hi, skip;
+    key_range(a, keys, row0, lo, skip);
+    key_range(a, keys, row1, skip, hi);
+    if (lo < hi) {
+      first = min(first, lo / kTile);
+      last = max(last, (hi + kTile - 1) / kTile);
+    }
+  }
+  const int n = max(0, last - first);
+
+  if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 4);
+    }
+    mbar_init(&o_full, 1);
+    abort_word = 0;
+    mbar_init_fence();
+  }
+  if (warp == 9) tmem_alloc(&tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const Waiter wait{&abort_word, &g_attn_fwd_error};
+
+  if (warp == 8) {
+    // ---- TMA: the query tiles, then K_0, V_0, K_1, V_1, ...
+    if (lane == 0 && n > 0) {
+      tma_prefetch(&map_q);
+      tma_prefetch(&map_k);
+      tma_prefetch(&map_v);
+      mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * C::kTileBytes);
+      for (int t = 0; t < (two ? 2 : 1); ++t) {
+        const int u = 2 * p + t;
+        load_tile<DP>(base + t * C::kTileBytes, &map_q, u / a.group * kTile, c * a.group + u % a.group, b, &q_full);
+      }
+      int i = 0;
+      for (; i < 2 * n; ++i) {
+        const int s = i % C::kSlots;
+        if (!wait(&kv_empty[s], (i / C::kSlots - 1) & 1)) break;
+        mbar_arrive_expect_tx(&kv_full[s], C::kTileBytes);
+        load_tile<DP>(ring + s * C::kTileBytes, i & 1 ? &map_v : &map_k, (first + i / 2) * kTile, c, b, &kv_full[s]);
+      }
+      if (i < 2 * n) {  // gave up: leave the copies in flight time to land
+        mbar_wait(&q_full, 0, kSpinLimit >> 10);
+        for (int k = max(0, i - C::kSlots); k < i; ++k)
+          mbar_wait(&kv_full[k % C::kSlots], (k / C::kSlots) & 1, kSpinLimit >> 10);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ---- the tensor cores
+    if (lane == 0 && n > 0) {
+      constexpr bool bf16 = !std::is_same<T, __half>::value;
+      constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
+      constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
+      const int tiles = two ? 2 : 1;
+      auto slot = [&](int i) { return ring + i % C::kSlots * C::kTileBytes; };
+      auto arrived = [&](int i) {
+        const bool ok = wait(&kv_full[i % C::kSlots], (i / C::kSlots) & 1);
+        tc_fence_after();
+        return ok;
+      };
+      bool go = wait(&q_full, 0) && arrived(0);
+      for (int t = 0; go && t < tiles; ++t) {
+        mma_head<DP>(tmem + t * kTile, base + t * C::kTileBytes, slot(0), by_head);
+        mma_commit(&s_full[t]);
+      }
+      if (go) mma_commit(&kv_empty[0]);
+      for (int j = 0; go && j < n; ++j) {
+        const int kn = 2 * j + 2, v = 2 * j + 1;
+        const bool more = j + 1 < n;
+        go = arrived(v);
+        for (int t = 0; go && t < tiles; ++t) {
+          if (!(go = wait(&p_full[t], j & 1))) break;
+          tc_fence_after();
+          mma_rows<DP>(tmem + C::kO + t * DP, tmem + t * kTile, slot(v), by_rows, j > 0);
+          if (t == tiles - 1) mma_commit(&kv_empty[v % C::kSlots]);
+          if (!more) continue;
+          if (t == 0 && !(go = arrived(kn))) break;
+          // over P_t, which the product before it reads first
+          mma_head<DP>(tmem + t * kTile, base + t * C::kTileBytes, slot(kn), by_head);
+          mma_commit(&s_full[t]);
+          if (t == tiles - 1) mma_commit(&kv_empty[kn % C::kSlots]);
+        }
+      }
+      mma_commit(&o_full);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax: four warps a tile, a thread a row
+    const int t = warp / 4, u = 2 * p + t;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + C::kO + t * DP;
+    const int i = u / a.group * kTile + (warp & 3) * 32 + lane;  // the query
+    const int64_t h = c * a.group + u % a.group;
+    const float scale2 = a.scale * kLog2e;
+    float top = -INFINITY, total = 0.0f;
+    bool ok = true;
+    if (t == 0 || two) {
+      int lo, hi;
+      key_range(a, keys, i, lo, hi);
+      for (int j = 0; j < n; ++j) {
+        if (!(ok = wait(&s_full[t], j & 1))) break;
+        tc_fence_after();
+        float s[kTile];
+        uint32_t(&r)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(s);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_ld32(s_at + k * 32, r[k]);
+        tmem_wait_ld();
+        const int key0 = (first + j) * kTile;
+        // columns [lo - key0, hi - key0) are seen; most tiles need no mask
+        if (__any_sync(0xFFFFFFFFu, lo > key0 || hi < key0 + kTile)) {
+          const int from = lo - key0, to = hi - key0;
+#pragma unroll
+          for (int k = 0; k < kTile; ++k) s[k] = k >= from && k < to ? s[k] : -INFINITY;
+        }
+        float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int k = 4; k < kTile; ++k) m4[k & 3] = fmaxf(m4[k & 3], s[k]);
+        const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // the first maximum, or one that has grown too far: rescale
+        const bool raise = m > top && (top == -INFINITY || (m - top) * scale2 > kStale);
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+          const float f = raise ? exp2_fast((top - m) * scale2) : 1.0f;
+          if (raise) top = m;
+          total *= f;
+          if (j > 0) {  // O is complete up to the tile before: its product was issued before this S
+#pragma unroll 1
+            for (int k = 0; k < DP; k += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_at + k, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(o_at + k, o);
+            }
+          }
+        }
+        const float minus = top == -INFINITY ? 0.0f : -top * scale2;
+        const uint64_t scale_pair = pair(scale2, scale2), minus_pair = pair(minus, minus);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const int e = half * 64 + 2 * k;
+            float x, y;
+            unpair(fma2(pair(s[e], s[e + 1]), scale_pair, minus_pair), x, y);
+            x = exp2_fast(x);
+            y = exp2_fast(y);
+            sum[k & 1] = add2(sum[k & 1], pair(x, y));
+            w[k] = round2<T>(x, y);
+          }
+          tmem_st32(s_at + half * 32, w);
+        }
+        float x, y;
+        unpair(add2(sum[0], sum[1]), x, y);
+        total += x + y;
+        if (t == 0 && key0 + kTile > keys && keys < a.k_len) {
+          // rows of V past the length: zeros. Tile 0's product is the first to
+          // read them, and waits for this thread.
+          if (!(ok = wait(&kv_full[(2 * j + 1) % C::kSlots], ((2 * j + 1) / C::kSlots) & 1))) break;
+          uint8_t* v = smem + (2 + (2 * j + 1) % C::kSlots) * C::kTileBytes;
+          const int row = (warp & 3) * 32 + lane;
+          if (key0 + row >= keys)
+#pragma unroll
+            for (int k = 0; k < DP / 8; ++k)
+              *reinterpret_cast<uint4*>(v + k / 8 * kTileChunk + row * 128 + k % 8 * 16) = make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);
+      }
+      if (n > 0 && ok) ok = wait(&o_full, 0);
+      tc_fence_after();
+      const bool none = total == 0.0f;  // no key seen (a seen key gives at least 2^-8 ... or NaN)
+      const float inv = none ? 0.0f : 1.0f / total;
+      T* out = static_cast<T*>(a.o) + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2];
+#pragma unroll 1
+      for (int k = 0; k < DP; k += 32) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(o_at + k, o);
+          tmem_wait_ld();
+        }
+        if (i < a.q_len && ok) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            if (k + g * 8 >= a.head_dim) break;
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = none ? 0u
+                          : round2<T>(__uint_as_float(o[g * 8 + 2 * e]) * inv,
+                                      __uint_as_float(o[g * 8 + 2 * e + 1]) * inv);
+            *reinterpret_cast<uint4*>(out + k + g * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (i < a.q_len && ok)
+        a.lse[(b * (int64_t)a.q_heads + h) * a.q_len + i] =
+            none ? -INFINITY : (top * scale2 + log2f(total)) * kLn2;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+template <typename T, int DP>
+cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+  using C = Fwd<DP>;
+  CUtensorMap q, k, v;
+  // without keys nothing is loaded, but the maps still have to be valid
+  const int64_t k_len = a.k_len > 0 ? a.k_len : 1;
+  if (!attn_map(&q, a.q, a.dtype, a.qs, a.batch, a.q_len, a.q_heads, a.head_dim) ||
+      !attn_map(&k, a.k_len > 0 ? a.k : a.q, a.dtype, a.ks, a.batch, k_len, a.kv_heads, a.head_dim) ||
+      !attn_map(&v, a.k_len > 0 ? a.v : a.q, a.dtype, a.vs, a.batch, k_len, a.kv_heads, a.head_dim))
+    return cudaErrorInvalidValue;
+  const int64_t q_tiles = (a.q_len + kTile - 1) / kTile, pairs = (q_tiles * a.group + 1) / 2;
+  const int64_t blocks = pairs * a.batch * a.kv_heads;
+  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(k_attn_fwd<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  k_attn_fwd<T, DP><<<(unsigned)blocks, kFwdThreads, C::kSmem, s>>>(q, k, v, a, (int)q_tiles, (int)pairs);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t forward_t(const AttnArgs& a, cudaStream_t s) {
+  return a.head_dim <= 64 ? run<T, 64>(a, s) : run<T, 128>(a, s);
+}
+
+}  // namespace
+
+ZG_ERROR_WORD(attn_fwd_error, g_attn_fwd_error)
+
+cudaError_t launch_attention_forward(const AttnArgs& a, int sms, cudaStream_t s) {
+  (void)sms;
+  return a.dtype == kF16 ? forward_t<__half>(a, s) : forward_t<__nv_bfloat16>(a, s);
+}
+
+}  // namespace zg

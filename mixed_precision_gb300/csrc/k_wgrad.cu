@@ -13,6 +13,7 @@
 // over its own run of tokens; each block then sends its sums to the block
 // that owns the columns (distributed shared memory), which adds the S parts
 // in order. No atomics, no workspace; the order of every sum is fixed.
+#include <cmath>
 #include <type_traits>
 
 #include "act.cuh"
@@ -425,27 +426,37 @@ struct Plan {
   int mt, bn, split;
 };
 
-// The tile and split with the least estimated time. A step of MT x BN takes
-// MT * BN * 2 cycles of MMA (128 x 64 tokens at 4096 products a cycle); a
-// block costs a fixed start and its outputs' way out, more through a cluster.
+// The tile and split with the least estimated time, in cycles. Measured on one
+// block per SM: a step of 64 tokens takes 1280 cycles in the 256 x 256 tile, 950
+// in 256 x 128 and 730 in 128 x 128 (1220 and 960 with rounded runs), a block
+// about 3000 to start, and its outputs' way out 6 cycles per 128 of them,
+// 28 through a cluster. Clusters leave some SMs idle: 148, 136 and 120 are
+// used by clusters of 2, 4 and 8. At 8192 x 2048 x 1024 the tile of 256 x 256
+// split in 4 takes 40 us, 128 x 128 without a split 59 us; at 4096 x 8192 x 4096
+// the unsplit 256 x 256 tile takes 220 us, 128 x 128 410 us.
 Plan wgrad_plan(int64_t tokens, int64_t n_out, int64_t n_in, bool round, int sms) {
   const int64_t steps = (tokens + kStep - 1) / kStep;
-  static const int shapes[][2] = {{2, 256}, {2, 128}, {1, 128}};
+  static const struct {
+    int mt, bn;
+    double step, step_round;  // step_round 0: not built
+  } shapes[] = {{2, 256, 1280, 0}, {2, 128, 950, 1220}, {1, 128, 730, 960}};
   Plan best{1, 128, 1};
   double least = 1e300;
-  for (const auto& sh : shapes)
-    for (int split = 1; split <= 8; split *= 2) {
-      if ((split > 1 && split > steps) || (round && sh[1] == 256)) break;
-      const double tiles = (double)((n_out + sh[0] * 128 - 1) / (sh[0] * 128)) * ((n_in + sh[1] - 1) / sh[1]);
-      const double waves = (double)(int64_t)((tiles * split + sms - 1) / sms);
-      const double mma = 2.0 * sh[0] * sh[1];
-      const double out = sh[0] * sh[1] * (split > 1 ? 12.0 : 6.0);
-      const double t = waves * (3000.0 + out + mma * (double)((steps + split - 1) / split));
+  for (const auto& sh : shapes) {
+    const double step = round ? sh.step_round : sh.step;
+    if (step == 0) continue;
+    const double tiles = (double)((n_out + sh.mt * 128 - 1) / (sh.mt * 128)) * ((n_in + sh.bn - 1) / sh.bn);
+    for (int split = 1; split <= 8 && split <= steps; split *= 2) {
+      const int used = split == 1 ? sms : split == 2 ? sms - 4 : split == 4 ? sms - 16 : sms - 32;
+      const double waves = std::ceil(tiles * split / (used > split ? used : split));
+      const double out = sh.mt * sh.bn * (split > 1 ? 28.0 : 6.0);
+      const double t = waves * (3000.0 + out + step * (double)((steps + split - 1) / split));
       if (t < least) {
         least = t;
-        best = Plan{sh[0], sh[1], split};
+        best = Plan{sh.mt, sh.bn, split};
       }
     }
+  }
   return best;
 }
 
@@ -487,15 +498,7 @@ cudaError_t wgrad_t(const WgradArgs& a, int sms, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t block_error_read_clear(unsigned* value, cudaStream_t s) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(value, g_wgrad_error, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
-  if (e != cudaSuccess) return e;
-  e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess || *value == 0) return e;
-  const unsigned zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_wgrad_error, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
-  return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
-}
+ZG_ERROR_WORD(wgrad_error, g_wgrad_error)
 
 cudaError_t launch_wgrad(const WgradArgs& a, int sms, cudaStream_t s) {
   if (a.tokens == 0) {

@@ -37,6 +37,20 @@ struct Waiter {
   }
 };
 
+// A translation unit's error word, read and cleared (host): *value |= the word.
+// Synchronises the stream.
+#define ZG_ERROR_WORD(name, word)                                                                          \
+  cudaError_t name(unsigned* value, cudaStream_t s) {                                                      \
+    unsigned now = 0;                                                                                      \
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&now, word, sizeof(now), 0, cudaMemcpyDeviceToHost, s);      \
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);                                                    \
+    if (e != cudaSuccess || now == 0) return e;                                                            \
+    *value |= now;                                                                                         \
+    const unsigned zero = 0;                                                                               \
+    e = cudaMemcpyToSymbolAsync(word, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);                  \
+    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;                                                \
+  }
+
 // ---- TMEM --------------------------------------------------------------------
 
 // One whole warp; cols a power of two, 32..512. The address goes to *slot.
