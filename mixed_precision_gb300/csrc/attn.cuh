@@ -101,6 +101,49 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uin
     mma_ts(d, a + k * 8, smem_desc(b + k * 2048, kTileChunk, 1024), idesc, add || k > 0);
 }
 
+// The same with a's 16-bit columns in two runs of 32, the second 64 columns on:
+// two warps wrote a row, each over its own half of the fp32 columns.
+template <int DP>
+__device__ __forceinline__ void mma_rows_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+#pragma unroll
+  for (int k = 0; k < kTile / 16; ++k)
+    mma_ts(d, a + k / 4 * 64 + k % 4 * 8, smem_desc(b + k * 2048, kTileChunk, 1024), idesc, add || k > 0);
+}
+
+// A row of a tile to zero; the caller fences.
+template <int DP>
+__device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
+#pragma unroll
+  for (int k = 0; k < DP / 8; ++k)
+    *reinterpret_cast<uint4*>(tile + k / 8 * kTileChunk + row * 128 + k % 8 * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// A row of sums in TMEM, times f, rounded to T and stored: elements [0, dim).
+// The whole warp calls it; `live` lanes store.
+template <typename T, int DP>
+__device__ __forceinline__ void store_row(uint32_t addr, float f, T* out, int dim, bool zero, bool live) {
+#pragma unroll 1
+  for (int k = 0; k < DP; k += 32) {
+    uint32_t o[32];
+    if (!zero) {
+      tmem_ld32(addr + k, o);
+      tmem_wait_ld();
+    }
+    if (live) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        if (k + g * 8 >= dim) break;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = zero ? 0u
+                      : round2<T>(__uint_as_float(o[g * 8 + 2 * e]) * f, __uint_as_float(o[g * 8 + 2 * e + 1]) * f);
+        *reinterpret_cast<uint4*>(out + k + g * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+}
+
 // Maps of a [batch, token, head, dim] tensor for tiles of 128 tokens x 64.
 inline bool attn_map(CUtensorMap* map, const void* base, int dtype, const int64_t s[3], int64_t batch, int64_t len,
                      int heads, int dim) {

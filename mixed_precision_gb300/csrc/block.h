@@ -1,6 +1,6 @@
 // Internal interface between the host side of the block operators
 // (block_api.cpp) and their kernels (k_norm.cu, k_act.cu, k_wgrad.cu,
-// k_attention.cu). Not part of the public ABI (include/zero.h is).
+// k_attn_fwd.cu, k_attn_bwd.cu). Not part of the public ABI (include/zero.h is).
 #pragma once
 
 #include <cstdint>
@@ -74,14 +74,16 @@ struct AttnArgs {
   const int32_t* lengths;
   float* lse;
   const float* lse_in;
-  float* delta;  // backward: [batch, q_heads, q_len] row sums of do * o
+  float* stats;  // backward: the rows' statistics (k_attn_bwd.cu)
 };
 cudaError_t launch_attention_forward(const AttnArgs& a, int sms, cudaStream_t s);
+int64_t attention_backward_bytes(const AttnArgs& a);
 cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s);
 
 // The kernels' error words on the current device (bit kErrWaitTimeout): *value
 // |= the word, which is cleared. Each synchronises the stream.
 cudaError_t wgrad_error(unsigned* value, cudaStream_t s);
 cudaError_t attn_fwd_error(unsigned* value, cudaStream_t s);
+cudaError_t attn_bwd_error(unsigned* value, cudaStream_t s);
 
 }  // namespace zg

@@ -212,10 +212,6 @@ int attention_args(const zero_attention_desc* d, bool backward, AttnArgs& a) {
   return ZERO_OK;
 }
 
-int64_t backward_bytes(const AttnArgs& a) {
-  return (a.batch * a.q_heads * a.q_len * 4 + 15) / 16 * 16;
-}
-
 }  // namespace
 
 extern "C" {
@@ -464,7 +460,7 @@ int zero_attention_backward_workspace(const zero_attention_desc* desc, int64_t* 
   if (bytes == nullptr) return fail(ZERO_ERR_INVALID, "bytes is NULL");
   AttnArgs a;
   if (int rc = attention_args(desc, true, a)) return rc;
-  *bytes = backward_bytes(a);
+  *bytes = attention_backward_bytes(a);
   return ZERO_OK;
 }
 
@@ -483,9 +479,9 @@ int zero_attention_backward(const zero_attention_desc* desc, const void* dout, c
     NEED(lse);
     NEED(dq);
     NEED(workspace);
-    if (workspace_bytes < backward_bytes(a))
+    if (workspace_bytes < attention_backward_bytes(a))
       return fail(ZERO_ERR_INVALID, "workspace of %lld bytes, %lld needed",
-                  (long long)workspace_bytes, (long long)backward_bytes(a));
+                  (long long)workspace_bytes, (long long)attention_backward_bytes(a));
   }
   if (a.k_len > 0) {
     NEED(k);
@@ -505,7 +501,7 @@ int zero_attention_backward(const zero_attention_desc* desc, const void* dout, c
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  a.delta = static_cast<float*>(workspace);
+  a.stats = static_cast<float*>(workspace);
   int sms;
   if (int rc = device_sms(&sms)) return rc;
   cudaError_t e = launch_attention_backward(a, sms, static_cast<cudaStream_t>(stream));
@@ -515,7 +511,8 @@ int zero_attention_backward(const zero_attention_desc* desc, const void* dout, c
 int zero_operator_status(void* stream) {
   Range r("zero_operator_status");
   unsigned error = 0;
-  cudaError_t (*const words[])(unsigned*, cudaStream_t) = {wgrad_error, attn_fwd_error};
+  cudaError_t (*const words[])(unsigned*, cudaStream_t) = {wgrad_error, attn_fwd_error,
+                                                            attn_bwd_error};
   for (auto word : words) {
     cudaError_t e = word(&error, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "operator status");

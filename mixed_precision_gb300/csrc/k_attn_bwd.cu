@@ -1,0 +1,510 @@
+// Attention backward. With p = exp(scale q.k - lse) on the pairs seen,
+//   delta = sum_d do o,  dp = do v^T,  ds = p (dp - delta),
+//   dq = scale ds k,  dk = scale ds^T q,  dv = p^T do.
+//
+// Two kernels, both on the tensor cores with p and ds kept in TMEM:
+//   k_attn_dq   a block per 128 query rows of a head, over its key tiles; it
+//               also writes the rows' statistics (-lse in powers of two, -delta).
+//   k_attn_dkv  a block per 128 keys of a key head, over the query tiles of all
+//               heads that share it: dk and dv are sums inside one block.
+// S and dp are computed in both (seven products a tile pair instead of five).
+// In exchange no gradient is added to global memory from two places: no atomic
+// adds, no fp32 copy of dq, and every sum has a fixed order.
+#include <type_traits>
+
+#include "attn.cuh"
+
+namespace zg {
+namespace {
+
+__device__ unsigned g_attn_bwd_error;
+
+constexpr int kBwdThreads = 10 * 32;  // eight softmax warps, the TMA warp, the MMA warp
+constexpr int kStats = 2 * kTile;     // floats of a query tile's statistics
+
+// ---------------------------------------------------------------------------
+// dq
+// ---------------------------------------------------------------------------
+
+template <int DP>
+struct Dq {
+  static constexpr int kTileBytes = DP / 64 * kTileChunk;
+  static constexpr int kK = 3, kV = 2;  // slots: a K tile is used again two tiles later than it is first
+  static constexpr int kSmem = (2 + kK + kV) * kTileBytes + 1024;
+  // TMEM: S twice (ds over it), dp, dq
+  static constexpr uint32_t kDp = 256, kDq = 384;
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    k_attn_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+              const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnArgs a,
+              int q_tiles) {
+  using C = Dq<DP>;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t q_full, k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV], s_full[2],
+      dp_full, dp_empty, ds_full[2], done;
+  __shared__ uint32_t tmem_slot, abort_word;
+  __shared__ float part[2][kTile];
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const uint32_t q_at = smem_u32(smem), do_at = q_at + C::kTileBytes, k_at = do_at + C::kTileBytes,
+                 v_at = k_at + C::kK * C::kTileBytes;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+  const int heads = (int)a.batch * a.q_heads;
+  const int bh = blockIdx.x % heads, qt = q_tiles - 1 - blockIdx.x / heads;  // most keys first
+  const int h = bh % a.q_heads, b = bh / a.q_heads, c = h / a.group;
+  const int keys = valid_keys(a, b), row0 = qt * kTile;
+  int lo, hi, skip;
+  key_range(a, keys, row0, lo, skip);
+  key_range(a, keys, min(row0 + kTile, (int)a.q_len) - 1, skip, hi);
+  const int first = lo / kTile, n = lo < hi ? (hi + kTile - 1) / kTile - first : 0;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&q_full, 1);
+    for (int s = 0; s < C::kK; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_empty[s], 1);
+    for (int s = 0; s < C::kV; ++s) mbar_init(&v_full[s], 1), mbar_init(&v_empty[s], 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&s_full[s], 1), mbar_init(&ds_full[s], 8);
+    mbar_init(&dp_full, 1);
+    mbar_init(&dp_empty, 8);
+    mbar_init(&done, 1);
+    abort_word = 0;
+    mbar_init_fence();
+  }
+  if (warp == 9) tmem_alloc(&tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const Waiter wait{&abort_word, &g_attn_bwd_error};
+
+  if (warp == 8) {
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(&q_full, 2 * C::kTileBytes);
+      load_tile<DP>(q_at, &map_q, row0, h, b, &q_full);
+      load_tile<DP>(do_at, &map_do, row0, h, b, &q_full);
+      int j = 0;
+      for (; j < n; ++j) {
+        const int ks = j % C::kK, vs = j % C::kV, token = (first + j) * kTile;
+        if (!wait(&k_empty[ks], (j / C::kK - 1) & 1)) break;
+        mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
+        load_tile<DP>(k_at + ks * C::kTileBytes, &map_k, token, c, b, &k_full[ks]);
+        if (!wait(&v_empty[vs], (j / C::kV - 1) & 1)) break;
+        mbar_arrive_expect_tx(&v_full[vs], C::kTileBytes);
+        load_tile<DP>(v_at + vs * C::kTileBytes, &map_v, token, c, b, &v_full[vs]);
+      }
+      if (j < n) {  // gave up: leave the copies in flight time to land
+        mbar_wait(&q_full, 0, kSpinLimit >> 10);
+        for (int i = max(0, j - C::kK); i <= j; ++i) {
+          mbar_wait(&k_full[i % C::kK], (i / C::kK) & 1, kSpinLimit >> 10);
+          mbar_wait(&v_full[i % C::kV], (i / C::kV) & 1, kSpinLimit >> 10);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0 && n > 0) {
+      constexpr bool bf16 = !std::is_same<T, __half>::value;
+      constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
+      constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
+      auto k_tile = [&](int j) { return k_at + j % C::kK * C::kTileBytes; };
+      auto make_s = [&](int j) {
+        if (!wait(&k_full[j % C::kK], (j / C::kK) & 1)) return false;
+        tc_fence_after();
+        mma_head<DP>(tmem + (j & 1) * kTile, q_at, k_tile(j), by_head);
+        mma_commit(&s_full[j & 1]);
+        return true;
+      };
+      auto make_dp = [&](int j) {
+        if (!wait(&v_full[j % C::kV], (j / C::kV) & 1)) return false;
+        tc_fence_after();
+        mma_head<DP>(tmem + C::kDp, do_at, v_at + j % C::kV * C::kTileBytes, by_head);
+        mma_commit(&dp_full);
+        mma_commit(&v_empty[j % C::kV]);
+        return true;
+      };
+      bool go = wait(&q_full, 0) && make_s(0) && make_dp(0) && (n < 2 || make_s(1));
+      for (int j = 0; go && j < n; ++j) {
+        // the next dp as soon as this one has been read, then dq from this ds
+        if (j + 1 < n) {
+          if (!(go = wait(&dp_empty, j & 1))) break;
+          tc_fence_after();
+          if (!(go = make_dp(j + 1))) break;
+        }
+        if (!(go = wait(&ds_full[j & 1], (j / 2) & 1))) break;
+        tc_fence_after();
+        mma_rows_halves<DP>(tmem + C::kDq, tmem + (j & 1) * kTile, k_tile(j), by_rows, j > 0);
+        mma_commit(&k_empty[j % C::kK]);
+        if (j + 2 < n) go = make_s(j + 2);
+      }
+      mma_commit(&done);
+    }
+    __syncwarp();
+  } else {
+    // ---- a thread half a row: columns [64 half, 64 half + 64) of each tile
+    const int half = warp / 4, row = (warp & 3) * 32 + lane, i = row0 + row;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const bool live = i < a.q_len;
+    const int64_t at = (b * (int64_t)a.q_heads + h) * a.q_len + i;
+    float delta = 0.0f;
+    if (live) {
+      const T* o = static_cast<const T*>(a.o_in) + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2];
+      const T* g = static_cast<const T*>(a.dout) + b * a.dos[0] + (int64_t)i * a.dos[1] + h * a.dos[2];
+      for (int d = half * (DP / 2); d < min(a.head_dim, (half + 1) * (DP / 2)); d += 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(o + d), y = *reinterpret_cast<const uint4*>(g + d);
+        const T *xe = reinterpret_cast<const T*>(&x), *ye = reinterpret_cast<const T*>(&y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) delta = fmaf(DT<T>::to_f32(xe[e]), DT<T>::to_f32(ye[e]), delta);
+      }
+    }
+    part[half][row] = delta;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const float minus_delta = -(part[0][row] + part[1][row]);
+    // a row that sees nothing (or is none) gets p = 2^-inf = 0 everywhere
+    const float lse = live ? a.lse_in[at] : -INFINITY;
+    const float minus_lse = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+    if (half == 0) {
+      float* st = a.stats + ((b * (int64_t)a.q_heads + h) * q_tiles + qt) * kStats + row;
+      st[0] = minus_lse;
+      st[kTile] = minus_delta;
+    }
+    key_range(a, keys, i, lo, hi);
+    const float scale2 = a.scale * kLog2e;
+    const uint64_t scale_pair = pair(scale2, scale2), lse_pair = pair(minus_lse, minus_lse),
+                   delta_pair = pair(minus_delta, minus_delta);
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t s_at = tmem + lanes + (j & 1) * kTile + half * 64;
+      if (!(ok = wait(&s_full[j & 1], (j / 2) & 1))) break;
+      tc_fence_after();
+      float p[64];
+      uint32_t(&r)[2][32] = reinterpret_cast<uint32_t(&)[2][32]>(p);
+      tmem_ld32(s_at, r[0]);
+      tmem_ld32(s_at + 32, r[1]);
+      tmem_wait_ld();
+      const int key0 = (first + j) * kTile + half * 64;
+#pragma unroll
+      for (int k = 0; k < 64; k += 2) {
+        unpair(fma2(pair(p[k], p[k + 1]), scale_pair, lse_pair), p[k], p[k + 1]);
+        p[k] = exp2_fast(p[k]);
+        p[k + 1] = exp2_fast(p[k + 1]);
+      }
+      const bool mask = __any_sync(0xFFFFFFFFu, lo > key0 || hi < key0 + 64);
+      const int from = lo - key0, to = hi - key0;
+      if (!(ok = wait(&dp_full, j & 1))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float dp[32];
+        tmem_ld32(tmem + lanes + C::kDp + half * 64 + q * 32, reinterpret_cast<uint32_t(&)[32]>(dp));
+        tmem_wait_ld();
+        if (q == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&dp_empty);
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float x, y;
+          unpair(mul2(pair(p[q * 32 + k], p[q * 32 + k + 1]), add2(pair(dp[k], dp[k + 1]), delta_pair)), x, y);
+          if (mask) {
+            x = q * 32 + k >= from && q * 32 + k < to ? x : 0.0f;
+            y = q * 32 + k + 1 >= from && q * 32 + k + 1 < to ? y : 0.0f;
+          }
+          w[k / 2] = round2<T>(x, y);
+        }
+        tmem_st16(s_at + q * 16, w);
+      }
+      // keys past the length: their ds is zero, and so must be what it meets
+      if (half == 0 && keys < a.k_len && (first + j + 1) * kTile > keys) {
+        if ((first + j) * kTile + row >= keys)
+          zero_row<DP>(smem + (2 + j % C::kK) * C::kTileBytes, row);
+        fence_async_smem();
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full[j & 1]);
+    }
+    if (n > 0 && ok) ok = wait(&done, 0);
+    tc_fence_after();
+    T* out = static_cast<T*>(a.dq) + b * a.dqs[0] + (int64_t)i * a.dqs[1] + h * a.dqs[2];
+    constexpr int kHalf = DP / 2;
+    store_row<T, kHalf>(tmem + lanes + C::kDq + half * kHalf, a.scale, out + half * kHalf, a.head_dim - half * kHalf,
+                        n == 0, live && ok);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dk, dv
+// ---------------------------------------------------------------------------
+
+template <int DP>
+struct Dkv {
+  static constexpr int kTileBytes = DP / 64 * kTileChunk;
+  static constexpr int kSlots = 2;  // of q and do each
+  static constexpr int kSmem = (2 + 2 * kSlots) * kTileBytes + kSlots * kStats * 4 + 1024;
+  // TMEM: S^T (p^T over it), dp^T (ds^T over it), dv, dk
+  static constexpr uint32_t kDp = 128, kDv = 256, kDk = 384;
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    k_attn_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnArgs a,
+               int q_tiles) {
+  using C = Dkv<DP>;
+  constexpr int kS = C::kSlots;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t kv_full, q_full[kS], q_empty[kS], do_full[kS], do_empty[kS], s_full, dp_full, p_full,
+      ds_full, done;
+  __shared__ uint32_t tmem_slot, abort_word;
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const uint32_t k_at = smem_u32(smem), v_at = k_at + C::kTileBytes, q_at = v_at + C::kTileBytes,
+                 do_at = q_at + kS * C::kTileBytes;
+  float* stats = reinterpret_cast<float*>(smem + (2 + 2 * kS) * C::kTileBytes);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+  const int heads = (int)a.batch * a.kv_heads;
+  const int bc = blockIdx.x % heads, kt = blockIdx.x / heads;  // most queries first
+  const int c = bc % a.kv_heads, b = bc / a.kv_heads;
+  const int keys = valid_keys(a, b), key0 = kt * kTile, off = (int)(a.k_len - a.q_len);
+  // query tiles [first, last) that see one of the tile's valid keys
+  int first = 0, last = q_tiles;
+  if (a.causal) first = max(0, key0 - off) / kTile;
+  if (a.window > 0) {
+    const int end = min(key0 + kTile, keys) - 1 - off + (int)a.window;  // queries before this
+    last = min(last, end <= 0 ? 0 : (end + kTile - 1) / kTile);
+  }
+  const int span = key0 < keys ? max(0, last - first) : 0, n = span * a.group;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&kv_full, 1);
+    for (int s = 0; s < kS; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+      mbar_init(&do_full[s], 1);
+      mbar_init(&do_empty[s], 1);
+    }
+    mbar_init(&s_full, 1);
+    mbar_init(&dp_full, 1);
+    mbar_init(&p_full, 8);
+    mbar_init(&ds_full, 8);
+    mbar_init(&done, 1);
+    abort_word = 0;
+    mbar_init_fence();
+  }
+  if (warp == 9) tmem_alloc(&tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const Waiter wait{&abort_word, &g_attn_bwd_error};
+
+  if (warp == 8) {
+    if (lane == 0 && n > 0) {
+      mbar_arrive_expect_tx(&kv_full, 2 * C::kTileBytes);
+      load_tile<DP>(k_at, &map_k, key0, c, b, &kv_full);
+      load_tile<DP>(v_at, &map_v, key0, c, b, &kv_full);
+      int i = 0;
+      for (; i < n; ++i) {
+        const int s = i % kS, h = c * a.group + i / span, qt = first + i % span;
+        if (!wait(&q_empty[s], (i / kS - 1) & 1)) break;
+        mbar_arrive_expect_tx(&q_full[s], C::kTileBytes + kStats * 4);
+        load_tile<DP>(q_at + s * C::kTileBytes, &map_q, qt * kTile, h, b, &q_full[s]);
+        bulk_g2s(stats + s * kStats, a.stats + ((b * (int64_t)a.q_heads + h) * q_tiles + qt) * kStats, kStats * 4,
+                 &q_full[s]);
+        if (!wait(&do_empty[s], (i / kS - 1) & 1)) break;
+        mbar_arrive_expect_tx(&do_full[s], C::kTileBytes);
+        load_tile<DP>(do_at + s * C::kTileBytes, &map_do, qt * kTile, h, b, &do_full[s]);
+      }
+      if (i < n) {  // gave up: leave the copies in flight time to land
+        mbar_wait(&kv_full, 0, kSpinLimit >> 10);
+        for (int k = max(0, i - kS); k <= i; ++k) {
+          mbar_wait(&q_full[k % kS], (k / kS) & 1, kSpinLimit >> 10);
+          mbar_wait(&do_full[k % kS], (k / kS) & 1, kSpinLimit >> 10);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0 && n > 0) {
+      constexpr bool bf16 = !std::is_same<T, __half>::value;
+      constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
+      constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
+      auto make_s = [&](int i) {
+        if (!wait(&q_full[i % kS], (i / kS) & 1)) return false;
+        tc_fence_after();
+        mma_head<DP>(tmem, k_at, q_at + i % kS * C::kTileBytes, by_head);
+        mma_commit(&s_full);
+        return true;
+      };
+      auto make_dp = [&](int i) {
+        if (!wait(&do_full[i % kS], (i / kS) & 1)) return false;
+        tc_fence_after();
+        mma_head<DP>(tmem + C::kDp, v_at, do_at + i % kS * C::kTileBytes, by_head);
+        mma_commit(&dp_full);
+        return true;
+      };
+      // While the warps make p the tensor core makes dk and the next dp, while
+      // they make ds it makes dv and the next S.
+      bool go = wait(&kv_full, 0) && make_s(0) && make_dp(0);
+      for (int i = 0; go && i < n; ++i) {
+        const int s = i % kS;
+        if (!(go = wait(&p_full, i & 1))) break;
+        tc_fence_after();
+        mma_rows_halves<DP>(tmem + C::kDv, tmem, do_at + s * C::kTileBytes, by_rows, i > 0);
+        mma_commit(&do_empty[s]);
+        if (i + 1 < n && !(go = make_s(i + 1))) break;
+        if (!(go = wait(&ds_full, i & 1))) break;
+        tc_fence_after();
+        mma_rows_halves<DP>(tmem + C::kDk, tmem + C::kDp, q_at + s * C::kTileBytes, by_rows, i > 0);
+        mma_commit(&q_empty[s]);
+        if (i + 1 < n && !(go = make_dp(i + 1))) break;
+      }
+      mma_commit(&done);
+    }
+    __syncwarp();
+  } else {
+    // ---- a thread half a key's row: columns (queries) [64 half, 64 half + 64)
+    const int half = warp / 4, key = key0 + (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21, s_at = tmem + lanes + half * 64, dp_at = s_at + C::kDp;
+    const float scale2 = a.scale * kLog2e;
+    const uint64_t scale_pair = pair(scale2, scale2);
+    // queries [lo, hi) that see the key
+    int lo = a.causal ? max(0, key - off) : 0;
+    int hi = a.window > 0 ? min((int)a.q_len, key - off + (int)a.window) : (int)a.q_len;
+    if (key >= keys) hi = lo = 0;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int s = i % kS, q0 = (first + i % span) * kTile + half * 64;
+      // the statistics came with the query tile
+      if (!(ok = wait(&q_full[s], (i / kS) & 1) && wait(&s_full, i & 1))) break;
+      tc_fence_after();
+      const uint64_t* lse = reinterpret_cast<const uint64_t*>(stats + s * kStats + half * 64);
+      const uint64_t* delta = lse + kTile / 2;
+      float p[64];
+      uint32_t(&r)[2][32] = reinterpret_cast<uint32_t(&)[2][32]>(p);
+      tmem_ld32(s_at, r[0]);
+      tmem_ld32(s_at + 32, r[1]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 64; k += 2) {
+        unpair(fma2(pair(p[k], p[k + 1]), scale_pair, lse[k / 2]), p[k], p[k + 1]);
+        p[k] = exp2_fast(p[k]);
+        p[k + 1] = exp2_fast(p[k + 1]);
+      }
+      const int from = lo - q0, to = hi - q0;
+      const bool mask = __any_sync(0xFFFFFFFFu, from > 0 || to < 64);
+      if (mask)
+#pragma unroll
+        for (int k = 0; k < 64; ++k) p[k] = k >= from && k < to ? p[k] : 0.0f;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[k] = round2<T>(p[q * 32 + 2 * k], p[q * 32 + 2 * k + 1]);
+        tmem_st16(s_at + q * 16, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full);
+      if (!(ok = wait(&dp_full, i & 1))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float dp[32];
+        tmem_ld32(dp_at + q * 32, reinterpret_cast<uint32_t(&)[32]>(dp));
+        tmem_wait_ld();
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float x, y;
+          unpair(mul2(pair(p[q * 32 + k], p[q * 32 + k + 1]), add2(pair(dp[k], dp[k + 1]), delta[q * 16 + k / 2])), x,
+                 y);
+          if (mask) {  // 0 times whatever dp is there
+            x = q * 32 + k >= from && q * 32 + k < to ? x : 0.0f;
+            y = q * 32 + k + 1 >= from && q * 32 + k + 1 < to ? y : 0.0f;
+          }
+          w[k / 2] = round2<T>(x, y);
+        }
+        tmem_st16(dp_at + q * 16, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full);
+    }
+    if (n > 0 && ok) ok = wait(&done, 0);
+    tc_fence_after();
+    // the first four warps store dk, the others dv
+    const bool live = key < a.k_len && ok;
+    const int64_t *st = half == 0 ? a.dks : a.dvs;
+    T* out = static_cast<T*>(half == 0 ? a.dk : a.dv) + b * st[0] + (int64_t)key * st[1] + c * st[2];
+    store_row<T, DP>(tmem + lanes + (half == 0 ? C::kDk : C::kDv), half == 0 ? a.scale : 1.0f, out, a.head_dim, n == 0,
+                     live);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+int64_t tiles(int64_t len) { return (len + kTile - 1) / kTile; }
+
+template <typename T, int DP>
+cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+  CUtensorMap q, g, k, v;
+  // a side without rows is never loaded, but its maps still have to be valid
+  const bool qs = a.q_len > 0, ks = a.k_len > 0;
+  const int64_t q_len = qs ? a.q_len : 1, k_len = ks ? a.k_len : 1;
+  if (!attn_map(&q, qs ? a.q : a.k, a.dtype, a.qs, a.batch, q_len, a.q_heads, a.head_dim) ||
+      !attn_map(&g, qs ? a.dout : a.k, a.dtype, a.dos, a.batch, q_len, a.q_heads, a.head_dim) ||
+      !attn_map(&k, ks ? a.k : a.q, a.dtype, a.ks, a.batch, k_len, a.kv_heads, a.head_dim) ||
+      !attn_map(&v, ks ? a.v : a.q, a.dtype, a.vs, a.batch, k_len, a.kv_heads, a.head_dim))
+    return cudaErrorInvalidValue;
+  const int64_t q_blocks = tiles(a.q_len) * a.batch * a.q_heads, k_blocks = tiles(a.k_len) * a.batch * a.kv_heads;
+  if (q_blocks > 0x7FFFFFFFll || k_blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(k_attn_dq<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dq<DP>::kSmem);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(k_attn_dkv<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dkv<DP>::kSmem);
+  if (e != cudaSuccess) return e;
+  const int q_tiles = (int)tiles(a.q_len);
+  if (q_blocks > 0)
+    k_attn_dq<T, DP><<<(unsigned)q_blocks, kBwdThreads, Dq<DP>::kSmem, s>>>(q, g, k, v, a, q_tiles);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (k_blocks > 0)
+    k_attn_dkv<T, DP><<<(unsigned)k_blocks, kBwdThreads, Dkv<DP>::kSmem, s>>>(q, g, k, v, a, q_tiles);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t backward_t(const AttnArgs& a, cudaStream_t s) {
+  return a.head_dim <= 64 ? run<T, 64>(a, s) : run<T, 128>(a, s);
+}
+
+}  // namespace
+
+ZG_ERROR_WORD(attn_bwd_error, g_attn_bwd_error)
+
+int64_t attention_backward_bytes(const AttnArgs& a) {
+  return a.batch * a.q_heads * tiles(a.q_len) * kStats * 4;
+}
+
+cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s) {
+  (void)sms;
+  return a.dtype == kF16 ? backward_t<__half>(a, s) : backward_t<__nv_bfloat16>(a, s);
+}
+
+}  // namespace zg

@@ -226,12 +226,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           // rows of V past the length: zeros. Tile 0's product is the first to
           // read them, and waits for this thread.
           if (!(ok = wait(&kv_full[(2 * j + 1) % C::kSlots], ((2 * j + 1) / C::kSlots) & 1))) break;
-          uint8_t* v = smem + (2 + (2 * j + 1) % C::kSlots) * C::kTileBytes;
           const int row = (warp & 3) * 32 + lane;
-          if (key0 + row >= keys)
-#pragma unroll
-            for (int k = 0; k < DP / 8; ++k)
-              *reinterpret_cast<uint4*>(v + k / 8 * kTileChunk + row * 128 + k % 8 * 16) = make_uint4(0, 0, 0, 0);
+          if (key0 + row >= keys) zero_row<DP>(smem + (2 + (2 * j + 1) % C::kSlots) * C::kTileBytes, row);
           fence_async_smem();
         }
         tmem_wait_st();
@@ -244,27 +240,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const bool none = total == 0.0f;  // no key seen (a seen key gives at least 2^-8 ... or NaN)
       const float inv = none ? 0.0f : 1.0f / total;
       T* out = static_cast<T*>(a.o) + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2];
-#pragma unroll 1
-      for (int k = 0; k < DP; k += 32) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32(o_at + k, o);
-          tmem_wait_ld();
-        }
-        if (i < a.q_len && ok) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            if (k + g * 8 >= a.head_dim) break;
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = none ? 0u
-                          : round2<T>(__uint_as_float(o[g * 8 + 2 * e]) * inv,
-                                      __uint_as_float(o[g * 8 + 2 * e + 1]) * inv);
-            *reinterpret_cast<uint4*>(out + k + g * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
+      // `none` may differ between the lanes of a warp: their sums are zeros
+      store_row<T, DP>(o_at, inv, out, a.head_dim, n == 0, i < a.q_len && ok);
       if (i < a.q_len && ok)
         a.lse[(b * (int64_t)a.q_heads + h) * a.q_len + i] =
             none ? -INFINITY : (top * scale2 + log2f(total)) * kLn2;
