@@ -475,9 +475,10 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const int64_t q_blocks = tiles(a.q_len) * a.batch * a.q_heads, k_blocks = tiles(a.k_len) * a.batch * a.kv_heads;
   if (q_blocks > 0x7FFFFFFFll || k_blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(k_attn_dq<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dq<DP>::kSmem);
+  static std::atomic<uint64_t> asked_dq{0}, asked_dkv{0};
+  cudaError_t e = allow_smem(k_attn_dq<T, DP>, Dq<DP>::kSmem, asked_dq);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(k_attn_dkv<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Dkv<DP>::kSmem);
+  e = allow_smem(k_attn_dkv<T, DP>, Dkv<DP>::kSmem, asked_dkv);
   if (e != cudaSuccess) return e;
   const int q_tiles = (int)tiles(a.q_len);
   if (q_blocks > 0)

@@ -268,7 +268,8 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
   const int64_t q_tiles = (a.q_len + kTile - 1) / kTile, pairs = (q_tiles * a.group + 1) / 2;
   const int64_t blocks = pairs * a.batch * a.kv_heads;
   if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(k_attn_fwd<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> asked{0};
+  cudaError_t e = allow_smem(k_attn_fwd<T, DP>, C::kSmem, asked);
   if (e != cudaSuccess) return e;
   k_attn_fwd<T, DP><<<(unsigned)blocks, kFwdThreads, C::kSmem, s>>>(q, k, v, a, (int)q_tiles, (int)pairs);
   return cudaGetLastError();

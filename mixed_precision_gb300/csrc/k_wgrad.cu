@@ -466,7 +466,8 @@ cudaError_t run(const WgradArgs& a, int split, cudaStream_t s) {
   CUtensorMap map;
   const uint64_t extent[2] = {(uint64_t)a.n_out, (uint64_t)a.tokens}, strides[1] = {(uint64_t)a.dy_stride * 2};
   if (!make_tensor_map(&map, a.dy, a.dtype == kBF16, 2, extent, strides, kStep)) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(k_wgrad<T, MT, BN, ROUND>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> asked{0};
+  cudaError_t e = allow_smem(k_wgrad<T, MT, BN, ROUND>, C::kSmem, asked);
   if (e != cudaSuccess) return e;
   const int n_tiles = (a.n_in + BN - 1) / BN;
   const int64_t m_tiles = (a.n_out + MT * 128 - 1) / (MT * 128);

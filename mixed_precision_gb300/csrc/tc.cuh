@@ -9,6 +9,7 @@
 //   MN-major: a row holds 64 elements along M or N for one contraction index.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda.h>
@@ -190,6 +191,23 @@ __device__ __forceinline__ void cluster_store(uint32_t addr, float v) {
 // block reaches on every path, timed out or not.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---- launches (host) ---------------------------------------------------------
+
+// Allow a kernel `bytes` of dynamic shared memory on the current device: asked
+// of the runtime once per kernel and device. `asked` is the kernel's own bit
+// set of devices; a device beyond 63 asks every time.
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel* kernel, int bytes, std::atomic<uint64_t>& asked) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit != 0 && (asked.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) asked.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 // ---- tensor maps (host) --------------------------------------------------------
