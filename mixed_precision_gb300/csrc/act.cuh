@@ -3,19 +3,61 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "block.h"
 #include "vec.cuh"
 
 namespace zg {
 
+// Two values rounded to T, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t round2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t round2<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t round2<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 8 elements as fp32, and 8 values rounded to T. 16-bit types go in pairs: a
+// bf16 is the upper half of its fp32, and one instruction rounds two values.
+template <typename T>
+__device__ __forceinline__ void widen8(const Pack8<T>& v, float (&x)[8]) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(v.e);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __uint_as_float(w[j] << 16);
+      x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = DT<T>::to_f32(v.e[j]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ Pack8<T> round8(const float (&x)[8]) {
+  Pack8<T> v;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v.e[j] = x[j];
+  } else {
+    uint32_t* w = reinterpret_cast<uint32_t*>(v.e);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = round2<T>(x[2 * j], x[2 * j + 1]);
+  }
+  return v;
+}
+
 // 8 values rounded to T and stored (16-byte aligned; 32 bytes for fp32).
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
-  Pack8<T> v;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v.e[j] = DT<T>::from_f32(x[j]);
-  store8_raw(p, v);
+  store8_raw(p, round8<T>(x));
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
@@ -41,21 +83,29 @@ __device__ __forceinline__ float act_scale(uint32_t byte) {
   return __uint_as_float(bits);
 }
 
-// round(x * inv) to nearest even, clamped to +-127. x * inv is below 128 in
-// magnitude (or NaN in a marked group, which converts to 0).
-__device__ __forceinline__ uint32_t act_code(float x, float inv) {
-  const int c = max(-127, min(127, __float2int_rn(x * inv)));
-  return static_cast<uint32_t>(c) & 0xFFu;
+// The codes of 8 values: round(x * inv) to nearest even, clamped to +-127. Adding
+// 1.5 * 2^23 rounds a small number to a whole one, whose low byte then is its
+// two's complement (the conversion instruction runs at an eighth of the rate).
+// A marked group (inv = 0) has codes 0.
+__device__ __forceinline__ uint2 act_codes8(const float (&x)[8], float inv) {
+  uint32_t c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    c[j] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fmul_rn(x[j], inv), -127.0f), 127.0f), 12582912.0f));
+  uint2 r;
+  r.x = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  r.y = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+  return inv == 0.0f ? make_uint2(0, 0) : r;
 }
 
-// 8 codes of 8 values.
-__device__ __forceinline__ uint2 act_codes8(const float (&x)[8], float inv) {
-  uint2 r;
-  r.x = act_code(x[0], inv) | act_code(x[1], inv) << 8 | act_code(x[2], inv) << 16 |
-        act_code(x[3], inv) << 24;
-  r.y = act_code(x[4], inv) | act_code(x[5], inv) << 8 | act_code(x[6], inv) << 16 |
-        act_code(x[7], inv) << 24;
-  return r;
+// 8 values restored: code * scale. 2^23 + 128 + code is an fp32 number made by a
+// byte move.
+__device__ __forceinline__ void act_restore8(uint2 q, float scale, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t w = (j < 4 ? q.x : q.y) ^ 0x80808080u;
+    v[j] = __fmul_rn(__fadd_rn(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7650 | (j & 3))), -8388736.0f), scale);
+  }
 }
 
 // The scale byte of 8 values held by each of 4 neighbouring lanes (a group of

@@ -4,6 +4,7 @@
 
 #include <cstdint>
 
+#include "act.cuh"
 #include "block.h"
 #include "tc.cuh"
 #include "vec.cuh"
@@ -58,20 +59,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
-}
-
-// Two values rounded to T, the first in the low half.
-template <typename T>
-__device__ __forceinline__ uint32_t round2(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t round2<__nv_bfloat16>(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <>
-__device__ __forceinline__ uint32_t round2<__half>(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // The 64-wide chunks of a [rows <= 128] x head tile, by one thread.

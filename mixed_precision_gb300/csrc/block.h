@@ -45,8 +45,8 @@ struct ActArgs {
   int8_t* q;
   uint8_t* scales;
 };
-cudaError_t launch_act_pack(const ActArgs& a, int sms, cudaStream_t s);
-cudaError_t launch_act_unpack(const ActArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_act_pack(const ActArgs& a, cudaStream_t s);
+cudaError_t launch_act_unpack(const ActArgs& a, cudaStream_t s);
 
 struct WgradArgs {
   const void* dy;
@@ -76,12 +76,13 @@ struct AttnArgs {
   const float* lse_in;
   float* stats;  // backward: the rows' statistics (k_attn_bwd.cu)
 };
-cudaError_t launch_attention_forward(const AttnArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_attention_forward(const AttnArgs& a, cudaStream_t s);
 int64_t attention_backward_bytes(const AttnArgs& a);
-cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_attention_backward(const AttnArgs& a, cudaStream_t s);
 
 // The kernels' error words on the current device (bit kErrWaitTimeout): *value
 // |= the word, which is cleared. Each synchronises the stream.
+cudaError_t norm_error(unsigned* value, cudaStream_t s);
 cudaError_t wgrad_error(unsigned* value, cudaStream_t s);
 cudaError_t attn_fwd_error(unsigned* value, cudaStream_t s);
 cudaError_t attn_bwd_error(unsigned* value, cudaStream_t s);

@@ -341,9 +341,7 @@ int zero_act_pack(const void* x, int64_t x_stride, int64_t rows, int64_t cols, i
   a.x = x;
   a.q = q;
   a.scales = scales;
-  int sms;
-  if (int rc = device_sms(&sms)) return rc;
-  cudaError_t e = launch_act_pack(a, sms, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_act_pack(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "activation pack launch");
 }
 
@@ -366,9 +364,7 @@ int zero_act_unpack(const int8_t* q, const uint8_t* scales, int64_t rows, int64_
   a.q_in = q;
   a.scales_in = scales;
   a.out = out;
-  int sms;
-  if (int rc = device_sms(&sms)) return rc;
-  cudaError_t e = launch_act_unpack(a, sms, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_act_unpack(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "activation restore launch");
 }
 
@@ -450,9 +446,7 @@ int zero_attention_forward(const zero_attention_desc* desc, const void* q, const
   a.lengths = key_lengths;
   a.o = o;
   a.lse = lse;
-  int sms;
-  if (int rc = device_sms(&sms)) return rc;
-  cudaError_t e = launch_attention_forward(a, sms, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_attention_forward(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "attention forward launch");
 }
 
@@ -502,17 +496,15 @@ int zero_attention_backward(const zero_attention_desc* desc, const void* dout, c
   a.dk = dk;
   a.dv = dv;
   a.stats = static_cast<float*>(workspace);
-  int sms;
-  if (int rc = device_sms(&sms)) return rc;
-  cudaError_t e = launch_attention_backward(a, sms, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_attention_backward(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "attention backward launch");
 }
 
 int zero_operator_status(void* stream) {
   Range r("zero_operator_status");
   unsigned error = 0;
-  cudaError_t (*const words[])(unsigned*, cudaStream_t) = {wgrad_error, attn_fwd_error,
-                                                            attn_bwd_error};
+  cudaError_t (*const words[])(unsigned*, cudaStream_t) = {norm_error, wgrad_error,
+                                                            attn_fwd_error, attn_bwd_error};
   for (auto word : words) {
     cudaError_t e = word(&error, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "operator status");

@@ -18,7 +18,7 @@ template <typename T, bool VEC>
 __device__ __forceinline__ void load_chunk(const T* row, int c, int cols, float (&x)[8]) {
   if constexpr (VEC) {
     if (c < cols) {
-      load8(row + c, x);
+      widen8(load8_raw(row + c), x);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = 0.0f;
@@ -29,44 +29,69 @@ __device__ __forceinline__ void load_chunk(const T* row, int c, int cols, float 
   }
 }
 
+// Division of numbers below 2^31 by a fixed one: n / d = n * mul >> shift, with
+// mul = floor(2^shift / d) + 1 and shift = 31 + ceil(log2 d).
+struct Divide {
+  uint64_t mul;
+  uint32_t d, shift;
+  explicit Divide(uint32_t by) : d(by) {
+    uint32_t l = 0;
+    while ((1ull << l) < by) ++l;
+    shift = 31 + l;
+    mul = (1ull << shift) / by + 1;
+  }
+  __device__ uint32_t operator()(uint32_t n) const { return static_cast<uint32_t>(n * mul >> shift); }
+};
+
+constexpr int kPer = 4;  // chunks a thread, all loaded before the first is used
+
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) k_act_pack(const ActArgs a) {
+__global__ void __launch_bounds__(256) k_act_pack(const ActArgs a, const Divide per_row, uint32_t total) {
   const T* x = static_cast<const T*>(a.x);
-  const uint32_t per_row = a.pitch / 8;  // chunks of a row, a multiple of 16
-  const int64_t total = a.rows * per_row;
-  // total is a multiple of 16 chunks but a warp is 32 lanes: the loop bound is
-  // rounded up so that whole warps reach the shuffles
-  const int64_t bound = (total + 31) / 32 * 32;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < bound; i += gridDim.x * 256ll) {
-    const bool live = i < total;
-    const int64_t row = live ? i / per_row : 0;
-    const int c = live ? static_cast<int>(i - row * per_row) * 8 : a.cols + 8;
-    float v[8];
-    load_chunk<T, VEC>(x + row * a.stride, c, a.cols, v);
-    const uint32_t byte = act_group_byte(v);
-    if (live) {
-      *reinterpret_cast<uint2*>(a.q + row * a.pitch + c) = act_codes8(v, act_inv_scale(byte));
-      if ((threadIdx.x & 3) == 0) a.scales[row * (a.pitch / kActGroup) + c / kActGroup] = byte;
+  const uint32_t first = blockIdx.x * (256u * kPer) + threadIdx.x;
+  float v[kPer][8];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const uint32_t i = first + k * 256;
+    const uint32_t row = i < total ? per_row(i) : 0;
+    // past the end: columns outside the row, read as zeros
+    const int c = i < total ? static_cast<int>(i - row * per_row.d) * 8 : a.pitch;
+    load_chunk<T, VEC>(x + row * a.stride, c, a.cols, v[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const uint32_t byte = act_group_byte(v[k]);  // whole warps
+    const uint32_t i = first + k * 256;
+    if (i < total) {  // chunk i of the codes, whose rows have no gaps
+      *reinterpret_cast<uint2*>(a.q + i * 8ll) = act_codes8(v[k], act_inv_scale(byte));
+      if ((threadIdx.x & 3) == 0) a.scales[i / 4] = byte;
     }
   }
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) k_act_unpack(const ActArgs a) {
+__global__ void __launch_bounds__(256) k_act_unpack(const ActArgs a, const Divide per_row, uint32_t total) {
   T* out = static_cast<T*>(a.out);
-  const uint32_t per_row = (a.cols + 7) / 8;
-  const int64_t total = a.rows * per_row;
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const int64_t row = i / per_row;
-    const int c = static_cast<int>(i - row * per_row) * 8;
-    const uint2 q = *reinterpret_cast<const uint2*>(a.q_in + row * a.pitch + c);
-    const float s = act_scale(a.scales_in[row * (a.pitch / kActGroup) + c / kActGroup]);
-    float v[8];
+  const uint32_t first = blockIdx.x * (256u * kPer) + threadIdx.x;
+  uint2 q[kPer];
+  uint32_t b[kPer];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t w = j < 4 ? q.x : q.y;
-      v[j] = static_cast<float>(static_cast<int8_t>(w >> 8 * (j & 3))) * s;
+  for (int k = 0; k < kPer; ++k) {
+    const uint32_t i = first + k * 256;
+    if (i < total) {
+      const uint32_t row = per_row(i), at = row * (a.pitch / 8) + (i - row * per_row.d);
+      q[k] = *reinterpret_cast<const uint2*>(a.q_in + at * 8ll);
+      b[k] = a.scales_in[at / 4];
     }
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const uint32_t i = first + k * 256;
+    if (i >= total) break;
+    const uint32_t row = per_row(i);
+    const int c = static_cast<int>(i - row * per_row.d) * 8;
+    float v[8];
+    act_restore8(q[k], act_scale(b[k]), v);
     T* o = out + row * a.stride + c;
     if constexpr (VEC) {
       store8(o, v);
@@ -79,47 +104,72 @@ __global__ void __launch_bounds__(256) k_act_unpack(const ActArgs a) {
 }
 
 template <typename T>
-cudaError_t pack_t(const ActArgs& a, int grid, bool vec, cudaStream_t s) {
+cudaError_t pack_t(const ActArgs& a, bool vec, cudaStream_t s) {
+  const Divide per_row(a.pitch / 8);
+  const uint32_t total = (uint32_t)a.rows * per_row.d, grid = (total + 256 * kPer - 1) / (256 * kPer);
   if (vec)
-    k_act_pack<T, true><<<grid, 256, 0, s>>>(a);
+    k_act_pack<T, true><<<grid, 256, 0, s>>>(a, per_row, total);
   else
-    k_act_pack<T, false><<<grid, 256, 0, s>>>(a);
+    k_act_pack<T, false><<<grid, 256, 0, s>>>(a, per_row, total);
   return cudaGetLastError();
 }
 template <typename T>
-cudaError_t unpack_t(const ActArgs& a, int grid, bool vec, cudaStream_t s) {
+cudaError_t unpack_t(const ActArgs& a, bool vec, cudaStream_t s) {
+  const Divide per_row((a.cols + 7) / 8);
+  const uint32_t total = (uint32_t)a.rows * per_row.d, grid = (total + 256 * kPer - 1) / (256 * kPer);
   if (vec)
-    k_act_unpack<T, true><<<grid, 256, 0, s>>>(a);
+    k_act_unpack<T, true><<<grid, 256, 0, s>>>(a, per_row, total);
   else
-    k_act_unpack<T, false><<<grid, 256, 0, s>>>(a);
+    k_act_unpack<T, false><<<grid, 256, 0, s>>>(a, per_row, total);
   return cudaGetLastError();
 }
 
-int act_grid(int64_t chunks, int sms) {
-  const int64_t want = (chunks + 255) / 256;
-  return static_cast<int>(want < sms * 8ll ? want : sms * 8ll);
+// The kernels count chunks in 31 bits: one launch for up to that many (17 G
+// elements), several beyond.
+template <typename Launch>
+cudaError_t by_rows(ActArgs a, int64_t elem_bytes, Launch launch) {
+  const int64_t most = ((int64_t(1) << 31) - 1) / (a.pitch / 8);
+  const int64_t rows = a.rows;
+  for (int64_t r = 0; r < rows; r += most) {
+    a.rows = rows - r < most ? rows - r : most;
+    const cudaError_t e = launch(a);
+    if (e != cudaSuccess) return e;
+    const int64_t step = a.rows * a.stride * elem_bytes, codes = a.rows * a.pitch;
+    if (a.x != nullptr) {
+      a.x = static_cast<const char*>(a.x) + step;
+      a.q += codes;
+      a.scales += codes / kActGroup;
+    } else {
+      a.out = static_cast<char*>(a.out) + step;
+      a.q_in += codes;
+      a.scales_in += codes / kActGroup;
+    }
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_act_pack(const ActArgs& a, int sms, cudaStream_t s) {
-  const int grid = act_grid(a.rows * (a.pitch / 8), sms);
+cudaError_t launch_act_pack(const ActArgs& a, cudaStream_t s) {
   const bool vec = a.cols % 8 == 0 && a.stride % 8 == 0;
-  switch (a.dtype) {
-    case kF32: return pack_t<float>(a, grid, vec, s);
-    case kF16: return pack_t<__half>(a, grid, vec, s);
-    default: return pack_t<__nv_bfloat16>(a, grid, vec, s);
-  }
+  return by_rows(a, a.dtype == kF32 ? 4 : 2, [&](const ActArgs& p) {
+    switch (p.dtype) {
+      case kF32: return pack_t<float>(p, vec, s);
+      case kF16: return pack_t<__half>(p, vec, s);
+      default: return pack_t<__nv_bfloat16>(p, vec, s);
+    }
+  });
 }
 
-cudaError_t launch_act_unpack(const ActArgs& a, int sms, cudaStream_t s) {
-  const int grid = act_grid(a.rows * ((a.cols + 7) / 8), sms);
+cudaError_t launch_act_unpack(const ActArgs& a, cudaStream_t s) {
   const bool vec = a.cols % 8 == 0 && a.stride % 8 == 0;
-  switch (a.dtype) {
-    case kF32: return unpack_t<float>(a, grid, vec, s);
-    case kF16: return unpack_t<__half>(a, grid, vec, s);
-    default: return unpack_t<__nv_bfloat16>(a, grid, vec, s);
-  }
+  return by_rows(a, a.dtype == kF32 ? 4 : 2, [&](const ActArgs& p) {
+    switch (p.dtype) {
+      case kF32: return unpack_t<float>(p, vec, s);
+      case kF16: return unpack_t<__half>(p, vec, s);
+      default: return unpack_t<__nv_bfloat16>(p, vec, s);
+    }
+  });
 }
 
 }  // namespace zg

@@ -503,8 +503,7 @@ int64_t attention_backward_bytes(const AttnArgs& a) {
   return a.batch * a.q_heads * tiles(a.q_len) * kStats * 4;
 }
 
-cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s) {
-  (void)sms;
+cudaError_t launch_attention_backward(const AttnArgs& a, cudaStream_t s) {
   return a.dtype == kF16 ? backward_t<__half>(a, s) : backward_t<__nv_bfloat16>(a, s);
 }
 

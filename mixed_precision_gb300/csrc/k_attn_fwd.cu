@@ -284,8 +284,7 @@ cudaError_t forward_t(const AttnArgs& a, cudaStream_t s) {
 
 ZG_ERROR_WORD(attn_fwd_error, g_attn_fwd_error)
 
-cudaError_t launch_attention_forward(const AttnArgs& a, int sms, cudaStream_t s) {
-  (void)sms;
+cudaError_t launch_attention_forward(const AttnArgs& a, cudaStream_t s) {
   return a.dtype == kF16 ? forward_t<__half>(a, s) : forward_t<__nv_bfloat16>(a, s);
 }
 

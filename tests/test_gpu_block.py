@@ -40,6 +40,11 @@ ROWS_COLS = [(1, 8), (3, 1), (5, 33), (2, 128), (67, 128), (1, 1000), (33, 1024)
              (9, 4096), (4, 8192), (2, 16256), (2, 20000), (1, 65536), (513, 72), (4099, 264)]
 
 
+# enough rows to go through shared memory, in teams of one to eight warps
+MANY_ROWS = [(2432, 264), (2500, 512), (3001, 520), (2433, 1024), (2432, 1032), (5000, 2048), (2600, 4096), (2440, 5000),
+             (2433, 8192)]
+
+
 def check_forward(x, w, eps, res, y, s, rstd):
     if res is not None:
         assert same_bits(s, (x.float() + res.float()).to(x.dtype))
@@ -50,7 +55,7 @@ def check_forward(x, w, eps, res, y, s, rstd):
         ref.close(y, want, want.abs() * (ref.U[x.dtype] + rel + 4 * ref.E) + ref.TINY[x.dtype], "y")
 
 
-@pytest.mark.parametrize("rows,cols", ROWS_COLS)
+@pytest.mark.parametrize("rows,cols", ROWS_COLS + MANY_ROWS)
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("with_res", [False, True])
 def test_norm_forward(rows, cols, dtype, with_res):
@@ -72,11 +77,12 @@ def test_norm_forward(rows, cols, dtype, with_res):
     assert y3 is None and torch.equal(alone.q, packed.q) and torch.equal(alone.scales, packed.scales)
 
 
-@pytest.mark.parametrize("cols,pad", [(128, 8), (1024, 40), (72, 3), (33, 5)])
-def test_norm_strided_rows_and_in_place_sum(cols, pad):
+@pytest.mark.parametrize("rows,cols,pad", [(50, 128, 8), (50, 1024, 40), (50, 72, 3), (50, 33, 5), (2500, 1024, 40),
+                                           (2500, 2056, 8)])
+def test_norm_strided_rows_and_in_place_sum(rows, cols, pad):
     g = gen(cols)
-    x = normal(g, 50, cols + pad, dtype=BF16)[:, :cols]
-    res = normal(g, 50, 2 * cols + 8, dtype=BF16)[:, 8:cols + 8]
+    x = normal(g, rows, cols + pad, dtype=BF16)[:, :cols]
+    res = normal(g, rows, 2 * cols + 8, dtype=BF16)[:, 8:cols + 8]
     w = normal(g, cols, dtype=BF16)
     y, s, rstd = block.rmsnorm_forward(x, w, 1e-6, residual=res)
     check_forward(x, w, 1e-6, res, y, s, rstd)
@@ -105,7 +111,7 @@ def test_norm_rows_far_apart():
     assert same_bits(dx, block.rmsnorm_backward(x.contiguous(), x.contiguous(), w, rstd)[0])
 
 
-@pytest.mark.parametrize("rows,cols", ROWS_COLS + [(20000, 128), (3000, 1024)])
+@pytest.mark.parametrize("rows,cols", ROWS_COLS + MANY_ROWS + [(20000, 128), (3000, 1024)])
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("with_dsum", [False, True])
 def test_norm_backward(rows, cols, dtype, with_dsum):
