@@ -61,6 +61,35 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// The largest of three values (a NaN among them is passed over).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// S outside columns [from, to): -inf.
+template <int N>
+__device__ __forceinline__ void mask_row(float (&s)[N], int from, int to) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) s[k] = k >= from && k < to ? s[k] : -INFINITY;
+}
+
+// Registers of a warpgroup's threads, given away and taken (all four warps).
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A barrier of n threads; id 1 and up.
+__device__ __forceinline__ void named_sync(int id, int n) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
 // The 64-wide chunks of a [rows <= 128] x head tile, by one thread.
 template <int DP>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int token, int head, int batch,
@@ -69,32 +98,29 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
   for (int i = 0; i < DP / 64; ++i) tma_load4(dst + i * kTileChunk, map, i * 64, token, head, batch, bar);
 }
 
-// d = a b^T over the head: both tiles K-major, DP elements.
+// Operand descriptors of a 128-row tile: read along the head (K-major), and
+// with its rows as the contraction (MN-major).
+__device__ __forceinline__ uint64_t head_desc(uint32_t tile) { return smem_desc(tile, 0, 1024); }
+__device__ __forceinline__ uint64_t rows_desc(uint32_t tile) { return smem_desc(tile, kTileChunk, 1024); }
+
+// d = a b^T over the head, DP elements. (Offsets are added to the descriptors'
+// address fields, in units of 16 bytes.)
 template <int DP>
-__device__ __forceinline__ void mma_head(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+__device__ __forceinline__ void mma_head(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t one) {
 #pragma unroll
   for (int k = 0; k < DP / 16; ++k) {
-    const uint32_t off = k / 4 * kTileChunk + k % 4 * 32;
-    mma_ss(d, smem_desc(a + off, 0, 1024), smem_desc(b + off, 0, 1024), idesc, k > 0);
+    const uint32_t off = (k / 4 * kTileChunk + k % 4 * 32) / 16;
+    mma_ss(d, a + off, b + off, idesc, k > 0, one);
   }
 }
 
-// d [+]= a b over 128 rows: a in TMEM, b a tile read with its rows as the
-// contraction (MN-major).
-template <int DP>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+// d [+]= a b over 128 rows: a in TMEM, 16-bit, its columns in two runs of 32,
+// the second 64 columns on: two warps wrote a row, each over its own half of
+// the fp32 columns.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t one) {
 #pragma unroll
   for (int k = 0; k < kTile / 16; ++k)
-    mma_ts(d, a + k * 8, smem_desc(b + k * 2048, kTileChunk, 1024), idesc, add || k > 0);
-}
-
-// The same with a's 16-bit columns in two runs of 32, the second 64 columns on:
-// two warps wrote a row, each over its own half of the fp32 columns.
-template <int DP>
-__device__ __forceinline__ void mma_rows_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
-#pragma unroll
-  for (int k = 0; k < kTile / 16; ++k)
-    mma_ts(d, a + k / 4 * 64 + k % 4 * 8, smem_desc(b + k * 2048, kTileChunk, 1024), idesc, add || k > 0);
+    mma_ts(d, a + k / 4 * 64 + k % 4 * 8, b + k * (2048 / 16), idesc, add || k > 0, one);
 }
 
 // A row of a tile to zero; the caller fences.

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t q_at = smem_u32(smem), do_at = q_at + C::kTileBytes, k_at = do_at + C::kTileBytes,
                  v_at = k_at + C::kK * C::kTileBytes;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
 
   const int heads = (int)a.batch * a.q_heads;
   const int bh = blockIdx.x % heads, qt = q_tiles - 1 - blockIdx.x / heads;  // most keys first
@@ -79,19 +79,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const Waiter wait{&abort_word, &g_attn_bwd_error};
 
   if (warp == 8) {
-    if (lane == 0 && n > 0) {
-      mbar_arrive_expect_tx(&q_full, 2 * C::kTileBytes);
-      load_tile<DP>(q_at, &map_q, row0, h, b, &q_full);
-      load_tile<DP>(do_at, &map_do, row0, h, b, &q_full);
+    if (n > 0) {
+      const uint32_t one = elect_one();
+      if (one) {
+        mbar_arrive_expect_tx(&q_full, 2 * C::kTileBytes);
+        load_tile<DP>(q_at, &map_q, row0, h, b, &q_full);
+        load_tile<DP>(do_at, &map_do, row0, h, b, &q_full);
+      }
       int j = 0;
       for (; j < n; ++j) {
         const int ks = j % C::kK, vs = j % C::kV, token = (first + j) * kTile;
         if (!wait(&k_empty[ks], (j / C::kK - 1) & 1)) break;
-        mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
-        load_tile<DP>(k_at + ks * C::kTileBytes, &map_k, token, c, b, &k_full[ks]);
+        if (one) {
+          mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
+          load_tile<DP>(k_at + ks * C::kTileBytes, &map_k, token, c, b, &k_full[ks]);
+        }
         if (!wait(&v_empty[vs], (j / C::kV - 1) & 1)) break;
-        mbar_arrive_expect_tx(&v_full[vs], C::kTileBytes);
-        load_tile<DP>(v_at + vs * C::kTileBytes, &map_v, token, c, b, &v_full[vs]);
+        if (one) {
+          mbar_arrive_expect_tx(&v_full[vs], C::kTileBytes);
+          load_tile<DP>(v_at + vs * C::kTileBytes, &map_v, token, c, b, &v_full[vs]);
+        }
       }
       if (j < n) {  // gave up: leave the copies in flight time to land
         mbar_wait(&q_full, 0, kSpinLimit >> 10);
@@ -101,29 +108,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
       }
     }
-    __syncwarp();
   } else if (warp == 9) {
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
       constexpr bool bf16 = !std::is_same<T, __half>::value;
       constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
       constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
-      auto k_tile = [&](int j) { return k_at + j % C::kK * C::kTileBytes; };
+      constexpr uint32_t kStep = C::kTileBytes / 16;
+      const uint32_t one = elect_one();
+      const uint64_t q_desc = head_desc(q_at), do_desc = head_desc(do_at), k_desc = head_desc(k_at),
+                     v_desc = head_desc(v_at), k_rows = rows_desc(k_at);
       auto make_s = [&](int j) {
         if (!wait(&k_full[j % C::kK], (j / C::kK) & 1)) return false;
         tc_fence_after();
-        mma_head<DP>(tmem + (j & 1) * kTile, q_at, k_tile(j), by_head);
-        mma_commit(&s_full[j & 1]);
+        mma_head<DP>(tmem + (j & 1) * kTile, q_desc, k_desc + j % C::kK * kStep, by_head, one);
+        mma_commit(&s_full[j & 1], one);
         return true;
       };
       auto make_dp = [&](int j) {
         if (!wait(&v_full[j % C::kV], (j / C::kV) & 1)) return false;
         tc_fence_after();
-        mma_head<DP>(tmem + C::kDp, do_at, v_at + j % C::kV * C::kTileBytes, by_head);
-        mma_commit(&dp_full);
-        mma_commit(&v_empty[j % C::kV]);
+        mma_head<DP>(tmem + C::kDp, do_desc, v_desc + j % C::kV * kStep, by_head, one);
+        mma_commit(&dp_full, one);
+        mma_commit(&v_empty[j % C::kV], one);
         return true;
       };
       bool go = wait(&q_full, 0) && make_s(0) && make_dp(0) && (n < 2 || make_s(1));
+#pragma unroll 1
       for (int j = 0; go && j < n; ++j) {
         // the next dp as soon as this one has been read, then dq from this ds
         if (j + 1 < n) {
@@ -133,13 +143,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (!(go = wait(&ds_full[j & 1], (j / 2) & 1))) break;
         tc_fence_after();
-        mma_rows_halves<DP>(tmem + C::kDq, tmem + (j & 1) * kTile, k_tile(j), by_rows, j > 0);
-        mma_commit(&k_empty[j % C::kK]);
+        mma_rows(tmem + C::kDq, tmem + (j & 1) * kTile, k_rows + j % C::kK * kStep, by_rows, j > 0, one);
+        mma_commit(&k_empty[j % C::kK], one);
         if (j + 2 < n) go = make_s(j + 2);
       }
-      mma_commit(&done);
+      mma_commit(&done, one);
     }
-    __syncwarp();
   } else {
     // ---- a thread half a row: columns [64 half, 64 half + 64) of each tile
     const int half = warp / 4, row = (warp & 3) * 32 + lane, i = row0 + row;
@@ -270,7 +279,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t k_at = smem_u32(smem), v_at = k_at + C::kTileBytes, q_at = v_at + C::kTileBytes,
                  do_at = q_at + kS * C::kTileBytes;
   float* stats = reinterpret_cast<float*>(smem + (2 + 2 * kS) * C::kTileBytes);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
 
   const int heads = (int)a.batch * a.kv_heads;
   const int bc = blockIdx.x % heads, kt = blockIdx.x / heads;  // most queries first
@@ -309,21 +318,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const Waiter wait{&abort_word, &g_attn_bwd_error};
 
   if (warp == 8) {
-    if (lane == 0 && n > 0) {
-      mbar_arrive_expect_tx(&kv_full, 2 * C::kTileBytes);
-      load_tile<DP>(k_at, &map_k, key0, c, b, &kv_full);
-      load_tile<DP>(v_at, &map_v, key0, c, b, &kv_full);
+    if (n > 0) {
+      const uint32_t one = elect_one();
+      if (one) {
+        mbar_arrive_expect_tx(&kv_full, 2 * C::kTileBytes);
+        load_tile<DP>(k_at, &map_k, key0, c, b, &kv_full);
+        load_tile<DP>(v_at, &map_v, key0, c, b, &kv_full);
+      }
       int i = 0;
       for (; i < n; ++i) {
         const int s = i % kS, h = c * a.group + i / span, qt = first + i % span;
         if (!wait(&q_empty[s], (i / kS - 1) & 1)) break;
-        mbar_arrive_expect_tx(&q_full[s], C::kTileBytes + kStats * 4);
-        load_tile<DP>(q_at + s * C::kTileBytes, &map_q, qt * kTile, h, b, &q_full[s]);
-        bulk_g2s(stats + s * kStats, a.stats + ((b * (int64_t)a.q_heads + h) * q_tiles + qt) * kStats, kStats * 4,
-                 &q_full[s]);
+        if (one) {
+          mbar_arrive_expect_tx(&q_full[s], C::kTileBytes + kStats * 4);
+          load_tile<DP>(q_at + s * C::kTileBytes, &map_q, qt * kTile, h, b, &q_full[s]);
+          bulk_g2s(stats + s * kStats, a.stats + ((b * (int64_t)a.q_heads + h) * q_tiles + qt) * kStats, kStats * 4,
+                   &q_full[s]);
+        }
         if (!wait(&do_empty[s], (i / kS - 1) & 1)) break;
-        mbar_arrive_expect_tx(&do_full[s], C::kTileBytes);
-        load_tile<DP>(do_at + s * C::kTileBytes, &map_do, qt * kTile, h, b, &do_full[s]);
+        if (one) {
+          mbar_arrive_expect_tx(&do_full[s], C::kTileBytes);
+          load_tile<DP>(do_at + s * C::kTileBytes, &map_do, qt * kTile, h, b, &do_full[s]);
+        }
       }
       if (i < n) {  // gave up: leave the copies in flight time to land
         mbar_wait(&kv_full, 0, kSpinLimit >> 10);
@@ -333,45 +349,48 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
       }
     }
-    __syncwarp();
   } else if (warp == 9) {
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
       constexpr bool bf16 = !std::is_same<T, __half>::value;
       constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
       constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
+      constexpr uint32_t kStep = C::kTileBytes / 16;
+      const uint32_t one = elect_one();
+      const uint64_t q_desc = head_desc(q_at), do_desc = head_desc(do_at), k_desc = head_desc(k_at),
+                     v_desc = head_desc(v_at), q_rows = rows_desc(q_at), do_rows = rows_desc(do_at);
       auto make_s = [&](int i) {
         if (!wait(&q_full[i % kS], (i / kS) & 1)) return false;
         tc_fence_after();
-        mma_head<DP>(tmem, k_at, q_at + i % kS * C::kTileBytes, by_head);
-        mma_commit(&s_full);
+        mma_head<DP>(tmem, k_desc, q_desc + i % kS * kStep, by_head, one);
+        mma_commit(&s_full, one);
         return true;
       };
       auto make_dp = [&](int i) {
         if (!wait(&do_full[i % kS], (i / kS) & 1)) return false;
         tc_fence_after();
-        mma_head<DP>(tmem + C::kDp, v_at, do_at + i % kS * C::kTileBytes, by_head);
-        mma_commit(&dp_full);
+        mma_head<DP>(tmem + C::kDp, v_desc, do_desc + i % kS * kStep, by_head, one);
+        mma_commit(&dp_full, one);
         return true;
       };
       // While the warps make p the tensor core makes dk and the next dp, while
       // they make ds it makes dv and the next S.
       bool go = wait(&kv_full, 0) && make_s(0) && make_dp(0);
+#pragma unroll 1
       for (int i = 0; go && i < n; ++i) {
         const int s = i % kS;
         if (!(go = wait(&p_full, i & 1))) break;
         tc_fence_after();
-        mma_rows_halves<DP>(tmem + C::kDv, tmem, do_at + s * C::kTileBytes, by_rows, i > 0);
-        mma_commit(&do_empty[s]);
+        mma_rows(tmem + C::kDv, tmem, do_rows + s * kStep, by_rows, i > 0, one);
+        mma_commit(&do_empty[s], one);
         if (i + 1 < n && !(go = make_s(i + 1))) break;
         if (!(go = wait(&ds_full, i & 1))) break;
         tc_fence_after();
-        mma_rows_halves<DP>(tmem + C::kDk, tmem + C::kDp, q_at + s * C::kTileBytes, by_rows, i > 0);
-        mma_commit(&q_empty[s]);
+        mma_rows(tmem + C::kDk, tmem + C::kDp, q_rows + s * kStep, by_rows, i > 0, one);
+        mma_commit(&q_empty[s], one);
         if (i + 1 < n && !(go = make_dp(i + 1))) break;
       }
-      mma_commit(&done);
+      mma_commit(&done, one);
     }
-    __syncwarp();
   } else {
     // ---- a thread half a key's row: columns (queries) [64 half, 64 half + 64)
     const int half = warp / 4, key = key0 + (warp & 3) * 32 + lane;

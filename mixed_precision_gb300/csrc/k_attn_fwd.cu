@@ -5,10 +5,13 @@
 // with two heads a group both tiles are the same rows of two heads. Keys and
 // values pass once through shared memory (TMA) in tiles of 128.
 //   S_t = Q_t K^T      tcgen05, S in TMEM (fp32)
-//   P_t = 2^(c S_t - c m)   a thread per row; P_t (16 bits) over S_t in TMEM
+//   P_t = 2^(c S_t - c m)   two threads a row, 64 keys each; P_t (16 bits) over
+//                      S_t in TMEM
 //   O_t += P_t V       tcgen05, P from TMEM, O in TMEM
-// The two tiles alternate: while four warps turn S_0 into P_0 the tensor core
-// works for tile 1, and the other way round. The row's maximum m is kept as
+// The two tiles alternate: while eight warps turn S_0 into P_0 the tensor core
+// works for tile 1, and the other way round. What bounds it is the chain from
+// one S through the softmax to the next; halving each thread's part of the row
+// shortens it. The row's maximum m is kept as
 // it was until it grows by more than 8 in the exponent of two: P stays
 // below 2^8, sums and O are fp32, and O is rescaled rarely (once or twice a
 // row on ordinary data) instead of in every tile.
@@ -24,7 +27,11 @@ namespace {
 
 __device__ unsigned g_attn_fwd_error;
 
-constexpr int kFwdThreads = 10 * 32;  // two softmax groups of four warps, the TMA warp, the MMA warp
+// Four softmax groups of four warps (tile, half of the keys), then a group of
+// which one warp issues the TMA loads and one the MMAs. The groups' registers
+// add up to the launch's: 512 x 104 + 128 x 64 = 640 x 96.
+constexpr int kFwdThreads = 20 * 32, kTmaWarp = 16, kMmaWarp = 17;
+constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
 constexpr float kStale = 8.0f;        // how far the maximum may lag, as an exponent of two
 
 template <int DP>
@@ -43,9 +50,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t q_full, kv_full[C::kSlots], kv_empty[C::kSlots], s_full[2], p_full[2], o_full;
   __shared__ uint32_t tmem_slot, abort_word;
+  __shared__ float tops[2][2][2][kTile];  // [turn][tile][half][row]: maxima, in the end sums
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem), ring = base + 2 * C::kTileBytes;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
 
   // blocks of the last query rows (most keys under a causal mask) come first
   const int bh = blockIdx.x % (int)(a.batch * a.kv_heads), p = pairs - 1 - blockIdx.x / (int)(a.batch * a.kv_heads);
@@ -74,36 +82,42 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      mbar_init(&p_full[t], 8);
     }
     mbar_init(&o_full, 1);
     abort_word = 0;
     mbar_init_fence();
   }
-  if (warp == 9) tmem_alloc(&tmem_slot, 512);
+  if (warp == kMmaWarp) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const Waiter wait{&abort_word, &g_attn_fwd_error};
 
-  if (warp == 8) {
+  if (warp >= kTmaWarp) fewer_registers<kOtherRegs>();
+  else more_registers<kSoftmaxRegs>();
+  if (warp == kTmaWarp) {
     // ---- TMA: the query tiles, then K_0, V_0, K_1, V_1, ...
-    if (lane == 0 && n > 0) {
-      tma_prefetch(&map_q);
-      tma_prefetch(&map_k);
-      tma_prefetch(&map_v);
-      mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * C::kTileBytes);
-      for (int t = 0; t < (two ? 2 : 1); ++t) {
-        const int u = 2 * p + t;
-        load_tile<DP>(base + t * C::kTileBytes, &map_q, u / a.group * kTile, c * a.group + u % a.group, b, &q_full);
+    if (n > 0) {
+      const uint32_t one = elect_one();
+      if (one) {
+        tma_prefetch(&map_k);
+        tma_prefetch(&map_v);
+        mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * C::kTileBytes);
+        for (int t = 0; t < (two ? 2 : 1); ++t) {
+          const int u = 2 * p + t;
+          load_tile<DP>(base + t * C::kTileBytes, &map_q, u / a.group * kTile, c * a.group + u % a.group, b, &q_full);
+        }
       }
       int i = 0;
       for (; i < 2 * n; ++i) {
         const int s = i % C::kSlots;
         if (!wait(&kv_empty[s], (i / C::kSlots - 1) & 1)) break;
-        mbar_arrive_expect_tx(&kv_full[s], C::kTileBytes);
-        load_tile<DP>(ring + s * C::kTileBytes, i & 1 ? &map_v : &map_k, (first + i / 2) * kTile, c, b, &kv_full[s]);
+        if (one) {
+          mbar_arrive_expect_tx(&kv_full[s], C::kTileBytes);
+          load_tile<DP>(ring + s * C::kTileBytes, i & 1 ? &map_v : &map_k, (first + i / 2) * kTile, c, b, &kv_full[s]);
+        }
       }
       if (i < 2 * n) {  // gave up: leave the copies in flight time to land
         mbar_wait(&q_full, 0, kSpinLimit >> 10);
@@ -111,52 +125,53 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           mbar_wait(&kv_full[k % C::kSlots], (k / C::kSlots) & 1, kSpinLimit >> 10);
       }
     }
-    __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp) {
     // ---- the tensor cores
-    if (lane == 0 && n > 0) {
+    if (n > 0) {
       constexpr bool bf16 = !std::is_same<T, __half>::value;
       constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
       constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
       const int tiles = two ? 2 : 1;
-      auto slot = [&](int i) { return ring + i % C::kSlots * C::kTileBytes; };
+      const uint32_t one = elect_one();
+      const uint64_t q_desc = head_desc(base), k_desc = head_desc(ring), v_desc = rows_desc(ring);
+      auto slot = [&](int i) { return static_cast<uint32_t>(i % C::kSlots * (C::kTileBytes / 16)); };
       auto arrived = [&](int i) {
         const bool ok = wait(&kv_full[i % C::kSlots], (i / C::kSlots) & 1);
         tc_fence_after();
         return ok;
       };
+      auto make_s = [&](int t, int i) {
+        mma_head<DP>(tmem + t * kTile, q_desc + t * (C::kTileBytes / 16), k_desc + slot(i), by_head, one);
+        mma_commit(&s_full[t], one);
+      };
       bool go = wait(&q_full, 0) && arrived(0);
-      for (int t = 0; go && t < tiles; ++t) {
-        mma_head<DP>(tmem + t * kTile, base + t * C::kTileBytes, slot(0), by_head);
-        mma_commit(&s_full[t]);
-      }
-      if (go) mma_commit(&kv_empty[0]);
+      for (int t = 0; go && t < tiles; ++t) make_s(t, 0);
+      if (go) mma_commit(&kv_empty[0], one);
+#pragma unroll 1
       for (int j = 0; go && j < n; ++j) {
         const int kn = 2 * j + 2, v = 2 * j + 1;
         const bool more = j + 1 < n;
         go = arrived(v);
+#pragma unroll 1
         for (int t = 0; go && t < tiles; ++t) {
           if (!(go = wait(&p_full[t], j & 1))) break;
           tc_fence_after();
-          mma_rows<DP>(tmem + C::kO + t * DP, tmem + t * kTile, slot(v), by_rows, j > 0);
-          if (t == tiles - 1) mma_commit(&kv_empty[v % C::kSlots]);
+          mma_rows(tmem + C::kO + t * DP, tmem + t * kTile, v_desc + slot(v), by_rows, j > 0, one);
+          if (t == tiles - 1) mma_commit(&kv_empty[v % C::kSlots], one);
           if (!more) continue;
           if (t == 0 && !(go = arrived(kn))) break;
-          // over P_t, which the product before it reads first
-          mma_head<DP>(tmem + t * kTile, base + t * C::kTileBytes, slot(kn), by_head);
-          mma_commit(&s_full[t]);
-          if (t == tiles - 1) mma_commit(&kv_empty[kn % C::kSlots]);
+          make_s(t, kn);  // over P_t, which the product before it reads first
+          if (t == tiles - 1) mma_commit(&kv_empty[kn % C::kSlots], one);
         }
       }
-      mma_commit(&o_full);
+      mma_commit(&o_full, one);
     }
-    __syncwarp();
-  } else {
-    // ---- softmax: four warps a tile, a thread a row
-    const int t = warp / 4, u = 2 * p + t;
+  } else if (warp < kTmaWarp) {
+    // ---- softmax: a thread half a row, keys [64 half, 64 half + 64) of each tile
+    const int t = warp / 8, half = warp / 4 & 1, u = 2 * p + t, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t s_at = tmem + lanes + t * kTile, o_at = tmem + lanes + C::kO + t * DP;
-    const int i = u / a.group * kTile + (warp & 3) * 32 + lane;  // the query
+    const uint32_t s_at = tmem + lanes + t * kTile + half * 64, o_at = tmem + lanes + C::kO + t * DP + half * (DP / 2);
+    const int i = u / a.group * kTile + row;  // the query
     const int64_t h = c * a.group + u % a.group;
     const float scale2 = a.scale * kLog2e;
     float top = -INFINITY, total = 0.0f;
@@ -165,24 +180,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       int lo, hi;
       key_range(a, keys, i, lo, hi);
       for (int j = 0; j < n; ++j) {
-        if (!(ok = wait(&s_full[t], j & 1))) break;
+        // a wait that gives up goes on to the barriers with what is there: the
+        // other half may be waiting in them
+        ok = wait(&s_full[t], j & 1) && ok;
         tc_fence_after();
-        float s[kTile];
-        uint32_t(&r)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(s);
+        const int key0 = (first + j) * kTile, from = lo - key0 - half * 64, to = hi - key0 - half * 64;
+        // columns [from, to) are seen; most tiles need no mask
+        const bool mask = __any_sync(0xFFFFFFFFu, from > 0 || to < 64);
+        // S is read twice, for the maximum and for P: 64 values kept between the
+        // two do not fit the registers of sixteen warps
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int q = 0; q < 64; q += 32) {
+          float s[32];
+          tmem_ld32(s_at + q, reinterpret_cast<uint32_t(&)[32]>(s));
+          tmem_wait_ld();
+          if (mask) mask_row<32>(s, from - q, to - q);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32(s_at + k * 32, r[k]);
-        tmem_wait_ld();
-        const int key0 = (first + j) * kTile;
-        // columns [lo - key0, hi - key0) are seen; most tiles need no mask
-        if (__any_sync(0xFFFFFFFFu, lo > key0 || hi < key0 + kTile)) {
-          const int from = lo - key0, to = hi - key0;
+          for (int k = 0; k < 32; k += 8)
 #pragma unroll
-          for (int k = 0; k < kTile; ++k) s[k] = k >= from && k < to ? s[k] : -INFINITY;
+            for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], s[k + e], s[k + 4 + e]);
         }
-        float m4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int k = 4; k < kTile; ++k) m4[k & 3] = fmaxf(m4[k & 3], s[k]);
-        const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        float m = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+        tops[j & 1][t][half][row] = m;
+        named_sync(1 + t, 256);
+        m = fmaxf(m, tops[j & 1][t][half ^ 1][row]);
         // the first maximum, or one that has grown too far: rescale
         const bool raise = m > top && (top == -INFINITY || (m - top) * scale2 > kStale);
         if (__any_sync(0xFFFFFFFFu, raise)) {
@@ -191,42 +213,44 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           total *= f;
           if (j > 0) {  // O is complete up to the tile before: its product was issued before this S
 #pragma unroll 1
-            for (int k = 0; k < DP; k += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_at + k, o);
+            for (int k = 0; k < DP / 2; k += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_at + k, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_at + k, o);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(o_at + k, o);
             }
           }
         }
         const float minus = top == -INFINITY ? 0.0f : -top * scale2;
         const uint64_t scale_pair = pair(scale2, scale2), minus_pair = pair(minus, minus);
         uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          float s[32];
+          tmem_ld32(s_at + q * 32, reinterpret_cast<uint32_t(&)[32]>(s));
+          tmem_wait_ld();
+          if (mask) mask_row<32>(s, from - q * 32, to - q * 32);
+          uint32_t w[16];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t w[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int e = half * 64 + 2 * k;
+          for (int k = 0; k < 16; ++k) {
             float x, y;
-            unpair(fma2(pair(s[e], s[e + 1]), scale_pair, minus_pair), x, y);
+            unpair(fma2(pair(s[2 * k], s[2 * k + 1]), scale_pair, minus_pair), x, y);
             x = exp2_fast(x);
             y = exp2_fast(y);
             sum[k & 1] = add2(sum[k & 1], pair(x, y));
             w[k] = round2<T>(x, y);
           }
-          tmem_st32(s_at + half * 32, w);
+          tmem_st16(s_at + q * 16, w);
         }
         float x, y;
         unpair(add2(sum[0], sum[1]), x, y);
         total += x + y;
-        if (t == 0 && key0 + kTile > keys && keys < a.k_len) {
+        if (t == 0 && half == 0 && key0 + kTile > keys && keys < a.k_len) {
           // rows of V past the length: zeros. Tile 0's product is the first to
           // read them, and waits for this thread.
-          if (!(ok = wait(&kv_full[(2 * j + 1) % C::kSlots], ((2 * j + 1) / C::kSlots) & 1))) break;
-          const int row = (warp & 3) * 32 + lane;
+          ok = wait(&kv_full[(2 * j + 1) % C::kSlots], ((2 * j + 1) / C::kSlots) & 1) && ok;
           if (key0 + row >= keys) zero_row<DP>(smem + (2 + (2 * j + 1) % C::kSlots) * C::kTileBytes, row);
           fence_async_smem();
         }
@@ -235,21 +259,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[t]);
       }
-      if (n > 0 && ok) ok = wait(&o_full, 0);
+      if (n > 0) ok = wait(&o_full, 0) && ok;
       tc_fence_after();
+      // both halves' sums, in the order of the keys
+      tops[n & 1][t][half][row] = total;
+      named_sync(1 + t, 256);
+      total = tops[n & 1][t][0][row] + tops[n & 1][t][1][row];
       const bool none = total == 0.0f;  // no key seen (a seen key gives at least 2^-8 ... or NaN)
       const float inv = none ? 0.0f : 1.0f / total;
-      T* out = static_cast<T*>(a.o) + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2];
+      T* out = static_cast<T*>(a.o) + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2] + half * (DP / 2);
       // `none` may differ between the lanes of a warp: their sums are zeros
-      store_row<T, DP>(o_at, inv, out, a.head_dim, n == 0, i < a.q_len && ok);
-      if (i < a.q_len && ok)
+      store_row<T, DP / 2>(o_at, inv, out, a.head_dim - half * (DP / 2), n == 0, i < a.q_len && ok);
+      if (half == 0 && i < a.q_len && ok)
         a.lse[(b * (int64_t)a.q_heads + h) * a.q_len + i] =
             none ? -INFINITY : (top * scale2 + log2f(total)) * kLn2;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_free(tmem, 512);
   }

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   // the swizzle is a function of address bits: tiles start on 1024 bytes
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
   const int rank = blockIdx.x % split, tile = blockIdx.x / split;
   const int n0 = tile % n_tiles * BN;
   const int64_t m0 = (int64_t)(tile / n_tiles) * (MT * 128);
@@ -291,48 +291,47 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       while (go && run + 1 < runs) go = move(run++);
   } else if (warp == kConvWarps) {
     // ---- dy tiles by TMA
-    if (lane == 0) {
-      int step = 0;
-      for (; step < steps; ++step) {
-        const int s = step % C::kStages;
-        if (step >= C::kStages && !wait(&empty[s], (step / C::kStages - 1) & 1)) break;
+    const uint32_t one = elect_one();
+    int step = 0;
+    for (; step < steps; ++step) {
+      const int s = step % C::kStages;
+      if (!wait(&empty[s], (step / C::kStages - 1) & 1)) break;
+      if (one) {
         mbar_arrive_expect_tx(&full[s], C::kABytes);
 #pragma unroll
         for (int i = 0; i < MT * 2; ++i)
           tma_load2(base + s * C::kStage + i * kChunk, &map, (int)m0 + i * 64, (int)((first + step) * kStep), &full[s]);
       }
-      if (step < steps)  // gave up: leave the copies in flight time to land
-        for (int i = max(0, step - C::kStages); i < step; ++i)
-          mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, kSpinLimit >> 10);
     }
-    __syncwarp();
+    if (step < steps)  // gave up: leave the copies in flight time to land
+      for (int i = max(0, step - C::kStages); i < step; ++i)
+        mbar_wait(&full[i % C::kStages], (i / C::kStages) & 1, kSpinLimit >> 10);
   } else {
     // ---- the tensor cores
-    if (lane == 0) {
-      constexpr uint32_t idesc = mma_desc(!std::is_same<T, __half>::value,
-                                          128, BN, true, true);
-      for (int step = 0; step < steps; ++step) {
-        const int s = step % C::kStages;
-        if (!wait(&full[s], (step / C::kStages) & 1)) break;
+    constexpr uint32_t idesc = mma_desc(!std::is_same<T, __half>::value, 128, BN, true, true);
+    const uint32_t one = elect_one();
+    const uint64_t a_desc = smem_desc(base, kChunk, 1024), b_desc = smem_desc(base + C::kABytes, kChunk, 1024);
+#pragma unroll 1
+    for (int step = 0; step < steps; ++step) {
+      const int s = step % C::kStages;
+      if (!wait(&full[s], (step / C::kStages) & 1)) break;
+      tc_fence_after();
+      const uint32_t at = s * (C::kStage / 16);  // in the descriptors' units of 16 bytes
+      const bool go_on = (ROUND ? step % kRun : step) > 0;
+#pragma unroll
+      for (int k = 0; k < kStep / 16; ++k)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          mma_ss(tmem + m * BN, a_desc + at + (m * 2 * kChunk + k * 2048) / 16, b_desc + at + k * 2048 / 16, idesc,
+                 go_on || k > 0, one);
+      mma_commit(&empty[s], one);
+      if (ROUND && step % kRun == kRun - 1 && step + 1 < steps) {
+        mma_commit(&done, one);
+        if (!wait(&moved, (step / kRun) & 1)) break;
         tc_fence_after();
-        const uint32_t at = base + s * C::kStage;
-#pragma unroll
-        for (int k = 0; k < kStep / 16; ++k)
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            mma_ss(tmem + m * BN, smem_desc(at + m * 2 * kChunk + k * 2048, kChunk, 1024),
-                   smem_desc(at + C::kABytes + k * 2048, kChunk, 1024), idesc,
-                   (ROUND ? step % kRun : step) > 0 || k > 0);
-        mma_commit(&empty[s]);
-        if (ROUND && step % kRun == kRun - 1 && step + 1 < steps) {
-          mma_commit(&done);
-          if (!wait(&moved, (step / kRun) & 1)) break;
-          tc_fence_after();
-        }
       }
-      mma_commit(&done);
     }
-    __syncwarp();
+    mma_commit(&done, one);
   }
   // Every MMA of the block has finished, and with it every read of the tiles
   // (and every TMA write: each was waited for before its MMAs).
