@@ -131,30 +131,40 @@ __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
     *reinterpret_cast<uint4*>(tile + k / 8 * kTileChunk + row * 128 + k % 8 * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// A row of sums in TMEM, times f, rounded to T and stored: elements [0, dim).
-// The whole warp calls it; `live` lanes store.
-template <typename T, int DP>
-__device__ __forceinline__ void store_row(uint32_t addr, float f, T* out, int dim, bool zero, bool live) {
-#pragma unroll 1
-  for (int k = 0; k < DP; k += 32) {
+// A thread's part of an output row: N sums from TMEM column addr, times f,
+// rounded to T, into a tile at [row][col0] (swizzled as TMA reads it). Rows
+// written straight to global memory would touch 32 lines an instruction (3.5 us
+// a block); a tile leaves by one bulk store. The whole warp calls it.
+template <typename T, int N>
+__device__ __forceinline__ void stage_row(uint8_t* tile, int row, int col0, uint32_t addr, float f, bool zero) {
+#pragma unroll
+  for (int k = 0; k < N; k += 32) {
     uint32_t o[32];
     if (!zero) {
       tmem_ld32(addr + k, o);
       tmem_wait_ld();
     }
-    if (live) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        if (k + g * 8 >= dim) break;
-        uint32_t w[4];
+    for (int g = 0; g < 4; ++g) {
+      uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = zero ? 0u
-                      : round2<T>(__uint_as_float(o[g * 8 + 2 * e]) * f, __uint_as_float(o[g * 8 + 2 * e + 1]) * f);
-        *reinterpret_cast<uint4*>(out + k + g * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int e = 0; e < 4; ++e)
+        w[e] = zero ? 0u : round2<T>(__uint_as_float(o[g * 8 + 2 * e]) * f, __uint_as_float(o[g * 8 + 2 * e + 1]) * f);
+      const int piece = (col0 + k) / 8 + g;
+      *reinterpret_cast<uint4*>(tile + piece / 8 * kTileChunk + row * 128 + (piece % 8 ^ (row & 7)) * 16) =
+          make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+}
+
+// The 64-wide chunks of a staged tile to the tensor, by one thread.
+template <int DP>
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t src, int dim, int token, int head,
+                                           int batch) {
+#pragma unroll
+  for (int i = 0; i < DP / 64; ++i)
+    if (i * 64 < dim) tma_store4(map, src + i * kTileChunk, i * 64, token, head, batch);
+  tma_store_done();
 }
 
 // Maps of a [batch, token, head, dim] tensor for tiles of 128 tokens x 64.

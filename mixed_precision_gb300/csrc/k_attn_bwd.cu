@@ -38,8 +38,8 @@ struct Dq {
 template <typename T, int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     k_attn_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
-              const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnArgs a,
-              int q_tiles) {
+              const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+              const __grid_constant__ CUtensorMap map_dq, const AttnArgs a, int q_tiles) {
   using C = Dq<DP>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t q_full, k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV], s_full[2],
@@ -60,7 +60,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   key_range(a, keys, min(row0 + kTile, (int)a.q_len) - 1, skip, hi);
   const int first = lo / kTile, n = lo < hi ? (hi + kTile - 1) / kTile - first : 0;
 
-  if (threadIdx.x == 0) {
+  // The TMA warp prepares the barriers and starts the first loads before the
+  // block's first barrier: TMEM's allocation takes place meanwhile.
+  auto load_k = [&](int j) {  // by one thread
+    const int s = j % C::kK;
+    mbar_arrive_expect_tx(&k_full[s], C::kTileBytes);
+    load_tile<DP>(k_at + s * C::kTileBytes, &map_k, (first + j) * kTile, c, b, &k_full[s]);
+  };
+  auto load_v = [&](int j) {
+    const int s = j % C::kV;
+    mbar_arrive_expect_tx(&v_full[s], C::kTileBytes);
+    load_tile<DP>(v_at + s * C::kTileBytes, &map_v, (first + j) * kTile, c, b, &v_full[s]);
+  };
+  const int early = min(n, C::kV);  // tiles into slots that nobody has used
+  if (warp == 8 && elect_one()) {
     mbar_init(&q_full, 1);
     for (int s = 0; s < C::kK; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_empty[s], 1);
     for (int s = 0; s < C::kV; ++s) mbar_init(&v_full[s], 1), mbar_init(&v_empty[s], 1);
@@ -70,6 +83,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(&done, 1);
     abort_word = 0;
     mbar_init_fence();
+    if (n > 0) {
+      mbar_arrive_expect_tx(&q_full, 2 * C::kTileBytes);
+      load_tile<DP>(q_at, &map_q, row0, h, b, &q_full);
+      load_tile<DP>(do_at, &map_do, row0, h, b, &q_full);
+      for (int j = 0; j < early; ++j) load_k(j), load_v(j);
+    }
   }
   if (warp == 9) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
@@ -78,34 +97,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tmem = tmem_slot;
   const Waiter wait{&abort_word, &g_attn_bwd_error};
 
+  griddep_trigger();
   if (warp == 8) {
-    if (n > 0) {
-      const uint32_t one = elect_one();
-      if (one) {
-        mbar_arrive_expect_tx(&q_full, 2 * C::kTileBytes);
-        load_tile<DP>(q_at, &map_q, row0, h, b, &q_full);
-        load_tile<DP>(do_at, &map_do, row0, h, b, &q_full);
-      }
-      int j = 0;
-      for (; j < n; ++j) {
-        const int ks = j % C::kK, vs = j % C::kV, token = (first + j) * kTile;
-        if (!wait(&k_empty[ks], (j / C::kK - 1) & 1)) break;
-        if (one) {
-          mbar_arrive_expect_tx(&k_full[ks], C::kTileBytes);
-          load_tile<DP>(k_at + ks * C::kTileBytes, &map_k, token, c, b, &k_full[ks]);
-        }
-        if (!wait(&v_empty[vs], (j / C::kV - 1) & 1)) break;
-        if (one) {
-          mbar_arrive_expect_tx(&v_full[vs], C::kTileBytes);
-          load_tile<DP>(v_at + vs * C::kTileBytes, &map_v, token, c, b, &v_full[vs]);
-        }
-      }
-      if (j < n) {  // gave up: leave the copies in flight time to land
-        mbar_wait(&q_full, 0, kSpinLimit >> 10);
-        for (int i = max(0, j - C::kK); i <= j; ++i) {
-          mbar_wait(&k_full[i % C::kK], (i / C::kK) & 1, kSpinLimit >> 10);
-          mbar_wait(&v_full[i % C::kV], (i / C::kV) & 1, kSpinLimit >> 10);
-        }
+    const uint32_t one = elect_one();
+    int j = early;
+    for (; j < n; ++j) {
+      if (!wait(&k_empty[j % C::kK], (j / C::kK - 1) & 1)) break;
+      if (one) load_k(j);
+      if (!wait(&v_empty[j % C::kV], (j / C::kV - 1) & 1)) break;
+      if (one) load_v(j);
+    }
+    if (j < n) {  // gave up: leave the copies in flight time to land
+      mbar_wait(&q_full, 0, kSpinLimit >> 10);
+      for (int i = max(0, j - C::kK); i <= j; ++i) {
+        mbar_wait(&k_full[i % C::kK], (i / C::kK) & 1, kSpinLimit >> 10);
+        mbar_wait(&v_full[i % C::kV], (i / C::kV) & 1, kSpinLimit >> 10);
       }
     }
   } else if (warp == 9) {
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     part[half][row] = delta;
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+    named_sync(1, 256);
     const float minus_delta = -(part[0][row] + part[1][row]);
     // a row that sees nothing (or is none) gets p = 2^-inf = 0 everywhere
     const float lse = live ? a.lse_in[at] : -INFINITY;
@@ -238,10 +244,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     if (n > 0 && ok) ok = wait(&done, 0);
     tc_fence_after();
-    T* out = static_cast<T*>(a.dq) + b * a.dqs[0] + (int64_t)i * a.dqs[1] + h * a.dqs[2];
-    constexpr int kHalf = DP / 2;
-    store_row<T, kHalf>(tmem + lanes + C::kDq + half * kHalf, a.scale, out + half * kHalf, a.head_dim - half * kHalf,
-                        n == 0, live && ok);
+    // the tile leaves from the place of its queries, which are done with
+    stage_row<T, DP / 2>(smem, row, half * (DP / 2), tmem + lanes + C::kDq + half * (DP / 2), a.scale, n == 0);
+    fence_async_smem();
+    named_sync(1, 256);
+    if (warp == 0 && __all_sync(0xFFFFFFFFu, ok) && elect_one()) store_tile<DP>(&map_dq, q_at, a.head_dim, row0, h, b);
   }
   tc_fence_before();
   __syncthreads();
@@ -267,8 +274,9 @@ struct Dkv {
 template <typename T, int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     k_attn_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
-               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnArgs a,
-               int q_tiles) {
+               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+               const __grid_constant__ CUtensorMap map_dk, const __grid_constant__ CUtensorMap map_dv,
+               const AttnArgs a, int q_tiles) {
   using C = Dkv<DP>;
   constexpr int kS = C::kSlots;
   extern __shared__ uint8_t raw[];
@@ -294,7 +302,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
   const int span = key0 < keys ? max(0, last - first) : 0, n = span * a.group;
 
-  if (threadIdx.x == 0) {
+  auto load_q = [&](int i) {  // with the tile's statistics; by one thread
+    const int s = i % kS, h = c * a.group + i / span, qt = first + i % span;
+    mbar_arrive_expect_tx(&q_full[s], C::kTileBytes + kStats * 4);
+    load_tile<DP>(q_at + s * C::kTileBytes, &map_q, qt * kTile, h, b, &q_full[s]);
+    bulk_g2s(stats + s * kStats, a.stats + ((b * (int64_t)a.q_heads + h) * q_tiles + qt) * kStats, kStats * 4,
+             &q_full[s]);
+  };
+  auto load_do = [&](int i) {
+    const int s = i % kS, h = c * a.group + i / span, qt = first + i % span;
+    mbar_arrive_expect_tx(&do_full[s], C::kTileBytes);
+    load_tile<DP>(do_at + s * C::kTileBytes, &map_do, qt * kTile, h, b, &do_full[s]);
+  };
+  const int early = min(n, kS);
+  if (warp == 8 && elect_one()) {
     mbar_init(&kv_full, 1);
     for (int s = 0; s < kS; ++s) {
       mbar_init(&q_full[s], 1);
@@ -309,6 +330,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(&done, 1);
     abort_word = 0;
     mbar_init_fence();
+    if (n > 0) {
+      mbar_arrive_expect_tx(&kv_full, 2 * C::kTileBytes);
+      load_tile<DP>(k_at, &map_k, key0, c, b, &kv_full);
+      load_tile<DP>(v_at, &map_v, key0, c, b, &kv_full);
+      for (int i = 0; i < early; ++i) load_do(i);
+    }
+    // The statistics are the kernel's before, which may still be running. Every
+    // block waits for it, so that this kernel does not end before that one.
+    griddep_wait();
+    for (int i = 0; i < early; ++i) load_q(i);
   }
   if (warp == 9) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
@@ -318,35 +349,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const Waiter wait{&abort_word, &g_attn_bwd_error};
 
   if (warp == 8) {
-    if (n > 0) {
-      const uint32_t one = elect_one();
-      if (one) {
-        mbar_arrive_expect_tx(&kv_full, 2 * C::kTileBytes);
-        load_tile<DP>(k_at, &map_k, key0, c, b, &kv_full);
-        load_tile<DP>(v_at, &map_v, key0, c, b, &kv_full);
-      }
-      int i = 0;
-      for (; i < n; ++i) {
-        const int s = i % kS, h = c * a.group + i / span, qt = first + i % span;
-        if (!wait(&q_empty[s], (i / kS - 1) & 1)) break;
-        if (one) {
-          mbar_arrive_expect_tx(&q_full[s], C::kTileBytes + kStats * 4);
-          load_tile<DP>(q_at + s * C::kTileBytes, &map_q, qt * kTile, h, b, &q_full[s]);
-          bulk_g2s(stats + s * kStats, a.stats + ((b * (int64_t)a.q_heads + h) * q_tiles + qt) * kStats, kStats * 4,
-                   &q_full[s]);
-        }
-        if (!wait(&do_empty[s], (i / kS - 1) & 1)) break;
-        if (one) {
-          mbar_arrive_expect_tx(&do_full[s], C::kTileBytes);
-          load_tile<DP>(do_at + s * C::kTileBytes, &map_do, qt * kTile, h, b, &do_full[s]);
-        }
-      }
-      if (i < n) {  // gave up: leave the copies in flight time to land
-        mbar_wait(&kv_full, 0, kSpinLimit >> 10);
-        for (int k = max(0, i - kS); k <= i; ++k) {
-          mbar_wait(&q_full[k % kS], (k / kS) & 1, kSpinLimit >> 10);
-          mbar_wait(&do_full[k % kS], (k / kS) & 1, kSpinLimit >> 10);
-        }
+    const uint32_t one = elect_one();
+    int i = early;
+    for (; i < n; ++i) {
+      if (!wait(&q_empty[i % kS], (i / kS - 1) & 1)) break;
+      if (one) load_q(i);
+      if (!wait(&do_empty[i % kS], (i / kS - 1) & 1)) break;
+      if (one) load_do(i);
+    }
+    if (i < n) {  // gave up: leave the copies in flight time to land
+      mbar_wait(&kv_full, 0, kSpinLimit >> 10);
+      for (int k = max(0, i - kS); k <= i; ++k) {
+        mbar_wait(&q_full[k % kS], (k / kS) & 1, kSpinLimit >> 10);
+        mbar_wait(&do_full[k % kS], (k / kS) & 1, kSpinLimit >> 10);
       }
     }
   } else if (warp == 9) {
@@ -464,12 +479,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     if (n > 0 && ok) ok = wait(&done, 0);
     tc_fence_after();
-    // the first four warps store dk, the others dv
-    const bool live = key < a.k_len && ok;
-    const int64_t *st = half == 0 ? a.dks : a.dvs;
-    T* out = static_cast<T*>(half == 0 ? a.dk : a.dv) + b * st[0] + (int64_t)key * st[1] + c * st[2];
-    store_row<T, DP>(tmem + lanes + (half == 0 ? C::kDk : C::kDv), half == 0 ? a.scale : 1.0f, out, a.head_dim, n == 0,
-                     live);
+    // the first four warps store dk, the others dv, from the query and do tiles'
+    // places, which are done with
+    const int slot = 2 + half * kS;
+    stage_row<T, DP>(smem + slot * C::kTileBytes, (warp & 3) * 32 + lane, 0,
+                     tmem + lanes + (half == 0 ? C::kDk : C::kDv), half == 0 ? a.scale : 1.0f, n == 0);
+    fence_async_smem();
+    named_sync(1 + half, 128);
+    if ((warp & 3) == 0 && __all_sync(0xFFFFFFFFu, ok) && elect_one())
+      store_tile<DP>(half == 0 ? &map_dk : &map_dv, k_at + slot * C::kTileBytes, a.head_dim, key0, c, b);
   }
   tc_fence_before();
   __syncthreads();
@@ -483,14 +501,17 @@ int64_t tiles(int64_t len) { return (len + kTile - 1) / kTile; }
 
 template <typename T, int DP>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
-  CUtensorMap q, g, k, v;
+  CUtensorMap q, g, k, v, dq, dk, dv;
   // a side without rows is never loaded, but its maps still have to be valid
   const bool qs = a.q_len > 0, ks = a.k_len > 0;
   const int64_t q_len = qs ? a.q_len : 1, k_len = ks ? a.k_len : 1;
   if (!attn_map(&q, qs ? a.q : a.k, a.dtype, a.qs, a.batch, q_len, a.q_heads, a.head_dim) ||
       !attn_map(&g, qs ? a.dout : a.k, a.dtype, a.dos, a.batch, q_len, a.q_heads, a.head_dim) ||
       !attn_map(&k, ks ? a.k : a.q, a.dtype, a.ks, a.batch, k_len, a.kv_heads, a.head_dim) ||
-      !attn_map(&v, ks ? a.v : a.q, a.dtype, a.vs, a.batch, k_len, a.kv_heads, a.head_dim))
+      !attn_map(&v, ks ? a.v : a.q, a.dtype, a.vs, a.batch, k_len, a.kv_heads, a.head_dim) ||
+      !attn_map(&dq, qs ? a.dq : a.dk, a.dtype, a.dqs, a.batch, q_len, a.q_heads, a.head_dim) ||
+      !attn_map(&dk, ks ? a.dk : a.dq, a.dtype, a.dks, a.batch, k_len, a.kv_heads, a.head_dim) ||
+      !attn_map(&dv, ks ? a.dv : a.dq, a.dtype, a.dvs, a.batch, k_len, a.kv_heads, a.head_dim))
     return cudaErrorInvalidValue;
   const int64_t q_blocks = tiles(a.q_len) * a.batch * a.q_heads, k_blocks = tiles(a.k_len) * a.batch * a.kv_heads;
   if (q_blocks > 0x7FFFFFFFll || k_blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
@@ -501,12 +522,22 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int q_tiles = (int)tiles(a.q_len);
   if (q_blocks > 0)
-    k_attn_dq<T, DP><<<(unsigned)q_blocks, kBwdThreads, Dq<DP>::kSmem, s>>>(q, g, k, v, a, q_tiles);
+    k_attn_dq<T, DP><<<(unsigned)q_blocks, kBwdThreads, Dq<DP>::kSmem, s>>>(q, g, k, v, dq, a, q_tiles);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (k_blocks > 0)
-    k_attn_dkv<T, DP><<<(unsigned)k_blocks, kBwdThreads, Dkv<DP>::kSmem, s>>>(q, g, k, v, a, q_tiles);
-  return cudaGetLastError();
+  if (k_blocks == 0) return cudaSuccess;
+  // its blocks may start while the last of dq's run
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)k_blocks);
+  cfg.blockDim = dim3(kBwdThreads);
+  cfg.dynamicSmemBytes = Dkv<DP>::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = q_blocks > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_attn_dkv<T, DP>, q, g, k, v, dk, dv, a, q_tiles);
 }
 
 template <typename T>

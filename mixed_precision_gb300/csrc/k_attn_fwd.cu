@@ -45,7 +45,8 @@ struct Fwd {
 template <typename T, int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     k_attn_fwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-               const __grid_constant__ CUtensorMap map_v, const AttnArgs a, int q_tiles, int pairs) {
+               const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o, const AttnArgs a,
+               int q_tiles, int pairs) {
   using C = Fwd<DP>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t q_full, kv_full[C::kSlots], kv_empty[C::kSlots], s_full[2], p_full[2], o_full;
@@ -74,7 +75,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
   const int n = max(0, last - first);
 
-  if (threadIdx.x == 0) {
+  // The TMA warp prepares the barriers and starts the first loads before the
+  // block's first barrier: TMEM's allocation takes place meanwhile.
+  auto load = [&](int i) {  // K and V tiles in turn, by one thread
+    const int s = i % C::kSlots;
+    mbar_arrive_expect_tx(&kv_full[s], C::kTileBytes);
+    load_tile<DP>(ring + s * C::kTileBytes, i & 1 ? &map_v : &map_k, (first + i / 2) * kTile, c, b, &kv_full[s]);
+  };
+  const int early = min(2 * n, C::kSlots);  // loads into slots that nobody has used
+  if (warp == kTmaWarp && elect_one()) {
     mbar_init(&q_full, 1);
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&kv_full[s], 1);
@@ -87,6 +96,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     mbar_init(&o_full, 1);
     abort_word = 0;
     mbar_init_fence();
+    if (n > 0) {
+      mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * C::kTileBytes);
+      for (int t = 0; t < (two ? 2 : 1); ++t) {
+        const int u = 2 * p + t;
+        load_tile<DP>(base + t * C::kTileBytes, &map_q, u / a.group * kTile, c * a.group + u % a.group, b, &q_full);
+      }
+      for (int i = 0; i < early; ++i) load(i);
+    }
   }
   if (warp == kMmaWarp) tmem_alloc(&tmem_slot, 512);
   tc_fence_before();
@@ -98,32 +115,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (warp >= kTmaWarp) fewer_registers<kOtherRegs>();
   else more_registers<kSoftmaxRegs>();
   if (warp == kTmaWarp) {
-    // ---- TMA: the query tiles, then K_0, V_0, K_1, V_1, ...
-    if (n > 0) {
-      const uint32_t one = elect_one();
-      if (one) {
-        tma_prefetch(&map_k);
-        tma_prefetch(&map_v);
-        mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * C::kTileBytes);
-        for (int t = 0; t < (two ? 2 : 1); ++t) {
-          const int u = 2 * p + t;
-          load_tile<DP>(base + t * C::kTileBytes, &map_q, u / a.group * kTile, c * a.group + u % a.group, b, &q_full);
-        }
-      }
-      int i = 0;
-      for (; i < 2 * n; ++i) {
-        const int s = i % C::kSlots;
-        if (!wait(&kv_empty[s], (i / C::kSlots - 1) & 1)) break;
-        if (one) {
-          mbar_arrive_expect_tx(&kv_full[s], C::kTileBytes);
-          load_tile<DP>(ring + s * C::kTileBytes, i & 1 ? &map_v : &map_k, (first + i / 2) * kTile, c, b, &kv_full[s]);
-        }
-      }
-      if (i < 2 * n) {  // gave up: leave the copies in flight time to land
-        mbar_wait(&q_full, 0, kSpinLimit >> 10);
-        for (int k = max(0, i - C::kSlots); k < i; ++k)
-          mbar_wait(&kv_full[k % C::kSlots], (k / C::kSlots) & 1, kSpinLimit >> 10);
-      }
+    // ---- TMA: K and V tiles
+    const uint32_t one = elect_one();
+    int i = early;
+    for (; i < 2 * n; ++i) {
+      if (!wait(&kv_empty[i % C::kSlots], (i / C::kSlots - 1) & 1)) break;
+      if (one) load(i);
+    }
+    if (i < 2 * n) {  // gave up: leave the copies in flight time to land
+      mbar_wait(&q_full, 0, kSpinLimit >> 10);
+      for (int k = max(0, i - C::kSlots); k < i; ++k)
+        mbar_wait(&kv_full[k % C::kSlots], (k / C::kSlots) & 1, kSpinLimit >> 10);
     }
   } else if (warp == kMmaWarp) {
     // ---- the tensor cores
@@ -267,9 +269,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       total = tops[n & 1][t][0][row] + tops[n & 1][t][1][row];
       const bool none = total == 0.0f;  // no key seen (a seen key gives at least 2^-8 ... or NaN)
       const float inv = none ? 0.0f : 1.0f / total;
-      T* out = static_cast<T*>(a.o) + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2] + half * (DP / 2);
-      // `none` may differ between the lanes of a warp: their sums are zeros
-      store_row<T, DP / 2>(o_at, inv, out, a.head_dim - half * (DP / 2), n == 0, i < a.q_len && ok);
+      // `none` may differ between the lanes of a warp: their sums are zeros.
+      // The tile leaves from the place of its queries, which are done with.
+      stage_row<T, DP / 2>(smem + t * C::kTileBytes, row, half * (DP / 2), o_at, inv, n == 0);
+      fence_async_smem();
+      named_sync(1 + t, 256);
+      if ((warp & 7) == 0 && __all_sync(0xFFFFFFFFu, ok) && elect_one())
+        store_tile<DP>(&map_o, base + t * C::kTileBytes, a.head_dim, u / a.group * kTile, (int)h, b);
       if (half == 0 && i < a.q_len && ok)
         a.lse[(b * (int64_t)a.q_heads + h) * a.q_len + i] =
             none ? -INFINITY : (top * scale2 + log2f(total)) * kLn2;
@@ -286,10 +292,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 template <typename T, int DP>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
   using C = Fwd<DP>;
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
   // without keys nothing is loaded, but the maps still have to be valid
   const int64_t k_len = a.k_len > 0 ? a.k_len : 1;
   if (!attn_map(&q, a.q, a.dtype, a.qs, a.batch, a.q_len, a.q_heads, a.head_dim) ||
+      !attn_map(&o, a.o, a.dtype, a.os, a.batch, a.q_len, a.q_heads, a.head_dim) ||
       !attn_map(&k, a.k_len > 0 ? a.k : a.q, a.dtype, a.ks, a.batch, k_len, a.kv_heads, a.head_dim) ||
       !attn_map(&v, a.k_len > 0 ? a.v : a.q, a.dtype, a.vs, a.batch, k_len, a.kv_heads, a.head_dim))
     return cudaErrorInvalidValue;
@@ -299,7 +306,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> asked{0};
   cudaError_t e = allow_smem(k_attn_fwd<T, DP>, C::kSmem, asked);
   if (e != cudaSuccess) return e;
-  k_attn_fwd<T, DP><<<(unsigned)blocks, kFwdThreads, C::kSmem, s>>>(q, k, v, a, (int)q_tiles, (int)pairs);
+  k_attn_fwd<T, DP><<<(unsigned)blocks, kFwdThreads, C::kSmem, s>>>(q, k, v, o, a, (int)q_tiles, (int)pairs);
   return cudaGetLastError();
 }
 

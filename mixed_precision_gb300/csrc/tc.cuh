@@ -188,6 +188,17 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, 
       "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
+// A tile from shared memory to the tensor (what lies outside it is dropped), in
+// the thread's current group of stores.
+__device__ __forceinline__ void tma_store4(const CUtensorMap* map, uint32_t src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(map),
+               "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+// End the group, and wait until its shared memory has been read.
+__device__ __forceinline__ void tma_store_done() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
+}
 // Make this thread's shared-memory writes visible to TMA and the tensor cores.
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
