@@ -69,10 +69,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // S outside columns [from, to): -inf.
-template <int N>
-__device__ __forceinline__ void mask_row(float (&s)[N], int from, int to) {
+__device__ __forceinline__ void mask_row(uint32_t (&s)[32], int from, int to) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) s[k] = k >= from && k < to ? s[k] : -INFINITY;
+  for (int k = 0; k < 32; ++k) s[k] = k >= from && k < to ? s[k] : 0xFF800000u;
 }
 
 // Registers of a warpgroup's threads, given away and taken (all four warps).
@@ -123,6 +122,13 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint64_t b, uin
     mma_ts(d, a + k / 4 * 64 + k % 4 * 8, b + k * (2048 / 16), idesc, add || k > 0, one);
 }
 
+// The same with a's columns in one run.
+__device__ __forceinline__ void mma_rows_run(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add,
+                                             uint32_t one) {
+#pragma unroll
+  for (int k = 0; k < kTile / 16; ++k) mma_ts(d, a + k * 8, b + k * (2048 / 16), idesc, add || k > 0, one);
+}
+
 // A row of a tile to zero; the caller fences.
 template <int DP>
 __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
@@ -137,7 +143,7 @@ __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
 // a block); a tile leaves by one bulk store. The whole warp calls it.
 template <typename T, int N>
 __device__ __forceinline__ void stage_row(uint8_t* tile, int row, int col0, uint32_t addr, float f, bool zero) {
-#pragma unroll
+#pragma unroll 1
   for (int k = 0; k < N; k += 32) {
     uint32_t o[32];
     if (!zero) {

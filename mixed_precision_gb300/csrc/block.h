@@ -14,6 +14,24 @@ namespace zg {
 constexpr int kActGroup = 32;   // elements of a packed row that share one scale
 constexpr int kActPitch = 128;  // a packed row is padded to a multiple of this
 
+// Division of numbers below 2^31 by a fixed one: n / d = n * mul >> shift, with
+// mul = floor(2^shift / d) + 1 and shift = 31 + ceil(log2 d).
+struct Divide {
+  uint64_t mul;
+  uint32_t d, shift;
+  Divide() = default;
+  explicit Divide(uint32_t by) : d(by) {
+    uint32_t l = 0;
+    while ((1ull << l) < by) ++l;
+    shift = 31 + l;
+    mul = (1ull << shift) / by + 1;
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return static_cast<uint32_t>(n * mul >> shift); }
+  __device__ __forceinline__ uint32_t mod(uint32_t n) const { return n - (*this)(n) * d; }
+#endif
+};
+
 struct NormArgs {
   int64_t rows;
   int cols, pitch;  // pitch: of the packed output
@@ -75,6 +93,7 @@ struct AttnArgs {
   float* lse;
   const float* lse_in;
   float* stats;  // backward: the rows' statistics (k_attn_bwd.cu)
+  Divide by_group, by_kv_heads, by_q_heads, by_batch_kv, by_batch_q;  // batch x heads
 };
 cudaError_t launch_attention_forward(const AttnArgs& a, cudaStream_t s);
 int64_t attention_backward_bytes(const AttnArgs& a);

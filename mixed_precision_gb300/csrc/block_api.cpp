@@ -183,6 +183,14 @@ int attention_args(const zero_attention_desc* d, bool backward, AttnArgs& a) {
   a.group = d->q_heads / d->kv_heads;
   a.head_dim = d->head_dim;
   a.dtype = d->dtype;
+  if (d->batch * d->q_heads > 0x7FFFFFFF) return fail(ZERO_ERR_INVALID, "too many heads");
+  if (d->batch > 0) {
+    a.by_group = Divide(a.group);
+    a.by_kv_heads = Divide(a.kv_heads);
+    a.by_q_heads = Divide(a.q_heads);
+    a.by_batch_kv = Divide((uint32_t)(d->batch * d->kv_heads));
+    a.by_batch_q = Divide((uint32_t)(d->batch * d->q_heads));
+  }
   a.causal = d->causal != 0;
   // a window wider than any distance is none
   a.window = d->window < d->q_len + d->k_len ? d->window : 0;

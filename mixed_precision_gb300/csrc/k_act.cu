@@ -29,20 +29,6 @@ __device__ __forceinline__ void load_chunk(const T* row, int c, int cols, float 
   }
 }
 
-// Division of numbers below 2^31 by a fixed one: n / d = n * mul >> shift, with
-// mul = floor(2^shift / d) + 1 and shift = 31 + ceil(log2 d).
-struct Divide {
-  uint64_t mul;
-  uint32_t d, shift;
-  explicit Divide(uint32_t by) : d(by) {
-    uint32_t l = 0;
-    while ((1ull << l) < by) ++l;
-    shift = 31 + l;
-    mul = (1ull << shift) / by + 1;
-  }
-  __device__ uint32_t operator()(uint32_t n) const { return static_cast<uint32_t>(n * mul >> shift); }
-};
-
 constexpr int kPer = 4;  // chunks a thread, all loaded before the first is used
 
 template <typename T, bool VEC>

@@ -51,9 +51,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                  v_at = k_at + C::kK * C::kTileBytes;
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
-  const int heads = (int)a.batch * a.q_heads;
-  const int bh = blockIdx.x % heads, qt = q_tiles - 1 - blockIdx.x / heads;  // most keys first
-  const int h = bh % a.q_heads, b = bh / a.q_heads, c = h / a.group;
+  const int turn = a.by_batch_q(blockIdx.x), bh = blockIdx.x - turn * a.by_batch_q.d;
+  const int qt = q_tiles - 1 - turn;  // most keys first
+  const int b = a.by_q_heads(bh), h = bh - b * a.q_heads, c = a.by_group(h);
   const int keys = valid_keys(a, b), row0 = qt * kTile;
   int lo, hi, skip;
   key_range(a, keys, row0, lo, skip);
@@ -90,7 +90,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int j = 0; j < early; ++j) load_k(j), load_v(j);
     }
   }
-  if (warp == 9) tmem_alloc(&tmem_slot, 512);
+  if (warp == 9) {
+    if (lane == 0) tma_prefetch(&map_dq);
+    __syncwarp();
+    tmem_alloc(&tmem_slot, 512);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -289,9 +293,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   float* stats = reinterpret_cast<float*>(smem + (2 + 2 * kS) * C::kTileBytes);
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
-  const int heads = (int)a.batch * a.kv_heads;
-  const int bc = blockIdx.x % heads, kt = blockIdx.x / heads;  // most queries first
-  const int c = bc % a.kv_heads, b = bc / a.kv_heads;
+  const int kt = a.by_batch_kv(blockIdx.x), bc = blockIdx.x - kt * a.by_batch_kv.d;  // most queries first
+  const int b = a.by_kv_heads(bc), c = bc - b * a.kv_heads;
   const int keys = valid_keys(a, b), key0 = kt * kTile, off = (int)(a.k_len - a.q_len);
   // query tiles [first, last) that see one of the tile's valid keys
   int first = 0, last = q_tiles;
@@ -302,15 +305,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
   const int span = key0 < keys ? max(0, last - first) : 0, n = span * a.group;
 
+  // item i: query tile first + i % span of the group's head i / span
   auto load_q = [&](int i) {  // with the tile's statistics; by one thread
-    const int s = i % kS, h = c * a.group + i / span, qt = first + i % span;
+    const int s = i % kS, g = i / span, h = c * a.group + g, qt = first + i - g * span;
     mbar_arrive_expect_tx(&q_full[s], C::kTileBytes + kStats * 4);
     load_tile<DP>(q_at + s * C::kTileBytes, &map_q, qt * kTile, h, b, &q_full[s]);
     bulk_g2s(stats + s * kStats, a.stats + ((b * (int64_t)a.q_heads + h) * q_tiles + qt) * kStats, kStats * 4,
              &q_full[s]);
   };
   auto load_do = [&](int i) {
-    const int s = i % kS, h = c * a.group + i / span, qt = first + i % span;
+    const int s = i % kS, g = i / span, h = c * a.group + g, qt = first + i - g * span;
     mbar_arrive_expect_tx(&do_full[s], C::kTileBytes);
     load_tile<DP>(do_at + s * C::kTileBytes, &map_do, qt * kTile, h, b, &do_full[s]);
   };
@@ -341,7 +345,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     griddep_wait();
     for (int i = 0; i < early; ++i) load_q(i);
   }
-  if (warp == 9) tmem_alloc(&tmem_slot, 512);
+  if (warp == 9) {
+    if (lane == 0) {
+      tma_prefetch(&map_dk);
+      tma_prefetch(&map_dv);
+    }
+    __syncwarp();
+    tmem_alloc(&tmem_slot, 512);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -417,8 +428,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int hi = a.window > 0 ? min((int)a.q_len, key - off + (int)a.window) : (int)a.q_len;
     if (key >= keys) hi = lo = 0;
     bool ok = true;
-    for (int i = 0; i < n; ++i) {
-      const int s = i % kS, q0 = (first + i % span) * kTile + half * 64;
+    for (int i = 0, qt = 0; i < n; ++i, qt = qt + 1 == span ? 0 : qt + 1) {
+      const int s = i % kS, q0 = (first + qt) * kTile + half * 64;
       // the statistics came with the query tile
       if (!(ok = wait(&q_full[s], (i / kS) & 1) && wait(&s_full, i & 1))) break;
       tc_fence_after();

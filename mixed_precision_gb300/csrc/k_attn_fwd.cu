@@ -57,14 +57,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
   // blocks of the last query rows (most keys under a causal mask) come first
-  const int bh = blockIdx.x % (int)(a.batch * a.kv_heads), p = pairs - 1 - blockIdx.x / (int)(a.batch * a.kv_heads);
-  const int c = bh % a.kv_heads, b = bh / a.kv_heads;
+  const int turn = a.by_batch_kv(blockIdx.x), bh = blockIdx.x - turn * a.by_batch_kv.d, p = pairs - 1 - turn;
+  const int b = a.by_kv_heads(bh), c = bh - b * a.kv_heads;
   const int units = q_tiles * a.group;
   const bool two = 2 * p + 1 < units;
   const int keys = valid_keys(a, b);
   int first = 0x7FFFFFFF, last = 0;  // key tiles [first, last) that either tile sees
   for (int t = 0; t < (two ? 2 : 1); ++t) {
-    const int row0 = (2 * p + t) / a.group * kTile, row1 = min(row0 + kTile, (int)a.q_len) - 1;
+    const int row0 = a.by_group(2 * p + t) * kTile, row1 = min(row0 + kTile, (int)a.q_len) - 1;
     int lo, hi, skip;
     key_range(a, keys, row0, lo, skip);
     key_range(a, keys, row1, skip, hi);
@@ -100,12 +100,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * C::kTileBytes);
       for (int t = 0; t < (two ? 2 : 1); ++t) {
         const int u = 2 * p + t;
-        load_tile<DP>(base + t * C::kTileBytes, &map_q, u / a.group * kTile, c * a.group + u % a.group, b, &q_full);
+        load_tile<DP>(base + t * C::kTileBytes, &map_q, a.by_group(u) * kTile, c * a.group + a.by_group.mod(u), b,
+                      &q_full);
       }
       for (int i = 0; i < early; ++i) load(i);
     }
   }
-  if (warp == kMmaWarp) tmem_alloc(&tmem_slot, 512);
+  if (warp == kMmaWarp) {
+    if (lane == 0) tma_prefetch(&map_o);
+    __syncwarp();
+    tmem_alloc(&tmem_slot, 512);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -173,8 +178,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int t = warp / 8, half = warp / 4 & 1, u = 2 * p + t, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_at = tmem + lanes + t * kTile + half * 64, o_at = tmem + lanes + C::kO + t * DP + half * (DP / 2);
-    const int i = u / a.group * kTile + row;  // the query
-    const int64_t h = c * a.group + u % a.group;
+    const int row0 = a.by_group(u) * kTile, i = row0 + row;  // the query
+    const int64_t h = c * a.group + a.by_group.mod(u);
     const float scale2 = a.scale * kLog2e;
     float top = -INFINITY, total = 0.0f;
     bool ok = true;
@@ -189,66 +194,64 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int key0 = (first + j) * kTile, from = lo - key0 - half * 64, to = hi - key0 - half * 64;
         // columns [from, to) are seen; most tiles need no mask
         const bool mask = __any_sync(0xFFFFFFFFu, from > 0 || to < 64);
-        // S is read twice, for the maximum and for P: 64 values kept between the
-        // two do not fit the registers of sixteen warps
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint32_t w[2][16];
+        float sums;
 #pragma unroll 1
-        for (int q = 0; q < 64; q += 32) {
-          float s[32];
-          tmem_ld32(s_at + q, reinterpret_cast<uint32_t(&)[32]>(s));
-          tmem_wait_ld();
-          if (mask) mask_row<32>(s, from - q, to - q);
+        for (int turn = 0;; turn ^= 1) {
+          const float minus = top == -INFINITY ? 0.0f : -top * scale2;
+          const uint64_t scale_pair = pair(scale2, scale2), minus_pair = pair(minus, minus);
+          uint64_t sum[2] = {0, 0};
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
+          for (int q = 0; q < 2; ++q) {
+            uint32_t r[32];
+            tmem_ld32(s_at + q * 32, r);
+            tmem_wait_ld();
+            if (mask) mask_row(r, from - q * 32, to - q * 32);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], s[k + e], s[k + 4 + e]);
-        }
-        float m = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
-        tops[j & 1][t][half][row] = m;
-        named_sync(1 + t, 256);
-        m = fmaxf(m, tops[j & 1][t][half ^ 1][row]);
-        // the first maximum, or one that has grown too far: rescale
-        const bool raise = m > top && (top == -INFINITY || (m - top) * scale2 > kStale);
-        if (__any_sync(0xFFFFFFFFu, raise)) {
+            for (int k = 0; k < 32; k += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                m4[e] = max3(m4[e], __uint_as_float(r[k + e]), __uint_as_float(r[k + 4 + e]));
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float x, y;
+              unpair(fma2(pair(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), scale_pair, minus_pair), x, y);
+              x = exp2_fast(x);
+              y = exp2_fast(y);
+              sum[k & 1] = add2(sum[k & 1], pair(x, y));
+              w[q][k] = round2<T>(x, y);
+            }
+          }
+          float x, y;
+          unpair(add2(sum[0], sum[1]), x, y);
+          sums = x + y;
+          float m = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
+          // the other half's maximum, from the warp with the same rows
+          tops[turn][t][half][row] = m;
+          named_sync(3 + warp / 8 * 4 + (warp & 3), 64);
+          m = fmaxf(m, tops[turn][t][half ^ 1][row]);
+          // the first maximum, or one that has grown too far: rescale, and again
+          const bool raise = m > top && (top == -INFINITY || (m - top) * scale2 > kStale);
+          if (!__any_sync(0xFFFFFFFFu, raise)) break;
           const float f = raise ? exp2_fast((top - m) * scale2) : 1.0f;
           if (raise) top = m;
           total *= f;
-          if (j > 0) {  // O is complete up to the tile before: its product was issued before this S
+          if (j == 0) continue;
+          // O is complete up to the tile before: its product was issued before this S
 #pragma unroll 1
-            for (int k = 0; k < DP / 2; k += 16) {
-              uint32_t o[16];
-              tmem_ld16(o_at + k, o);
-              tmem_wait_ld();
+          for (int k = 0; k < DP / 2; k += 16) {
+            uint32_t o[16];
+            tmem_ld16(o_at + k, o);
+            tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(o_at + k, o);
-            }
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(o_at + k, o);
           }
         }
-        const float minus = top == -INFINITY ? 0.0f : -top * scale2;
-        const uint64_t scale_pair = pair(scale2, scale2), minus_pair = pair(minus, minus);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          float s[32];
-          tmem_ld32(s_at + q * 32, reinterpret_cast<uint32_t(&)[32]>(s));
-          tmem_wait_ld();
-          if (mask) mask_row<32>(s, from - q * 32, to - q * 32);
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float x, y;
-            unpair(fma2(pair(s[2 * k], s[2 * k + 1]), scale_pair, minus_pair), x, y);
-            x = exp2_fast(x);
-            y = exp2_fast(y);
-            sum[k & 1] = add2(sum[k & 1], pair(x, y));
-            w[k] = round2<T>(x, y);
-          }
-          tmem_st16(s_at + q * 16, w);
-        }
-        float x, y;
-        unpair(add2(sum[0], sum[1]), x, y);
-        total += x + y;
+        total += sums;
+        tmem_st16(s_at, w[0]);
+        tmem_st16(s_at + 16, w[1]);
         if (t == 0 && half == 0 && key0 + kTile > keys && keys < a.k_len) {
           // rows of V past the length: zeros. Tile 0's product is the first to
           // read them, and waits for this thread.
@@ -264,9 +267,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (n > 0) ok = wait(&o_full, 0) && ok;
       tc_fence_after();
       // both halves' sums, in the order of the keys
-      tops[n & 1][t][half][row] = total;
       named_sync(1 + t, 256);
-      total = tops[n & 1][t][0][row] + tops[n & 1][t][1][row];
+      tops[0][t][half][row] = total;
+      named_sync(1 + t, 256);
+      total = tops[0][t][0][row] + tops[0][t][1][row];
       const bool none = total == 0.0f;  // no key seen (a seen key gives at least 2^-8 ... or NaN)
       const float inv = none ? 0.0f : 1.0f / total;
       // `none` may differ between the lanes of a warp: their sums are zeros.
@@ -275,7 +279,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       fence_async_smem();
       named_sync(1 + t, 256);
       if ((warp & 7) == 0 && __all_sync(0xFFFFFFFFu, ok) && elect_one())
-        store_tile<DP>(&map_o, base + t * C::kTileBytes, a.head_dim, u / a.group * kTile, (int)h, b);
+        store_tile<DP>(&map_o, base + t * C::kTileBytes, a.head_dim, row0, (int)h, b);
       if (half == 0 && i < a.q_len && ok)
         a.lse[(b * (int64_t)a.q_heads + h) * a.q_len + i] =
             none ? -INFINITY : (top * scale2 + log2f(total)) * kLn2;
