@@ -113,20 +113,14 @@ __device__ __forceinline__ void mma_head(uint32_t d, uint64_t a, uint64_t b, uin
   }
 }
 
-// d [+]= a b over 128 rows: a in TMEM, 16-bit, its columns in two runs of 32,
-// the second 64 columns on: two warps wrote a row, each over its own half of
-// the fp32 columns.
+// d [+]= a b over 128 rows: a in TMEM, 16-bit, written by PARTS warps a row, each
+// over the front of its own 128 / PARTS fp32 columns.
+template <int PARTS>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t one) {
+  constexpr int kRun = kTile / 16 / PARTS;  // steps in one warp's part
 #pragma unroll
   for (int k = 0; k < kTile / 16; ++k)
-    mma_ts(d, a + k / 4 * 64 + k % 4 * 8, b + k * (2048 / 16), idesc, add || k > 0, one);
-}
-
-// The same with a's columns in one run.
-__device__ __forceinline__ void mma_rows_run(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add,
-                                             uint32_t one) {
-#pragma unroll
-  for (int k = 0; k < kTile / 16; ++k) mma_ts(d, a + k * 8, b + k * (2048 / 16), idesc, add || k > 0, one);
+    mma_ts(d, a + k / kRun * (kTile / PARTS) + k % kRun * 8, b + k * (2048 / 16), idesc, add || k > 0, one);
 }
 
 // A row of a tile to zero; the caller fences.
@@ -144,14 +138,14 @@ __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
 template <typename T, int N>
 __device__ __forceinline__ void stage_row(uint8_t* tile, int row, int col0, uint32_t addr, float f, bool zero) {
 #pragma unroll 1
-  for (int k = 0; k < N; k += 32) {
-    uint32_t o[32];
+  for (int k = 0; k < N; k += 16) {
+    uint32_t o[16];
     if (!zero) {
-      tmem_ld32(addr + k, o);
+      tmem_ld16(addr + k, o);
       tmem_wait_ld();
     }
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < 2; ++g) {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)

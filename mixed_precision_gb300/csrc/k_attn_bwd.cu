@@ -19,7 +19,11 @@ namespace {
 
 __device__ unsigned g_attn_bwd_error;
 
-constexpr int kBwdThreads = 10 * 32;  // eight softmax warps, the TMA warp, the MMA warp
+// Sixteen softmax warps (four a row of a tile, 32 columns each), the TMA warp,
+// the MMA warp. With eight the softmax's chain was longer than the products it
+// overlaps.
+constexpr int kParts = 4, kCols = kTile / kParts, kSoftWarps = 4 * kParts, kSoftThreads = kSoftWarps * 32;
+constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kBwdThreads = (kSoftWarps + 2) * 32;
 constexpr int kStats = 2 * kTile;     // floats of a query tile's statistics
 
 // ---------------------------------------------------------------------------
@@ -73,13 +77,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     load_tile<DP>(v_at + s * C::kTileBytes, &map_v, (first + j) * kTile, c, b, &v_full[s]);
   };
   const int early = min(n, C::kV);  // tiles into slots that nobody has used
-  if (warp == 8 && elect_one()) {
+  if (warp == kTmaWarp && elect_one()) {
     mbar_init(&q_full, 1);
     for (int s = 0; s < C::kK; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_empty[s], 1);
     for (int s = 0; s < C::kV; ++s) mbar_init(&v_full[s], 1), mbar_init(&v_empty[s], 1);
-    for (int s = 0; s < 2; ++s) mbar_init(&s_full[s], 1), mbar_init(&ds_full[s], 8);
+    for (int s = 0; s < 2; ++s) mbar_init(&s_full[s], 1), mbar_init(&ds_full[s], kSoftWarps);
     mbar_init(&dp_full, 1);
-    mbar_init(&dp_empty, 8);
+    mbar_init(&dp_empty, kSoftWarps);
     mbar_init(&done, 1);
     abort_word = 0;
     mbar_init_fence();
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int j = 0; j < early; ++j) load_k(j), load_v(j);
     }
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     if (lane == 0) tma_prefetch(&map_dq);
     __syncwarp();
     tmem_alloc(&tmem_slot, 512);
@@ -102,7 +106,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const Waiter wait{&abort_word, &g_attn_bwd_error};
 
   griddep_trigger();
-  if (warp == 8) {
+  if (warp == kTmaWarp) {
     const uint32_t one = elect_one();
     int j = early;
     for (; j < n; ++j) {
@@ -118,7 +122,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         mbar_wait(&v_full[i % C::kV], (i / C::kV) & 1, kSpinLimit >> 10);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp) {
     if (n > 0) {
       constexpr bool bf16 = !std::is_same<T, __half>::value;
       constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
@@ -153,36 +157,36 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (!(go = wait(&ds_full[j & 1], (j / 2) & 1))) break;
         tc_fence_after();
-        mma_rows(tmem + C::kDq, tmem + (j & 1) * kTile, k_rows + j % C::kK * kStep, by_rows, j > 0, one);
+        mma_rows<kParts>(tmem + C::kDq, tmem + (j & 1) * kTile, k_rows + j % C::kK * kStep, by_rows, j > 0, one);
         mma_commit(&k_empty[j % C::kK], one);
         if (j + 2 < n) go = make_s(j + 2);
       }
       mma_commit(&done, one);
     }
   } else {
-    // ---- a thread half a row: columns [64 half, 64 half + 64) of each tile
-    const int half = warp / 4, row = (warp & 3) * 32 + lane, i = row0 + row;
+    // ---- a thread a quarter of a row: columns [32 part, 32 part + 32) of each tile
+    const int quarter = warp / 4, row = (warp & 3) * 32 + lane, i = row0 + row;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const bool live = i < a.q_len;
     const int64_t at = (b * (int64_t)a.q_heads + h) * a.q_len + i;
     float delta = 0.0f;
-    if (live) {
+    if (live && quarter < 2) {  // half the head each
       const T* o = static_cast<const T*>(a.o_in) + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2];
       const T* g = static_cast<const T*>(a.dout) + b * a.dos[0] + (int64_t)i * a.dos[1] + h * a.dos[2];
-      for (int d = half * (DP / 2); d < min(a.head_dim, (half + 1) * (DP / 2)); d += 8) {
-        const uint4 x = *reinterpret_cast<const uint4*>(o + d), y = *reinterpret_cast<const uint4*>(g + d);
-        const T *xe = reinterpret_cast<const T*>(&x), *ye = reinterpret_cast<const T*>(&y);
+      for (int d = quarter * (DP / 2); d < min(a.head_dim, (quarter + 1) * (DP / 2)); d += 8) {
+        float x[8], y[8];
+        widen8(load8_raw(o + d), x);
+        widen8(load8_raw(g + d), y);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) delta = fmaf(DT<T>::to_f32(xe[e]), DT<T>::to_f32(ye[e]), delta);
+        for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
       }
     }
-    part[half][row] = delta;
-    named_sync(1, 256);
-    const float minus_delta = -(part[0][row] + part[1][row]);
     // a row that sees nothing (or is none) gets p = 2^-inf = 0 everywhere
     const float lse = live ? a.lse_in[at] : -INFINITY;
-    const float minus_lse = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-    if (half == 0) {
+    if (quarter < 2) part[quarter][row] = delta;
+    named_sync(1, kSoftThreads);
+    const float minus_delta = -(part[0][row] + part[1][row]), minus_lse = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+    if (quarter == 0) {
       float* st = a.stats + ((b * (int64_t)a.q_heads + h) * q_tiles + qt) * kStats + row;
       st[0] = minus_lse;
       st[kTile] = minus_delta;
@@ -192,51 +196,49 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint64_t scale_pair = pair(scale2, scale2), lse_pair = pair(minus_lse, minus_lse),
                    delta_pair = pair(minus_delta, minus_delta);
     bool ok = true;
+#pragma unroll 1
     for (int j = 0; j < n; ++j) {
-      const uint32_t s_at = tmem + lanes + (j & 1) * kTile + half * 64;
+      const uint32_t s_at = tmem + lanes + (j & 1) * kTile + quarter * kCols;
       if (!(ok = wait(&s_full[j & 1], (j / 2) & 1))) break;
       tc_fence_after();
-      float p[64];
-      uint32_t(&r)[2][32] = reinterpret_cast<uint32_t(&)[2][32]>(p);
-      tmem_ld32(s_at, r[0]);
-      tmem_ld32(s_at + 32, r[1]);
+      uint32_t p[kCols];
+      tmem_ld32(s_at, p);
       tmem_wait_ld();
-      const int key0 = (first + j) * kTile + half * 64;
 #pragma unroll
-      for (int k = 0; k < 64; k += 2) {
-        unpair(fma2(pair(p[k], p[k + 1]), scale_pair, lse_pair), p[k], p[k + 1]);
-        p[k] = exp2_fast(p[k]);
-        p[k + 1] = exp2_fast(p[k + 1]);
+      for (int k = 0; k < kCols; k += 2) {
+        float x, y;
+        unpair(fma2(pair(__uint_as_float(p[k]), __uint_as_float(p[k + 1])), scale_pair, lse_pair), x, y);
+        p[k] = __float_as_uint(exp2_fast(x));
+        p[k + 1] = __float_as_uint(exp2_fast(y));
       }
-      const bool mask = __any_sync(0xFFFFFFFFu, lo > key0 || hi < key0 + 64);
-      const int from = lo - key0, to = hi - key0;
       if (!(ok = wait(&dp_full, j & 1))) break;
       tc_fence_after();
+      uint32_t dp[kCols];
+      tmem_ld32(tmem + lanes + C::kDp + quarter * kCols, dp);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dp_empty);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float dp[32];
-        tmem_ld32(tmem + lanes + C::kDp + half * 64 + q * 32, reinterpret_cast<uint32_t(&)[32]>(dp));
-        tmem_wait_ld();
-        if (q == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&dp_empty);
-        }
-        uint32_t w[16];
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float x, y;
-          unpair(mul2(pair(p[q * 32 + k], p[q * 32 + k + 1]), add2(pair(dp[k], dp[k + 1]), delta_pair)), x, y);
-          if (mask) {
-            x = q * 32 + k >= from && q * 32 + k < to ? x : 0.0f;
-            y = q * 32 + k + 1 >= from && q * 32 + k + 1 < to ? y : 0.0f;
-          }
-          w[k / 2] = round2<T>(x, y);
-        }
-        tmem_st16(s_at + q * 16, w);
+      for (int k = 0; k < kCols; k += 2) {
+        float x, y;
+        unpair(mul2(pair(__uint_as_float(p[k]), __uint_as_float(p[k + 1])),
+                    add2(pair(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), delta_pair)),
+               x, y);
+        p[k] = __float_as_uint(x);
+        p[k + 1] = __float_as_uint(y);
       }
+      const int key0 = (first + j) * kTile + quarter * kCols, from = lo - key0, to = hi - key0;
+      if (__any_sync(0xFFFFFFFFu, from > 0 || to < kCols)) {  // whatever p and dp are there
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) p[k] = k >= from && k < to ? p[k] : 0u;
+      }
+      uint32_t w[kCols / 2];
+#pragma unroll
+      for (int k = 0; k < kCols; k += 2) w[k / 2] = round2<T>(__uint_as_float(p[k]), __uint_as_float(p[k + 1]));
+      tmem_st16(s_at, w);
       // keys past the length: their ds is zero, and so must be what it meets
-      if (half == 0 && keys < a.k_len && (first + j + 1) * kTile > keys) {
+      if (quarter == 0 && keys < a.k_len && (first + j + 1) * kTile > keys) {
         if ((first + j) * kTile + row >= keys)
           zero_row<DP>(smem + (2 + j % C::kK) * C::kTileBytes, row);
         fence_async_smem();
@@ -249,14 +251,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (n > 0 && ok) ok = wait(&done, 0);
     tc_fence_after();
     // the tile leaves from the place of its queries, which are done with
-    stage_row<T, DP / 2>(smem, row, half * (DP / 2), tmem + lanes + C::kDq + half * (DP / 2), a.scale, n == 0);
+    constexpr int kOut = DP / kParts;
+    stage_row<T, kOut>(smem, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale, n == 0);
     fence_async_smem();
-    named_sync(1, 256);
+    named_sync(1, kSoftThreads);
     if (warp == 0 && __all_sync(0xFFFFFFFFu, ok) && elect_one()) store_tile<DP>(&map_dq, q_at, a.head_dim, row0, h, b);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_free(tmem, 512);
   }
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     load_tile<DP>(do_at + s * C::kTileBytes, &map_do, qt * kTile, h, b, &do_full[s]);
   };
   const int early = min(n, kS);
-  if (warp == 8 && elect_one()) {
+  if (warp == kTmaWarp && elect_one()) {
     mbar_init(&kv_full, 1);
     for (int s = 0; s < kS; ++s) {
       mbar_init(&q_full[s], 1);
@@ -329,8 +332,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     mbar_init(&s_full, 1);
     mbar_init(&dp_full, 1);
-    mbar_init(&p_full, 8);
-    mbar_init(&ds_full, 8);
+    mbar_init(&p_full, kSoftWarps);
+    mbar_init(&ds_full, kSoftWarps);
     mbar_init(&done, 1);
     abort_word = 0;
     mbar_init_fence();
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     griddep_wait();
     for (int i = 0; i < early; ++i) load_q(i);
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     if (lane == 0) {
       tma_prefetch(&map_dk);
       tma_prefetch(&map_dv);
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tmem = tmem_slot;
   const Waiter wait{&abort_word, &g_attn_bwd_error};
 
-  if (warp == 8) {
+  if (warp == kTmaWarp) {
     const uint32_t one = elect_one();
     int i = early;
     for (; i < n; ++i) {
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         mbar_wait(&do_full[k % kS], (k / kS) & 1, kSpinLimit >> 10);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == kMmaWarp) {
     if (n > 0) {
       constexpr bool bf16 = !std::is_same<T, __half>::value;
       constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
@@ -406,21 +409,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int s = i % kS;
         if (!(go = wait(&p_full, i & 1))) break;
         tc_fence_after();
-        mma_rows(tmem + C::kDv, tmem, do_rows + s * kStep, by_rows, i > 0, one);
+        mma_rows<kParts>(tmem + C::kDv, tmem, do_rows + s * kStep, by_rows, i > 0, one);
         mma_commit(&do_empty[s], one);
         if (i + 1 < n && !(go = make_s(i + 1))) break;
         if (!(go = wait(&ds_full, i & 1))) break;
         tc_fence_after();
-        mma_rows(tmem + C::kDk, tmem + C::kDp, q_rows + s * kStep, by_rows, i > 0, one);
+        mma_rows<kParts>(tmem + C::kDk, tmem + C::kDp, q_rows + s * kStep, by_rows, i > 0, one);
         mma_commit(&q_empty[s], one);
         if (i + 1 < n && !(go = make_dp(i + 1))) break;
       }
       mma_commit(&done, one);
     }
   } else {
-    // ---- a thread half a key's row: columns (queries) [64 half, 64 half + 64)
-    const int half = warp / 4, key = key0 + (warp & 3) * 32 + lane;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21, s_at = tmem + lanes + half * 64, dp_at = s_at + C::kDp;
+    // ---- a thread a quarter of a key's row: columns (queries) [32 quarter, ...)
+    const int quarter = warp / 4, row = (warp & 3) * 32 + lane, key = key0 + row;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21, s_at = tmem + lanes + quarter * kCols, dp_at = s_at + C::kDp;
     const float scale2 = a.scale * kLog2e;
     const uint64_t scale_pair = pair(scale2, scale2);
     // queries [lo, hi) that see the key
@@ -428,61 +431,58 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int hi = a.window > 0 ? min((int)a.q_len, key - off + (int)a.window) : (int)a.q_len;
     if (key >= keys) hi = lo = 0;
     bool ok = true;
+#pragma unroll 1
     for (int i = 0, qt = 0; i < n; ++i, qt = qt + 1 == span ? 0 : qt + 1) {
-      const int s = i % kS, q0 = (first + qt) * kTile + half * 64;
+      const int s = i % kS, q0 = (first + qt) * kTile + quarter * kCols;
       // the statistics came with the query tile
       if (!(ok = wait(&q_full[s], (i / kS) & 1) && wait(&s_full, i & 1))) break;
       tc_fence_after();
-      const uint64_t* lse = reinterpret_cast<const uint64_t*>(stats + s * kStats + half * 64);
+      const uint64_t* lse = reinterpret_cast<const uint64_t*>(stats + s * kStats + quarter * kCols);
       const uint64_t* delta = lse + kTile / 2;
-      float p[64];
-      uint32_t(&r)[2][32] = reinterpret_cast<uint32_t(&)[2][32]>(p);
-      tmem_ld32(s_at, r[0]);
-      tmem_ld32(s_at + 32, r[1]);
+      uint32_t p[kCols], w[kCols / 2];
+      tmem_ld32(s_at, p);
       tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < 64; k += 2) {
-        unpair(fma2(pair(p[k], p[k + 1]), scale_pair, lse[k / 2]), p[k], p[k + 1]);
-        p[k] = exp2_fast(p[k]);
-        p[k + 1] = exp2_fast(p[k + 1]);
+      for (int k = 0; k < kCols; k += 2) {
+        float x, y;
+        unpair(fma2(pair(__uint_as_float(p[k]), __uint_as_float(p[k + 1])), scale_pair, lse[k / 2]), x, y);
+        p[k] = __float_as_uint(exp2_fast(x));
+        p[k + 1] = __float_as_uint(exp2_fast(y));
       }
       const int from = lo - q0, to = hi - q0;
-      const bool mask = __any_sync(0xFFFFFFFFu, from > 0 || to < 64);
-      if (mask)
+      const bool mask = __any_sync(0xFFFFFFFFu, from > 0 || to < kCols);
+      if (mask) {
 #pragma unroll
-        for (int k = 0; k < 64; ++k) p[k] = k >= from && k < to ? p[k] : 0.0f;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t w[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) w[k] = round2<T>(p[q * 32 + 2 * k], p[q * 32 + 2 * k + 1]);
-        tmem_st16(s_at + q * 16, w);
+        for (int k = 0; k < kCols; ++k) p[k] = k >= from && k < to ? p[k] : 0u;
       }
+#pragma unroll
+      for (int k = 0; k < kCols; k += 2) w[k / 2] = round2<T>(__uint_as_float(p[k]), __uint_as_float(p[k + 1]));
+      tmem_st16(s_at, w);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full);
       if (!(ok = wait(&dp_full, i & 1))) break;
       tc_fence_after();
+      uint32_t dp[kCols];
+      tmem_ld32(dp_at, dp);
+      tmem_wait_ld();
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float dp[32];
-        tmem_ld32(dp_at + q * 32, reinterpret_cast<uint32_t(&)[32]>(dp));
-        tmem_wait_ld();
-        uint32_t w[16];
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float x, y;
-          unpair(mul2(pair(p[q * 32 + k], p[q * 32 + k + 1]), add2(pair(dp[k], dp[k + 1]), delta[q * 16 + k / 2])), x,
-                 y);
-          if (mask) {  // 0 times whatever dp is there
-            x = q * 32 + k >= from && q * 32 + k < to ? x : 0.0f;
-            y = q * 32 + k + 1 >= from && q * 32 + k + 1 < to ? y : 0.0f;
-          }
-          w[k / 2] = round2<T>(x, y);
-        }
-        tmem_st16(dp_at + q * 16, w);
+      for (int k = 0; k < kCols; k += 2) {
+        float x, y;
+        unpair(mul2(pair(__uint_as_float(p[k]), __uint_as_float(p[k + 1])),
+                    add2(pair(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), delta[k / 2])),
+               x, y);
+        p[k] = __float_as_uint(x);
+        p[k + 1] = __float_as_uint(y);
       }
+      if (mask) {  // 0 times whatever dp is there
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) p[k] = k >= from && k < to ? p[k] : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < kCols; k += 2) w[k / 2] = round2<T>(__uint_as_float(p[k]), __uint_as_float(p[k + 1]));
+      tmem_st16(dp_at, w);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -490,19 +490,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     if (n > 0 && ok) ok = wait(&done, 0);
     tc_fence_after();
-    // the first four warps store dk, the others dv, from the query and do tiles'
-    // places, which are done with
-    const int slot = 2 + half * kS;
-    stage_row<T, DP>(smem + slot * C::kTileBytes, (warp & 3) * 32 + lane, 0,
-                     tmem + lanes + (half == 0 ? C::kDk : C::kDv), half == 0 ? a.scale : 1.0f, n == 0);
+    // the first eight warps store dk, the others dv, half a row a thread, from the
+    // query and do tiles' places, which are done with
+    const int second = quarter / 2, slot = 2 + second * kS, col0 = (quarter & 1) * (DP / 2);
+    stage_row<T, DP / 2>(smem + slot * C::kTileBytes, row, col0, tmem + lanes + (second ? C::kDv : C::kDk) + col0,
+                         second ? 1.0f : a.scale, n == 0);
     fence_async_smem();
-    named_sync(1 + half, 128);
-    if ((warp & 3) == 0 && __all_sync(0xFFFFFFFFu, ok) && elect_one())
-      store_tile<DP>(half == 0 ? &map_dk : &map_dv, k_at + slot * C::kTileBytes, a.head_dim, key0, c, b);
+    named_sync(1 + second, kSoftThreads / 2);
+    if ((warp & 7) == 0 && __all_sync(0xFFFFFFFFu, ok) && elect_one())
+      store_tile<DP>(second ? &map_dv : &map_dk, k_at + slot * C::kTileBytes, a.head_dim, key0, c, b);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_free(tmem, 512);
   }

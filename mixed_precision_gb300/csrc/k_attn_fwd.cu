@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         for (int t = 0; go && t < tiles; ++t) {
           if (!(go = wait(&p_full[t], j & 1))) break;
           tc_fence_after();
-          mma_rows(tmem + C::kO + t * DP, tmem + t * kTile, v_desc + slot(v), by_rows, j > 0, one);
+          mma_rows<2>(tmem + C::kO + t * DP, tmem + t * kTile, v_desc + slot(v), by_rows, j > 0, one);
           if (t == tiles - 1) mma_commit(&kv_empty[v % C::kSlots], one);
           if (!more) continue;
           if (t == 0 && !(go = arrived(kn))) break;
