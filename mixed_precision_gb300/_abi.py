@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libzero_gb300.so")
@@ -81,15 +82,12 @@ class zero_attention_desc(ctypes.Structure):
             "dk_strides", "dv_strides")]
 
 
-class attention_desc_flat(ctypes.Structure):
-    """zero_attention_desc with its stride arrays spelled out: the same memory,
-    several times quicker to fill from Python."""
-    _fields_ = [f for f in zero_attention_desc._fields_ if f[1] is not ctypes.c_int64 * 3] + \
-        [(f"{n}_{i}", ctypes.c_int64) for n, t in zero_attention_desc._fields_
-         if t is ctypes.c_int64 * 3 for i in range(3)]
-
-
-assert ctypes.sizeof(attention_desc_flat) == ctypes.sizeof(zero_attention_desc)
+# The same descriptors as packed bytes (several times quicker to fill from
+# Python than a Structure): the calls below take either.
+RMSNORM_DESC = struct.Struct("=5q2id")
+ATTENTION_DESC = struct.Struct("=3q6iqd24q")
+assert RMSNORM_DESC.size == ctypes.sizeof(zero_rmsnorm_desc)
+assert ATTENTION_DESC.size == ctypes.sizeof(zero_attention_desc)
 
 ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p)
 FREE_FN = ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_void_p)
@@ -149,11 +147,9 @@ def lib() -> ctypes.CDLL:
             "zero_dist_update": [P, P, P],
             "zero_dist_update_buckets": [P, P, I, I, P],
             "zero_dist_widen": [P, P, P, P],
-            "zero_rmsnorm_forward": [ctypes.POINTER(zero_rmsnorm_desc)] + [P] * 9,
-            "zero_rmsnorm_backward_workspace": [ctypes.POINTER(zero_rmsnorm_desc),
-                                                ctypes.POINTER(I64)],
-            "zero_rmsnorm_backward": [ctypes.POINTER(zero_rmsnorm_desc)] + [P] * 7 +
-                                     [I, P, I64, P],
+            "zero_rmsnorm_forward": [P] * 10,
+            "zero_rmsnorm_backward_workspace": [P, ctypes.POINTER(I64)],
+            "zero_rmsnorm_backward": [P] * 8 + [I, P, I64, P],
             "zero_act_layout": [I64, I64] + [ctypes.POINTER(I64)] * 3,
             "zero_act_pack": [P, I64, I64, I64, I, P, P, P],
             "zero_act_unpack": [P, P, I64, I64, P, I64, I, P],
@@ -385,22 +381,26 @@ def zero_dist_widen(layout: int, grads: int, out: int, stream: int) -> None:
     _check(lib().zero_dist_widen(layout, grads, out, stream or None))
 
 
-def zero_rmsnorm_forward(desc: zero_rmsnorm_desc, x: int, residual: int, weight: int, sum_out: int,
+def _desc(desc):
+    return desc if type(desc) is bytes or desc is None else ctypes.byref(desc)
+
+
+def zero_rmsnorm_forward(desc, x: int, residual: int, weight: int, sum_out: int,
                          y: int, q: int, scales: int, rstd: int, stream: int) -> None:
-    _check(lib().zero_rmsnorm_forward(desc, x, residual, weight, sum_out, y, q, scales, rstd,
+    _check(lib().zero_rmsnorm_forward(_desc(desc), x, residual, weight, sum_out, y, q, scales, rstd,
                                       stream))
 
 
-def zero_rmsnorm_backward_workspace(desc: zero_rmsnorm_desc) -> int:
+def zero_rmsnorm_backward_workspace(desc) -> int:
     n = ctypes.c_int64()
-    _check(lib().zero_rmsnorm_backward_workspace(desc, n))
+    _check(lib().zero_rmsnorm_backward_workspace(_desc(desc), n))
     return n.value
 
 
-def zero_rmsnorm_backward(desc: zero_rmsnorm_desc, dy: int, x: int, weight: int, rstd: int, dsum: int,
+def zero_rmsnorm_backward(desc, dy: int, x: int, weight: int, rstd: int, dsum: int,
                           dx: int, dweight: int, dweight_dtype: int, workspace: int,
                           workspace_bytes: int, stream: int) -> None:
-    _check(lib().zero_rmsnorm_backward(desc, dy, x, weight, rstd, dsum, dx, dweight, dweight_dtype,
+    _check(lib().zero_rmsnorm_backward(_desc(desc), dy, x, weight, rstd, dsum, dx, dweight, dweight_dtype,
                                        workspace, workspace_bytes, stream))
 
 
@@ -434,21 +434,21 @@ def zero_act_weight_grad(dy: int, dy_stride: int, dtype: int, q: int, scales: in
                                       dw_dtype, accumulate, workspace, workspace_bytes, stream))
 
 
-def zero_attention_forward(desc: zero_attention_desc, q: int, k: int, v: int, key_lengths: int, o: int,
+def zero_attention_forward(desc, q: int, k: int, v: int, key_lengths: int, o: int,
                            lse: int, stream: int) -> None:
-    _check(lib().zero_attention_forward(ctypes.byref(desc), q, k, v, key_lengths, o, lse, stream))
+    _check(lib().zero_attention_forward(_desc(desc), q, k, v, key_lengths, o, lse, stream))
 
 
-def zero_attention_backward_workspace(desc: zero_attention_desc) -> int:
+def zero_attention_backward_workspace(desc) -> int:
     n = ctypes.c_int64()
-    _check(lib().zero_attention_backward_workspace(ctypes.byref(desc), n))
+    _check(lib().zero_attention_backward_workspace(_desc(desc), n))
     return n.value
 
 
-def zero_attention_backward(desc: zero_attention_desc, dout: int, q: int, k: int, v: int, o: int,
+def zero_attention_backward(desc, dout: int, q: int, k: int, v: int, o: int,
                             lse: int, key_lengths: int, dq: int, dk: int, dv: int, workspace: int,
                             workspace_bytes: int, stream: int) -> None:
-    _check(lib().zero_attention_backward(ctypes.byref(desc), dout, q, k, v, o, lse, key_lengths, dq, dk, dv,
+    _check(lib().zero_attention_backward(_desc(desc), dout, q, k, v, o, lse, key_lengths, dq, dk, dv,
                                          workspace, workspace_bytes, stream))
 
 

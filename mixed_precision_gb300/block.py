@@ -10,8 +10,13 @@ streams' work stays the caller's job, as with any torch operation.
 
 Wrong shapes, types, devices or layouts raise ValueError here, or ZeroError
 (ZERO_ERR_INVALID) from the library; nothing is enqueued then.
+
+The checks are written out in each function: at a few microseconds a kernel,
+helper calls would be a good part of a short call's time.
 """
 from __future__ import annotations
+
+import functools
 
 import torch
 
@@ -19,20 +24,20 @@ from . import _abi as abi
 
 DTYPE_CODE = {torch.float32: abi.ZERO_F32, torch.float16: abi.ZERO_F16,
               torch.bfloat16: abi.ZERO_BF16}
-HALF = (torch.float16, torch.bfloat16)
+HALF_CODE = {torch.float16: abi.ZERO_F16, torch.bfloat16: abi.ZERO_BF16}
 _F32 = torch.float32
+_empty = torch.empty
+_current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream  # without building a Stream object
 
 
-def _stream(stream, *tensors):
+def _stream(stream, tensors):
     """(the handle to launch on, `stream` if it is not torch's current one, else
     None). All tensors (None: absent) must be on the current device."""
-    index = tensors[0].get_device()
+    index = _current_device()
     for t in tensors:
         if t is not None and t.get_device() != index:
-            raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
-    if index < 0 or index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current CUDA device, got {tensors[0].device}")
+            raise ValueError(f"tensors must be on the current CUDA device {index}, got {t.device}")
     handle = _raw_stream(index)
     if stream is None or stream.cuda_stream == handle:
         return handle, None
@@ -42,41 +47,29 @@ def _stream(stream, *tensors):
     return stream.cuda_stream, stream
 
 
-def _empty(side, shape, dtype, device):
+def _new(side, shape, dtype, device):
+    """A new tensor, of the side stream if the call has one."""
     if side is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(side):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype=dtype, device=device)
 
 
-def _ptr(t) -> int | None:
-    return None if t is None else t.data_ptr()
+def _got(name, t, want):
+    return ValueError(f"{name}: expected {want}, got {tuple(t.shape)} of {t.dtype}, strides {t.stride()}")
 
 
-def _rows(t, name, shape, dtype) -> int:
+def _row_step(t, name, shape, dtype) -> int:
     """The row stride of a [rows, cols] tensor whose rows are contiguous."""
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
-    step, inner = t.stride()
-    if inner != 1 and shape[1] > 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    step, inner = t.stride() if t.dim() == 2 else (0, 0)
+    if t.shape != shape or t.dtype is not dtype or (inner != 1 and shape[1] > 1):
+        raise _got(name, t, f"{tuple(shape)} of {dtype} with contiguous rows")
     return step if shape[0] > 1 else shape[1]
 
 
 def _given(t, name, shape, dtype) -> None:
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {tuple(shape)} of {dtype}, got "
-                         f"{tuple(t.shape)} of {t.dtype}")
-
-
-def _matrix(x, name) -> None:
-    if x.dim() != 2 or x.dtype not in DTYPE_CODE:
-        raise ValueError(f"{name}: expected [rows, cols] of fp32, fp16 or bf16, got {tuple(x.shape)} of {x.dtype}")
-
-
-def _weight(weight, cols) -> None:
-    if weight.dtype not in DTYPE_CODE or weight.shape != (cols,) or not weight.is_contiguous():
-        raise ValueError(f"weight: expected a contiguous [{cols}]")
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise _got(name, t, f"a contiguous {tuple(shape)} of {dtype}")
 
 
 # ---------------------------------------------------------------------------
@@ -98,8 +91,8 @@ class PackedActivation:
         pitch = (cols + 127) // 128 * 128
         self.rows, self.cols = rows, cols
         if q is None:
-            q = _empty(stream, (rows, pitch), torch.int8, device)
-            scales = _empty(stream, (rows, pitch // 32), torch.uint8, device)
+            q = _new(stream, (rows, pitch), torch.int8, device)
+            scales = _new(stream, (rows, pitch // 32), torch.uint8, device)
         else:
             _given(q, "q", (rows, pitch), torch.int8)
             if scales is None:
@@ -109,27 +102,27 @@ class PackedActivation:
 
     def save(self, x: torch.Tensor, stream=None) -> "PackedActivation":
         """Pack x [rows, cols] (fp32, fp16 or bf16; its row stride is free)."""
-        _matrix(x, "x")
-        step = _rows(x, "x", (self.rows, self.cols), x.dtype)
-        handle, _ = _stream(stream, x, self.q, self.scales)
-        abi.zero_act_pack(x.data_ptr(), step, self.rows, self.cols, DTYPE_CODE[x.dtype],
-                          self.q.data_ptr(), self.scales.data_ptr(), handle)
+        dtype, q, scales = x.dtype, self.q, self.scales
+        code = DTYPE_CODE.get(dtype)
+        if code is None:
+            raise _got("x", x, "fp32, fp16 or bf16")
+        step = _row_step(x, "x", (self.rows, self.cols), dtype)
+        handle, _ = _stream(stream, (x, q, scales))
+        abi.zero_act_pack(x.data_ptr(), step, self.rows, self.cols, code, q.data_ptr(), scales.data_ptr(), handle)
         return self
 
     def restore(self, dtype: torch.dtype | None = None, out=None, stream=None) -> torch.Tensor:
         """The activation's values in `dtype` (default: out's, or bf16)."""
         if dtype is None:
             dtype = out.dtype if out is not None else torch.bfloat16
-        if dtype not in DTYPE_CODE:
+        code, q, scales, rows, cols = DTYPE_CODE.get(dtype), self.q, self.scales, self.rows, self.cols
+        if code is None:
             raise ValueError(f"unsupported type {dtype}")
-        handle, side = _stream(stream, self.q, self.scales, out)
-        step = self.cols
+        step = cols if out is None else _row_step(out, "out", (rows, cols), dtype)
+        handle, side = _stream(stream, (q, scales, out))
         if out is None:
-            out = _empty(side, (self.rows, self.cols), dtype, self.q.device)
-        else:
-            step = _rows(out, "out", (self.rows, self.cols), dtype)
-        abi.zero_act_unpack(self.q.data_ptr(), self.scales.data_ptr(), self.rows, self.cols,
-                            out.data_ptr(), step, DTYPE_CODE[dtype], handle)
+            out = _new(side, (rows, cols), dtype, q.device)
+        abi.zero_act_unpack(q.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), step, code, handle)
         return out
 
 
@@ -141,28 +134,28 @@ def weight_grad(dy: torch.Tensor, packed: PackedActivation, out=None, dtype=None
     dy [tokens, n_out]: its row stride is a multiple of 8 elements. dw is fp32
     or dy's type (`dtype`; default out's, or dy's). `accumulate` adds to an
     fp32 `out` (main gradients over micro-batches)."""
-    if dy.dim() != 2 or dy.shape[0] != packed.rows or dy.dtype not in HALF:
-        raise ValueError(f"dy: expected [{packed.rows}, n_out] of fp16 or bf16, got {tuple(dy.shape)} of {dy.dtype}")
+    code, q, scales, cols = HALF_CODE.get(dy.dtype), packed.q, packed.scales, packed.cols
+    if code is None or dy.dim() != 2 or dy.shape[0] != packed.rows:
+        raise _got("dy", dy, f"[{packed.rows}, n_out] of fp16 or bf16")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     tokens, n_out = dy.shape
     step, inner = dy.stride()
     if inner != 1 and n_out > 1:
-        raise ValueError("dy: the elements of a row must be contiguous")
+        raise _got("dy", dy, "contiguous rows")
     if tokens <= 1:
         step = (n_out + 7) // 8 * 8
     if dtype is None:
         dtype = out.dtype if out is not None else dy.dtype
     if dtype not in DTYPE_CODE:
         raise ValueError(f"unsupported type {dtype}")
-    handle, side = _stream(stream, dy, packed.q, packed.scales, out)
+    handle, side = _stream(stream, (dy, q, scales, out))
     if out is None:
-        out = _empty(side, (n_out, packed.cols), dtype, dy.device)
+        out = _new(side, (n_out, cols), dtype, q.device)
     else:
-        _given(out, "out", (n_out, packed.cols), dtype)
-    abi.zero_act_weight_grad(dy.data_ptr(), step, DTYPE_CODE[dy.dtype], packed.q.data_ptr(),
-                             packed.scales.data_ptr(), tokens, n_out, packed.cols, out.data_ptr(),
-                             DTYPE_CODE[dtype], accumulate, None, 0, handle)
+        _given(out, "out", (n_out, cols), dtype)
+    abi.zero_act_weight_grad(dy.data_ptr(), step, code, q.data_ptr(), scales.data_ptr(), tokens, n_out, cols,
+                             out.data_ptr(), DTYPE_CODE[dtype], accumulate, None, 0, handle)
     return out
 
 
@@ -178,41 +171,54 @@ def rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, re
 
     `packed` also receives y in 8 bits, from the same pass; with want_out=False
     y is not written (returned as None). sum_out may be x or residual itself."""
-    _matrix(x, "x")
-    shape, dtype = x.shape, x.dtype
+    shape, dtype, device = x.shape, x.dtype, x.device
+    code, wcode = DTYPE_CODE.get(dtype), DTYPE_CODE.get(weight.dtype)
+    if code is None or len(shape) != 2:
+        raise _got("x", x, "[rows, cols] of fp32, fp16 or bf16")
     rows, cols = shape
-    x_step = _rows(x, "x", shape, dtype)
-    r_step = cols if residual is None else _rows(residual, "residual", shape, dtype)
-    _weight(weight, cols)
-    q = scales = None
+    x_step = _row_step(x, "x", shape, dtype)
+    if wcode is None or weight.shape != (cols,) or not weight.is_contiguous():
+        raise _got("weight", weight, f"a contiguous [{cols}] of fp32, fp16 or bf16")
+    q = scales = q_ptr = scales_ptr = None
     if packed is not None:
         if packed.rows != rows or packed.cols != cols:
             raise ValueError(f"packed: {packed.rows} x {packed.cols} for x of {rows} x {cols}")
         q, scales = packed.q, packed.scales
-    handle, side = _stream(stream, x, weight, residual, out, sum_out, rstd, q, scales)
-    if not want_out:
-        if out is not None or packed is None:
-            raise ValueError("want_out=False goes with packed and without out")
-    elif out is None:
-        out = _empty(side, shape, dtype, x.device)
-    else:
-        _given(out, "out", shape, dtype)
-    if residual is None:
-        if sum_out is not None:
-            raise ValueError("sum_out without a residual")
-    elif sum_out is None:
-        sum_out = _empty(side, shape, dtype, x.device)
-    else:
-        _given(sum_out, "sum_out", shape, dtype)
+        q_ptr, scales_ptr = q.data_ptr(), scales.data_ptr()
+    handle, side = _stream(stream, (x, weight, residual, out, sum_out, rstd, q, scales))
+    r_step, r_ptr, sum_ptr, total = cols, None, None, x
+    if residual is not None:
+        r_step, r_ptr = _row_step(residual, "residual", shape, dtype), residual.data_ptr()
+        if sum_out is None:
+            sum_out = _new(side, shape, dtype, device)
+        else:
+            _given(sum_out, "sum_out", shape, dtype)
+        total, sum_ptr = sum_out, sum_out.data_ptr()
+    elif sum_out is not None:
+        raise ValueError("sum_out without a residual")
+    out_ptr = None
+    if want_out:
+        if out is None:
+            out = _new(side, shape, dtype, device)
+        else:
+            _given(out, "out", shape, dtype)
+        out_ptr = out.data_ptr()
+    elif out is not None or packed is None:
+        raise ValueError("want_out=False goes with packed and without out")
     if rstd is None:
-        rstd = _empty(side, (rows,), _F32, x.device)
+        rstd = _new(side, rows, _F32, device)
     else:
         _given(rstd, "rstd", (rows,), _F32)
-    desc = abi.zero_rmsnorm_desc(rows, cols, x_step, r_step, cols, DTYPE_CODE[dtype],
-                                 DTYPE_CODE[weight.dtype], eps)
-    abi.zero_rmsnorm_forward(desc, x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(sum_out),
-                             _ptr(out), _ptr(q), _ptr(scales), rstd.data_ptr(), handle)
-    return out, (x if residual is None else sum_out), rstd
+    abi.zero_rmsnorm_forward(abi.RMSNORM_DESC.pack(rows, cols, x_step, r_step, cols, code, wcode, eps), x.data_ptr(),
+                             r_ptr, weight.data_ptr(), sum_ptr, out_ptr, q_ptr, scales_ptr, rstd.data_ptr(), handle)
+    return out, total, rstd
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_scratch(rows, cols) -> int:
+    """Scratch bytes of a norm's backward: a function of its sizes."""
+    return abi.zero_rmsnorm_backward_workspace(
+        abi.RMSNORM_DESC.pack(rows, cols, cols, cols, cols, abi.ZERO_F32, abi.ZERO_F32, 0.0))
 
 
 def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -221,34 +227,37 @@ def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rs
     is the gradient of x and of the residual; dsum, the gradient that reaches
     s by its other use, is added to it. dweight: fp32 sums stored as
     dweight_dtype (default: dweight's type, or weight's)."""
-    _matrix(x, "x")
-    shape, dtype = x.shape, x.dtype
+    shape, dtype, device = x.shape, x.dtype, x.device
+    code, wcode = DTYPE_CODE.get(dtype), DTYPE_CODE.get(weight.dtype)
+    if code is None or len(shape) != 2:
+        raise _got("x", x, "[rows, cols] of fp32, fp16 or bf16")
     rows, cols = shape
-    x_step = _rows(x, "x", shape, dtype)
-    dy_step = _rows(dy, "dy", shape, dtype)
-    r_step = cols if dsum is None else _rows(dsum, "dsum", shape, dtype)
-    _weight(weight, cols)
+    x_step, dy_step = _row_step(x, "x", shape, dtype), _row_step(dy, "dy", shape, dtype)
+    r_step, r_ptr = cols, None
+    if dsum is not None:
+        r_step, r_ptr = _row_step(dsum, "dsum", shape, dtype), dsum.data_ptr()
+    if wcode is None or weight.shape != (cols,) or not weight.is_contiguous():
+        raise _got("weight", weight, f"a contiguous [{cols}] of fp32, fp16 or bf16")
     _given(rstd, "rstd", (rows,), _F32)
     if dweight_dtype is None:
         dweight_dtype = dweight.dtype if dweight is not None else weight.dtype
-    if dweight_dtype not in DTYPE_CODE:
+    dcode = DTYPE_CODE.get(dweight_dtype)
+    if dcode is None:
         raise ValueError(f"unsupported type {dweight_dtype}")
-    handle, side = _stream(stream, x, dy, weight, rstd, dsum, dx, dweight)
+    handle, side = _stream(stream, (x, dy, weight, rstd, dsum, dx, dweight))
     if dx is None:
-        dx = _empty(side, shape, dtype, x.device)
+        dx = _new(side, shape, dtype, device)
     else:
         _given(dx, "dx", shape, dtype)
     if dweight is None:
-        dweight = _empty(side, (cols,), dweight_dtype, x.device)
+        dweight = _new(side, cols, dweight_dtype, device)
     else:
         _given(dweight, "dweight", (cols,), dweight_dtype)
-    desc = abi.zero_rmsnorm_desc(rows, cols, x_step, r_step, dy_step, DTYPE_CODE[dtype],
-                                 DTYPE_CODE[weight.dtype], 0.0)
-    nbytes = abi.zero_rmsnorm_backward_workspace(desc)
-    space = _empty(side, nbytes, torch.uint8, x.device) if nbytes else None
-    abi.zero_rmsnorm_backward(desc, dy.data_ptr(), x.data_ptr(), weight.data_ptr(), rstd.data_ptr(),
-                              _ptr(dsum), dx.data_ptr(), dweight.data_ptr(),
-                              DTYPE_CODE[dweight_dtype], _ptr(space), nbytes, handle)
+    nbytes = _norm_scratch(rows, cols)
+    space = _new(side, nbytes, torch.uint8, device)
+    abi.zero_rmsnorm_backward(abi.RMSNORM_DESC.pack(rows, cols, x_step, r_step, dy_step, code, wcode, 0.0),
+                              dy.data_ptr(), x.data_ptr(), weight.data_ptr(), rstd.data_ptr(), r_ptr, dx.data_ptr(),
+                              dweight.data_ptr(), dcode, space.data_ptr(), nbytes, handle)
     return dx, dweight
 
 
@@ -256,36 +265,29 @@ def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rs
 # Attention's training pair
 # ---------------------------------------------------------------------------
 
-
 def _steps(t, name, shape, dtype):
-    """{batch, token, head} strides of a [batch, length, heads, head_dim] tensor."""
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{name}: expected {tuple(shape)} of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    """Strides of a [batch, length, heads, head_dim] tensor, head elements contiguous."""
     steps = t.stride()
-    if steps[3] != 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
-    return steps[:3]
+    if t.shape != shape or t.dtype is not dtype or steps[3] != 1:
+        raise _got(name, t, f"{tuple(shape)} of {dtype} with contiguous heads")
+    return steps
 
 
 def _attention_sizes(q, k, causal, window, key_lengths, scale):
     """The leading fields of the call's descriptor, and the shape of k and v."""
-    if q.dim() != 4 or k.dim() != 4 or q.dtype not in HALF:
-        raise ValueError("q, k, v: expected [batch, length, heads, head_dim] of fp16 or bf16, got "
-                         f"{tuple(q.shape)} and {tuple(k.shape)} of {q.dtype}")
-    batch, q_len, q_heads, dim = q.shape
-    _, k_len, kv_heads, _ = k.shape
+    q_shape, k_shape = q.shape, k.shape
+    code = HALF_CODE.get(q.dtype)
+    if code is None or len(q_shape) != 4 or len(k_shape) != 4:
+        raise _got("q", q, "[batch, length, heads, head_dim] of fp16 or bf16, as k and v")
+    batch, q_len, q_heads, dim = q_shape
+    _, k_len, kv_heads, _ = k_shape
     if key_lengths is not None:
         _given(key_lengths, "key_lengths", (batch,), torch.int32)
-    sizes = (batch, q_len, k_len, q_heads, kv_heads, dim, DTYPE_CODE[q.dtype], causal, 0, window,
-             dim ** -0.5 if scale is None else scale)
-    return sizes, (batch, k_len, kv_heads, dim)
+    return (batch, q_len, k_len, q_heads, kv_heads, dim, code, causal, 0, window,
+            dim ** -0.5 if scale is None else scale), (batch, k_len, kv_heads, dim)
 
 
-def _like(t, side, ref, name):
-    """The given output, or a new contiguous one of ref's shape; its strides."""
-    if t is None:
-        t = _empty(side, ref.shape, ref.dtype, ref.device)
-    return t, _steps(t, name, ref.shape, ref.dtype)
+_ZEROS = (0,) * 12
 
 
 def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
@@ -298,20 +300,33 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal:
     (`causal`) and j > i + k_len - q_len - window (`window` > 0). A query that
     sees no key has o = 0 and lse = -inf. scale: default head_dim^-1/2. lse is
     fp32 [batch, q_heads, q_len]."""
-    sizes, shape = _attention_sizes(q, k, causal, window, key_lengths, scale)
-    dtype = q.dtype
-    q_steps, k_steps, v_steps = _steps(q, "q", q.shape, dtype), _steps(k, "k", shape, dtype), _steps(v, "v", shape, dtype)
-    handle, side = _stream(stream, q, k, v, key_lengths, out, lse)
-    out, o_steps = _like(out, side, q, "out")
+    sizes, kv_shape = _attention_sizes(q, k, causal, window, key_lengths, scale)
+    dtype, shape, device = q.dtype, q.shape, q.device
+    qb, qt, qh, _ = _steps(q, "q", shape, dtype)
+    kb, kt, kh, _ = _steps(k, "k", kv_shape, dtype)
+    vb, vt, vh, _ = _steps(v, "v", kv_shape, dtype)
+    handle, side = _stream(stream, (q, k, v, key_lengths, out, lse))
+    if out is None:
+        out = _new(side, shape, dtype, device)
+    ob, ot, oh, _ = _steps(out, "out", shape, dtype)
     rows = (sizes[0], sizes[3], sizes[1])
     if lse is None:
-        lse = _empty(side, rows, _F32, q.device)
+        lse = _new(side, rows, _F32, device)
     else:
         _given(lse, "lse", rows, _F32)
-    desc = abi.attention_desc_flat(*sizes, *q_steps, *k_steps, *v_steps, *o_steps)
-    abi.zero_attention_forward(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(key_lengths),
-                               out.data_ptr(), lse.data_ptr(), handle)
+    desc = abi.ATTENTION_DESC.pack(*sizes, qb, qt, qh, kb, kt, kh, vb, vt, vh, ob, ot, oh, *_ZEROS)
+    abi.zero_attention_forward(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                               None if key_lengths is None else key_lengths.data_ptr(), out.data_ptr(),
+                               lse.data_ptr(), handle)
     return out, lse
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_scratch(batch, q_len, q_heads) -> int:
+    """Scratch bytes of attention's backward: a function of the query rows."""
+    steps = (max(q_len, 1) * q_heads * 8, q_heads * 8, 8)
+    return abi.zero_attention_backward_workspace(
+        abi.ATTENTION_DESC.pack(batch, q_len, q_len, q_heads, q_heads, 8, abi.ZERO_F16, 0, 0, 0, 1.0, *steps * 8))
 
 
 def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -321,21 +336,32 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     """(dq, dk, dv) from dout, the forward's tensors and the same mask; the
     probabilities are recomputed from lse. dk and dv are summed over the query
     heads that share a key head."""
-    sizes, shape = _attention_sizes(q, k, causal, window, key_lengths, scale)
-    dtype, q_shape = q.dtype, q.shape
-    steps = (*_steps(q, "q", q_shape, dtype), *_steps(k, "k", shape, dtype), *_steps(v, "v", shape, dtype),
-             *_steps(o, "o", q_shape, dtype), *_steps(dout, "dout", q_shape, dtype))
-    _given(lse, "lse", (sizes[0], sizes[3], sizes[1]), _F32)
-    handle, side = _stream(stream, q, k, v, o, dout, lse, key_lengths, dq, dk, dv)
-    dq, dq_steps = _like(dq, side, q, "dq")
-    dk, dk_steps = _like(dk, side, k, "dk")
-    dv, dv_steps = _like(dv, side, v, "dv")
-    desc = abi.attention_desc_flat(*sizes, *steps, *dq_steps, *dk_steps, *dv_steps)
-    nbytes = abi.zero_attention_backward_workspace(desc)
-    space = _empty(side, nbytes, torch.uint8, q.device) if nbytes else None
-    abi.zero_attention_backward(desc, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                o.data_ptr(), lse.data_ptr(), _ptr(key_lengths), dq.data_ptr(),
-                                dk.data_ptr(), dv.data_ptr(), _ptr(space), nbytes, handle)
+    sizes, kv_shape = _attention_sizes(q, k, causal, window, key_lengths, scale)
+    dtype, shape, device = q.dtype, q.shape, q.device
+    qb, qt, qh, _ = _steps(q, "q", shape, dtype)
+    kb, kt, kh, _ = _steps(k, "k", kv_shape, dtype)
+    vb, vt, vh, _ = _steps(v, "v", kv_shape, dtype)
+    ob, ot, oh, _ = _steps(o, "o", shape, dtype)
+    gb, gt, gh, _ = _steps(dout, "dout", shape, dtype)
+    batch, q_heads, q_len = sizes[0], sizes[3], sizes[1]
+    _given(lse, "lse", (batch, q_heads, q_len), _F32)
+    handle, side = _stream(stream, (q, k, v, o, dout, lse, key_lengths, dq, dk, dv))
+    if dq is None:
+        dq = _new(side, shape, dtype, device)
+    if dk is None:
+        dk = _new(side, kv_shape, dtype, device)
+    if dv is None:
+        dv = _new(side, kv_shape, dtype, device)
+    dqb, dqt, dqh, _ = _steps(dq, "dq", shape, dtype)
+    dkb, dkt, dkh, _ = _steps(dk, "dk", kv_shape, dtype)
+    dvb, dvt, dvh, _ = _steps(dv, "dv", kv_shape, dtype)
+    nbytes = _attention_scratch(batch, q_len, q_heads)
+    space = _new(side, nbytes, torch.uint8, device)
+    desc = abi.ATTENTION_DESC.pack(*sizes, qb, qt, qh, kb, kt, kh, vb, vt, vh, ob, ot, oh, gb, gt, gh, dqb, dqt, dqh,
+                                   dkb, dkt, dkh, dvb, dvt, dvh)
+    abi.zero_attention_backward(desc, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                lse.data_ptr(), None if key_lengths is None else key_lengths.data_ptr(),
+                                dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), space.data_ptr(), nbytes, handle)
     return dq, dk, dv
 
 
