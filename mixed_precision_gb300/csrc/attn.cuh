@@ -172,7 +172,7 @@ inline bool attn_map(CUtensorMap* map, const void* base, int dtype, const int64_
                      int heads, int dim) {
   const uint64_t n[4] = {(uint64_t)dim, (uint64_t)len, (uint64_t)heads, (uint64_t)batch};
   const uint64_t b[3] = {(uint64_t)s[1] * 2, (uint64_t)s[2] * 2, (uint64_t)s[0] * 2};
-  return make_tensor_map(map, base, dtype == kBF16, 4, n, b, kTile);
+  return make_tensor_map(map, base, dtype, 4, n, b, kTile);
 }
 
 }  // namespace zg

@@ -159,7 +159,8 @@ __device__ __forceinline__ void add32(uint32_t addr, uint32_t (&r)[32]) {
 
 template <typename T, int MT, int BN, bool ROUND>
 __global__ void __launch_bounds__(kWgThreads, 1)
-    k_wgrad(const __grid_constant__ CUtensorMap map, const WgradArgs a, int n_tiles, int split, int per_split) {
+    k_wgrad(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_dw, const WgradArgs a,
+            int n_tiles, int split, int per_split, bool tiles_out) {
   using C = Tile<MT, BN, ROUND>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], done, moved;
@@ -338,7 +339,59 @@ __global__ void __launch_bounds__(kWgThreads, 1)
   const bool ok = wait(&done, steps > 0 ? (runs - 1) & 1 : 0);
   tc_fence_after();
 
-  if (split == 1) {
+  if (split == 1 && tiles_out) {
+    // ---- the sums as a swizzled tile in the stages' place, which are done with,
+    // and out by bulk stores. Rows written from registers touch 32 lines an
+    // instruction: 8 us for a tile of 256 x 256.
+    const bool f32 = a.dw_dtype == kF32;
+    const int width = f32 ? 32 : 64, rows_bytes = 128 * BN * (f32 ? 4 : 2);  // of 128 rows
+    // fp32 sums of 256 x 256 do not fit at once: 128 rows after the other
+    const bool again = MT * rows_bytes > C::kStages * C::kStage;
+    static_assert(128 * BN * 4 <= C::kStages * C::kStage, "128 rows fit");
+#pragma unroll 1
+    for (int m = 0; m < MT; ++m) {
+      const int region = again ? 0 : m * rows_bytes;
+      if (again && m > 0) __syncthreads();  // the rows before have been read
+      if (warp < kConvWarps && ok) {
+#pragma unroll 1
+        for (int c = half; c < half + BN / kParts; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(mine + m * BN + c, r);
+          if (ROUND && runs > 1) add32(mine + (MT + m) * BN + c, r);
+          tmem_wait_ld();
+          uint8_t* to = smem + region + c / width * (128 * 128) + row * 128;
+          if (f32) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              *reinterpret_cast<uint4*>(to + (g ^ (row & 7)) * 16) =
+                  make_uint4(r[4 * g], r[4 * g + 1], r[4 * g + 2], r[4 * g + 3]);
+          } else {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = round2<T>(__uint_as_float(r[g * 8 + 2 * e]), __uint_as_float(r[g * 8 + 2 * e + 1]));
+              *reinterpret_cast<uint4*>(to + ((c / 32 % 2 * 4 + g) ^ (row & 7)) * 16) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        fence_async_smem();
+      }
+      __syncthreads();
+      if (warp == kConvWarps && __all_sync(0xFFFFFFFFu, ok) && m0 + m * 128 < a.n_out && elect_one()) {
+        for (int c = 0; c < BN / width && n0 + c * width < a.n_in; ++c) {
+          const uint32_t from = base + region + c * (128 * 128);
+          if (a.accumulate)
+            tma_add2(&map_dw, from, n0 + c * width, (int)m0 + m * 128);
+          else
+            tma_store2(&map_dw, from, n0 + c * width, (int)m0 + m * 128);
+        }
+        tma_store_done();
+      }
+    }
+  } else if (split == 1) {
     if (warp < kConvWarps && ok) {
 #pragma unroll 1
       for (int m = 0; m < MT; ++m)
@@ -425,31 +478,31 @@ struct Plan {
   int mt, bn, split;
 };
 
-// The tile and split with the least estimated time, in cycles. Measured on one
-// block per SM: a step of 64 tokens takes 1280 cycles in the 256 x 256 tile, 950
-// in 256 x 128 and 730 in 128 x 128 (1220 and 960 with rounded runs), a block
-// about 3000 to start, and its outputs' way out 6 cycles per 128 of them,
-// 28 through a cluster. Clusters leave some SMs idle: 148, 136 and 120 are
-// used by clusters of 2, 4 and 8. At 8192 x 2048 x 1024 the tile of 256 x 256
-// split in 4 takes 40 us, 128 x 128 without a split 59 us; at 4096 x 8192 x 4096
-// the unsplit 256 x 256 tile takes 220 us, 128 x 128 410 us.
+// The tile and split with the least estimated time, in cycles. Measured with one
+// block per SM at 1.9 GHz: a step of 64 tokens takes 1150 cycles in the 256 x 256
+// tile, 690 in 256 x 128 and 526 in 128 x 128 (852 and 685 with rounded runs); a
+// block's start and end take 15200, 12700 and 10200 (17700, 16900), and a
+// cluster's sum 25 more for each 128 outputs. Clusters leave some SMs idle: 148,
+// 136 and 120 are used by clusters of 2, 4 and 8. At 8192 x 2048 x 1024 the tile
+// of 256 x 128 split in 2 takes 34 us, 128 x 128 without a split 41 us; at
+// 4096 x 8192 x 4096 the unsplit 256 x 256 tile takes 185 us, 128 x 128 310 us.
 Plan wgrad_plan(int64_t tokens, int64_t n_out, int64_t n_in, bool round, int sms) {
   const int64_t steps = (tokens + kStep - 1) / kStep;
   static const struct {
     int mt, bn;
-    double step, step_round;  // step_round 0: not built
-  } shapes[] = {{2, 256, 1280, 0}, {2, 128, 950, 1220}, {1, 128, 730, 960}};
+    double step, ends, step_round, ends_round;  // step_round 0: not built
+  } shapes[] = {{2, 256, 1150, 15200, 0, 0}, {2, 128, 690, 12700, 852, 17700}, {1, 128, 526, 10200, 685, 16900}};
   Plan best{1, 128, 1};
   double least = 1e300;
   for (const auto& sh : shapes) {
-    const double step = round ? sh.step_round : sh.step;
+    const double step = round ? sh.step_round : sh.step, ends = round ? sh.ends_round : sh.ends;
     if (step == 0) continue;
     const double tiles = (double)((n_out + sh.mt * 128 - 1) / (sh.mt * 128)) * ((n_in + sh.bn - 1) / sh.bn);
     for (int split = 1; split <= 8 && split <= steps; split *= 2) {
       const int used = split == 1 ? sms : split == 2 ? sms - 4 : split == 4 ? sms - 16 : sms - 32;
       const double waves = std::ceil(tiles * split / (used > split ? used : split));
-      const double out = sh.mt * sh.bn * (split > 1 ? 28.0 : 6.0);
-      const double t = waves * (3000.0 + out + step * (double)((steps + split - 1) / split));
+      const double t = waves * (ends + (split > 1 ? 25.0 * sh.mt * sh.bn : 0.0) +
+                                step * (double)((steps + split - 1) / split));
       if (t < least) {
         least = t;
         best = Plan{sh.mt, sh.bn, split};
@@ -462,9 +515,15 @@ Plan wgrad_plan(int64_t tokens, int64_t n_out, int64_t n_in, bool round, int sms
 template <typename T, int MT, int BN, bool ROUND>
 cudaError_t run(const WgradArgs& a, int split, cudaStream_t s) {
   using C = Tile<MT, BN, ROUND>;
-  CUtensorMap map;
+  CUtensorMap map, map_dw{};
   const uint64_t extent[2] = {(uint64_t)a.n_out, (uint64_t)a.tokens}, strides[1] = {(uint64_t)a.dy_stride * 2};
-  if (!make_tensor_map(&map, a.dy, a.dtype == kBF16, 2, extent, strides, kStep)) return cudaErrorInvalidValue;
+  if (!make_tensor_map(&map, a.dy, a.dtype, 2, extent, strides, kStep)) return cudaErrorInvalidValue;
+  // dw's rows have to start on 16 bytes to leave as tiles
+  const uint64_t out_extent[2] = {(uint64_t)a.n_in, (uint64_t)a.n_out};
+  const uint64_t out_strides[1] = {(uint64_t)a.n_in * (a.dw_dtype == kF32 ? 4 : 2)};
+  const bool tiles_out = out_strides[0] % 16 == 0;
+  if (tiles_out && !make_tensor_map(&map_dw, a.dw, a.dw_dtype, 2, out_extent, out_strides, 128))
+    return cudaErrorInvalidValue;
   static std::atomic<uint64_t> asked{0};
   cudaError_t e = allow_smem(k_wgrad<T, MT, BN, ROUND>, C::kSmem, asked);
   if (e != cudaSuccess) return e;
@@ -483,7 +542,8 @@ cudaError_t run(const WgradArgs& a, int split, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_wgrad<T, MT, BN, ROUND>, map, a, n_tiles, split, (int)((steps + split - 1) / split));
+  return cudaLaunchKernelEx(&cfg, k_wgrad<T, MT, BN, ROUND>, map, map_dw, a, n_tiles, split,
+                            (int)((steps + split - 1) / split), tiles_out);
 }
 
 template <typename T>

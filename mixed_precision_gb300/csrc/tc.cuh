@@ -195,6 +195,17 @@ __device__ __forceinline__ void tma_store4(const CUtensorMap* map, uint32_t src,
                "r"(src), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
 }
+__device__ __forceinline__ void tma_store2(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map), "r"(src),
+               "r"(x), "r"(y)
+               : "memory");
+}
+// The same, added to what is there.
+__device__ __forceinline__ void tma_add2(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
 // End the group, and wait until its shared memory has been read.
 __device__ __forceinline__ void tma_store_done() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -239,10 +250,10 @@ inline cudaError_t allow_smem(Kernel* kernel, int bytes, std::atomic<uint64_t>& 
 
 // ---- tensor maps (host) --------------------------------------------------------
 
-// A map of up to 4 dimensions of 16-bit elements, boxes of 64 x rows (x 1 x 1)
-// with the 128-byte swizzle; out-of-range elements read as zero. strides: bytes,
-// of dimensions 1 and up. False if the driver refuses it.
-bool make_tensor_map(CUtensorMap* map, const void* base, bool bf16, int dims, const uint64_t* extent,
+// A map of up to 4 dimensions of elements of `dtype`, boxes of 128 bytes x rows
+// (x 1 x 1) with the 128-byte swizzle; out-of-range elements read as zero.
+// strides: bytes, of dimensions 1 and up. False if the driver refuses it.
+bool make_tensor_map(CUtensorMap* map, const void* base, int dtype, int dims, const uint64_t* extent,
                      const uint64_t* strides, uint32_t box_rows);
 
 }  // namespace zg

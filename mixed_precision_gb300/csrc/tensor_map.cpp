@@ -28,16 +28,18 @@ static EncodeFn encoder() {
   return reinterpret_cast<EncodeFn>(f);
 }
 
-bool make_tensor_map(CUtensorMap* map, const void* base, bool bf16, int dims, const uint64_t* extent,
+bool make_tensor_map(CUtensorMap* map, const void* base, int dtype, int dims, const uint64_t* extent,
                      const uint64_t* strides, uint32_t box_rows) {
   EncodeFn encode = encoder();
   if (encode == nullptr) return false;
-  const cuuint32_t box[4] = {64, box_rows, 1, 1}, step[4] = {1, 1, 1, 1};
+  const CUtensorMapDataType type = dtype == kF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const cuuint32_t box[4] = {dtype == kF32 ? 32u : 64u, box_rows, 1, 1}, step[4] = {1, 1, 1, 1};
   cuuint64_t n[4], s[3];
   for (int i = 0; i < dims; ++i) n[i] = extent[i];
   for (int i = 0; i + 1 < dims; ++i) s[i] = strides[i];
-  return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims,
-                const_cast<void*>(base), n, s, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  return encode(map, type, dims, const_cast<void*>(base), n, s, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
