@@ -68,11 +68,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// S outside columns [from, to): -inf.
-__device__ __forceinline__ void mask_row(uint32_t (&s)[32], int from, int to) {
-#pragma unroll
-  for (int k = 0; k < 32; ++k) s[k] = k >= from && k < to ? s[k] : 0xFF800000u;
+// Bit k: whether column k of 32 lies in [from, to).
+__device__ __forceinline__ uint32_t seen_bits(int from, int to) {
+  const uint32_t low = from <= 0 ? 0xFFFFFFFFu : from >= 32 ? 0u : 0xFFFFFFFFu << from;
+  const uint32_t high = to >= 32 ? 0xFFFFFFFFu : to <= 0 ? 0u : (1u << to) - 1u;
+  return low & high;
 }
+// Values whose bit is not set: `other`. (Testing bits of one word takes a third
+// of the instructions of comparing every column with both ends.)
+__device__ __forceinline__ void mask_row(uint32_t (&s)[32], uint32_t bits, uint32_t other) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) s[k] = bits & 1u << k ? s[k] : other;
+}
+constexpr uint32_t kMinusInf = 0xFF800000u;
 
 // Registers of a warpgroup's threads, given away and taken (all four warps).
 template <int N>
@@ -137,15 +145,19 @@ __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
 // a block); a tile leaves by one bulk store. The whole warp calls it.
 template <typename T, int N>
 __device__ __forceinline__ void stage_row(uint8_t* tile, int row, int col0, uint32_t addr, float f, bool zero) {
+  constexpr int kStep = N % 32 == 0 ? 32 : 16;
 #pragma unroll 1
-  for (int k = 0; k < N; k += 16) {
-    uint32_t o[16];
+  for (int k = 0; k < N; k += kStep) {
+    uint32_t o[kStep];
     if (!zero) {
-      tmem_ld16(addr + k, o);
+      if constexpr (kStep == 32)
+        tmem_ld32(addr + k, o);
+      else
+        tmem_ld16(addr + k, o);
       tmem_wait_ld();
     }
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < kStep / 8; ++g) {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)

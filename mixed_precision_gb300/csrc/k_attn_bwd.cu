@@ -230,8 +230,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       const int key0 = (first + j) * kTile + quarter * kCols, from = lo - key0, to = hi - key0;
       if (__any_sync(0xFFFFFFFFu, from > 0 || to < kCols)) {  // whatever p and dp are there
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) p[k] = k >= from && k < to ? p[k] : 0u;
+        mask_row(p, seen_bits(from, to), 0u);
       }
       uint32_t w[kCols / 2];
 #pragma unroll
@@ -452,8 +451,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int from = lo - q0, to = hi - q0;
       const bool mask = __any_sync(0xFFFFFFFFu, from > 0 || to < kCols);
       if (mask) {
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) p[k] = k >= from && k < to ? p[k] : 0u;
+        mask_row(p, seen_bits(from, to), 0u);
       }
 #pragma unroll
       for (int k = 0; k < kCols; k += 2) w[k / 2] = round2<T>(__uint_as_float(p[k]), __uint_as_float(p[k + 1]));
@@ -477,8 +475,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         p[k + 1] = __float_as_uint(y);
       }
       if (mask) {  // 0 times whatever dp is there
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) p[k] = k >= from && k < to ? p[k] : 0u;
+        mask_row(p, seen_bits(from, to), 0u);
       }
 #pragma unroll
       for (int k = 0; k < kCols; k += 2) w[k / 2] = round2<T>(__uint_as_float(p[k]), __uint_as_float(p[k + 1]));

@@ -186,6 +186,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (t == 0 || two) {
       int lo, hi;
       key_range(a, keys, i, lo, hi);
+      if (n > 0) {  // nothing to go by yet: the first tile's maximum
+        ok = wait(&s_full[t], 0);
+        tc_fence_after();
+        const int from = lo - first * kTile - half * 64, to = hi - first * kTile - half * 64;
+        float m = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < 64; q += 32) {
+          uint32_t r[32];
+          tmem_ld32(s_at + q, r);
+          tmem_wait_ld();
+          mask_row(r, seen_bits(from - q, to - q), kMinusInf);
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) m = max3(m, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+        }
+        tops[1][t][half][row] = m;
+        named_sync(3 + warp / 8 * 4 + (warp & 3), 64);
+        top = fmaxf(m, tops[1][t][half ^ 1][row]);
+      }
+#pragma unroll 1
       for (int j = 0; j < n; ++j) {
         // a wait that gives up goes on to the barriers with what is there: the
         // other half may be waiting in them
@@ -207,7 +226,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             uint32_t r[32];
             tmem_ld32(s_at + q * 32, r);
             tmem_wait_ld();
-            if (mask) mask_row(r, from - q * 32, to - q * 32);
+            if (mask) mask_row(r, seen_bits(from - q * 32, to - q * 32), kMinusInf);
 #pragma unroll
             for (int k = 0; k < 32; k += 8)
 #pragma unroll
@@ -237,7 +256,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const float f = raise ? exp2_fast((top - m) * scale2) : 1.0f;
           if (raise) top = m;
           total *= f;
-          if (j == 0) continue;
           // O is complete up to the tile before: its product was issued before this S
 #pragma unroll 1
           for (int k = 0; k < DP / 2; k += 16) {
