@@ -11,8 +11,9 @@ streams' work stays the caller's job, as with any torch operation.
 Wrong shapes, types, devices or layouts raise ValueError here, or ZeroError
 (ZERO_ERR_INVALID) from the library; nothing is enqueued then.
 
-The checks are written out in each function: at a few microseconds a kernel,
-helper calls would be a good part of a short call's time.
+The checks are written out in each function and the library's entry points
+called directly: at a few microseconds a kernel, helper calls would be a good
+part of a short call's time.
 """
 from __future__ import annotations
 
@@ -27,7 +28,8 @@ DTYPE_CODE = {torch.float32: abi.ZERO_F32, torch.float16: abi.ZERO_F16,
 HALF_CODE = {torch.float16: abi.ZERO_F16, torch.bfloat16: abi.ZERO_BF16}
 _F32 = torch.float32
 _empty = torch.empty
-_current_device = torch.cuda.current_device
+_current_device = torch._C._cuda_getDevice
+_norm_desc, _attention_desc = abi.RMSNORM_DESC.pack, abi.ATTENTION_DESC.pack
 _raw_stream = torch._C._cuda_getCurrentRawStream  # without building a Stream object
 
 
@@ -53,6 +55,11 @@ def _new(side, shape, dtype, device):
         return _empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(side):
         return _empty(shape, dtype=dtype, device=device)
+
+
+def _library():
+    """The loaded library (abi.lib(), without the call once it is loaded)."""
+    return abi._lib or abi.lib()
 
 
 def _got(name, t, want):
@@ -108,7 +115,10 @@ class PackedActivation:
             raise _got("x", x, "fp32, fp16 or bf16")
         step = _row_step(x, "x", (self.rows, self.cols), dtype)
         handle, _ = _stream(stream, (x, q, scales))
-        abi.zero_act_pack(x.data_ptr(), step, self.rows, self.cols, code, q.data_ptr(), scales.data_ptr(), handle)
+        rc = _library().zero_act_pack(x.data_ptr(), step, self.rows, self.cols, code, q.data_ptr(), scales.data_ptr(),
+                                      handle)
+        if rc:
+            abi._check(rc)
         return self
 
     def restore(self, dtype: torch.dtype | None = None, out=None, stream=None) -> torch.Tensor:
@@ -122,7 +132,9 @@ class PackedActivation:
         handle, side = _stream(stream, (q, scales, out))
         if out is None:
             out = _new(side, (rows, cols), dtype, q.device)
-        abi.zero_act_unpack(q.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), step, code, handle)
+        rc = _library().zero_act_unpack(q.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(), step, code, handle)
+        if rc:
+            abi._check(rc)
         return out
 
 
@@ -154,8 +166,10 @@ def weight_grad(dy: torch.Tensor, packed: PackedActivation, out=None, dtype=None
         out = _new(side, (n_out, cols), dtype, q.device)
     else:
         _given(out, "out", (n_out, cols), dtype)
-    abi.zero_act_weight_grad(dy.data_ptr(), step, code, q.data_ptr(), scales.data_ptr(), tokens, n_out, cols,
-                             out.data_ptr(), DTYPE_CODE[dtype], accumulate, None, 0, handle)
+    rc = _library().zero_act_weight_grad(dy.data_ptr(), step, code, q.data_ptr(), scales.data_ptr(), tokens, n_out,
+                                         cols, out.data_ptr(), DTYPE_CODE[dtype], accumulate, None, 0, handle)
+    if rc:
+        abi._check(rc)
     return out
 
 
@@ -176,7 +190,11 @@ def rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, re
     if code is None or len(shape) != 2:
         raise _got("x", x, "[rows, cols] of fp32, fp16 or bf16")
     rows, cols = shape
-    x_step = _row_step(x, "x", shape, dtype)
+    x_step, inner = x.stride()
+    if inner != 1 and cols > 1:
+        raise _got("x", x, "contiguous rows")
+    if rows <= 1:
+        x_step = cols
     if wcode is None or weight.shape != (cols,) or not weight.is_contiguous():
         raise _got("weight", weight, f"a contiguous [{cols}] of fp32, fp16 or bf16")
     q = scales = q_ptr = scales_ptr = None
@@ -209,8 +227,11 @@ def rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, re
         rstd = _new(side, rows, _F32, device)
     else:
         _given(rstd, "rstd", (rows,), _F32)
-    abi.zero_rmsnorm_forward(abi.RMSNORM_DESC.pack(rows, cols, x_step, r_step, cols, code, wcode, eps), x.data_ptr(),
-                             r_ptr, weight.data_ptr(), sum_ptr, out_ptr, q_ptr, scales_ptr, rstd.data_ptr(), handle)
+    rc = _library().zero_rmsnorm_forward(_norm_desc(rows, cols, x_step, r_step, cols, code, wcode, eps), x.data_ptr(),
+                                         r_ptr, weight.data_ptr(), sum_ptr, out_ptr, q_ptr, scales_ptr,
+                                         rstd.data_ptr(), handle)
+    if rc:
+        abi._check(rc)
     return out, total, rstd
 
 
@@ -218,7 +239,7 @@ def rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, re
 def _norm_scratch(rows, cols) -> int:
     """Scratch bytes of a norm's backward: a function of its sizes."""
     return abi.zero_rmsnorm_backward_workspace(
-        abi.RMSNORM_DESC.pack(rows, cols, cols, cols, cols, abi.ZERO_F32, abi.ZERO_F32, 0.0))
+        _norm_desc(rows, cols, cols, cols, cols, abi.ZERO_F32, abi.ZERO_F32, 0.0))
 
 
 def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -255,9 +276,11 @@ def rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rs
         _given(dweight, "dweight", (cols,), dweight_dtype)
     nbytes = _norm_scratch(rows, cols)
     space = _new(side, nbytes, torch.uint8, device)
-    abi.zero_rmsnorm_backward(abi.RMSNORM_DESC.pack(rows, cols, x_step, r_step, dy_step, code, wcode, 0.0),
-                              dy.data_ptr(), x.data_ptr(), weight.data_ptr(), rstd.data_ptr(), r_ptr, dx.data_ptr(),
-                              dweight.data_ptr(), dcode, space.data_ptr(), nbytes, handle)
+    rc = _library().zero_rmsnorm_backward(_norm_desc(rows, cols, x_step, r_step, dy_step, code, wcode, 0.0),
+                                          dy.data_ptr(), x.data_ptr(), weight.data_ptr(), rstd.data_ptr(), r_ptr,
+                                          dx.data_ptr(), dweight.data_ptr(), dcode, space.data_ptr(), nbytes, handle)
+    if rc:
+        abi._check(rc)
     return dx, dweight
 
 
@@ -287,9 +310,6 @@ def _attention_sizes(q, k, causal, window, key_lengths, scale):
             dim ** -0.5 if scale is None else scale), (batch, k_len, kv_heads, dim)
 
 
-_ZEROS = (0,) * 12
-
-
 def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
                       window: int = 0, key_lengths=None, scale: float | None = None, out=None, lse=None,
                       stream=None):
@@ -308,16 +328,20 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal:
     handle, side = _stream(stream, (q, k, v, key_lengths, out, lse))
     if out is None:
         out = _new(side, shape, dtype, device)
-    ob, ot, oh, _ = _steps(out, "out", shape, dtype)
+        ob, ot, oh, _ = out.stride()
+    else:
+        ob, ot, oh, _ = _steps(out, "out", shape, dtype)
     rows = (sizes[0], sizes[3], sizes[1])
     if lse is None:
         lse = _new(side, rows, _F32, device)
     else:
         _given(lse, "lse", rows, _F32)
-    desc = abi.ATTENTION_DESC.pack(*sizes, qb, qt, qh, kb, kt, kh, vb, vt, vh, ob, ot, oh, *_ZEROS)
-    abi.zero_attention_forward(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                               None if key_lengths is None else key_lengths.data_ptr(), out.data_ptr(),
-                               lse.data_ptr(), handle)
+    rc = _library().zero_attention_forward(
+        _attention_desc(*sizes, qb, qt, qh, kb, kt, kh, vb, vt, vh, ob, ot, oh, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), None if key_lengths is None else key_lengths.data_ptr(),
+        out.data_ptr(), lse.data_ptr(), handle)
+    if rc:
+        abi._check(rc)
     return out, lse
 
 
@@ -326,7 +350,7 @@ def _attention_scratch(batch, q_len, q_heads) -> int:
     """Scratch bytes of attention's backward: a function of the query rows."""
     steps = (max(q_len, 1) * q_heads * 8, q_heads * 8, 8)
     return abi.zero_attention_backward_workspace(
-        abi.ATTENTION_DESC.pack(batch, q_len, q_len, q_heads, q_heads, 8, abi.ZERO_F16, 0, 0, 0, 1.0, *steps * 8))
+        _attention_desc(batch, q_len, q_len, q_heads, q_heads, 8, abi.ZERO_F16, 0, 0, 0, 1.0, *steps * 8))
 
 
 def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -348,20 +372,29 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     handle, side = _stream(stream, (q, k, v, o, dout, lse, key_lengths, dq, dk, dv))
     if dq is None:
         dq = _new(side, shape, dtype, device)
+        dqb, dqt, dqh, _ = dq.stride()
+    else:
+        dqb, dqt, dqh, _ = _steps(dq, "dq", shape, dtype)
     if dk is None:
         dk = _new(side, kv_shape, dtype, device)
+        dkb, dkt, dkh, _ = dk.stride()
+    else:
+        dkb, dkt, dkh, _ = _steps(dk, "dk", kv_shape, dtype)
     if dv is None:
         dv = _new(side, kv_shape, dtype, device)
-    dqb, dqt, dqh, _ = _steps(dq, "dq", shape, dtype)
-    dkb, dkt, dkh, _ = _steps(dk, "dk", kv_shape, dtype)
-    dvb, dvt, dvh, _ = _steps(dv, "dv", kv_shape, dtype)
+        dvb, dvt, dvh, _ = dv.stride()
+    else:
+        dvb, dvt, dvh, _ = _steps(dv, "dv", kv_shape, dtype)
     nbytes = _attention_scratch(batch, q_len, q_heads)
     space = _new(side, nbytes, torch.uint8, device)
-    desc = abi.ATTENTION_DESC.pack(*sizes, qb, qt, qh, kb, kt, kh, vb, vt, vh, ob, ot, oh, gb, gt, gh, dqb, dqt, dqh,
-                                   dkb, dkt, dkh, dvb, dvt, dvh)
-    abi.zero_attention_backward(desc, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                lse.data_ptr(), None if key_lengths is None else key_lengths.data_ptr(),
-                                dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), space.data_ptr(), nbytes, handle)
+    rc = _library().zero_attention_backward(
+        _attention_desc(*sizes, qb, qt, qh, kb, kt, kh, vb, vt, vh, ob, ot, oh, gb, gt, gh, dqb, dqt, dqh,
+                        dkb, dkt, dkh, dvb, dvt, dvh),
+        dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+        None if key_lengths is None else key_lengths.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+        space.data_ptr(), nbytes, handle)
+    if rc:
+        abi._check(rc)
     return dq, dk, dv
 
 

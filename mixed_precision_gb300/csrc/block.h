@@ -97,7 +97,7 @@ struct AttnArgs {
 };
 cudaError_t launch_attention_forward(const AttnArgs& a, cudaStream_t s);
 int64_t attention_backward_bytes(const AttnArgs& a);
-cudaError_t launch_attention_backward(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s);
 
 // The kernels' error words on the current device (bit kErrWaitTimeout): *value
 // |= the word, which is cleared. Each synchronises the stream.

@@ -504,7 +504,9 @@ int zero_attention_backward(const zero_attention_desc* desc, const void* dout, c
   a.dk = dk;
   a.dv = dv;
   a.stats = static_cast<float*>(workspace);
-  cudaError_t e = launch_attention_backward(a, static_cast<cudaStream_t>(stream));
+  int sms;
+  if (int rc = device_sms(&sms)) return rc;
+  cudaError_t e = launch_attention_backward(a, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "attention backward launch");
 }
 

@@ -39,15 +39,18 @@ struct Dq {
   static constexpr uint32_t kDp = 256, kDq = 384;
 };
 
+// A block takes one piece of work after the other (128 query rows of a head): the
+// loads of the next start while the last ends. Pieces with most keys come first;
+// every other round runs backwards, so that the rounds' differences even out.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     k_attn_dq(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-              const __grid_constant__ CUtensorMap map_dq, const AttnArgs a, int q_tiles) {
+              const __grid_constant__ CUtensorMap map_dq, const AttnArgs a, int q_tiles, int pieces) {
   using C = Dq<DP>;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t q_full, k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV], s_full[2],
-      dp_full, dp_empty, ds_full[2], done;
+  __shared__ __align__(8) uint64_t q_full, q_free, k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV],
+      s_full[2], dp_full, dp_empty, ds_full[2], done, dq_free;
   __shared__ uint32_t tmem_slot, abort_word;
   __shared__ float part[2][kTile];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -55,43 +58,60 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                  v_at = k_at + C::kK * C::kTileBytes;
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
-  const int turn = a.by_batch_q(blockIdx.x), bh = blockIdx.x - turn * a.by_batch_q.d;
-  const int qt = q_tiles - 1 - turn;  // most keys first
-  const int b = a.by_q_heads(bh), h = bh - b * a.q_heads, c = a.by_group(h);
-  const int keys = valid_keys(a, b), row0 = qt * kTile;
-  int lo, hi, skip;
-  key_range(a, keys, row0, lo, skip);
-  key_range(a, keys, min(row0 + kTile, (int)a.q_len) - 1, skip, hi);
-  const int first = lo / kTile, n = lo < hi ? (hi + kTile - 1) / kTile - first : 0;
+  struct Piece {
+    int h, b, c, row0, keys, first, n;  // n key tiles from `first`
+  };
+  auto piece = [&](int round, Piece& p) {
+    const int grid = gridDim.x, at = round * grid + (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    if (at >= pieces) return false;
+    const int turn = a.by_batch_q(at), bh = at - turn * a.by_batch_q.d;
+    p.b = a.by_q_heads(bh);
+    p.h = bh - p.b * a.q_heads;
+    p.c = a.by_group(p.h);
+    p.row0 = (q_tiles - 1 - turn) * kTile;
+    p.keys = valid_keys(a, p.b);
+    int lo, hi, skip;
+    key_range(a, p.keys, p.row0, lo, skip);
+    key_range(a, p.keys, min(p.row0 + kTile, (int)a.q_len) - 1, skip, hi);
+    p.first = lo / kTile;
+    p.n = lo < hi ? (hi + kTile - 1) / kTile - p.first : 0;
+    return true;
+  };
 
   // The TMA warp prepares the barriers and starts the first loads before the
   // block's first barrier: TMEM's allocation takes place meanwhile.
-  auto load_k = [&](int j) {  // by one thread
-    const int s = j % C::kK;
+  auto load_k = [&](const Piece& p, int j, int at) {  // by one thread; `at`: tiles loaded before
+    const int s = at % C::kK;
     mbar_arrive_expect_tx(&k_full[s], C::kTileBytes);
-    load_tile<DP>(k_at + s * C::kTileBytes, &map_k, (first + j) * kTile, c, b, &k_full[s]);
+    load_tile<DP>(k_at + s * C::kTileBytes, &map_k, (p.first + j) * kTile, p.c, p.b, &k_full[s]);
   };
-  auto load_v = [&](int j) {
-    const int s = j % C::kV;
+  auto load_v = [&](const Piece& p, int j, int at) {
+    const int s = at % C::kV;
     mbar_arrive_expect_tx(&v_full[s], C::kTileBytes);
-    load_tile<DP>(v_at + s * C::kTileBytes, &map_v, (first + j) * kTile, c, b, &v_full[s]);
+    load_tile<DP>(v_at + s * C::kTileBytes, &map_v, (p.first + j) * kTile, p.c, p.b, &v_full[s]);
   };
-  const int early = min(n, C::kV);  // tiles into slots that nobody has used
+  auto load_q = [&](const Piece& p) {
+    mbar_arrive_expect_tx(&q_full, 2 * C::kTileBytes);
+    load_tile<DP>(q_at, &map_q, p.row0, p.h, p.b, &q_full);
+    load_tile<DP>(do_at, &map_do, p.row0, p.h, p.b, &q_full);
+  };
   if (warp == kTmaWarp && elect_one()) {
     mbar_init(&q_full, 1);
+    mbar_init(&q_free, 1);
     for (int s = 0; s < C::kK; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_empty[s], 1);
     for (int s = 0; s < C::kV; ++s) mbar_init(&v_full[s], 1), mbar_init(&v_empty[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&s_full[s], 1), mbar_init(&ds_full[s], kSoftWarps);
     mbar_init(&dp_full, 1);
     mbar_init(&dp_empty, kSoftWarps);
     mbar_init(&done, 1);
+    mbar_init(&dq_free, kSoftWarps);
     abort_word = 0;
     mbar_init_fence();
-    if (n > 0) {
-      mbar_arrive_expect_tx(&q_full, 2 * C::kTileBytes);
-      load_tile<DP>(q_at, &map_q, row0, h, b, &q_full);
-      load_tile<DP>(do_at, &map_do, row0, h, b, &q_full);
-      for (int j = 0; j < early; ++j) load_k(j), load_v(j);
+    Piece p;
+    if (piece(0, p) && p.n > 0) {
+      load_q(p);
+      load_k(p, 0, 0);
+      load_v(p, 0, 0);
     }
   }
   if (warp == kMmaWarp) {
@@ -106,155 +126,193 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const Waiter wait{&abort_word, &g_attn_bwd_error};
 
   griddep_trigger();
+  Piece p;
   if (warp == kTmaWarp) {
     const uint32_t one = elect_one();
-    int j = early;
-    for (; j < n; ++j) {
-      if (!wait(&k_empty[j % C::kK], (j / C::kK - 1) & 1)) break;
-      if (one) load_k(j);
-      if (!wait(&v_empty[j % C::kV], (j / C::kV - 1) & 1)) break;
-      if (one) load_v(j);
-    }
-    if (j < n) {  // gave up: leave the copies in flight time to land
-      mbar_wait(&q_full, 0, kSpinLimit >> 10);
-      for (int i = max(0, j - C::kK); i <= j; ++i) {
-        mbar_wait(&k_full[i % C::kK], (i / C::kK) & 1, kSpinLimit >> 10);
-        mbar_wait(&v_full[i % C::kV], (i / C::kV) & 1, kSpinLimit >> 10);
-      }
-    }
-  } else if (warp == kMmaWarp) {
-    if (n > 0) {
-      constexpr bool bf16 = !std::is_same<T, __half>::value;
-      constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
-      constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
-      constexpr uint32_t kStep = C::kTileBytes / 16;
-      const uint32_t one = elect_one();
-      const uint64_t q_desc = head_desc(q_at), do_desc = head_desc(do_at), k_desc = head_desc(k_at),
-                     v_desc = head_desc(v_at), k_rows = rows_desc(k_at);
-      auto make_s = [&](int j) {
-        if (!wait(&k_full[j % C::kK], (j / C::kK) & 1)) return false;
-        tc_fence_after();
-        mma_head<DP>(tmem + (j & 1) * kTile, q_desc, k_desc + j % C::kK * kStep, by_head, one);
-        mma_commit(&s_full[j & 1], one);
-        return true;
-      };
-      auto make_dp = [&](int j) {
-        if (!wait(&v_full[j % C::kV], (j / C::kV) & 1)) return false;
-        tc_fence_after();
-        mma_head<DP>(tmem + C::kDp, do_desc, v_desc + j % C::kV * kStep, by_head, one);
-        mma_commit(&dp_full, one);
-        mma_commit(&v_empty[j % C::kV], one);
-        return true;
-      };
-      bool go = wait(&q_full, 0) && make_s(0) && make_dp(0) && (n < 2 || make_s(1));
-#pragma unroll 1
-      for (int j = 0; go && j < n; ++j) {
-        // the next dp as soon as this one has been read, then dq from this ds
-        if (j + 1 < n) {
-          if (!(go = wait(&dp_empty, j & 1))) break;
-          tc_fence_after();
-          if (!(go = make_dp(j + 1))) break;
+    bool go = true;
+    for (int round = 0, at = 0; go && piece(round, p); at += p.n, ++round) {
+      for (int j = round == 0 ? 1 : 0; go && j < p.n; ++j) {
+        // the queries' place is free once the piece before has left from it; its
+        // first key tiles do not wait for that
+        if (j == min(p.n, C::kV) - 1 && round > 0) {
+          if (j == 0) {
+            if (!(go = wait(&k_empty[at % C::kK], (at / C::kK - 1) & 1))) break;
+            if (one) load_k(p, 0, at);
+            if (!(go = wait(&v_empty[at % C::kV], (at / C::kV - 1) & 1))) break;
+            if (one) load_v(p, 0, at);
+          }
+          if (!(go = wait(&q_free, (round - 1) & 1))) break;
+          if (one) load_q(p);
+          if (j == 0) continue;
         }
-        if (!(go = wait(&ds_full[j & 1], (j / 2) & 1))) break;
+        const int t = at + j;
+        if (!(go = wait(&k_empty[t % C::kK], (t / C::kK - 1) & 1))) break;
+        if (one) load_k(p, j, t);
+        if (!(go = wait(&v_empty[t % C::kV], (t / C::kV - 1) & 1))) break;
+        if (one) load_v(p, j, t);
+      }
+      if (go && p.n == 0 && round > 0) go = wait(&q_free, (round - 1) & 1);  // keep its turns in step
+    }
+    if (!go)  // gave up: leave the copies in flight time to land
+      for (int i = 0; i < 64; ++i) mbar_try_wait(&q_free, 0) && mbar_try_wait(&q_free, 1);
+  } else if (warp == kMmaWarp) {
+    constexpr bool bf16 = !std::is_same<T, __half>::value;
+    constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
+    constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
+    constexpr uint32_t kStep = C::kTileBytes / 16;
+    const uint32_t one = elect_one();
+    const uint64_t q_desc = head_desc(q_at), do_desc = head_desc(do_at), k_desc = head_desc(k_at),
+                   v_desc = head_desc(v_at), k_rows = rows_desc(k_at);
+    // t: key tiles since the block's start
+    auto make_s = [&](int t) {
+      if (!wait(&k_full[t % C::kK], (t / C::kK) & 1)) return false;
+      tc_fence_after();
+      mma_head<DP>(tmem + (t & 1) * kTile, q_desc, k_desc + t % C::kK * kStep, by_head, one);
+      mma_commit(&s_full[t & 1], one);
+      return true;
+    };
+    auto make_dp = [&](int t) {
+      if (!wait(&v_full[t % C::kV], (t / C::kV) & 1)) return false;
+      tc_fence_after();
+      mma_head<DP>(tmem + C::kDp, do_desc, v_desc + t % C::kV * kStep, by_head, one);
+      mma_commit(&dp_full, one);
+      mma_commit(&v_empty[t % C::kV], one);
+      return true;
+    };
+    bool go = true;
+    for (int round = 0, at = 0, live = 0; go && piece(round, p); at += p.n, ++round) {
+      if (p.n == 0) continue;
+      // the S and dp of the piece before have been read: its last ds was waited for
+      go = wait(&q_full, live & 1) && make_s(at) && make_dp(at) && (p.n < 2 || make_s(at + 1));
+#pragma unroll 1
+      for (int j = 0; go && j < p.n; ++j) {
+        const int t = at + j;
+        // the next dp as soon as this one has been read, then dq from this ds
+        if (!(go = wait(&dp_empty, t & 1))) break;
         tc_fence_after();
-        mma_rows<kParts>(tmem + C::kDq, tmem + (j & 1) * kTile, k_rows + j % C::kK * kStep, by_rows, j > 0, one);
-        mma_commit(&k_empty[j % C::kK], one);
-        if (j + 2 < n) go = make_s(j + 2);
+        if (j + 1 < p.n && !(go = make_dp(t + 1))) break;
+        if (!(go = wait(&ds_full[t & 1], (t / 2) & 1))) break;
+        if (j == 0 && live > 0 && !(go = wait(&dq_free, (live - 1) & 1))) break;
+        tc_fence_after();
+        mma_rows<kParts>(tmem + C::kDq, tmem + (t & 1) * kTile, k_rows + t % C::kK * kStep, by_rows, j > 0, one);
+        mma_commit(&k_empty[t % C::kK], one);
+        if (j + 2 < p.n) go = make_s(t + 2);
       }
       mma_commit(&done, one);
+      ++live;
     }
   } else {
     // ---- a thread a quarter of a row: columns [32 part, 32 part + 32) of each tile
-    const int quarter = warp / 4, row = (warp & 3) * 32 + lane, i = row0 + row;
+    const int quarter = warp / 4, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const bool live = i < a.q_len;
-    const int64_t at = (b * (int64_t)a.q_heads + h) * a.q_len + i;
-    float delta = 0.0f;
-    if (live && quarter < 2) {  // half the head each
-      const T* o = static_cast<const T*>(a.o_in) + b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2];
-      const T* g = static_cast<const T*>(a.dout) + b * a.dos[0] + (int64_t)i * a.dos[1] + h * a.dos[2];
-      for (int d = quarter * (DP / 2); d < min(a.head_dim, (quarter + 1) * (DP / 2)); d += 8) {
-        float x[8], y[8];
-        widen8(load8_raw(o + d), x);
-        widen8(load8_raw(g + d), y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
-      }
-    }
-    // a row that sees nothing (or is none) gets p = 2^-inf = 0 everywhere
-    const float lse = live ? a.lse_in[at] : -INFINITY;
-    if (quarter < 2) part[quarter][row] = delta;
-    named_sync(1, kSoftThreads);
-    const float minus_delta = -(part[0][row] + part[1][row]), minus_lse = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-    if (quarter == 0) {
-      float* st = a.stats + ((b * (int64_t)a.q_heads + h) * q_tiles + qt) * kStats + row;
-      st[0] = minus_lse;
-      st[kTile] = minus_delta;
-    }
-    key_range(a, keys, i, lo, hi);
     const float scale2 = a.scale * kLog2e;
-    const uint64_t scale_pair = pair(scale2, scale2), lse_pair = pair(minus_lse, minus_lse),
-                   delta_pair = pair(minus_delta, minus_delta);
+    const uint64_t scale_pair = pair(scale2, scale2);
+    // A wait that gives up ends the waits of every later piece too; the barriers
+    // of the softmax warps are passed all the same, so none is left in one.
     bool ok = true;
 #pragma unroll 1
-    for (int j = 0; j < n; ++j) {
-      const uint32_t s_at = tmem + lanes + (j & 1) * kTile + quarter * kCols;
-      if (!(ok = wait(&s_full[j & 1], (j / 2) & 1))) break;
-      tc_fence_after();
-      uint32_t p[kCols];
-      tmem_ld32(s_at, p);
-      tmem_wait_ld();
+    for (int round = 0, at = 0, live = 0; piece(round, p); at += p.n, ++round) {
+      const int i = p.row0 + row;
+      const bool in = i < a.q_len;
+      const int64_t head = p.b * (int64_t)a.q_heads + p.h;
+      float delta = 0.0f;
+      if (in && quarter < 2) {  // half the head each
+        const T* o = static_cast<const T*>(a.o_in) + p.b * a.os[0] + (int64_t)i * a.os[1] + p.h * a.os[2];
+        const T* g = static_cast<const T*>(a.dout) + p.b * a.dos[0] + (int64_t)i * a.dos[1] + p.h * a.dos[2];
+        for (int d = quarter * (DP / 2); d < min(a.head_dim, (quarter + 1) * (DP / 2)); d += 8) {
+          float x[8], y[8];
+          widen8(load8_raw(o + d), x);
+          widen8(load8_raw(g + d), y);
 #pragma unroll
-      for (int k = 0; k < kCols; k += 2) {
-        float x, y;
-        unpair(fma2(pair(__uint_as_float(p[k]), __uint_as_float(p[k + 1])), scale_pair, lse_pair), x, y);
-        p[k] = __float_as_uint(exp2_fast(x));
-        p[k + 1] = __float_as_uint(exp2_fast(y));
+          for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
+        }
       }
-      if (!(ok = wait(&dp_full, j & 1))) break;
+      // a row that sees nothing (or is none) gets p = 2^-inf = 0 everywhere
+      const float lse = in ? a.lse_in[head * a.q_len + i] : -INFINITY;
+      if (quarter < 2) part[quarter][row] = delta;
+      named_sync(1, kSoftThreads);
+      const float minus_delta = -(part[0][row] + part[1][row]),
+                  minus_lse = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+      if (quarter == 0) {
+        float* st = a.stats + (head * q_tiles + p.row0 / kTile) * kStats + row;
+        st[0] = minus_lse;
+        st[kTile] = minus_delta;
+      }
+      int lo, hi;
+      key_range(a, p.keys, i, lo, hi);
+      const uint64_t lse_pair = pair(minus_lse, minus_lse), delta_pair = pair(minus_delta, minus_delta);
+#pragma unroll 1
+      for (int j = 0; ok && j < p.n; ++j) {
+        const int t = at + j;
+        const uint32_t s_at = tmem + lanes + (t & 1) * kTile + quarter * kCols;
+        if (!(ok = wait(&s_full[t & 1], (t / 2) & 1))) break;
+        tc_fence_after();
+        uint32_t e[kCols];
+        tmem_ld32(s_at, e);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < kCols; k += 2) {
+          float x, y;
+          unpair(fma2(pair(__uint_as_float(e[k]), __uint_as_float(e[k + 1])), scale_pair, lse_pair), x, y);
+          e[k] = __float_as_uint(exp2_fast(x));
+          e[k + 1] = __float_as_uint(exp2_fast(y));
+        }
+        if (!(ok = wait(&dp_full, t & 1))) break;
+        tc_fence_after();
+        uint32_t dp[kCols];
+        tmem_ld32(tmem + lanes + C::kDp + quarter * kCols, dp);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&dp_empty);
+#pragma unroll
+        for (int k = 0; k < kCols; k += 2) {
+          float x, y;
+          unpair(mul2(pair(__uint_as_float(e[k]), __uint_as_float(e[k + 1])),
+                      add2(pair(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), delta_pair)),
+                 x, y);
+          e[k] = __float_as_uint(x);
+          e[k + 1] = __float_as_uint(y);
+        }
+        const int key0 = (p.first + j) * kTile + quarter * kCols, from = lo - key0, to = hi - key0;
+        if (__any_sync(0xFFFFFFFFu, from > 0 || to < kCols))  // whatever p and dp are there
+          mask_row(e, seen_bits(from, to), 0u);
+        uint32_t w[kCols / 2];
+#pragma unroll
+        for (int k = 0; k < kCols; k += 2) w[k / 2] = round2<T>(__uint_as_float(e[k]), __uint_as_float(e[k + 1]));
+        tmem_st16(s_at, w);
+        // keys past the length: their ds is zero, and so must be what it meets
+        if (quarter == 0 && p.keys < a.k_len && (p.first + j + 1) * kTile > p.keys) {
+          if ((p.first + j) * kTile + row >= p.keys) zero_row<DP>(smem + (2 + t % C::kK) * C::kTileBytes, row);
+          fence_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ds_full[t & 1]);
+      }
+      if (p.n > 0) {
+        ok = ok && wait(&done, live & 1);
+        ++live;
+      }
       tc_fence_after();
-      uint32_t dp[kCols];
-      tmem_ld32(tmem + lanes + C::kDp + quarter * kCols, dp);
-      tmem_wait_ld();
+      // the tile leaves from the place of its queries, which are done with
+      constexpr int kOut = DP / kParts;
+      stage_row<T, kOut>(smem, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale, p.n == 0);
+      fence_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&dp_empty);
-#pragma unroll
-      for (int k = 0; k < kCols; k += 2) {
-        float x, y;
-        unpair(mul2(pair(__uint_as_float(p[k]), __uint_as_float(p[k + 1])),
-                    add2(pair(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), delta_pair)),
-               x, y);
-        p[k] = __float_as_uint(x);
-        p[k + 1] = __float_as_uint(y);
+      if (lane == 0 && p.n > 0) mbar_arrive(&dq_free);
+      named_sync(1, kSoftThreads);
+      if (warp == 0) {
+        const bool all = __all_sync(0xFFFFFFFFu, ok);
+        if (elect_one()) {
+          if (all) store_tile<DP>(&map_dq, q_at, a.head_dim, p.row0, p.h, p.b);
+          mbar_arrive(&q_free);
+        }
+        __syncwarp();
       }
-      const int key0 = (first + j) * kTile + quarter * kCols, from = lo - key0, to = hi - key0;
-      if (__any_sync(0xFFFFFFFFu, from > 0 || to < kCols)) {  // whatever p and dp are there
-        mask_row(p, seen_bits(from, to), 0u);
-      }
-      uint32_t w[kCols / 2];
-#pragma unroll
-      for (int k = 0; k < kCols; k += 2) w[k / 2] = round2<T>(__uint_as_float(p[k]), __uint_as_float(p[k + 1]));
-      tmem_st16(s_at, w);
-      // keys past the length: their ds is zero, and so must be what it meets
-      if (quarter == 0 && keys < a.k_len && (first + j + 1) * kTile > keys) {
-        if ((first + j) * kTile + row >= keys)
-          zero_row<DP>(smem + (2 + j % C::kK) * C::kTileBytes, row);
-        fence_async_smem();
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ds_full[j & 1]);
     }
-    if (n > 0 && ok) ok = wait(&done, 0);
-    tc_fence_after();
-    // the tile leaves from the place of its queries, which are done with
-    constexpr int kOut = DP / kParts;
-    stage_row<T, kOut>(smem, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale, n == 0);
-    fence_async_smem();
-    named_sync(1, kSoftThreads);
-    if (warp == 0 && __all_sync(0xFFFFFFFFu, ok) && elect_one()) store_tile<DP>(&map_dq, q_at, a.head_dim, row0, h, b);
   }
   tc_fence_before();
   __syncthreads();
@@ -508,7 +566,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 int64_t tiles(int64_t len) { return (len + kTile - 1) / kTile; }
 
 template <typename T, int DP>
-cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+cudaError_t run(const AttnArgs& a, int sms, cudaStream_t s) {
   CUtensorMap q, g, k, v, dq, dk, dv;
   // a side without rows is never loaded, but its maps still have to be valid
   const bool qs = a.q_len > 0, ks = a.k_len > 0;
@@ -522,7 +580,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
       !attn_map(&dv, ks ? a.dv : a.dq, a.dtype, a.dvs, a.batch, k_len, a.kv_heads, a.head_dim))
     return cudaErrorInvalidValue;
   const int64_t q_blocks = tiles(a.q_len) * a.batch * a.q_heads, k_blocks = tiles(a.k_len) * a.batch * a.kv_heads;
-  if (q_blocks > 0x7FFFFFFFll || k_blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  if (q_blocks > 0x70000000ll || k_blocks > 0x70000000ll) return cudaErrorInvalidConfiguration;
   static std::atomic<uint64_t> asked_dq{0}, asked_dkv{0};
   cudaError_t e = allow_smem(k_attn_dq<T, DP>, Dq<DP>::kSmem, asked_dq);
   if (e != cudaSuccess) return e;
@@ -530,7 +588,8 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int q_tiles = (int)tiles(a.q_len);
   if (q_blocks > 0)
-    k_attn_dq<T, DP><<<(unsigned)q_blocks, kBwdThreads, Dq<DP>::kSmem, s>>>(q, g, k, v, dq, a, q_tiles);
+    k_attn_dq<T, DP><<<(unsigned)(q_blocks < sms ? q_blocks : sms), kBwdThreads, Dq<DP>::kSmem, s>>>(
+        q, g, k, v, dq, a, q_tiles, (int)q_blocks);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (k_blocks == 0) return cudaSuccess;
@@ -549,8 +608,8 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t backward_t(const AttnArgs& a, cudaStream_t s) {
-  return a.head_dim <= 64 ? run<T, 64>(a, s) : run<T, 128>(a, s);
+cudaError_t backward_t(const AttnArgs& a, int sms, cudaStream_t s) {
+  return a.head_dim <= 64 ? run<T, 64>(a, sms, s) : run<T, 128>(a, sms, s);
 }
 
 }  // namespace
@@ -561,8 +620,8 @@ int64_t attention_backward_bytes(const AttnArgs& a) {
   return a.batch * a.q_heads * tiles(a.q_len) * kStats * 4;
 }
 
-cudaError_t launch_attention_backward(const AttnArgs& a, cudaStream_t s) {
-  return a.dtype == kF16 ? backward_t<__half>(a, s) : backward_t<__nv_bfloat16>(a, s);
+cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s) {
+  return a.dtype == kF16 ? backward_t<__half>(a, sms, s) : backward_t<__nv_bfloat16>(a, sms, s);
 }
 
 }  // namespace zg
