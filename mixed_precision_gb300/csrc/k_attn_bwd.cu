@@ -34,7 +34,10 @@ template <int DP>
 struct Dq {
   static constexpr int kTileBytes = DP / 64 * kTileChunk;
   static constexpr int kK = 3, kV = 2;  // slots: a K tile is used again two tiles later than it is first
-  static constexpr int kSmem = (2 + kK + kV) * kTileBytes + 1024;
+  // Pieces whose queries are in shared memory: with two, where they fit, the next
+  // piece's first products run while this one's result leaves.
+  static constexpr int kQ = DP == 64 ? 2 : 1;
+  static constexpr int kSmem = (2 * kQ + kK + kV) * kTileBytes + 1024;
   // TMEM: S twice (ds over it), dp, dq
   static constexpr uint32_t kDp = 256, kDq = 384;
 };
@@ -49,12 +52,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               const __grid_constant__ CUtensorMap map_dq, const AttnArgs a, int q_tiles, int pieces) {
   using C = Dq<DP>;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t q_full, q_free, k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV],
+  __shared__ __align__(8) uint64_t q_full[C::kQ], q_free[C::kQ], k_full[C::kK], k_empty[C::kK], v_full[C::kV], v_empty[C::kV],
       s_full[2], dp_full, dp_empty, ds_full[2], done, dq_free;
   __shared__ uint32_t tmem_slot, abort_word;
   __shared__ float part[2][kTile];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  const uint32_t q_at = smem_u32(smem), do_at = q_at + C::kTileBytes, k_at = do_at + C::kTileBytes,
+  // queries and do of kQ pieces, then the K and V slots
+  const uint32_t q_at = smem_u32(smem), k_at = q_at + 2 * C::kQ * C::kTileBytes,
                  v_at = k_at + C::kK * C::kTileBytes;
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
@@ -90,14 +94,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_arrive_expect_tx(&v_full[s], C::kTileBytes);
     load_tile<DP>(v_at + s * C::kTileBytes, &map_v, (p.first + j) * kTile, p.c, p.b, &v_full[s]);
   };
-  auto load_q = [&](const Piece& p) {
-    mbar_arrive_expect_tx(&q_full, 2 * C::kTileBytes);
-    load_tile<DP>(q_at, &map_q, p.row0, p.h, p.b, &q_full);
-    load_tile<DP>(do_at, &map_do, p.row0, p.h, p.b, &q_full);
+  auto load_q = [&](const Piece& p, int s) {
+    mbar_arrive_expect_tx(&q_full[s], 2 * C::kTileBytes);
+    load_tile<DP>(q_at + 2 * s * C::kTileBytes, &map_q, p.row0, p.h, p.b, &q_full[s]);
+    load_tile<DP>(q_at + (2 * s + 1) * C::kTileBytes, &map_do, p.row0, p.h, p.b, &q_full[s]);
   };
   if (warp == kTmaWarp && elect_one()) {
-    mbar_init(&q_full, 1);
-    mbar_init(&q_free, 1);
+    for (int s = 0; s < C::kQ; ++s) mbar_init(&q_full[s], 1), mbar_init(&q_free[s], 1);
     for (int s = 0; s < C::kK; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_empty[s], 1);
     for (int s = 0; s < C::kV; ++s) mbar_init(&v_full[s], 1), mbar_init(&v_empty[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&s_full[s], 1), mbar_init(&ds_full[s], kSoftWarps);
@@ -109,7 +112,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init_fence();
     Piece p;
     if (piece(0, p) && p.n > 0) {
-      load_q(p);
+      load_q(p, 0);
       load_k(p, 0, 0);
       load_v(p, 0, 0);
     }
@@ -131,38 +134,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t one = elect_one();
     bool go = true;
     for (int round = 0, at = 0; go && piece(round, p); at += p.n, ++round) {
+      const int s = round % C::kQ;
+      auto next_q = [&] {  // the place is free once the piece before in it has left
+        go = wait(&q_free[s], (round / C::kQ - 1) & 1);
+        if (go && one && p.n > 0 && round > 0) load_q(p, s);
+      };
+      if (C::kQ > 1 || p.n == 0) next_q();
       for (int j = round == 0 ? 1 : 0; go && j < p.n; ++j) {
-        // the queries' place is free once the piece before has left from it; its
-        // first key tiles do not wait for that
-        if (j == min(p.n, C::kV) - 1 && round > 0) {
-          if (j == 0) {
-            if (!(go = wait(&k_empty[at % C::kK], (at / C::kK - 1) & 1))) break;
-            if (one) load_k(p, 0, at);
-            if (!(go = wait(&v_empty[at % C::kV], (at / C::kV - 1) & 1))) break;
-            if (one) load_v(p, 0, at);
-          }
-          if (!(go = wait(&q_free, (round - 1) & 1))) break;
-          if (one) load_q(p);
-          if (j == 0) continue;
-        }
         const int t = at + j;
         if (!(go = wait(&k_empty[t % C::kK], (t / C::kK - 1) & 1))) break;
         if (one) load_k(p, j, t);
         if (!(go = wait(&v_empty[t % C::kV], (t / C::kV - 1) & 1))) break;
         if (one) load_v(p, j, t);
+        if (C::kQ == 1 && j == 0) next_q();  // the first key tile does not wait for it
       }
-      if (go && p.n == 0 && round > 0) go = wait(&q_free, (round - 1) & 1);  // keep its turns in step
     }
     if (!go)  // gave up: leave the copies in flight time to land
-      for (int i = 0; i < 64; ++i) mbar_try_wait(&q_free, 0) && mbar_try_wait(&q_free, 1);
+      for (int i = 0; i < 64; ++i) mbar_try_wait(&q_free[0], 0) && mbar_try_wait(&q_free[0], 1);
   } else if (warp == kMmaWarp) {
     constexpr bool bf16 = !std::is_same<T, __half>::value;
     constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
     constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
     constexpr uint32_t kStep = C::kTileBytes / 16;
     const uint32_t one = elect_one();
-    const uint64_t q_desc = head_desc(q_at), do_desc = head_desc(do_at), k_desc = head_desc(k_at),
-                   v_desc = head_desc(v_at), k_rows = rows_desc(k_at);
+    const uint64_t k_desc = head_desc(k_at), v_desc = head_desc(v_at), k_rows = rows_desc(k_at);
+    uint64_t q_desc = 0, do_desc = 0;
     // t: key tiles since the block's start
     auto make_s = [&](int t) {
       if (!wait(&k_full[t % C::kK], (t / C::kK) & 1)) return false;
@@ -180,10 +176,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       return true;
     };
     bool go = true;
+    uint32_t turns = 0;  // bit s: the parity of q_full[s]
     for (int round = 0, at = 0, live = 0; go && piece(round, p); at += p.n, ++round) {
       if (p.n == 0) continue;
+      const int s = round % C::kQ;
+      q_desc = head_desc(q_at + 2 * s * C::kTileBytes);
+      do_desc = q_desc + kStep;
+      const uint32_t turn = turns >> s & 1;
+      turns ^= 1u << s;
       // the S and dp of the piece before have been read: its last ds was waited for
-      go = wait(&q_full, live & 1) && make_s(at) && make_dp(at) && (p.n < 2 || make_s(at + 1));
+      go = wait(&q_full[s], turn) && make_s(at) && make_dp(at) && (p.n < 2 || make_s(at + 1));
 #pragma unroll 1
       for (int j = 0; go && j < p.n; ++j) {
         const int t = at + j;
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_st16(s_at, w);
         // keys past the length: their ds is zero, and so must be what it meets
         if (quarter == 0 && p.keys < a.k_len && (p.first + j + 1) * kTile > p.keys) {
-          if ((p.first + j) * kTile + row >= p.keys) zero_row<DP>(smem + (2 + t % C::kK) * C::kTileBytes, row);
+          if ((p.first + j) * kTile + row >= p.keys) zero_row<DP>(smem + (2 * C::kQ + t % C::kK) * C::kTileBytes, row);
           fence_async_smem();
         }
         tmem_wait_st();
@@ -298,7 +300,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_after();
       // the tile leaves from the place of its queries, which are done with
       constexpr int kOut = DP / kParts;
-      stage_row<T, kOut>(smem, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale, p.n == 0);
+      const int slot = round % C::kQ, place = 2 * slot * C::kTileBytes;
+      stage_row<T, kOut>(smem + place, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale, p.n == 0);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -307,8 +310,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (warp == 0) {
         const bool all = __all_sync(0xFFFFFFFFu, ok);
         if (elect_one()) {
-          if (all) store_tile<DP>(&map_dq, q_at, a.head_dim, p.row0, p.h, p.b);
-          mbar_arrive(&q_free);
+          if (all) store_tile<DP>(&map_dq, q_at + place, a.head_dim, p.row0, p.h, p.b);
+          mbar_arrive(&q_free[slot]);
         }
         __syncwarp();
       }
