@@ -133,13 +133,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (warp == kTmaWarp) {
     const uint32_t one = elect_one();
     bool go = true;
-    for (int round = 0, at = 0; go && piece(round, p); at += p.n, ++round) {
-      const int s = round % C::kQ;
+    for (int round = 0, at = 0, live = 0; go && piece(round, p); at += p.n, ++round) {
+      if (p.n == 0) continue;
+      const int s = live % C::kQ;
       auto next_q = [&] {  // the place is free once the piece before in it has left
-        go = wait(&q_free[s], (round / C::kQ - 1) & 1);
-        if (go && one && p.n > 0 && round > 0) load_q(p, s);
+        go = wait(&q_free[s], (live / C::kQ - 1) & 1);
+        if (go && one && round > 0) load_q(p, s);
       };
-      if (C::kQ > 1 || p.n == 0) next_q();
+      if (C::kQ > 1) next_q();
       for (int j = round == 0 ? 1 : 0; go && j < p.n; ++j) {
         const int t = at + j;
         if (!(go = wait(&k_empty[t % C::kK], (t / C::kK - 1) & 1))) break;
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (one) load_v(p, j, t);
         if (C::kQ == 1 && j == 0) next_q();  // the first key tile does not wait for it
       }
+      ++live;
     }
     if (!go)  // gave up: leave the copies in flight time to land
       for (int i = 0; i < 64; ++i) mbar_try_wait(&q_free[0], 0) && mbar_try_wait(&q_free[0], 1);
@@ -176,16 +178,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       return true;
     };
     bool go = true;
-    uint32_t turns = 0;  // bit s: the parity of q_full[s]
     for (int round = 0, at = 0, live = 0; go && piece(round, p); at += p.n, ++round) {
       if (p.n == 0) continue;
-      const int s = round % C::kQ;
+      const int s = live % C::kQ;
       q_desc = head_desc(q_at + 2 * s * C::kTileBytes);
       do_desc = q_desc + kStep;
-      const uint32_t turn = turns >> s & 1;
-      turns ^= 1u << s;
       // the S and dp of the piece before have been read: its last ds was waited for
-      go = wait(&q_full[s], turn) && make_s(at) && make_dp(at) && (p.n < 2 || make_s(at + 1));
+      go = wait(&q_full[s], (live / C::kQ) & 1) && make_s(at) && make_dp(at) && (p.n < 2 || make_s(at + 1));
 #pragma unroll 1
       for (int j = 0; go && j < p.n; ++j) {
         const int t = at + j;
@@ -240,6 +239,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         st[0] = minus_lse;
         st[kTile] = minus_delta;
       }
+      if (p.n == 0) {  // no key is seen; no place in shared memory is its own
+        if (in) {
+          T* dq = static_cast<T*>(a.dq) + p.b * a.dqs[0] + (int64_t)i * a.dqs[1] + p.h * a.dqs[2];
+          for (int d = quarter * (DP / kParts); d < min(a.head_dim, (quarter + 1) * (DP / kParts)); d += 8)
+            *reinterpret_cast<uint4*>(dq + d) = make_uint4(0, 0, 0, 0);
+        }
+        named_sync(1, kSoftThreads);  // the halves' sums have been read
+        continue;
+      }
       int lo, hi;
       key_range(a, p.keys, i, lo, hi);
       const uint64_t lse_pair = pair(minus_lse, minus_lse), delta_pair = pair(minus_delta, minus_delta);
@@ -293,19 +301,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ds_full[t & 1]);
       }
-      if (p.n > 0) {
-        ok = ok && wait(&done, live & 1);
-        ++live;
-      }
+      ok = ok && wait(&done, live & 1);
       tc_fence_after();
       // the tile leaves from the place of its queries, which are done with
       constexpr int kOut = DP / kParts;
-      const int slot = round % C::kQ, place = 2 * slot * C::kTileBytes;
-      stage_row<T, kOut>(smem + place, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale, p.n == 0);
+      const int slot = live % C::kQ, place = 2 * slot * C::kTileBytes;
+      stage_row<T, kOut>(smem + place, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale, false);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0 && p.n > 0) mbar_arrive(&dq_free);
+      if (lane == 0) mbar_arrive(&dq_free);
       named_sync(1, kSoftThreads);
       if (warp == 0) {
         const bool all = __all_sync(0xFFFFFFFFu, ok);
@@ -315,6 +320,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         __syncwarp();
       }
+      ++live;
     }
   }
   tc_fence_before();

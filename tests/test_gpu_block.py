@@ -388,6 +388,28 @@ def test_attention_longer(dtype):
     check_attention(2, 1100, 1300, 3, 1, 96, dtype, window=300, ragged=True)
 
 
+@pytest.mark.parametrize("D", [40, 64, 128])
+@pytest.mark.parametrize("live", [0, 1, 3])
+def test_attention_many_rows_of_which_most_see_nothing(D, live):
+    """Several query tiles for every multiprocessor, with empty ones in runs."""
+    B, Sq, Sk, H = 400, 130, 140, 3
+    q, k, v, do, _ = attention_case(B, Sq, Sk, H, 1, D, BF16, False, 0, False)
+    lengths = torch.zeros(B, dtype=torch.int32, device="cuda")
+    if live:
+        lengths[::live] = torch.randint(1, Sk + 1, (len(range(0, B, live)),), generator=gen(D), device="cuda").int()
+        lengths[100:200] = 0
+    for b in range(B):
+        k[b, int(lengths[b]):] = math.nan
+        v[b, int(lengths[b]):] = math.nan
+    o, lse = block.attention_forward(q, k, v, key_lengths=lengths)
+    out = [torch.full_like(t, math.nan) for t in (q, k, v)]
+    block.attention_backward(do, q, k, v, o, lse, key_lengths=lengths, dq=out[0], dk=out[1], dv=out[2])
+    want = ref.attention_backward(do, q, k, v, o, lse, False, 0, lengths, D ** -0.5)
+    for got, name in zip(out, ("dq", "dk", "dv")):
+        ref.close(got, *want[name], name)
+    block.check()
+
+
 def test_attention_scale_and_large_logits():
     check_attention(1, 200, 200, 2, 2, 64, BF16, causal=True, scale=1.0)  # logits of +-50: near one-hot rows
     check_attention(1, 200, 200, 2, 2, 64, BF16, causal=True, scale=1e-4)
