@@ -95,7 +95,7 @@ struct AttnArgs {
   float* stats;  // backward: the rows' statistics (k_attn_bwd.cu)
   Divide by_group, by_kv_heads, by_q_heads, by_batch_kv, by_batch_q;  // batch x heads
 };
-cudaError_t launch_attention_forward(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attention_forward(const AttnArgs& a, int sms, cudaStream_t s);
 int64_t attention_backward_bytes(const AttnArgs& a);
 cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s);
 

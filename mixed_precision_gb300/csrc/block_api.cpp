@@ -454,7 +454,9 @@ int zero_attention_forward(const zero_attention_desc* desc, const void* q, const
   a.lengths = key_lengths;
   a.o = o;
   a.lse = lse;
-  cudaError_t e = launch_attention_forward(a, static_cast<cudaStream_t>(stream));
+  int sms;
+  if (int rc = device_sms(&sms)) return rc;
+  cudaError_t e = launch_attention_forward(a, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "attention forward launch");
 }
 

@@ -42,68 +42,85 @@ struct Fwd {
   static constexpr uint32_t kO = 256;  // TMEM: S_0, S_1 at 0, 128; O_0, O_1 from here, DP columns each
 };
 
+// A block takes one piece of work after the other: while a piece's result leaves,
+// the next one's keys and values arrive, and its first products start as soon as
+// its queries are there. Pieces with most keys come first; every other round runs
+// backwards, so that the rounds' differences even out. Pieces that see no key
+// touch no barrier and no shared memory: slots and phases count the others.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     k_attn_fwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o, const AttnArgs a,
-               int q_tiles, int pairs) {
+               int units, int pairs, int pieces) {
   using C = Fwd<DP>;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t q_full, kv_full[C::kSlots], kv_empty[C::kSlots], s_full[2], p_full[2], o_full;
+  __shared__ __align__(8) uint64_t q_full[2], q_free[2], kv_full[C::kSlots], kv_empty[C::kSlots], s_full[2], p_full[2],
+      o_full[2], o_free[2];
   __shared__ uint32_t tmem_slot, abort_word;
   __shared__ float tops[2][2][2][kTile];  // [turn][tile][half][row]: maxima, in the end sums
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem), ring = base + 2 * C::kTileBytes;
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
-  // blocks of the last query rows (most keys under a causal mask) come first
-  const int turn = a.by_batch_kv(blockIdx.x), bh = blockIdx.x - turn * a.by_batch_kv.d, p = pairs - 1 - turn;
-  const int b = a.by_kv_heads(bh), c = bh - b * a.kv_heads;
-  const int units = q_tiles * a.group;
-  const bool two = 2 * p + 1 < units;
-  const int keys = valid_keys(a, b);
-  int first = 0x7FFFFFFF, last = 0;  // key tiles [first, last) that either tile sees
-  for (int t = 0; t < (two ? 2 : 1); ++t) {
-    const int row0 = a.by_group(2 * p + t) * kTile, row1 = min(row0 + kTile, (int)a.q_len) - 1;
-    int lo, hi, skip;
-    key_range(a, keys, row0, lo, skip);
-    key_range(a, keys, row1, skip, hi);
-    if (lo < hi) {
-      first = min(first, lo / kTile);
-      last = max(last, (hi + kTile - 1) / kTile);
+  struct Piece {
+    int b, c, u, tiles, keys, first, n;  // query tiles (units) u ... and n key tiles from `first`
+  };
+  auto piece = [&](int round, Piece& w) {
+    const int grid = gridDim.x, at = round * grid + (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    if (at >= pieces) return false;
+    const int turn = a.by_batch_kv(at), bh = at - turn * a.by_batch_kv.d;
+    w.b = a.by_kv_heads(bh);
+    w.c = bh - w.b * a.kv_heads;
+    w.u = 2 * (pairs - 1 - turn);
+    w.tiles = min(2, units - w.u);
+    w.keys = valid_keys(a, w.b);
+    int last = 0;  // key tiles [first, last) that one of the query tiles sees
+    w.first = 0x7FFFFFFF;
+    for (int t = 0; t < w.tiles; ++t) {
+      const int row0 = a.by_group(w.u + t) * kTile, row1 = min(row0 + kTile, (int)a.q_len) - 1;
+      int lo, hi, skip;
+      key_range(a, w.keys, row0, lo, skip);
+      key_range(a, w.keys, row1, skip, hi);
+      if (lo < hi) {
+        w.first = min(w.first, lo / kTile);
+        last = max(last, (hi + kTile - 1) / kTile);
+      }
     }
-  }
-  const int n = max(0, last - first);
+    w.n = max(0, last - w.first);
+    return true;
+  };
 
   // The TMA warp prepares the barriers and starts the first loads before the
   // block's first barrier: TMEM's allocation takes place meanwhile.
-  auto load = [&](int i) {  // K and V tiles in turn, by one thread
-    const int s = i % C::kSlots;
+  auto load = [&](const Piece& w, int i, int at) {  // K and V tiles in turn, by one thread; `at`: loads before
+    const int s = (at + i) % C::kSlots;
     mbar_arrive_expect_tx(&kv_full[s], C::kTileBytes);
-    load_tile<DP>(ring + s * C::kTileBytes, i & 1 ? &map_v : &map_k, (first + i / 2) * kTile, c, b, &kv_full[s]);
+    load_tile<DP>(ring + s * C::kTileBytes, i & 1 ? &map_v : &map_k, (w.first + i / 2) * kTile, w.c, w.b, &kv_full[s]);
   };
-  const int early = min(2 * n, C::kSlots);  // loads into slots that nobody has used
+  auto load_q = [&](const Piece& w, int t) {
+    mbar_arrive_expect_tx(&q_full[t], C::kTileBytes);
+    load_tile<DP>(base + t * C::kTileBytes, &map_q, a.by_group(w.u + t) * kTile, w.c * a.group + a.by_group.mod(w.u + t),
+                  w.b, &q_full[t]);
+  };
   if (warp == kTmaWarp && elect_one()) {
-    mbar_init(&q_full, 1);
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&q_full[t], 1);
+      mbar_init(&q_free[t], 1);
       mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t], 8);
+      mbar_init(&o_full[t], 1);
+      mbar_init(&o_free[t], 8);
     }
-    mbar_init(&o_full, 1);
     abort_word = 0;
     mbar_init_fence();
-    if (n > 0) {
-      mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * C::kTileBytes);
-      for (int t = 0; t < (two ? 2 : 1); ++t) {
-        const int u = 2 * p + t;
-        load_tile<DP>(base + t * C::kTileBytes, &map_q, a.by_group(u) * kTile, c * a.group + a.by_group.mod(u), b,
-                      &q_full);
-      }
-      for (int i = 0; i < early; ++i) load(i);
+    Piece w;
+    if (piece(0, w) && w.n > 0) {
+      for (int t = 0; t < w.tiles; ++t) load_q(w, t);
+      for (int i = 0; i < min(2 * w.n, C::kSlots); ++i) load(w, i, 0);
     }
   }
   if (warp == kMmaWarp) {
@@ -119,75 +136,119 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   if (warp >= kTmaWarp) fewer_registers<kOtherRegs>();
   else more_registers<kSoftmaxRegs>();
+  // Counted over the pieces with keys: `at` K and V tiles, done[t] pieces of
+  // query tile t, steps[t] its key tiles.
+  Piece w;
   if (warp == kTmaWarp) {
-    // ---- TMA: K and V tiles
     const uint32_t one = elect_one();
-    int i = early;
-    for (; i < 2 * n; ++i) {
-      if (!wait(&kv_empty[i % C::kSlots], (i / C::kSlots - 1) & 1)) break;
-      if (one) load(i);
+    int done[2] = {0, 0}, at = 0;
+    bool go = true;
+    for (int round = 0; go && piece(round, w); ++round) {
+      if (w.n == 0) continue;
+      const int early = min(2 * w.n, C::kSlots);
+      for (int i = round == 0 ? early : 0; go && i < 2 * w.n; ++i) {
+        if (!(go = wait(&kv_empty[(at + i) % C::kSlots], ((at + i) / C::kSlots - 1) & 1))) break;
+        if (one) load(w, i, at);
+        if (i != early - 1) continue;
+        // the queries' places are free once the results before have left
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (t < w.tiles && go && (go = wait(&q_free[t], (done[t] - 1) & 1)) && one) load_q(w, t);
+      }
+      at += 2 * w.n;
+      ++done[0];
+      done[1] += w.tiles - 1;
     }
-    if (i < 2 * n) {  // gave up: leave the copies in flight time to land
-      mbar_wait(&q_full, 0, kSpinLimit >> 10);
-      for (int k = max(0, i - C::kSlots); k < i; ++k)
-        mbar_wait(&kv_full[k % C::kSlots], (k / C::kSlots) & 1, kSpinLimit >> 10);
-    }
+    if (!go)  // gave up: leave the copies in flight time to land
+      for (int i = 0; i < 64; ++i) mbar_try_wait(&q_free[0], 0) && mbar_try_wait(&q_free[0], 1);
   } else if (warp == kMmaWarp) {
     // ---- the tensor cores
-    if (n > 0) {
-      constexpr bool bf16 = !std::is_same<T, __half>::value;
-      constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
-      constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
-      const int tiles = two ? 2 : 1;
-      const uint32_t one = elect_one();
-      const uint64_t q_desc = head_desc(base), k_desc = head_desc(ring), v_desc = rows_desc(ring);
-      auto slot = [&](int i) { return static_cast<uint32_t>(i % C::kSlots * (C::kTileBytes / 16)); };
-      auto arrived = [&](int i) {
-        const bool ok = wait(&kv_full[i % C::kSlots], (i / C::kSlots) & 1);
+    constexpr bool bf16 = !std::is_same<T, __half>::value;
+    constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
+    constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
+    const uint32_t one = elect_one();
+    const uint64_t q_desc = head_desc(base), k_desc = head_desc(ring), v_desc = rows_desc(ring);
+    auto slot = [&](int i) { return static_cast<uint32_t>(i % C::kSlots * (C::kTileBytes / 16)); };
+    auto arrived = [&](int i) {
+      const bool ok = wait(&kv_full[i % C::kSlots], (i / C::kSlots) & 1);
+      tc_fence_after();
+      return ok;
+    };
+    auto make_s = [&](int t, int i) {
+      mma_head<DP>(tmem + t * kTile, q_desc + t * (C::kTileBytes / 16), k_desc + slot(i), by_head, one);
+      mma_commit(&s_full[t], one);
+    };
+    uint32_t done[2] = {0, 0}, steps[2] = {0, 0};
+    int at = 0;
+    bool go = true;
+    for (int round = 0; go && piece(round, w); ++round) {
+      if (w.n == 0) continue;
+      go = arrived(at);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t >= w.tiles || !go) break;
+        if (!(go = wait(&q_full[t], done[t] & 1))) break;
         tc_fence_after();
-        return ok;
-      };
-      auto make_s = [&](int t, int i) {
-        mma_head<DP>(tmem + t * kTile, q_desc + t * (C::kTileBytes / 16), k_desc + slot(i), by_head, one);
-        mma_commit(&s_full[t], one);
-      };
-      bool go = wait(&q_full, 0) && arrived(0);
-      for (int t = 0; go && t < tiles; ++t) make_s(t, 0);
-      if (go) mma_commit(&kv_empty[0], one);
+        make_s(t, at);
+      }
+      if (go) mma_commit(&kv_empty[at % C::kSlots], one);
 #pragma unroll 1
-      for (int j = 0; go && j < n; ++j) {
-        const int kn = 2 * j + 2, v = 2 * j + 1;
-        const bool more = j + 1 < n;
+      for (int j = 0; go && j < w.n; ++j) {
+        const int kn = at + 2 * j + 2, v = at + 2 * j + 1;
+        const bool more = j + 1 < w.n;
         go = arrived(v);
-#pragma unroll 1
-        for (int t = 0; go && t < tiles; ++t) {
-          if (!(go = wait(&p_full[t], j & 1))) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t >= w.tiles || !go) break;
+          if (!(go = wait(&p_full[t], (steps[t] + j) & 1))) break;
+          if (j == 0 && done[t] > 0 && !(go = wait(&o_free[t], (done[t] - 1) & 1))) break;
           tc_fence_after();
           mma_rows<2>(tmem + C::kO + t * DP, tmem + t * kTile, v_desc + slot(v), by_rows, j > 0, one);
-          if (t == tiles - 1) mma_commit(&kv_empty[v % C::kSlots], one);
-          if (!more) continue;
+          if (t == w.tiles - 1) mma_commit(&kv_empty[v % C::kSlots], one);
+          if (!more) {
+            mma_commit(&o_full[t], one);
+            continue;
+          }
           if (t == 0 && !(go = arrived(kn))) break;
           make_s(t, kn);  // over P_t, which the product before it reads first
-          if (t == tiles - 1) mma_commit(&kv_empty[kn % C::kSlots], one);
+          if (t == w.tiles - 1) mma_commit(&kv_empty[kn % C::kSlots], one);
         }
       }
-      mma_commit(&o_full, one);
+      at += 2 * w.n;
+      ++done[0];
+      steps[0] += w.n;
+      if (w.tiles == 2) ++done[1], steps[1] += w.n;
     }
   } else if (warp < kTmaWarp) {
     // ---- softmax: a thread half a row, keys [64 half, 64 half + 64) of each tile
-    const int t = warp / 8, half = warp / 4 & 1, u = 2 * p + t, row = (warp & 3) * 32 + lane;
+    const int t = warp / 8, half = warp / 4 & 1, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_at = tmem + lanes + t * kTile + half * 64, o_at = tmem + lanes + C::kO + t * DP + half * (DP / 2);
-    const int row0 = a.by_group(u) * kTile, i = row0 + row;  // the query
-    const int64_t h = c * a.group + a.by_group.mod(u);
     const float scale2 = a.scale * kLog2e;
-    float top = -INFINITY, total = 0.0f;
     bool ok = true;
-    if (t == 0 || two) {
+    uint32_t done = 0, steps = 0;  // of this tile
+    int at = 0;
+#pragma unroll 1
+    for (int round = 0; piece(round, w); at += 2 * w.n, ++round) {
+      if (t >= w.tiles) continue;
+      const int keys = w.keys, first = w.first, n = w.n;
+      const int row0 = a.by_group(w.u + t) * kTile, i = row0 + row;  // the query
+      const int h = w.c * a.group + a.by_group.mod(w.u + t);
+      float* lse = a.lse + (w.b * (int64_t)a.q_heads + h) * a.q_len + i;
+      if (n == 0) {
+        if (i < a.q_len) {
+          T* o = static_cast<T*>(a.o) + w.b * a.os[0] + (int64_t)i * a.os[1] + h * a.os[2];
+          for (int d = half * (DP / 2); d < min(a.head_dim, (half + 1) * (DP / 2)); d += 8)
+            *reinterpret_cast<uint4*>(o + d) = make_uint4(0, 0, 0, 0);
+          if (half == 0) *lse = -INFINITY;
+        }
+        continue;
+      }
+      float top, total = 0.0f;
       int lo, hi;
       key_range(a, keys, i, lo, hi);
-      if (n > 0) {  // nothing to go by yet: the first tile's maximum
-        ok = wait(&s_full[t], 0);
+      {  // nothing to go by yet: the first tile's maximum
+        ok = wait(&s_full[t], steps & 1) && ok;
         tc_fence_after();
         const int from = lo - first * kTile - half * 64, to = hi - first * kTile - half * 64;
         float m = -INFINITY;
@@ -208,7 +269,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int j = 0; j < n; ++j) {
         // a wait that gives up goes on to the barriers with what is there: the
         // other half may be waiting in them
-        ok = wait(&s_full[t], j & 1) && ok;
+        ok = wait(&s_full[t], (steps + j) & 1) && ok;
         tc_fence_after();
         const int key0 = (first + j) * kTile, from = lo - key0 - half * 64, to = hi - key0 - half * 64;
         // columns [from, to) are seen; most tiles need no mask
@@ -273,8 +334,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (t == 0 && half == 0 && key0 + kTile > keys && keys < a.k_len) {
           // rows of V past the length: zeros. Tile 0's product is the first to
           // read them, and waits for this thread.
-          ok = wait(&kv_full[(2 * j + 1) % C::kSlots], ((2 * j + 1) / C::kSlots) & 1) && ok;
-          if (key0 + row >= keys) zero_row<DP>(smem + (2 + (2 * j + 1) % C::kSlots) * C::kTileBytes, row);
+          const int v = at + 2 * j + 1;
+          ok = wait(&kv_full[v % C::kSlots], (v / C::kSlots) & 1) && ok;
+          if (key0 + row >= keys) zero_row<DP>(smem + (2 + v % C::kSlots) * C::kTileBytes, row);
           fence_async_smem();
         }
         tmem_wait_st();
@@ -282,25 +344,33 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[t]);
       }
-      if (n > 0) ok = wait(&o_full, 0) && ok;
+      ok = wait(&o_full[t], done & 1) && ok;
       tc_fence_after();
       // both halves' sums, in the order of the keys
-      named_sync(1 + t, 256);
       tops[0][t][half][row] = total;
-      named_sync(1 + t, 256);
+      named_sync(3 + warp / 8 * 4 + (warp & 3), 64);
       total = tops[0][t][0][row] + tops[0][t][1][row];
       const bool none = total == 0.0f;  // no key seen (a seen key gives at least 2^-8 ... or NaN)
       const float inv = none ? 0.0f : 1.0f / total;
       // `none` may differ between the lanes of a warp: their sums are zeros.
       // The tile leaves from the place of its queries, which are done with.
-      stage_row<T, DP / 2>(smem + t * C::kTileBytes, row, half * (DP / 2), o_at, inv, n == 0);
+      stage_row<T, DP / 2>(smem + t * C::kTileBytes, row, half * (DP / 2), o_at, inv, false);
       fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[t]);
+      if (half == 0 && i < a.q_len && ok) *lse = none ? -INFINITY : (top * scale2 + log2f(total)) * kLn2;
       named_sync(1 + t, 256);
-      if ((warp & 7) == 0 && __all_sync(0xFFFFFFFFu, ok) && elect_one())
-        store_tile<DP>(&map_o, base + t * C::kTileBytes, a.head_dim, row0, (int)h, b);
-      if (half == 0 && i < a.q_len && ok)
-        a.lse[(b * (int64_t)a.q_heads + h) * a.q_len + i] =
-            none ? -INFINITY : (top * scale2 + log2f(total)) * kLn2;
+      if ((warp & 7) == 0) {
+        const bool all = __all_sync(0xFFFFFFFFu, ok);
+        if (elect_one()) {
+          if (all) store_tile<DP>(&map_o, base + t * C::kTileBytes, a.head_dim, row0, h, w.b);
+          mbar_arrive(&q_free[t]);
+        }
+        __syncwarp();
+      }
+      ++done;
+      steps += n;
     }
   }
   tc_fence_before();
@@ -312,7 +382,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }
 
 template <typename T, int DP>
-cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+cudaError_t run(const AttnArgs& a, int sms, cudaStream_t s) {
   using C = Fwd<DP>;
   CUtensorMap q, k, v, o;
   // without keys nothing is loaded, but the maps still have to be valid
@@ -324,25 +394,26 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const int64_t q_tiles = (a.q_len + kTile - 1) / kTile, pairs = (q_tiles * a.group + 1) / 2;
   const int64_t blocks = pairs * a.batch * a.kv_heads;
-  if (blocks > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
+  if (blocks > 0x70000000ll) return cudaErrorInvalidConfiguration;
   static std::atomic<uint64_t> asked{0};
   cudaError_t e = allow_smem(k_attn_fwd<T, DP>, C::kSmem, asked);
   if (e != cudaSuccess) return e;
-  k_attn_fwd<T, DP><<<(unsigned)blocks, kFwdThreads, C::kSmem, s>>>(q, k, v, o, a, (int)q_tiles, (int)pairs);
+  k_attn_fwd<T, DP><<<(unsigned)(blocks < sms ? blocks : sms), kFwdThreads, C::kSmem, s>>>(
+      q, k, v, o, a, (int)(q_tiles * a.group), (int)pairs, (int)blocks);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t forward_t(const AttnArgs& a, cudaStream_t s) {
-  return a.head_dim <= 64 ? run<T, 64>(a, s) : run<T, 128>(a, s);
+cudaError_t forward_t(const AttnArgs& a, int sms, cudaStream_t s) {
+  return a.head_dim <= 64 ? run<T, 64>(a, sms, s) : run<T, 128>(a, sms, s);
 }
 
 }  // namespace
 
 ZG_ERROR_WORD(attn_fwd_error, g_attn_fwd_error)
 
-cudaError_t launch_attention_forward(const AttnArgs& a, cudaStream_t s) {
-  return a.dtype == kF16 ? forward_t<__half>(a, s) : forward_t<__nv_bfloat16>(a, s);
+cudaError_t launch_attention_forward(const AttnArgs& a, int sms, cudaStream_t s) {
+  return a.dtype == kF16 ? forward_t<__half>(a, sms, s) : forward_t<__nv_bfloat16>(a, sms, s);
 }
 
 }  // namespace zg

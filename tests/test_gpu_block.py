@@ -390,9 +390,10 @@ def test_attention_longer(dtype):
 
 @pytest.mark.parametrize("D", [40, 64, 128])
 @pytest.mark.parametrize("live", [0, 1, 3])
-def test_attention_many_rows_of_which_most_see_nothing(D, live):
+@pytest.mark.parametrize("Sq", [130, 100])
+def test_attention_many_rows_of_which_most_see_nothing(D, live, Sq):
     """Several query tiles for every multiprocessor, with empty ones in runs."""
-    B, Sq, Sk, H = 400, 130, 140, 3
+    B, Sk, H = 400, 140, 3
     q, k, v, do, _ = attention_case(B, Sq, Sk, H, 1, D, BF16, False, 0, False)
     lengths = torch.zeros(B, dtype=torch.int32, device="cuda")
     if live:
@@ -401,7 +402,11 @@ def test_attention_many_rows_of_which_most_see_nothing(D, live):
     for b in range(B):
         k[b, int(lengths[b]):] = math.nan
         v[b, int(lengths[b]):] = math.nan
-    o, lse = block.attention_forward(q, k, v, key_lengths=lengths)
+    o, lse = torch.full_like(q, math.nan), torch.full((B, H, Sq), math.nan, device="cuda")
+    block.attention_forward(q, k, v, key_lengths=lengths, out=o, lse=lse)
+    ro, rl, to, tl = ref.attention_forward(q, k, v, False, 0, lengths, D ** -0.5)
+    ref.close(lse, rl, tl, "lse")
+    ref.close(o, ro, to, "o")
     out = [torch.full_like(t, math.nan) for t in (q, k, v)]
     block.attention_backward(do, q, k, v, o, lse, key_lengths=lengths, dq=out[0], dk=out[1], dv=out[2])
     want = ref.attention_backward(do, q, k, v, o, lse, False, 0, lengths, D ** -0.5)
