@@ -144,24 +144,22 @@ __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
 // written straight to global memory would touch 32 lines an instruction (3.5 us
 // a block); a tile leaves by one bulk store. The whole warp calls it.
 template <typename T, int N>
-__device__ __forceinline__ void stage_row(uint8_t* tile, int row, int col0, uint32_t addr, float f, bool zero) {
+__device__ __forceinline__ void stage_row(uint8_t* tile, int row, int col0, uint32_t addr, float f) {
   constexpr int kStep = N % 32 == 0 ? 32 : 16;
 #pragma unroll 1
   for (int k = 0; k < N; k += kStep) {
     uint32_t o[kStep];
-    if (!zero) {
-      if constexpr (kStep == 32)
-        tmem_ld32(addr + k, o);
-      else
-        tmem_ld16(addr + k, o);
-      tmem_wait_ld();
-    }
+    if constexpr (kStep == 32)
+      tmem_ld32(addr + k, o);
+    else
+      tmem_ld16(addr + k, o);
+    tmem_wait_ld();
 #pragma unroll
     for (int g = 0; g < kStep / 8; ++g) {
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        w[e] = zero ? 0u : round2<T>(__uint_as_float(o[g * 8 + 2 * e]) * f, __uint_as_float(o[g * 8 + 2 * e + 1]) * f);
+        w[e] = round2<T>(__uint_as_float(o[g * 8 + 2 * e]) * f, __uint_as_float(o[g * 8 + 2 * e + 1]) * f);
       const int piece = (col0 + k) / 8 + g;
       *reinterpret_cast<uint4*>(tile + piece / 8 * kTileChunk + row * 128 + (piece % 8 ^ (row & 7)) * 16) =
           make_uint4(w[0], w[1], w[2], w[3]);
@@ -177,6 +175,21 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* map, uint32_t src,
   for (int i = 0; i < DP / 64; ++i)
     if (i * 64 < dim) tma_store4(map, src + i * kTileChunk, i * 64, token, head, batch);
   tma_store_done();
+}
+
+// Blocks for `pieces` of work: one a multiprocessor, each with its share of the
+// pieces, or with key lengths and less than four pieces a multiprocessor one a
+// piece. A block that goes on to its next piece overlaps that one's start with
+// this one's end, but the shares are fixed, and lengths unknown to the host may
+// make them unequal; blocks of one piece start wherever one has ended. With
+// random lengths, shares against single pieces:
+//   6 x 1021, 12/4 heads of 64, window 256   forward 22.9, 17.8 us; backward 41.6, 38.3
+//   2 x 4096, 16/8 heads of 128, causal      forward 62.0, 57.3 us; backward 225, 207
+//   16 x 2048, 16/8 heads of 128, causal     forward 188, 191 us
+//   32 x 1024, 16/4 heads of 64, causal      forward 119, 131 us
+inline unsigned attn_grid(const AttnArgs& a, int64_t pieces, int sms) {
+  const bool single = pieces < sms || (a.lengths != nullptr && pieces < 4ll * sms);
+  return static_cast<unsigned>(single ? pieces : sms);
 }
 
 // Maps of a [batch, token, head, dim] tensor for tiles of 128 tokens x 64.

@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // the tile leaves from the place of its queries, which are done with
       constexpr int kOut = DP / kParts;
       const int slot = live % C::kQ, place = 2 * slot * C::kTileBytes;
-      stage_row<T, kOut>(smem + place, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale, false);
+      stage_row<T, kOut>(smem + place, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -344,17 +344,21 @@ struct Dkv {
   static constexpr uint32_t kDp = 128, kDv = 256, kDk = 384;
 };
 
+// As k_attn_dq, a block takes one piece after the other (128 keys of a key head).
+// The next piece's keys and values load after the last products that read
+// these; its first S and dp run while dk and dv leave through the places of the
+// last query tile.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     k_attn_dkv(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
                const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                const __grid_constant__ CUtensorMap map_dk, const __grid_constant__ CUtensorMap map_dv,
-               const AttnArgs a, int q_tiles) {
+               const AttnArgs a, int q_tiles, int pieces) {
   using C = Dkv<DP>;
   constexpr int kS = C::kSlots;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t kv_full, q_full[kS], q_empty[kS], do_full[kS], do_empty[kS], s_full, dp_full, p_full,
-      ds_full, done;
+  __shared__ __align__(8) uint64_t kv_full, kv_free, q_full[kS], q_empty[kS], do_full[kS], do_empty[kS], s_full, dp_full,
+      p_full, ds_full, done, sums_free, out_free[2];
   __shared__ uint32_t tmem_slot, abort_word;
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t k_at = smem_u32(smem), v_at = k_at + C::kTileBytes, q_at = v_at + C::kTileBytes,
@@ -362,34 +366,51 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   float* stats = reinterpret_cast<float*>(smem + (2 + 2 * kS) * C::kTileBytes);
   const int warp = warp_number(), lane = threadIdx.x & 31;
 
-  const int kt = a.by_batch_kv(blockIdx.x), bc = blockIdx.x - kt * a.by_batch_kv.d;  // most queries first
-  const int b = a.by_kv_heads(bc), c = bc - b * a.kv_heads;
-  const int keys = valid_keys(a, b), key0 = kt * kTile, off = (int)(a.k_len - a.q_len);
-  // query tiles [first, last) that see one of the tile's valid keys
-  int first = 0, last = q_tiles;
-  if (a.causal) first = max(0, key0 - off) / kTile;
-  if (a.window > 0) {
-    const int end = min(key0 + kTile, keys) - 1 - off + (int)a.window;  // queries before this
-    last = min(last, end <= 0 ? 0 : (end + kTile - 1) / kTile);
-  }
-  const int span = key0 < keys ? max(0, last - first) : 0, n = span * a.group;
+  struct Piece {
+    int b, c, key0, keys, first, span, n;  // query tiles first ... first + span of each head: n items
+  };
+  const int off = (int)(a.k_len - a.q_len);
+  auto piece = [&](int round, Piece& p) {
+    const int grid = gridDim.x, at = round * grid + (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    if (at >= pieces) return false;
+    const int kt = a.by_batch_kv(at), bc = at - kt * a.by_batch_kv.d;  // most queries first
+    p.b = a.by_kv_heads(bc);
+    p.c = bc - p.b * a.kv_heads;
+    p.keys = valid_keys(a, p.b);
+    p.key0 = kt * kTile;
+    // query tiles [first, last) that see one of the tile's valid keys
+    int last = q_tiles;
+    p.first = a.causal ? max(0, p.key0 - off) / kTile : 0;
+    if (a.window > 0) {
+      const int end = min(p.key0 + kTile, p.keys) - 1 - off + (int)a.window;  // queries before this
+      last = min(last, end <= 0 ? 0 : (end + kTile - 1) / kTile);
+    }
+    p.span = p.key0 < p.keys ? max(0, last - p.first) : 0;
+    p.n = p.span * a.group;
+    return true;
+  };
 
-  // item i: query tile first + i % span of the group's head i / span
-  auto load_q = [&](int i) {  // with the tile's statistics; by one thread
-    const int s = i % kS, g = i / span, h = c * a.group + g, qt = first + i - g * span;
+  // item i: query tile first + i % span of the group's head i / span; `at`: items before
+  auto load_q = [&](const Piece& p, int i, int at) {  // with the tile's statistics; by one thread
+    const int s = (at + i) % kS, g = i / p.span, h = p.c * a.group + g, qt = p.first + i - g * p.span;
     mbar_arrive_expect_tx(&q_full[s], C::kTileBytes + kStats * 4);
-    load_tile<DP>(q_at + s * C::kTileBytes, &map_q, qt * kTile, h, b, &q_full[s]);
-    bulk_g2s(stats + s * kStats, a.stats + ((b * (int64_t)a.q_heads + h) * q_tiles + qt) * kStats, kStats * 4,
+    load_tile<DP>(q_at + s * C::kTileBytes, &map_q, qt * kTile, h, p.b, &q_full[s]);
+    bulk_g2s(stats + s * kStats, a.stats + ((p.b * (int64_t)a.q_heads + h) * q_tiles + qt) * kStats, kStats * 4,
              &q_full[s]);
   };
-  auto load_do = [&](int i) {
-    const int s = i % kS, g = i / span, h = c * a.group + g, qt = first + i - g * span;
+  auto load_do = [&](const Piece& p, int i, int at) {
+    const int s = (at + i) % kS, g = i / p.span, h = p.c * a.group + g, qt = p.first + i - g * p.span;
     mbar_arrive_expect_tx(&do_full[s], C::kTileBytes);
-    load_tile<DP>(do_at + s * C::kTileBytes, &map_do, qt * kTile, h, b, &do_full[s]);
+    load_tile<DP>(do_at + s * C::kTileBytes, &map_do, qt * kTile, h, p.b, &do_full[s]);
   };
-  const int early = min(n, kS);
+  auto load_kv = [&](const Piece& p) {
+    mbar_arrive_expect_tx(&kv_full, 2 * C::kTileBytes);
+    load_tile<DP>(k_at, &map_k, p.key0, p.c, p.b, &kv_full);
+    load_tile<DP>(v_at, &map_v, p.key0, p.c, p.b, &kv_full);
+  };
   if (warp == kTmaWarp && elect_one()) {
     mbar_init(&kv_full, 1);
+    mbar_init(&kv_free, 1);
     for (int s = 0; s < kS; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&q_empty[s], 1);
@@ -401,18 +422,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     mbar_init(&p_full, kSoftWarps);
     mbar_init(&ds_full, kSoftWarps);
     mbar_init(&done, 1);
+    mbar_init(&sums_free, kSoftWarps);
+    for (int d = 0; d < 2; ++d) mbar_init(&out_free[d], 2);
     abort_word = 0;
     mbar_init_fence();
-    if (n > 0) {
-      mbar_arrive_expect_tx(&kv_full, 2 * C::kTileBytes);
-      load_tile<DP>(k_at, &map_k, key0, c, b, &kv_full);
-      load_tile<DP>(v_at, &map_v, key0, c, b, &kv_full);
-      for (int i = 0; i < early; ++i) load_do(i);
-    }
+    Piece p;
+    const int early = piece(0, p) ? min(p.n, kS) : 0;
+    if (early > 0) load_kv(p);
+    for (int i = 0; i < early; ++i) load_do(p, i, 0);
     // The statistics are the kernel's before, which may still be running. Every
     // block waits for it, so that this kernel does not end before that one.
     griddep_wait();
-    for (int i = 0; i < early; ++i) load_q(i);
+    for (int i = 0; i < early; ++i) load_q(p, i, 0);
   }
   if (warp == kMmaWarp) {
     if (lane == 0) {
@@ -428,141 +449,177 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t tmem = tmem_slot;
   const Waiter wait{&abort_word, &g_attn_bwd_error};
 
+  // `at` items and `live` pieces before, counted over the pieces with items
+  Piece p;
   if (warp == kTmaWarp) {
     const uint32_t one = elect_one();
-    int i = early;
-    for (; i < n; ++i) {
-      if (!wait(&q_empty[i % kS], (i / kS - 1) & 1)) break;
-      if (one) load_q(i);
-      if (!wait(&do_empty[i % kS], (i / kS - 1) & 1)) break;
-      if (one) load_do(i);
-    }
-    if (i < n) {  // gave up: leave the copies in flight time to land
-      mbar_wait(&kv_full, 0, kSpinLimit >> 10);
-      for (int k = max(0, i - kS); k <= i; ++k) {
-        mbar_wait(&q_full[k % kS], (k / kS) & 1, kSpinLimit >> 10);
-        mbar_wait(&do_full[k % kS], (k / kS) & 1, kSpinLimit >> 10);
+    bool go = true;
+    for (int round = 0, at = 0, live = 0; go && piece(round, p); at += p.n, ++round) {
+      if (p.n == 0) continue;
+      if (round > 0 && (go = wait(&kv_free, (live - 1) & 1)) && one) load_kv(p);
+      for (int i = 0; go && i < max(p.n, 2); ++i) {
+        // the second item's place is the one that the piece before leaves through
+        if (i == 1 && live > 0 && !(go = wait(&out_free[(live - 1) & 1], (live - 1) / 2 & 1))) break;
+        if (i == p.n) break;
+        if (round == 0 && i < kS) continue;
+        const int s = (at + i) % kS, turn = ((at + i) / kS - 1) & 1;
+        if (!(go = wait(&q_empty[s], turn))) break;
+        if (one) load_q(p, i, at);
+        if (!(go = wait(&do_empty[s], turn))) break;
+        if (one) load_do(p, i, at);
       }
+      ++live;
     }
+    if (!go)  // gave up: leave the copies in flight time to land
+      for (int i = 0; i < 64; ++i) mbar_try_wait(&kv_free, 0) && mbar_try_wait(&kv_free, 1);
   } else if (warp == kMmaWarp) {
-    if (n > 0) {
-      constexpr bool bf16 = !std::is_same<T, __half>::value;
-      constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
-      constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
-      constexpr uint32_t kStep = C::kTileBytes / 16;
-      const uint32_t one = elect_one();
-      const uint64_t q_desc = head_desc(q_at), do_desc = head_desc(do_at), k_desc = head_desc(k_at),
-                     v_desc = head_desc(v_at), q_rows = rows_desc(q_at), do_rows = rows_desc(do_at);
-      auto make_s = [&](int i) {
-        if (!wait(&q_full[i % kS], (i / kS) & 1)) return false;
-        tc_fence_after();
-        mma_head<DP>(tmem, k_desc, q_desc + i % kS * kStep, by_head, one);
-        mma_commit(&s_full, one);
-        return true;
-      };
-      auto make_dp = [&](int i) {
-        if (!wait(&do_full[i % kS], (i / kS) & 1)) return false;
-        tc_fence_after();
-        mma_head<DP>(tmem + C::kDp, v_desc, do_desc + i % kS * kStep, by_head, one);
-        mma_commit(&dp_full, one);
-        return true;
-      };
+    constexpr bool bf16 = !std::is_same<T, __half>::value;
+    constexpr uint32_t by_head = mma_desc(bf16, kTile, kTile, false, false);
+    constexpr uint32_t by_rows = mma_desc(bf16, kTile, DP, false, true);
+    constexpr uint32_t kStep = C::kTileBytes / 16;
+    const uint32_t one = elect_one();
+    const uint64_t q_desc = head_desc(q_at), do_desc = head_desc(do_at), k_desc = head_desc(k_at),
+                   v_desc = head_desc(v_at), q_rows = rows_desc(q_at), do_rows = rows_desc(do_at);
+    auto make_s = [&](int t) {  // t: items since the block's start
+      if (!wait(&q_full[t % kS], (t / kS) & 1)) return false;
+      tc_fence_after();
+      mma_head<DP>(tmem, k_desc, q_desc + t % kS * kStep, by_head, one);
+      mma_commit(&s_full, one);
+      return true;
+    };
+    auto make_dp = [&](int t, bool last) {
+      if (!wait(&do_full[t % kS], (t / kS) & 1)) return false;
+      tc_fence_after();
+      mma_head<DP>(tmem + C::kDp, v_desc, do_desc + t % kS * kStep, by_head, one);
+      mma_commit(&dp_full, one);
+      if (last) mma_commit(&kv_free, one);
+      return true;
+    };
+    bool go = true;
+    for (int round = 0, at = 0, live = 0; go && piece(round, p); at += p.n, ++round) {
+      if (p.n == 0) continue;
       // While the warps make p the tensor core makes dk and the next dp, while
-      // they make ds it makes dv and the next S.
-      bool go = wait(&kv_full, 0) && make_s(0) && make_dp(0);
+      // they make ds it makes dv and the next S. (The S and dp of the piece before
+      // have been read: its last ds was waited for.)
+      go = wait(&kv_full, live & 1) && make_s(at) && make_dp(at, p.n == 1);
 #pragma unroll 1
-      for (int i = 0; go && i < n; ++i) {
-        const int s = i % kS;
-        if (!(go = wait(&p_full, i & 1))) break;
+      for (int i = 0; go && i < p.n; ++i) {
+        const int t = at + i, s = t % kS;
+        if (!(go = wait(&p_full, t & 1))) break;
+        if (i == 0 && live > 0 && !(go = wait(&sums_free, (live - 1) & 1))) break;
         tc_fence_after();
         mma_rows<kParts>(tmem + C::kDv, tmem, do_rows + s * kStep, by_rows, i > 0, one);
         mma_commit(&do_empty[s], one);
-        if (i + 1 < n && !(go = make_s(i + 1))) break;
-        if (!(go = wait(&ds_full, i & 1))) break;
+        if (i + 1 < p.n && !(go = make_s(t + 1))) break;
+        if (!(go = wait(&ds_full, t & 1))) break;
         tc_fence_after();
         mma_rows<kParts>(tmem + C::kDk, tmem + C::kDp, q_rows + s * kStep, by_rows, i > 0, one);
         mma_commit(&q_empty[s], one);
-        if (i + 1 < n && !(go = make_dp(i + 1))) break;
+        if (i + 1 < p.n && !(go = make_dp(t + 1, i + 2 == p.n))) break;
       }
       mma_commit(&done, one);
+      ++live;
     }
   } else {
     // ---- a thread a quarter of a key's row: columns (queries) [32 quarter, ...)
-    const int quarter = warp / 4, row = (warp & 3) * 32 + lane, key = key0 + row;
+    const int quarter = warp / 4, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21, s_at = tmem + lanes + quarter * kCols, dp_at = s_at + C::kDp;
     const float scale2 = a.scale * kLog2e;
     const uint64_t scale_pair = pair(scale2, scale2);
-    // queries [lo, hi) that see the key
-    int lo = a.causal ? max(0, key - off) : 0;
-    int hi = a.window > 0 ? min((int)a.q_len, key - off + (int)a.window) : (int)a.q_len;
-    if (key >= keys) hi = lo = 0;
+    // The first eight warps store dk, the others dv, half a row a thread.
+    const int second = quarter / 2, col0 = (quarter & 1) * (DP / 2);
     bool ok = true;
 #pragma unroll 1
-    for (int i = 0, qt = 0; i < n; ++i, qt = qt + 1 == span ? 0 : qt + 1) {
-      const int s = i % kS, q0 = (first + qt) * kTile + quarter * kCols;
-      // the statistics came with the query tile
-      if (!(ok = wait(&q_full[s], (i / kS) & 1) && wait(&s_full, i & 1))) break;
+    for (int round = 0, at = 0, live = 0; piece(round, p); at += p.n, ++round) {
+      const int key = p.key0 + row;
+      if (p.n == 0) {  // seen by no query
+        const int64_t* step = second ? a.dvs : a.dks;
+        T* out = static_cast<T*>(second ? a.dv : a.dk) + p.b * step[0] + (int64_t)key * step[1] + p.c * step[2];
+        if (key < a.k_len)
+          for (int d = col0; d < min(a.head_dim, col0 + DP / 2); d += 8)
+            *reinterpret_cast<uint4*>(out + d) = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      // queries [lo, hi) that see the key
+      int lo = a.causal ? max(0, key - off) : 0;
+      int hi = a.window > 0 ? min((int)a.q_len, key - off + (int)a.window) : (int)a.q_len;
+      if (key >= p.keys) hi = lo = 0;
+#pragma unroll 1
+      for (int i = 0, qt = 0; ok && i < p.n; ++i, qt = qt + 1 == p.span ? 0 : qt + 1) {
+        const int t = at + i, s = t % kS, q0 = (p.first + qt) * kTile + quarter * kCols;
+        // the statistics came with the query tile
+        if (!(ok = wait(&q_full[s], (t / kS) & 1) && wait(&s_full, t & 1))) break;
+        tc_fence_after();
+        const uint64_t* lse = reinterpret_cast<const uint64_t*>(stats + s * kStats + quarter * kCols);
+        const uint64_t* delta = lse + kTile / 2;
+        uint32_t e[kCols], w[kCols / 2];
+        tmem_ld32(s_at, e);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < kCols; k += 2) {
+          float x, y;
+          unpair(fma2(pair(__uint_as_float(e[k]), __uint_as_float(e[k + 1])), scale_pair, lse[k / 2]), x, y);
+          e[k] = __float_as_uint(exp2_fast(x));
+          e[k + 1] = __float_as_uint(exp2_fast(y));
+        }
+        const int from = lo - q0, to = hi - q0;
+        const bool mask = __any_sync(0xFFFFFFFFu, from > 0 || to < kCols);
+        if (mask) {
+          mask_row(e, seen_bits(from, to), 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kCols; k += 2) w[k / 2] = round2<T>(__uint_as_float(e[k]), __uint_as_float(e[k + 1]));
+        tmem_st16(s_at, w);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full);
+        if (!(ok = wait(&dp_full, t & 1))) break;
+        tc_fence_after();
+        uint32_t dp[kCols];
+        tmem_ld32(dp_at, dp);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < kCols; k += 2) {
+          float x, y;
+          unpair(mul2(pair(__uint_as_float(e[k]), __uint_as_float(e[k + 1])),
+                      add2(pair(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), delta[k / 2])),
+                 x, y);
+          e[k] = __float_as_uint(x);
+          e[k + 1] = __float_as_uint(y);
+        }
+        if (mask) {  // 0 times whatever dp is there
+          mask_row(e, seen_bits(from, to), 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kCols; k += 2) w[k / 2] = round2<T>(__uint_as_float(e[k]), __uint_as_float(e[k + 1]));
+        tmem_st16(dp_at, w);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ds_full);
+      }
+      ok = ok && wait(&done, live & 1);
       tc_fence_after();
-      const uint64_t* lse = reinterpret_cast<const uint64_t*>(stats + s * kStats + quarter * kCols);
-      const uint64_t* delta = lse + kTile / 2;
-      uint32_t p[kCols], w[kCols / 2];
-      tmem_ld32(s_at, p);
-      tmem_wait_ld();
-#pragma unroll
-      for (int k = 0; k < kCols; k += 2) {
-        float x, y;
-        unpair(fma2(pair(__uint_as_float(p[k]), __uint_as_float(p[k + 1])), scale_pair, lse[k / 2]), x, y);
-        p[k] = __float_as_uint(exp2_fast(x));
-        p[k + 1] = __float_as_uint(exp2_fast(y));
-      }
-      const int from = lo - q0, to = hi - q0;
-      const bool mask = __any_sync(0xFFFFFFFFu, from > 0 || to < kCols);
-      if (mask) {
-        mask_row(p, seen_bits(from, to), 0u);
-      }
-#pragma unroll
-      for (int k = 0; k < kCols; k += 2) w[k / 2] = round2<T>(__uint_as_float(p[k]), __uint_as_float(p[k + 1]));
-      tmem_st16(s_at, w);
-      tmem_wait_st();
+      // from the last item's places, which are done with
+      const int slot = 2 + second * kS + (at + p.n - 1) % kS;
+      stage_row<T, DP / 2>(smem + slot * C::kTileBytes, row, col0, tmem + lanes + (second ? C::kDv : C::kDk) + col0,
+                           second ? 1.0f : a.scale);
+      fence_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full);
-      if (!(ok = wait(&dp_full, i & 1))) break;
-      tc_fence_after();
-      uint32_t dp[kCols];
-      tmem_ld32(dp_at, dp);
-      tmem_wait_ld();
-#pragma unroll
-      for (int k = 0; k < kCols; k += 2) {
-        float x, y;
-        unpair(mul2(pair(__uint_as_float(p[k]), __uint_as_float(p[k + 1])),
-                    add2(pair(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), delta[k / 2])),
-               x, y);
-        p[k] = __float_as_uint(x);
-        p[k + 1] = __float_as_uint(y);
+      if (lane == 0) mbar_arrive(&sums_free);
+      named_sync(1 + second, kSoftThreads / 2);
+      if ((warp & 7) == 0) {
+        const bool all = __all_sync(0xFFFFFFFFu, ok);
+        if (elect_one()) {
+          if (all) store_tile<DP>(second ? &map_dv : &map_dk, k_at + slot * C::kTileBytes, a.head_dim, p.key0, p.c, p.b);
+          mbar_arrive(&out_free[live & 1]);
+        }
+        __syncwarp();
       }
-      if (mask) {  // 0 times whatever dp is there
-        mask_row(p, seen_bits(from, to), 0u);
-      }
-#pragma unroll
-      for (int k = 0; k < kCols; k += 2) w[k / 2] = round2<T>(__uint_as_float(p[k]), __uint_as_float(p[k + 1]));
-      tmem_st16(dp_at, w);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ds_full);
+      ++live;
     }
-    if (n > 0 && ok) ok = wait(&done, 0);
-    tc_fence_after();
-    // the first eight warps store dk, the others dv, half a row a thread, from the
-    // query and do tiles' places, which are done with
-    const int second = quarter / 2, slot = 2 + second * kS, col0 = (quarter & 1) * (DP / 2);
-    stage_row<T, DP / 2>(smem + slot * C::kTileBytes, row, col0, tmem + lanes + (second ? C::kDv : C::kDk) + col0,
-                         second ? 1.0f : a.scale, n == 0);
-    fence_async_smem();
-    named_sync(1 + second, kSoftThreads / 2);
-    if ((warp & 7) == 0 && __all_sync(0xFFFFFFFFu, ok) && elect_one())
-      store_tile<DP>(second ? &map_dv : &map_dk, k_at + slot * C::kTileBytes, a.head_dim, key0, c, b);
   }
   tc_fence_before();
   __syncthreads();
@@ -596,15 +653,17 @@ cudaError_t run(const AttnArgs& a, int sms, cudaStream_t s) {
   e = allow_smem(k_attn_dkv<T, DP>, Dkv<DP>::kSmem, asked_dkv);
   if (e != cudaSuccess) return e;
   const int q_tiles = (int)tiles(a.q_len);
+  // Shares for dq also where attn_grid would take single blocks: with 6 x 1021,
+  // 12/4 heads of 64 and random lengths dq, dk and dv take 38 us, else 40.
   if (q_blocks > 0)
     k_attn_dq<T, DP><<<(unsigned)(q_blocks < sms ? q_blocks : sms), kBwdThreads, Dq<DP>::kSmem, s>>>(
         q, g, k, v, dq, a, q_tiles, (int)q_blocks);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (k_blocks == 0) return cudaSuccess;
-  // its blocks may start while the last of dq's run
+  // its blocks start while the last of dq's run
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)k_blocks);
+  cfg.gridDim = dim3(attn_grid(a, k_blocks, sms));
   cfg.blockDim = dim3(kBwdThreads);
   cfg.dynamicSmemBytes = Dkv<DP>::kSmem;
   cfg.stream = s;
@@ -613,7 +672,7 @@ cudaError_t run(const AttnArgs& a, int sms, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = q_blocks > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_attn_dkv<T, DP>, q, g, k, v, dk, dv, a, q_tiles);
+  return cudaLaunchKernelEx(&cfg, k_attn_dkv<T, DP>, q, g, k, v, dk, dv, a, q_tiles, (int)k_blocks);
 }
 
 template <typename T>

@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float inv = none ? 0.0f : 1.0f / total;
       // `none` may differ between the lanes of a warp: their sums are zeros.
       // The tile leaves from the place of its queries, which are done with.
-      stage_row<T, DP / 2>(smem + t * C::kTileBytes, row, half * (DP / 2), o_at, inv, false);
+      stage_row<T, DP / 2>(smem + t * C::kTileBytes, row, half * (DP / 2), o_at, inv);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -398,7 +398,7 @@ cudaError_t run(const AttnArgs& a, int sms, cudaStream_t s) {
   static std::atomic<uint64_t> asked{0};
   cudaError_t e = allow_smem(k_attn_fwd<T, DP>, C::kSmem, asked);
   if (e != cudaSuccess) return e;
-  k_attn_fwd<T, DP><<<(unsigned)(blocks < sms ? blocks : sms), kFwdThreads, C::kSmem, s>>>(
+  k_attn_fwd<T, DP><<<attn_grid(a, blocks, sms), kFwdThreads, C::kSmem, s>>>(
       q, k, v, o, a, (int)(q_tiles * a.group), (int)pairs, (int)blocks);
   return cudaGetLastError();
 }
