@@ -3,8 +3,10 @@
 // pack: for each group of 32 elements along the row, the power of two that
 // brings the largest magnitude to 64..127 (found from the exponent bits, no
 // logarithm), then round-to-nearest codes. restore: code * scale. A thread
-// holds 8 elements, four neighbouring lanes one group. Both are bound by HBM:
-// b + 1.03 bytes per element.
+// holds 8 elements, four neighbouring lanes one group; four such chunks a thread
+// are loaded before the first is used. Both are bound by HBM, b + 1.03 bytes per
+// element, pack nearly as much by its instructions (70 % of the issue slots):
+// 16384 x 2048 in bf16 packs in 20.1 us (5.05 TB/s), restores in 17.3 us (5.9).
 #include "act.cuh"
 #include "block.h"
 #include "vec.cuh"

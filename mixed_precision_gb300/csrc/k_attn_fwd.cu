@@ -1,20 +1,26 @@
 // Attention forward: o = softmax(scale q k^T) v and the rows' log-sum-exp.
 //
-// A block takes two tiles of 128 query rows that share their keys: tiles of
-// the query heads of one key head, counted tile by tile and head by head, so
-// with two heads a group both tiles are the same rows of two heads. Keys and
-// values pass once through shared memory (TMA) in tiles of 128.
+// A piece of work is two tiles of 128 query rows that share their keys: tiles
+// of the query heads of one key head, counted tile by tile and head by head,
+// so with two heads a group both tiles are the same rows of two heads. Keys
+// and values pass once through shared memory (TMA) in tiles of 128.
 //   S_t = Q_t K^T      tcgen05, S in TMEM (fp32)
 //   P_t = 2^(c S_t - c m)   two threads a row, 64 keys each; P_t (16 bits) over
 //                      S_t in TMEM
 //   O_t += P_t V       tcgen05, P from TMEM, O in TMEM
 // The two tiles alternate: while eight warps turn S_0 into P_0 the tensor core
-// works for tile 1, and the other way round. What bounds it is the chain from
-// one S through the softmax to the next; halving each thread's part of the row
-// shortens it. The row's maximum m is kept as
-// it was until it grows by more than 8 in the exponent of two: P stays
-// below 2^8, sums and O are fp32, and O is rescaled rarely (once or twice a
-// row on ordinary data) instead of in every tile.
+// works for tile 1, and the other way round. The row's maximum m is kept as it
+// was until it grows by more than 8 in the exponent of two: P stays below 2^8,
+// sums and O are fp32, and O is rescaled rarely (once or twice a row on ordinary
+// data) instead of in every tile. The first tile's maximum is taken alone, so
+// that tile is not worked on twice.
+//
+// What bounds it is the chain from one S through the softmax to the next; two
+// threads a row instead of one shorten it (1 x 8192, 16/8 heads of 128, no mask:
+// 450 us with one, 400 with two). Measured in bf16, 16/8 heads of 128, causal:
+// 1 x 8192 187 us (1470 TFLOP/s), 4 x 2048 65 us (1050); blocks that end with
+// each piece took 196 and 75 us. 16 heads of 64, 4 x 2048: 62 us (550), where a
+// pair's products are half as long but the softmax is not.
 //
 // Keys past a batch entry's length: their S is replaced by -inf, and their
 // rows of V (whatever they hold) by zeros in shared memory.
