@@ -259,6 +259,13 @@ def test_weight_grad_long(tokens, n_out, n_in):
     check_wgrad(tokens, n_out, n_in, BF16, BF16, view=True)
 
 
+@pytest.mark.parametrize("tokens", [1, 63, 65, 130, 321, 450])
+@pytest.mark.parametrize("n_out,n_in,dtype", [(8200, 5000, BF16), (6000, 8192, F16), (40000, 264, BF16)])
+def test_weight_grad_many_tiles(tokens, n_out, n_in, dtype):
+    """More tiles than multiprocessors, of one step to several."""
+    check_wgrad(tokens, n_out, n_in, dtype, dtype)
+
+
 def test_weight_grad_exact():
     """Small whole numbers: every product and sum is exact, so is the result."""
     g = gen(11)
