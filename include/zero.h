@@ -707,7 +707,8 @@ int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const int
  *   lengths), j <= i + k_len - q_len with `causal`, and j > i + k_len - q_len -
  *   window with window > 0. What lies past key_lengths is never used, whatever
  *   it holds. A query that sees no key has o = 0, lse = -inf and passes no
- *   gradient.
+ *   gradient. (Inside the length a NaN or inf in k or v may also reach queries
+ *   that the causal mask or the window keeps from it: a weight of 0 times it.)
  *   scale       of the products q.k; > 0. */
 typedef struct {
   int64_t batch, q_len, k_len; /* lengths up to 2^28 */
