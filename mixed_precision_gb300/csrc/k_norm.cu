@@ -595,15 +595,20 @@ constexpr int kSmemPerSm = 220 * 1024;
 // direct against through shared memory, bf16 with dsum:
 //   16384 x 1024   33.1, 28.7     4096 x 8192   74.6, 56.8    1024 x 1024   7.7, 6.9
 //   16384 x 2048   69.0, 49.1     1024 x 4096   19.7, 15.2     512 x 4096   9.6, 13.0
-// Short rows do as well or better directly (65536 x 256: 31.0, 31.8; x 128: 18.2,
-// 31.0), and so does fp32, whose loads are twice as long (16384 x 1024: 47 us,
+// Short rows do better directly (65536 x 256: 27.6, 31.8; x 128: 16.4, 31.0),
+// and so does fp32, whose loads are twice as long (16384 x 1024: 47 us,
 // 5.7 TB/s). Forward has the registers: through shared memory it took 48 us
 // where it takes 23 (16384 x 1024).
 Shape norm_shape(int64_t rows, int n, int elem_bytes, int tensors, bool backward) {
   Shape s = direct_shape(rows, n);
   const int stage = n * 8 * elem_bytes * tensors;
   // what the registers allow
-  int per_sm = (!backward ? 2048 : s.chunks == 1 ? 768 : 512) / s.threads;
+  const int fit_threads = !backward ? 2048 : s.chunks > 1 ? 512 : elem_bytes == 2 ? 1024 : 768;
+  // Backward with short rows that fill the machine: larger blocks leave fewer
+  // parts of dw to add up. 128 threads against 256, bf16 with dsum: 65536 x 256
+  // 28.6, 27.6 us; 65536 x 64 9.8, 8.8.
+  if (backward && s.team <= 32 && rows >= 152ll * fit_threads / s.team) s.threads = 256;
+  int per_sm = fit_threads / s.threads;
   if (backward) s.smem = s.threads / s.team * n * 32;
   if (backward && n > 32 && rows >= kStreamRows && elem_bytes == 2) {
     s.stream = true;
