@@ -577,7 +577,8 @@ Shape direct_shape(int64_t rows, int n) {
   Shape s{};
   s.chunks = 1;
   while (s.chunks < 4 && n > 32 * s.chunks) s.chunks *= 2;
-  while (s.chunks > 1 && rows * (pow2_at_least(n) / s.chunks) < 152 * 512 && n / s.chunks < 256) s.chunks /= 2;
+  while (s.chunks > 1 && rows * (pow2_at_least(n) / s.chunks) < 152 * 512 && pow2_at_least(n) / s.chunks < 256)
+    s.chunks /= 2;  // a team is 256 threads at most
   const int team = pow2_at_least((n + s.chunks - 1) / s.chunks);
   s.team = team < 4 ? 4 : team;  // the packed output's groups are 4 neighbouring lanes
   s.threads = s.team > 32 ? s.team : 128;

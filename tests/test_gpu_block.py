@@ -40,6 +40,10 @@ ROWS_COLS = [(1, 8), (3, 1), (5, 33), (2, 128), (67, 128), (1, 1000), (33, 1024)
              (9, 4096), (4, 8192), (2, 16256), (2, 20000), (1, 65536), (513, 72), (4099, 264)]
 
 
+# few rows, which are spread over as many threads as a block has
+FEW_ROWS = [(1, 2056), (60, 2368), (83, 3256), (3, 4088), (40, 4104), (5, 5000), (300, 6000), (2, 8184), (700, 3000)]
+
+
 # enough rows to go through shared memory, in teams of one to eight warps
 MANY_ROWS = [(2432, 264), (2500, 512), (3001, 520), (2433, 1024), (2432, 1032), (5000, 2048), (2600, 4096), (2440, 5000),
              (2433, 8192)]
@@ -55,7 +59,7 @@ def check_forward(x, w, eps, res, y, s, rstd):
         ref.close(y, want, want.abs() * (ref.U[x.dtype] + rel + 4 * ref.E) + ref.TINY[x.dtype], "y")
 
 
-@pytest.mark.parametrize("rows,cols", ROWS_COLS + MANY_ROWS)
+@pytest.mark.parametrize("rows,cols", ROWS_COLS + FEW_ROWS + MANY_ROWS)
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("with_res", [False, True])
 def test_norm_forward(rows, cols, dtype, with_res):
@@ -111,7 +115,7 @@ def test_norm_rows_far_apart():
     assert same_bits(dx, block.rmsnorm_backward(x.contiguous(), x.contiguous(), w, rstd)[0])
 
 
-@pytest.mark.parametrize("rows,cols", ROWS_COLS + MANY_ROWS + [(20000, 128), (3000, 1024)])
+@pytest.mark.parametrize("rows,cols", ROWS_COLS + FEW_ROWS + MANY_ROWS + [(20000, 128), (3000, 1024)])
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("with_dsum", [False, True])
 def test_norm_backward(rows, cols, dtype, with_dsum):
