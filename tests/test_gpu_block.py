@@ -426,6 +426,16 @@ def test_attention_many_rows_of_which_most_see_nothing(D, live, Sq):
     block.check()
 
 
+@pytest.mark.parametrize("B,Sq,Sk,H,K,causal,window", [
+    (500, 100, 100, 1, 1, True, 0), (450, 60, 300, 2, 1, False, 0), (200, 300, 60, 2, 2, True, 0),
+    (200, 129, 129, 2, 1, True, 0), (120, 400, 500, 1, 1, True, 20), (150, 700, 100, 1, 1, True, 30),
+    (90, 1, 700, 6, 2, True, 0)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_many_pieces_for_a_block(B, Sq, Sk, H, K, causal, window, D):
+    """Pieces of one tile to a few, several for every multiprocessor, some without a key."""
+    check_attention(B, Sq, Sk, H, K, D, BF16, causal, window)
+
+
 def test_attention_scale_and_large_logits():
     check_attention(1, 200, 200, 2, 2, 64, BF16, causal=True, scale=1.0)  # logits of +-50: near one-hot rows
     check_attention(1, 200, 200, 2, 2, 64, BF16, causal=True, scale=1e-4)
