@@ -60,6 +60,11 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   store8_raw(p, round8<T>(x));
 }
 
+// Bytes from a row's codes to those `rows` further on. (A row may be 2^30 bytes:
+// two of them leave 32 bits.)
+__host__ __device__ constexpr int64_t code_rows(int64_t rows, int pitch) { return rows * pitch; }
+static_assert(code_rows(2, 1 << 30) == int64_t(1) << 31, "offsets in 64 bits");
+
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // Scale byte of a group from the bits of its largest magnitude (as integers,

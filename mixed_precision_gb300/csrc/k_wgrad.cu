@@ -223,21 +223,23 @@ __global__ void __launch_bounds__(kWgThreads, 1)
     // reaches only columns that it makes NaN anyway.
     const int8_t* qp = a.q + min(n0 + c, a.pitch - 8);
     const uint8_t* sp = a.scales + min(n0 + lane % kWords * 128, a.pitch - 128) / kActGroup;
-    const int q_row = kRows * a.pitch, s_pitch = a.pitch / kActGroup;
+    const int64_t q_row = code_rows(kRows, a.pitch);
+    const int s_pitch = a.pitch / kActGroup;
     uint2 q[kAhead][kRounds];
     uint32_t b[kAhead];
     auto fetch = [&](int slot, int step) {
       if (step >= steps) return;
       const int64_t t0 = (first + step) * kStep;
       if (t0 + kStep <= a.tokens) {
-        const int8_t* p = qp + (t0 + r0) * a.pitch;
+        const int8_t* p = qp + code_rows(t0 + r0, a.pitch);
 #pragma unroll
-        for (int i = 0; i < kRounds; ++i) q[slot][i] = *reinterpret_cast<const uint2*>(p + (int64_t)i * q_row);
+        for (int i = 0; i < kRounds; ++i) q[slot][i] = *reinterpret_cast<const uint2*>(p + i * q_row);
         b[slot] = *reinterpret_cast<const uint32_t*>(sp + (t0 + srow) * s_pitch);
       } else {
 #pragma unroll
         for (int i = 0; i < kRounds; ++i)
-          q[slot][i] = *reinterpret_cast<const uint2*>(qp + min(t0 + r0 + i * kRows, a.tokens - 1) * a.pitch);
+          q[slot][i] =
+              *reinterpret_cast<const uint2*>(qp + code_rows(min(t0 + r0 + i * kRows, a.tokens - 1), a.pitch));
         b[slot] = *reinterpret_cast<const uint32_t*>(sp + min(t0 + srow, a.tokens - 1) * s_pitch);
       }
     };
