@@ -318,9 +318,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (lane == 0) mbar_arrive(&dq_free);
       named_sync(1, kSoftThreads);
       if (warp == 0) {
-        const bool all = __all_sync(0xFFFFFFFFu, ok);
         if (elect_one()) {
-          if (all) store_tile<DP>(&map_dq, q_at + place, a.head_dim, p.row0, p.h, p.b);
+          if (!wait.gave_up()) store_tile<DP>(&map_dq, q_at + place, a.head_dim, p.row0, p.h, p.b);
           mbar_arrive(&q_free[slot]);
         }
         __syncwarp();
@@ -612,9 +611,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (lane == 0) mbar_arrive(&sums_free);
       named_sync(1 + second, kSoftThreads / 2);
       if ((warp & 7) == 0) {
-        const bool all = __all_sync(0xFFFFFFFFu, ok);
         if (elect_one()) {
-          if (all) store_tile<DP>(second ? &map_dv : &map_dk, k_at + slot * C::kTileBytes, a.head_dim, p.key0, p.c, p.b);
+          if (!wait.gave_up())
+            store_tile<DP>(second ? &map_dv : &map_dk, k_at + slot * C::kTileBytes, a.head_dim, p.key0, p.c, p.b);
           mbar_arrive(&out_free[live & 1]);
         }
         __syncwarp();

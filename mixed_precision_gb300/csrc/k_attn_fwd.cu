@@ -368,9 +368,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (half == 0 && i < a.q_len && ok) *lse = none ? -INFINITY : (top * scale2 + log2f(total)) * kLn2;
       named_sync(1 + t, 256);
       if ((warp & 7) == 0) {
-        const bool all = __all_sync(0xFFFFFFFFu, ok);
         if (elect_one()) {
-          if (all) store_tile<DP>(&map_o, base + t * C::kTileBytes, a.head_dim, row0, h, w.b);
+          if (!wait.gave_up()) store_tile<DP>(&map_o, base + t * C::kTileBytes, a.head_dim, row0, h, w.b);
           mbar_arrive(&q_free[t]);
         }
         __syncwarp();

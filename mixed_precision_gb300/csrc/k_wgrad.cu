@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         fence_async_smem();
       }
       __syncthreads();
-      if (warp == kConvWarps && __all_sync(0xFFFFFFFFu, ok) && m0 + m * 128 < a.n_out && elect_one()) {
+      if (warp == kConvWarps && !wait.gave_up() && m0 + m * 128 < a.n_out && elect_one()) {
         for (int c = 0; c < BN / width && n0 + c * width < a.n_in; ++c) {
           const uint32_t from = base + region + c * (128 * 128);
           if (a.accumulate)

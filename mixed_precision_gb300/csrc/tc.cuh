@@ -36,6 +36,10 @@ struct Waiter {
     atomicOr(error, kErrWaitTimeout);
     return false;
   }
+  // Whether a wait of the block has given up. Asked after a barrier behind the
+  // waits in question: a warp's own waits do not tell (one for a phase whose
+  // parity has come round again passes early).
+  __device__ __forceinline__ bool gave_up() const { return *abort != 0; }
 };
 
 // A translation unit's error word, read and cleared (host): *value |= the word.
