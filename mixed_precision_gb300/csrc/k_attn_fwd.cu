@@ -356,9 +356,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       tops[0][t][half][row] = total;
       named_sync(3 + warp / 8 * 4 + (warp & 3), 64);
       total = tops[0][t][0][row] + tops[0][t][1][row];
-      const bool none = total == 0.0f;  // no key seen (a seen key gives at least 2^-8 ... or NaN)
+      const bool none = lo >= hi;  // no key seen
+      // A row whose keys' products are all -inf has a sum of 0 too, but no softmax.
+      if (!none && total == 0.0f) total = __uint_as_float(0x7FC00000u);
       const float inv = none ? 0.0f : 1.0f / total;
-      // `none` may differ between the lanes of a warp: their sums are zeros.
       // The tile leaves from the place of its queries, which are done with.
       stage_row<T, DP / 2>(smem + t * C::kTileBytes, row, half * (DP / 2), o_at, inv);
       fence_async_smem();

@@ -1,6 +1,8 @@
 """The block operators at their edges: the largest sizes they take, infinities in
 queries, fp16 gradients far from one, non-finite rows beside masked ones, every
 way out of the weight gradient, outputs in place of inputs, scratch sizes."""
+import math
+
 import pytest
 import torch
 
@@ -9,6 +11,53 @@ from mixed_precision_gb300 import block
 pytestmark = pytest.mark.gpu
 
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, *shape, dtype=F32, scale=1.0):
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def same_bits(a, b):
+    t = torch.int32 if a.dtype == F32 else torch.int16
+    return torch.equal(a.contiguous().view(t), b.contiguous().view(t))
+
+
+def qkv(g, B, Sq, Sk, H, K, D, dtype, dout=0.1):
+    return (normal(g, B, Sq, H, D, dtype=dtype), normal(g, B, Sk, K, D, dtype=dtype, scale=1.5),
+            normal(g, B, Sk, K, D, dtype=dtype), normal(g, B, Sq, H, D, dtype=dtype, scale=dout))
+
+
+# ---------------------------------------------------------------------------
+# Attention: infinities in q
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_row_of_infinite_products(dtype, D):
+    """A row that sees keys, every one of whose products is -inf, has no softmax:
+    NaN in o, lse and dq, not the zeros of a row that sees no key."""
+    g = gen(D)
+    q, k, v, do = qkv(g, 1, 300, 300, 2, 1, D, dtype)
+    k[..., 0] = k[..., 0].abs() + 0.5
+    clean = block.attention_forward(q, k, v, causal=True)
+    for row in (0, 5, 150):  # one key, a few, more than a tile
+        q[0, row, 0, 0] = -math.inf
+    q[0, 200, 0, 0] = math.inf
+    bad = torch.zeros(300, dtype=torch.bool, device="cuda")
+    bad[[0, 5, 150, 200]] = True
+    o, lse = block.attention_forward(q, k, v, causal=True)
+    assert bool(o[0, bad, 0].isnan().all()) and bool(lse[0, 0, bad].isnan().all())
+    assert same_bits(o[0, ~bad], clean[0][0, ~bad]) and same_bits(lse[0, :, ~bad], clean[1][0, :, ~bad])
+    assert same_bits(o[0, :, 1], clean[0][0, :, 1])
+    dq, _, _ = block.attention_backward(do, q, k, v, o, lse, causal=True)
+    assert bool(dq[0, bad, 0].isnan().all()) and bool(dq[0, :, 1].isfinite().all())
+    assert bool(dq[0, ~bad, 0].isfinite().all())
 
 
 # ---------------------------------------------------------------------------
