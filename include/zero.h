@@ -706,9 +706,10 @@ int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const int
  *   Query i sees key j when j < key_lengths[b] (all k_len keys without
  *   lengths), j <= i + k_len - q_len with `causal`, and j > i + k_len - q_len -
  *   window with window > 0. What lies past key_lengths is never used, whatever
- *   it holds. A query that sees no key has o = 0, lse = -inf and passes no
- *   gradient. (Inside the length a NaN or inf in k or v may also reach queries
- *   that the causal mask or the window keeps from it: a weight of 0 times it.)
+ *   it holds. A query that sees no key has o = 0, lse = -inf, dq = 0 and passes
+ *   no gradient; a key that no query sees has dk = dv = 0. (A NaN or inf in a
+ *   row of q, k, v or dout may also reach rows that see something but that the
+ *   causal mask or the window keeps from it: a weight of 0 times it.)
  *   scale       of the products q.k; > 0. */
 typedef struct {
   int64_t batch, q_len, k_len; /* lengths up to 2^28 */

@@ -140,11 +140,12 @@ __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
 }
 
 // A thread's part of an output row: N sums from TMEM column addr, times f,
-// rounded to T, into a tile at [row][col0] (swizzled as TMA reads it). Rows
+// rounded to T, into a tile at [row][col0] (swizzled as TMA reads it); zeros
+// unless `live`, whatever the sums are (0 times a NaN of another row). Rows
 // written straight to global memory would touch 32 lines an instruction (3.5 us
 // a block); a tile leaves by one bulk store. The whole warp calls it.
 template <typename T, int N>
-__device__ __forceinline__ void stage_row(uint8_t* tile, int row, int col0, uint32_t addr, float f) {
+__device__ __forceinline__ void stage_row(uint8_t* tile, int row, int col0, uint32_t addr, float f, bool live) {
   constexpr int kStep = N % 32 == 0 ? 32 : 16;
 #pragma unroll 1
   for (int k = 0; k < N; k += kStep) {
@@ -164,6 +165,11 @@ __device__ __forceinline__ void stage_row(uint8_t* tile, int row, int col0, uint
       *reinterpret_cast<uint4*>(tile + piece / 8 * kTileChunk + row * 128 + (piece % 8 ^ (row & 7)) * 16) =
           make_uint4(w[0], w[1], w[2], w[3]);
     }
+  }
+  if (!live) {  // seldom
+    for (int piece = col0 / 8; piece < (col0 + N) / 8; ++piece)
+      *reinterpret_cast<uint4*>(tile + piece / 8 * kTileChunk + row * 128 + (piece % 8 ^ (row & 7)) * 16) =
+          make_uint4(0, 0, 0, 0);
   }
 }
 

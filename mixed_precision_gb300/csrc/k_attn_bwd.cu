@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // the tile leaves from the place of its queries, which are done with
       constexpr int kOut = DP / kParts;
       const int slot = live % C::kQ, place = 2 * slot * C::kTileBytes;
-      stage_row<T, kOut>(smem + place, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale);
+      stage_row<T, kOut>(smem + place, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale,
+                         lo < hi);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -604,7 +605,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // from the last item's places, which are done with
       const int slot = 2 + second * kS + (at + p.n - 1) % kS;
       stage_row<T, DP / 2>(smem + slot * C::kTileBytes, row, col0, tmem + lanes + (second ? C::kDv : C::kDk) + col0,
-                           second ? 1.0f : a.scale);
+                           second ? 1.0f : a.scale, lo < hi);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();

@@ -359,9 +359,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const bool none = lo >= hi;  // no key seen
       // A row whose keys' products are all -inf has a sum of 0 too, but no softmax.
       if (!none && total == 0.0f) total = __uint_as_float(0x7FC00000u);
-      const float inv = none ? 0.0f : 1.0f / total;
       // The tile leaves from the place of its queries, which are done with.
-      stage_row<T, DP / 2>(smem + t * C::kTileBytes, row, half * (DP / 2), o_at, inv);
+      stage_row<T, DP / 2>(smem + t * C::kTileBytes, row, half * (DP / 2), o_at, 1.0f / total, !none);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();

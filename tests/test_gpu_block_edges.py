@@ -61,6 +61,30 @@ def test_attention_row_of_infinite_products(dtype, D):
 
 
 # ---------------------------------------------------------------------------
+# Attention: non-finite rows beside rows and keys that are masked
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_what_nobody_sees_stays_zero(dtype, D):
+    """A query that sees no key has o = 0 and dq = 0, a key that no query sees dk =
+    dv = 0, whatever the tile's other rows hold."""
+    g = gen(D + 1)
+    q, k, v, do = qkv(g, 2, 300, 200, 2, 1, D, dtype)  # causal: queries below 100 see nothing
+    lengths = torch.tensor([200, 150], dtype=torch.int32, device="cuda")
+    k[0, 3], v[0, 4] = math.nan, math.inf
+    do[1, 299, 1, 5], q[1, 280, 0, 7] = math.nan, math.inf
+    mask = dict(causal=True, key_lengths=lengths)
+    o, lse = block.attention_forward(q, k, v, **mask)
+    assert bool((o[:, :100] == 0).all()) and bool((lse[:, :, :100] == -math.inf).all())
+    assert bool(o[0, 104:].isnan().all())
+    dq, dk, dv = block.attention_backward(do, q, k, v, o, lse, **mask)
+    assert bool((dq[:, :100] == 0).all())
+    assert bool((dk[1, 150:] == 0).all()) and bool((dv[1, 150:] == 0).all())
+    assert bool(dv[1, :150].isnan().any())
+
+
+# ---------------------------------------------------------------------------
 # Weight gradient
 # ---------------------------------------------------------------------------
 
