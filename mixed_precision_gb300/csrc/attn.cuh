@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "act.cuh"
 #include "block.h"
@@ -28,6 +29,16 @@ __device__ __forceinline__ void key_range(const AttnArgs& a, int keys, int i, in
   hi = a.causal ? min(keys, d + 1) : keys;
   lo = a.window > 0 ? max(0, d - static_cast<int>(a.window) + 1) : 0;
 }
+
+// 16-bit operands in fp16 are kept high in its range, as powers of two that are
+// taken out again in fp32: fp16 keeps its 11 bits down to 2^-14 only, and a
+// weight below that is part of many small ones, a gradient often below it as a
+// whole. bf16 has fp32's range and needs none of this.
+//   forward   p = 2^(s - m), at most 2^8 (the maximum m may lag), times 2^7
+//   backward  p, at most 1, times 2^14; ds = p (dp - delta) by the power of two
+//             that brings its bound below 2^15 (k_attn_bwd.cu)
+template <typename T>
+constexpr bool kNarrow = std::is_same<T, __half>::value;
 
 // 2^x; 0 for -inf, about 2^-22 relative error.
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -166,10 +177,12 @@ __device__ __forceinline__ void stage_row(uint8_t* tile, int row, int col0, uint
           make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
-  if (!live) {  // seldom
+  if (__any_sync(0xFFFFFFFFu, !live)) {  // seldom
+#pragma unroll 1
     for (int piece = col0 / 8; piece < (col0 + N) / 8; ++piece)
-      *reinterpret_cast<uint4*>(tile + piece / 8 * kTileChunk + row * 128 + (piece % 8 ^ (row & 7)) * 16) =
-          make_uint4(0, 0, 0, 0);
+      if (!live)
+        *reinterpret_cast<uint4*>(tile + piece / 8 * kTileChunk + row * 128 + (piece % 8 ^ (row & 7)) * 16) =
+            make_uint4(0, 0, 0, 0);
   }
 }
 

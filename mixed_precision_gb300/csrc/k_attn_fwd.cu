@@ -10,8 +10,9 @@
 //   O_t += P_t V       tcgen05, P from TMEM, O in TMEM
 // The two tiles alternate: while eight warps turn S_0 into P_0 the tensor core
 // works for tile 1, and the other way round. The row's maximum m is kept as it
-// was until it grows by more than 8 in the exponent of two: P stays below 2^8,
-// sums and O are fp32, and O is rescaled rarely (once or twice a row on ordinary
+// was until it grows by more than 8 in the exponent of two: P stays below 2^8
+// (in fp16 it is held 2^7 higher: weights down to 2^-21 of the largest keep all
+// their bits, the error of smaller ones is 2^-32 of it), sums and O are fp32, and O is rescaled rarely (once or twice a row on ordinary
 // data) instead of in every tile. The first tile's maximum is taken alone, so
 // that tile is not worked on twice.
 //
@@ -38,7 +39,12 @@ __device__ unsigned g_attn_fwd_error;
 // add up to the launch's: 512 x 104 + 128 x 64 = 640 x 96.
 constexpr int kFwdThreads = 20 * 32, kTmaWarp = 16, kMmaWarp = 17;
 constexpr int kSoftmaxRegs = 104, kOtherRegs = 64;
-constexpr float kStale = 8.0f;        // how far the maximum may lag, as an exponent of two
+// How far the maximum may lag, as an exponent of two. In fp16 p and its sums are
+// lifted by what then is left below the largest number, 2^16. (A lag of 3 and a
+// lift of 12: 1 x 8192 192 to 209 us, 4 x 2048 70 to 76, for more rescaling.)
+constexpr float kStale = 8.0f;
+template <typename T>
+constexpr float kLift = kNarrow<T> ? 15.0f - kStale : 0.0f;
 
 template <int DP>
 struct Fwd {
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         tops[1][t][half][row] = m;
         named_sync(3 + warp / 8 * 4 + (warp & 3), 64);
-        top = fmaxf(m, tops[1][t][half ^ 1][row]);
+        top = lo < hi ? fmaxf(m, tops[1][t][half ^ 1][row]) : 0.0f;
       }
 #pragma unroll 1
       for (int j = 0; j < n; ++j) {
@@ -284,7 +290,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         float sums;
 #pragma unroll 1
         for (int turn = 0;; turn ^= 1) {
-          const float minus = top == -INFINITY ? 0.0f : -top * scale2;
+          float minus = top == -INFINITY ? 0.0f : -top * scale2;
+          if constexpr (kNarrow<T>) minus = __fadd_rn(minus, kLift<T>);  // fused it took a register more, and spilled
           const uint64_t scale_pair = pair(scale2, scale2), minus_pair = pair(minus, minus);
           uint64_t sum[2] = {0, 0};
           float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -356,16 +363,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       tops[0][t][half][row] = total;
       named_sync(3 + warp / 8 * 4 + (warp & 3), 64);
       total = tops[0][t][0][row] + tops[0][t][1][row];
-      const bool none = lo >= hi;  // no key seen
-      // A row whose keys' products are all -inf has a sum of 0 too, but no softmax.
-      if (!none && total == 0.0f) total = __uint_as_float(0x7FC00000u);
+      // No key seen: the sum is 0 and top still is. (Products that are all -inf have
+      // a sum of 0 too, but no softmax: NaN, in o by 0 times 1 / 0.)
+      const bool none = total == 0.0f && top == 0.0f;
       // The tile leaves from the place of its queries, which are done with.
       stage_row<T, DP / 2>(smem + t * C::kTileBytes, row, half * (DP / 2), o_at, 1.0f / total, !none);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[t]);
-      if (half == 0 && i < a.q_len && ok) *lse = none ? -INFINITY : (top * scale2 + log2f(total)) * kLn2;
+      if (half == 0 && i < a.q_len && ok) {
+        const float l = (top * scale2 + (log2f(total) - kLift<T>)) * kLn2;
+        *lse = none ? -INFINITY : total == 0.0f ? __uint_as_float(0x7FC00000u) : l;
+      }
       named_sync(1 + t, 256);
       if ((warp & 7) == 0) {
         if (elect_one()) {

@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import _block_ref as ref
 from mixed_precision_gb300 import block
 
 pytestmark = pytest.mark.gpu
@@ -58,6 +59,27 @@ def test_attention_row_of_infinite_products(dtype, D):
     dq, _, _ = block.attention_backward(do, q, k, v, o, lse, causal=True)
     assert bool(dq[0, bad, 0].isnan().all()) and bool(dq[0, :, 1].isfinite().all())
     assert bool(dq[0, ~bad, 0].isfinite().all())
+
+
+# ---------------------------------------------------------------------------
+# Attention in fp16: weights and gradients over the range of the type
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("Sk", [4096, 65536])
+def test_attention_fp16_weak_keys_add_up(Sk):
+    """A key takes nearly all of the weight, and its value is zero: what is left is
+    the others' (Sk - 1) e^-18. A weight is off by its rounding, or by half a step
+    of fp16's smallest numbers, 2^-25, of which 2^7 are taken out again."""
+    D = 64
+    q = torch.zeros(1, 128, 1, D, dtype=F16, device="cuda")
+    k = torch.zeros(1, Sk, 1, D, dtype=F16, device="cuda")
+    q[..., 0], k[0, 7, 0, 0] = 12, 12  # a logit of 12 * 12 / 8
+    v = torch.ones_like(k)
+    v[0, 7] = 0
+    o, _ = block.attention_forward(q, k, v)
+    p = math.exp(-18.0)
+    want = (Sk - 1) * p / (1 + (Sk - 1) * p)
+    assert float((o.double() - want).abs().max()) <= (Sk - 1) * 2 ** -32 + want * (2 * ref.U[F16] + 2 ** -16) + 2 ** -25
 
 
 # ---------------------------------------------------------------------------
