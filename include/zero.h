@@ -731,7 +731,11 @@ int zero_attention_forward(const zero_attention_desc* desc, const void* q, const
                            void* stream);
 
 /* The gradients of q, k and v from o's, recomputing the probabilities from
- * lse. dk and dv are summed over the query heads that share them.
+ * lse. dk and dv are summed over the query heads that share them. Sums and
+ * statistics are fp32; the weights p and their gradients ds are rounded to dtype
+ * where they become operands of a product (in forward p too), in fp16 with a
+ * power of two taken out that keeps ds in range: what fits is what the results
+ * themselves fit.
  *   workspace  zero_attention_backward_workspace bytes. */
 int zero_attention_backward_workspace(const zero_attention_desc* desc, int64_t* bytes);
 int zero_attention_backward(const zero_attention_desc* desc, const void* dout, const void* q,

@@ -347,7 +347,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal:
 
 @functools.lru_cache(maxsize=256)
 def _attention_scratch(batch, q_len, q_heads) -> int:
-    """Scratch bytes of attention's backward: a function of the query rows."""
+    """Scratch bytes of attention's backward, enough for both types and any sharing of keys."""
     steps = (max(q_len, 1) * q_heads * 8, q_heads * 8, 8)
     return abi.zero_attention_backward_workspace(
         _attention_desc(batch, q_len, q_len, q_heads, q_heads, 8, abi.ZERO_F16, 0, 0, 0, 1.0, *steps * 8))

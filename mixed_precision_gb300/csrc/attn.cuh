@@ -39,6 +39,7 @@ __device__ __forceinline__ void key_range(const AttnArgs& a, int keys, int i, in
 //             that brings its bound below 2^15 (k_attn_bwd.cu)
 template <typename T>
 constexpr bool kNarrow = std::is_same<T, __half>::value;
+__device__ __forceinline__ float power_of_two(int n) { return __uint_as_float((127 + n) << 23); }  // |n| < 127
 
 // 2^x; 0 for -inf, about 2^-22 relative error.
 __device__ __forceinline__ float exp2_fast(float x) {

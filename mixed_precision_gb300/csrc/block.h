@@ -92,7 +92,11 @@ struct AttnArgs {
   const int32_t* lengths;
   float* lse;
   const float* lse_in;
-  float* stats;  // backward: the rows' statistics (k_attn_bwd.cu)
+  // backward, from the workspace (k_attn_bwd.cu): the rows' statistics; in fp16
+  // the key heads' largest |v| in v_parts parts and bounds of |dp - delta|
+  float* stats;
+  uint32_t *v_top, *ds_top;
+  int v_parts;
   Divide by_group, by_kv_heads, by_q_heads, by_batch_kv, by_batch_q;  // batch x heads
 };
 cudaError_t launch_attention_forward(const AttnArgs& a, int sms, cudaStream_t s);

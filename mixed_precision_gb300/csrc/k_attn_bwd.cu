@@ -11,6 +11,18 @@
 // In exchange no gradient is added to global memory from two places: no atomic
 // adds, no fp32 copy of dq, and every sum has a fixed order.
 //
+// p and ds become operands of the inputs' type. In fp16 they are scaled, since
+// ds may leave its range where dq, dk and dv do not, above and below: p by 2^14,
+// and ds by the power of two that brings the bound
+//   |dp - delta| <= sum_d |do| max |v| + |delta|
+// below 2^15; of a row's own bound for dq, of the largest among the key head's
+// rows for dk, whose sums run over rows. A third kernel, before, finds max |v| of
+// each key head (finite ones; a row with a non-finite bound is not scaled). The
+// factors go into lse's place in the exponent and come out with the sums' scale;
+// dk's costs one product a pair. fp16 takes for all this (captured, caches
+// flushed) 591 us instead of 576 at 1 x 8192, 157 instead of 150 at 4 x 2048 with
+// 16 heads of 64, 51 instead of 46 at 6 x 1021 with a window of 256.
+//
 // Bound by the tensor cores for heads of 128 (68 and 80 % of their cycles), by
 // the softmax warps for heads of 64. Measured in bf16, both kernels, counting
 // the five products: 16/8 heads of 128, causal, 1 x 8192 558 us (1230 TFLOP/s),
@@ -31,6 +43,56 @@ constexpr int kParts = 4, kCols = kTile / kParts, kSoftWarps = 4 * kParts, kSoft
 constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kBwdThreads = (kSoftWarps + 2) * 32;
 constexpr int kStats = 2 * kTile;     // floats of a query tile's statistics
 
+// fp16: exponents of the operands' largest value, and of p's scale.
+constexpr int kTopExp = 14, kLiftP = 14;
+constexpr int kBoundParts = 32;       // max |v| of a key head is found in up to this many parts
+
+// The exponent of the power of two for ds with this bound (its bits): none if it
+// is not finite. (A bound other than zero is at least 2^-48.)
+__device__ __forceinline__ int ds_lift(uint32_t bound) {
+  const int e = static_cast<int>(bound >> 23 & 0xFFu) - 127;
+  return e == 128 ? 0 : kTopExp - max(e, -60);
+}
+
+// fp16, before the others: the largest finite |v| of each key head's valid keys, in
+// a.v_parts parts, and zeros where dq collects the bounds. Reads v once.
+__global__ void __launch_bounds__(256) k_attn_bounds(const AttnArgs a, const Divide by_chunks, int64_t work) {
+  __shared__ uint32_t tops[8];
+  griddep_trigger();
+  const int per = static_cast<int>((a.k_len + a.v_parts - 1) / a.v_parts);
+  for (int64_t at = blockIdx.x; at < work; at += gridDim.x) {
+    const int64_t bc = at / a.v_parts, b = bc / a.kv_heads;
+    const int part = static_cast<int>(at - bc * a.v_parts), first = part * per;
+    const __half* v = static_cast<const __half*>(a.v) + b * a.vs[0] + first * a.vs[1] + (bc - b * a.kv_heads) * a.vs[2];
+    const uint32_t n = max(0, min(per, valid_keys(a, b) - first)) * by_chunks.d;  // chunks of 8 elements
+    uint32_t top = 0;  // of two halves
+    for (uint32_t i = threadIdx.x; i < n; i += 4 * 256) {
+      uint4 u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t k = min(i + j * 256, n - 1), row = by_chunks(k);
+        u[j] = *reinterpret_cast<const uint4*>(v + row * a.vs[1] + (k - row * by_chunks.d) * 8);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t w = (e == 0 ? u[j].x : e == 1 ? u[j].y : e == 2 ? u[j].z : u[j].w) & 0x7FFF7FFFu;
+          top = __vmaxu2(top, w & ~__vcmpgeu2(w, 0x7C007C00u));
+        }
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x / 32] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 0; w < 8; ++w) top = max(top, tops[w]);
+      a.v_top[bc * kBoundParts + part] = __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
+      if (part == 0) a.ds_top[bc] = 0;
+    }
+    __syncthreads();
+  }
+}
+
 // ---------------------------------------------------------------------------
 // dq
 // ---------------------------------------------------------------------------
@@ -43,6 +105,7 @@ struct Dq {
   // piece's first products run while this one's result leaves.
   static constexpr int kQ = DP == 64 ? 2 : 1;
   static constexpr int kSmem = (2 * kQ + kK + kV) * kTileBytes + 1024;
+  static_assert(kSmem + 1800 <= 227 * 1024, "beside the kernel's own shared memory");
   // TMEM: S twice (ds over it), dp, dq
   static constexpr uint32_t kDp = 256, kDq = 384;
 };
@@ -61,6 +124,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       v_empty[C::kV], s_full[2], dp_full, dp_empty, ds_full[2], done, dq_free;
   __shared__ uint32_t tmem_slot, abort_word;
   __shared__ float part[2][kTile];
+  // fp16: halves of the sums of |do|, fp32 numbers rounded up to their upper 16
+  // bits (32 would be more than the shared memory left beside the tiles)
+  __shared__ uint16_t sizes[kNarrow<T> ? 2 : 1][kNarrow<T> ? kTile : 1];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   // queries and do of kQ pieces, then the K and V slots
   const uint32_t q_at = smem_u32(smem), k_at = q_at + 2 * C::kQ * C::kTileBytes,
@@ -221,7 +287,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int i = p.row0 + row;
       const bool in = i < a.q_len;
       const int64_t head = p.b * (int64_t)a.q_heads + p.h;
-      float delta = 0.0f;
+      float delta = 0.0f, size = 0.0f;
       if (in && quarter < 2) {  // half the head each
         const T* o = static_cast<const T*>(a.o_in) + p.b * a.os[0] + (int64_t)i * a.os[1] + p.h * a.os[2];
         const T* g = static_cast<const T*>(a.dout) + p.b * a.dos[0] + (int64_t)i * a.dos[1] + p.h * a.dos[2];
@@ -230,18 +296,39 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           widen8(load8_raw(o + d), x);
           widen8(load8_raw(g + d), y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) delta = fmaf(x[e], y[e], delta);
+          for (int e = 0; e < 8; ++e) {
+            delta = fmaf(x[e], y[e], delta);
+            if constexpr (kNarrow<T>) size += fabsf(y[e]);
+          }
         }
       }
       // a row that sees nothing (or is none) gets p = 2^-inf = 0 everywhere
       const float lse = in ? a.lse_in[head * a.q_len + i] : -INFINITY;
-      if (quarter < 2) part[quarter][row] = delta;
+      if (quarter < 2) {
+        part[quarter][row] = delta;
+        if constexpr (kNarrow<T>)
+          sizes[quarter][row] = static_cast<uint16_t>(min((__float_as_uint(size) >> 16) + 1, 0x7FFFu));
+      }
       named_sync(1, kSoftThreads);
       const float minus_delta = -(part[0][row] + part[1][row]),
                   minus_lse = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+      int lift = 0;  // of ds
+      if constexpr (kNarrow<T>) {
+        const int64_t bc = p.b * (int64_t)a.kv_heads + p.c;
+        if (round == 0) griddep_wait();  // for max |v|; nothing has been written before
+        const uint32_t v_top =
+            __reduce_max_sync(0xFFFFFFFFu, lane < a.v_parts ? a.v_top[bc * kBoundParts + lane] : 0u);
+        size = __uint_as_float(sizes[0][row] << 16) + __uint_as_float(sizes[1][row] << 16);
+        const uint32_t bound = __float_as_uint(fmaf(size, __uint_as_float(v_top), fabsf(minus_delta)));
+        lift = ds_lift(bound);
+        if (quarter == 0) {
+          const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, in && bound < 0x7F800000u ? bound : 0u);
+          if (lane == 0) atomicMax(&a.ds_top[bc], most);  // the same in any order
+        }
+      }
       if (quarter == 0) {
         float* st = a.stats + (head * q_tiles + p.row0 / kTile) * kStats + row;
-        st[0] = minus_lse;
+        st[0] = kNarrow<T> ? minus_lse + kLiftP : minus_lse;
         st[kTile] = minus_delta;
       }
       if (p.n == 0) {  // no key is seen; no place in shared memory is its own
@@ -255,7 +342,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       int lo, hi;
       key_range(a, p.keys, i, lo, hi);
-      const uint64_t lse_pair = pair(minus_lse, minus_lse), delta_pair = pair(minus_delta, minus_delta);
+      const float minus = kNarrow<T> ? minus_lse + static_cast<float>(lift) : minus_lse;  // p is only a factor of ds here
+      const uint64_t lse_pair = pair(minus, minus), delta_pair = pair(minus_delta, minus_delta);
 #pragma unroll 1
       for (int j = 0; ok && j < p.n; ++j) {
         const int t = at + j;
@@ -311,8 +399,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // the tile leaves from the place of its queries, which are done with
       constexpr int kOut = DP / kParts;
       const int slot = live % C::kQ, place = 2 * slot * C::kTileBytes;
-      stage_row<T, kOut>(smem + place, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut, a.scale,
-                         lo < hi);
+      stage_row<T, kOut>(smem + place, row, quarter * kOut, tmem + lanes + C::kDq + quarter * kOut,
+                         kNarrow<T> ? a.scale * power_of_two(-lift) : a.scale, lo < hi);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -549,6 +637,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int lo = a.causal ? max(0, key - off) : 0;
       int hi = a.window > 0 ? min((int)a.q_len, key - off + (int)a.window) : (int)a.q_len;
       if (key >= p.keys) hi = lo = 0;
+      // p is 2^kLiftP times itself: what is missing to the lift of ds
+      const int lift = kNarrow<T> ? ds_lift(a.ds_top[p.b * (int64_t)a.kv_heads + p.c]) : 0;
+      const float rest = kNarrow<T> ? power_of_two(lift - kLiftP) : 1.0f;
+      const uint64_t rest_pair = pair(rest, rest);
 #pragma unroll 1
       for (int i = 0, qt = 0; ok && i < p.n; ++i, qt = qt + 1 == p.span ? 0 : qt + 1) {
         const int t = at + i, s = t % kS, q0 = (p.first + qt) * kTile + quarter * kCols;
@@ -585,9 +677,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int k = 0; k < kCols; k += 2) {
           float x, y;
-          unpair(mul2(pair(__uint_as_float(e[k]), __uint_as_float(e[k + 1])),
-                      add2(pair(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), delta[k / 2])),
-                 x, y);
+          uint64_t d = add2(pair(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), delta[k / 2]);
+          if constexpr (kNarrow<T>) d = mul2(d, rest_pair);
+          unpair(mul2(pair(__uint_as_float(e[k]), __uint_as_float(e[k + 1])), d), x, y);
           e[k] = __float_as_uint(x);
           e[k + 1] = __float_as_uint(y);
         }
@@ -605,7 +697,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // from the last item's places, which are done with
       const int slot = 2 + second * kS + (at + p.n - 1) % kS;
       stage_row<T, DP / 2>(smem + slot * C::kTileBytes, row, col0, tmem + lanes + (second ? C::kDv : C::kDk) + col0,
-                           second ? 1.0f : a.scale, lo < hi);
+                           (second ? 1.0f : a.scale) * (kNarrow<T> ? power_of_two(second ? -kLiftP : -lift) : 1.0f),
+                           lo < hi);
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -656,22 +749,31 @@ cudaError_t run(const AttnArgs& a, int sms, cudaStream_t s) {
   const int q_tiles = (int)tiles(a.q_len);
   // Shares for dq also where attn_grid would take single blocks: with 6 x 1021,
   // 12/4 heads of 64 and random lengths dq, dk and dv take 38 us, else 40.
-  if (q_blocks > 0)
-    k_attn_dq<T, DP><<<(unsigned)(q_blocks < sms ? q_blocks : sms), kBwdThreads, Dq<DP>::kSmem, s>>>(
-        q, g, k, v, dq, a, q_tiles, (int)q_blocks);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  if (k_blocks == 0) return cudaSuccess;
-  // its blocks start while the last of dq's run
+  // Each kernel's blocks start while the last of the one before run, and wait for
+  // it where they need its results.
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(attn_grid(a, k_blocks, sms));
   cfg.blockDim = dim3(kBwdThreads);
-  cfg.dynamicSmemBytes = Dkv<DP>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  if (q_blocks > 0) {
+    if (a.v_parts > 0) {
+      const int64_t work = a.batch * a.kv_heads * a.v_parts;
+      k_attn_bounds<<<(unsigned)(work < sms * 8ll ? work : sms * 8ll), 256, 0, s>>>(a, Divide(a.head_dim / 8), work);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+      cfg.numAttrs = 1;
+    }
+    cfg.gridDim = dim3((unsigned)(q_blocks < sms ? q_blocks : sms));
+    cfg.dynamicSmemBytes = Dq<DP>::kSmem;
+    e = cudaLaunchKernelEx(&cfg, k_attn_dq<T, DP>, q, g, k, v, dq, a, q_tiles, (int)q_blocks);
+    if (e != cudaSuccess) return e;
+  }
+  if (k_blocks == 0) return cudaSuccess;
+  cfg.gridDim = dim3(attn_grid(a, k_blocks, sms));
+  cfg.dynamicSmemBytes = Dkv<DP>::kSmem;
   cfg.numAttrs = q_blocks > 0 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, k_attn_dkv<T, DP>, q, g, k, v, dk, dv, a, q_tiles, (int)k_blocks);
 }
@@ -686,11 +788,17 @@ cudaError_t backward_t(const AttnArgs& a, int sms, cudaStream_t s) {
 ZG_ERROR_WORD(attn_bwd_error, g_attn_bwd_error)
 
 int64_t attention_backward_bytes(const AttnArgs& a) {
-  return a.batch * a.q_heads * tiles(a.q_len) * kStats * 4;
+  const int64_t bounds = a.dtype == kF16 ? a.batch * a.kv_heads * (kBoundParts + 1) : 0;
+  return (a.batch * a.q_heads * tiles(a.q_len) * kStats + bounds) * 4;
 }
 
-cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s) {
-  return a.dtype == kF16 ? backward_t<__half>(a, sms, s) : backward_t<__nv_bfloat16>(a, sms, s);
+cudaError_t launch_attention_backward(const AttnArgs& args, int sms, cudaStream_t s) {
+  AttnArgs a = args;
+  if (a.dtype != kF16) return backward_t<__nv_bfloat16>(a, sms, s);
+  a.v_top = reinterpret_cast<uint32_t*>(a.stats + a.batch * a.q_heads * tiles(a.q_len) * kStats);
+  a.ds_top = a.v_top + a.batch * a.kv_heads * kBoundParts;
+  a.v_parts = static_cast<int>(tiles(a.k_len) < kBoundParts ? tiles(a.k_len) : kBoundParts);
+  return backward_t<__half>(a, sms, s);
 }
 
 }  // namespace zg

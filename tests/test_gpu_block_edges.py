@@ -82,6 +82,112 @@ def test_attention_fp16_weak_keys_add_up(Sk):
     assert float((o.double() - want).abs().max()) <= (Sk - 1) * 2 ** -32 + want * (2 * ref.U[F16] + 2 ** -16) + 2 ** -25
 
 
+def gradients(do, q, k, v, o, lse, causal, lengths, scale):
+    """{name: (gradient in 64 bits, tolerance)}, and the largest |p (dp - delta)|.
+
+    p and ds are operands of the type with a power of two taken out that keeps
+    the largest possible one below 2^15: each is off by U of itself, and by
+    half the type's smallest step, which that power makes 2^-39 of the bound
+    |dp - delta| <= |do|_1 max|v| + |delta| of the key head's rows (for p, whose
+    bound is 1, 2^-39). The rest as in _block_ref.attention_backward."""
+    U, E = ref.U[q.dtype], ref.E
+    B, Sq, H, D = q.shape
+    Sk, K = k.shape[1], k.shape[2]
+    z = lambda t: torch.zeros(t.shape, dtype=torch.float64, device=t.device)  # noqa: E731
+    g, top = {n: z(t) for n, t in (("dq", q), ("dk", k), ("dv", v))}, 0.0
+    tol = {n: torch.zeros_like(t) for n, t in g.items()}
+    for b in range(B):
+        n = Sk if lengths is None else int(lengths[b])
+        ok = ref.seen(Sq, Sk, causal, 0, n).to(q.device)[:, :n]
+        rows = ok.any(1)
+        if n == 0:
+            continue
+        ok = ok[rows]
+        for c in range(K):
+            kk, vv = k[b, :n, c].double(), v[b, :n, c].double()
+            heads = []
+            for h in range(c * H // K, (c + 1) * H // K):
+                qq, gg, oo = (t[b, rows, h].double() for t in (q, do, o))
+                delta = (gg * oo).sum(1, keepdim=True)
+                heads.append((h, qq, gg, oo, delta, gg.abs().sum(1, keepdim=True) * vv.abs().max() + delta.abs()))
+            bound = max(float(x[-1].max()) for x in heads)
+            for h, qq, gg, oo, delta, own in heads:
+                ll = lse[b, h, rows].double()[:, None]
+                d = 2 * D * E * (qq.abs() @ kk.abs().t() * scale).amax(1, keepdim=True) + 2 ** -17 + 4 * E * ll.abs()
+                p = (qq @ kk.t() * scale - ll).masked_fill(~ok, -math.inf).exp()
+                x = gg @ vv.t() - delta
+                ds = p * x
+                top = max(top, float(ds.abs().max()))
+                dots = 2 * D * E * (gg.abs() @ vv.abs().t() + (gg * oo).abs().sum(1, keepdim=True))
+                off = p * (d * x.abs() + 2 * dots) + U * ds.abs()
+                # a row's own bound for dq, the head's for dk
+                off_q, off_k = off + 2 ** -39 * own * ok, off + 2 ** -39 * bound * ok
+                off_p = p * (d + U) + 2 ** -39 * ok
+                g["dq"][b, rows, h] = scale * (ds @ kk)
+                tol["dq"][b, rows, h] = scale * (off_q @ kk.abs() + Sk * E * (ds.abs() @ kk.abs()))
+                g["dk"][b, :n, c] += scale * (ds.t() @ qq)
+                tol["dk"][b, :n, c] += scale * (off_k.t() @ qq.abs() + Sq * E * (ds.abs().t() @ qq.abs()))
+                g["dv"][b, :n, c] += p.t() @ gg
+                tol["dv"][b, :n, c] += off_p.t() @ gg.abs() + Sq * E * (p.t() @ gg.abs())
+    return {n: (g[n], tol[n] + U * g[n].abs() + ref.TINY[q.dtype] / 2) for n in g}, top
+
+
+def check_range(q, k, v, do, causal=True, lengths=None):
+    scale = q.shape[-1] ** -0.5
+    o, lse = block.attention_forward(q, k, v, causal=causal, key_lengths=lengths)
+    got = block.attention_backward(do, q, k, v, o, lse, causal=causal, key_lengths=lengths)
+    want, top = gradients(do, q, k, v, o, lse, causal, lengths, scale)
+    for t, name in zip(got, ("dq", "dk", "dv")):
+        assert float(want[name][0].abs().max()) < 65504  # the result itself fits the type
+        ref.close(t, *want[name], name)
+    block.check()
+    return top
+
+
+@pytest.mark.parametrize("D,dout", [(64, 7e3), (128, 6e3)])
+def test_attention_fp16_large_gradients(D, dout):
+    """p (dp - delta) leaves fp16, dq, dk and dv do not."""
+    g = torch.Generator()
+    g.manual_seed(1)
+    q, k, v, do = ((torch.randn(1, 512, heads, D, generator=g) * scale).to(F16).cuda()
+                   for heads, scale in ((2, 1), (1, 1.5), (1, 2), (2, dout)))
+    assert check_range(q, k, v, do) > 65504
+
+
+@pytest.mark.parametrize("Sq,D,dout", [(2048, 64, 1e-4), (1000, 128, 1e-4), (1500, 80, 1e-5)])
+def test_attention_fp16_small_gradients(Sq, D, dout):
+    """p (dp - delta) is below fp16's normal numbers."""
+    q, k, v, do = qkv(gen(Sq), 1, Sq, Sq, 2, 1, D, F16, dout=dout)
+    assert check_range(q, k, v, do) < 2 ** -10
+
+
+def test_attention_fp16_rows_of_unlike_size():
+    g = gen(6)
+    q, k, v, do = qkv(g, 2, 700, 700, 4, 2, 64, F16, dout=1.0)
+    do = (do.float() * torch.exp2(torch.randint(-13, 9, (2, 700, 4, 1), generator=g, device="cuda").float())).half()
+    do[0, 100:300] = 0
+    lengths = torch.tensor([700, 391], dtype=torch.int32, device="cuda")
+    k[1, 391:] = math.nan
+    v[1, 391:] = math.inf
+    check_range(q, k, v, do, lengths=lengths)
+    check_range(q, k, v.mul_(100), (do.float() / 256).half(), causal=False, lengths=lengths)
+
+
+def test_attention_fp16_weak_weights_in_dv():
+    """128 x 100 e^-18, of weights below fp16's smallest normal number."""
+    Sk, D = 4096, 64
+    q = torch.zeros(1, 128, 1, D, dtype=F16, device="cuda")
+    k = torch.zeros(1, Sk, 1, D, dtype=F16, device="cuda")
+    q[..., 0], k[0, 7, 0, 0] = 12, 12  # a logit of 12 * 12 / 8
+    v = torch.ones_like(k)
+    o, lse = block.attention_forward(q, k, v)
+    _, _, dv = block.attention_backward(torch.full_like(q, 100), q, k, v, o, lse)
+    want = 128 * 100 * math.exp(-18.0) / (1 + (Sk - 1) * math.exp(-18.0))
+    weak = torch.cat([dv[0, :7], dv[0, 8:]]).double()
+    # the weight's rounding and the result's, the exponent's; half a step of the smallest numbers
+    assert float((weak - want).abs().max()) <= want * (2 * ref.U[F16] + 2 ** -14) + 2 ** -25
+
+
 # ---------------------------------------------------------------------------
 # Attention: non-finite rows beside rows and keys that are masked
 # ---------------------------------------------------------------------------
