@@ -702,7 +702,9 @@ int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const int
  *               h / (q_heads / kv_heads).
  *   Strides     {batch, token, head} in elements, multiples of 8 (a dimension
  *               of size 1 may have any); elements of a head are contiguous.
- *               Outputs' elements must not overlap.
+ *               Outputs' elements must not overlap, nor an output an input,
+ *               except in place: o may be q itself, dq o, dk and dv k or v
+ *               (the same address and strides).
  *   Query i sees key j when j < key_lengths[b] (all k_len keys without
  *   lengths), j <= i + k_len - q_len with `causal`, and j > i + k_len - q_len -
  *   window with window > 0. What lies past key_lengths is never used, whatever

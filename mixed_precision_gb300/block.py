@@ -319,7 +319,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal:
     Query i sees key j when j < key_lengths[b], j <= i + k_len - q_len
     (`causal`) and j > i + k_len - q_len - window (`window` > 0). A query that
     sees no key has o = 0 and lse = -inf. scale: default head_dim^-1/2. lse is
-    fp32 [batch, q_heads, q_len]."""
+    fp32 [batch, q_heads, q_len]. out may be q itself."""
     sizes, kv_shape = _attention_sizes(q, k, causal, window, key_lengths, scale)
     dtype, shape, device = q.dtype, q.shape, q.device
     qb, qt, qh, _ = _steps(q, "q", shape, dtype)
@@ -359,7 +359,8 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
                        stream=None):
     """(dq, dk, dv) from dout, the forward's tensors and the same mask; the
     probabilities are recomputed from lse. dk and dv are summed over the query
-    heads that share a key head."""
+    heads that share a key head. dq may be o itself, dk and dv k or v; they may
+    overlap no other input."""
     sizes, kv_shape = _attention_sizes(q, k, causal, window, key_lengths, scale)
     dtype, shape, device = q.dtype, q.shape, q.device
     qb, qt, qh, _ = _steps(q, "q", shape, dtype)

@@ -156,6 +156,62 @@ int check_disjoint(const int64_t s[3], const int64_t n[3], int64_t dim, const ch
   return ZERO_OK;
 }
 
+// A [batch, token, head, dim] tensor of 16-bit elements.
+struct View {
+  const void* base;
+  const int64_t *s, *n;
+  int64_t dim;
+  const char* name;
+
+  int64_t span() const {  // elements from the first to behind the last
+    int64_t e = dim;
+    for (int i = 0; i < 3; ++i) e += (n[i] - 1) * s[i];
+    return e;
+  }
+  // Where steps of the period are left out: the elements' extent in it; 0 if it
+  // is none (a stride above it that is no multiple).
+  int64_t extent(int64_t period) const {
+    int64_t e = dim;
+    for (int i = 0; i < 3; ++i) {
+      if (n[i] == 1 || s[i] % period == 0) continue;
+      if (s[i] > period) return 0;
+      e += (n[i] - 1) * s[i];
+    }
+    return e <= period ? e : 0;
+  }
+};
+
+bool same_place(const View& x, const View& y) {
+  bool same = x.base == y.base;
+  for (int i = 0; i < 3; ++i) same = same && x.n[i] == y.n[i] && (x.n[i] == 1 || x.s[i] == y.s[i]);
+  return same;
+}
+
+// Whether no element of x is one of y's: their ranges are apart, or they lie side
+// by side in the steps of one of their strides (heads of one projection, halves
+// of one row). Interleaved in any other way they count as overlapping.
+bool apart(const View& x, const View& y) {
+  for (int i = 0; i < 3; ++i)
+    if (x.n[i] == 0 || y.n[i] == 0) return true;
+  const int64_t d = (static_cast<const char*>(y.base) - static_cast<const char*>(x.base)) / 2;
+  if (d >= x.span() || -d >= y.span()) return true;
+  for (const View* v : {&x, &y})
+    for (int i = 0; i < 3; ++i) {
+      const int64_t period = v->s[i], ex = x.extent(period), ey = y.extent(period);
+      if (v->n[i] == 1 || ex == 0 || ey == 0) continue;
+      const int64_t r = (d % period + period) % period;
+      if (r >= ex && r + ey <= period) return true;
+    }
+  return false;
+}
+
+// An output may not overlap an input that is read after it has been written.
+// in_place: but be exactly it, where each element is read by whom it is written.
+int check_output(const View& out, const View& in, bool in_place) {
+  if ((in_place && same_place(out, in)) || apart(out, in)) return ZERO_OK;
+  return fail(ZERO_ERR_INVALID, "%s overlaps %s", out.name, in.name);
+}
+
 int attention_args(const zero_attention_desc* d, bool backward, AttnArgs& a) {
   if (d == nullptr) return fail(ZERO_ERR_INVALID, "desc is NULL");
   if (d->batch < 0 || d->batch > kMaxLen || d->q_len < 0 || d->q_len > kMaxLen || d->k_len < 0 ||
@@ -448,6 +504,11 @@ int zero_attention_forward(const zero_attention_desc* desc, const void* q, const
   NEED(lse);
   if ((reinterpret_cast<uintptr_t>(key_lengths) & 3u) != 0)
     return fail(ZERO_ERR_INVALID, "key_lengths is not 4-byte aligned");
+  const int64_t nq[3] = {a.batch, a.q_len, a.q_heads}, nk[3] = {a.batch, a.k_len, a.kv_heads}, dim = a.head_dim;
+  const View to{o, a.os, nq, dim, "o"};
+  if (int rc = check_output(to, {q, a.qs, nq, dim, "q"}, true)) return rc;
+  if (int rc = check_output(to, {k, a.ks, nk, dim, "k"}, false)) return rc;
+  if (int rc = check_output(to, {v, a.vs, nk, dim, "v"}, false)) return rc;
   a.q = q;
   a.k = k;
   a.v = v;
@@ -495,6 +556,20 @@ int zero_attention_backward(const zero_attention_desc* desc, const void* dout, c
   }
   if ((reinterpret_cast<uintptr_t>(key_lengths) & 3u) != 0)
     return fail(ZERO_ERR_INVALID, "key_lengths is not 4-byte aligned");
+  const int64_t nq[3] = {a.batch, a.q_len, a.q_heads}, nk[3] = {a.batch, a.k_len, a.kv_heads}, dim = a.head_dim;
+  const View tq{dq, a.dqs, nq, dim, "dq"}, tk{dk, a.dks, nk, dim, "dk"}, tv{dv, a.dvs, nk, dim, "dv"};
+  const View from_q{q, a.qs, nq, dim, "q"}, from_do{dout, a.dos, nq, dim, "dout"}, from_k{k, a.ks, nk, dim, "k"},
+      from_v{v, a.vs, nk, dim, "v"}, from_o{o, a.os, nq, dim, "o"};
+  const struct {
+    const View &out, &in;
+    bool in_place;
+  } pairs[] = {
+      {tq, from_q, false}, {tq, from_do, false}, {tq, from_k, false}, {tq, from_v, false}, {tq, from_o, true},
+      {tk, from_q, false}, {tk, from_do, false}, {tk, from_k, true},  {tk, from_v, true},  {tv, from_q, false},
+      {tv, from_do, false}, {tv, from_k, true},  {tv, from_v, true},  {tq, tk, false},     {tq, tv, false},
+      {tk, tv, false}};
+  for (const auto& p : pairs)
+    if (int rc = check_output(p.out, p.in, p.in_place)) return rc;
   a.dout = dout;
   a.q = q;
   a.k = k;

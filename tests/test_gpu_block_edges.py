@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import _block_ref as ref
+from mixed_precision_gb300 import _abi as abi
 from mixed_precision_gb300 import block
 
 pytestmark = pytest.mark.gpu
@@ -210,6 +211,57 @@ def test_attention_what_nobody_sees_stays_zero(dtype, D):
     assert bool((dq[:, :100] == 0).all())
     assert bool((dk[1, 150:] == 0).all()) and bool((dv[1, 150:] == 0).all())
     assert bool(dv[1, :150].isnan().any())
+
+
+# ---------------------------------------------------------------------------
+# Attention: outputs in the place of inputs
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,D", [(F16, 64), (BF16, 128), (BF16, 72)])
+def test_attention_in_place(dtype, D):
+    q, k, v, do = qkv(gen(D), 3, 700, 500, 4, 2, D, dtype)
+    lengths = torch.tensor([500, 0, 333], dtype=torch.int32, device="cuda")
+    mask = dict(causal=True, key_lengths=lengths)
+    o, lse = block.attention_forward(q, k, v, **mask)
+    want = block.attention_backward(do, q, k, v, o, lse, **mask)
+    held = q.clone()
+    o2, lse2 = block.attention_forward(held, k, v, out=held, **mask)
+    assert o2 is held and same_bits(o, o2) and same_bits(lse, lse2)
+    for first in (0, 1):  # dk over k and dv over v, and the other way round
+        a, b, c = o.clone(), k.clone(), v.clone()
+        places = (b, c) if first == 0 else (c, b)
+        got = block.attention_backward(do, q, b, c, a, lse, dq=a, dk=places[0], dv=places[1], **mask)
+        assert all(same_bits(x, y) for x, y in zip(got, want))
+
+
+def test_attention_gradients_in_one_buffer():
+    """q, k and v as parts of a projection's rows, dq, dk and dv as parts of its gradient."""
+    g = gen(4)
+    B, S, H, K, D = 2, 300, 4, 2, 64
+    rows = normal(g, B, S, H + 2 * K, D, dtype=BF16)
+    grad = torch.full_like(rows, math.nan)
+    parts = lambda t: (t[:, :, :H], t[:, :, H:H + K], t[:, :, H + K:])  # noqa: E731
+    q, k, v = parts(rows)
+    do = normal(g, B, S, H, D, dtype=BF16)
+    o, lse = block.attention_forward(q, k, v, causal=True)
+    dq, dk, dv = parts(grad)
+    block.attention_backward(do, q, k, v, o, lse, causal=True, dq=dq, dk=dk, dv=dv)
+    want = block.attention_backward(do, *(t.contiguous() for t in (q, k, v)), o, lse, causal=True)
+    assert same_bits(grad, torch.cat(want, 2))
+
+
+def test_attention_refuses_outputs_over_inputs():
+    q, k, v, do = qkv(gen(5), 1, 64, 64, 2, 2, 64, BF16)
+    o, lse = block.attention_forward(q, k, v)
+    for call in (lambda: block.attention_forward(q, k, v, out=k), lambda: block.attention_forward(q, k, v, out=v),
+                 lambda: block.attention_backward(do, q, k, v, o, lse, dq=q),
+                 lambda: block.attention_backward(do, q, k, v, o, lse, dq=do),
+                 lambda: block.attention_backward(do, q, k, v, o, lse, dk=q),
+                 lambda: block.attention_backward(do, q, k, v, o, lse, dv=do),
+                 lambda: block.attention_backward(do, q, k, v, o, lse, dk=k, dv=k)):
+        with pytest.raises(abi.ZeroError) as e:
+            call()
+        assert e.value.code == abi.ZERO_ERR_INVALID
 
 
 # ---------------------------------------------------------------------------
