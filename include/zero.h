@@ -641,7 +641,8 @@ typedef struct {
  *   residual   may be NULL; then sum_out must be NULL too.
  *   sum_out    receives s (required with a residual); may be x or residual
  *              itself when that one's stride is cols.
- *   y          may be NULL when only the packed copy is wanted.
+ *   y          may be NULL when only the packed copy is wanted; may be x or the
+ *              residual itself when that one's stride is cols, not sum_out.
  *   q, scales  both NULL, or a packed activation of rows x cols that receives
  *              exactly what zero_act_pack makes of y.
  *   rstd       fp32 [rows]; may be NULL. */

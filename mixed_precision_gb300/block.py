@@ -184,7 +184,8 @@ def rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, re
     y = s * rstd * weight, rstd = (mean(s^2) + eps)^(-1/2) in fp32.
 
     `packed` also receives y in 8 bits, from the same pass; with want_out=False
-    y is not written (returned as None). sum_out may be x or residual itself."""
+    y is not written (returned as None). sum_out may be x or residual itself, out
+    too if it is not sum_out."""
     shape, dtype, device = x.shape, x.dtype, x.device
     code, wcode = DTYPE_CODE.get(dtype), DTYPE_CODE.get(weight.dtype)
     if code is None or len(shape) != 2:

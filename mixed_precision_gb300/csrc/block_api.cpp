@@ -299,6 +299,11 @@ int zero_rmsnorm_forward(const zero_rmsnorm_desc* desc, const void* x, const voi
   } else if (sum_out != nullptr) {
     return fail(ZERO_ERR_INVALID, "sum_out without a residual");
   }
+  if (y != nullptr) {
+    if (y == sum_out) return fail(ZERO_ERR_INVALID, "y may not be sum_out itself");
+    if ((y == x && desc->x_stride != desc->cols) || (y == residual && desc->residual_stride != desc->cols))
+      return fail(ZERO_ERR_INVALID, "y may be an input itself only when its stride is cols");
+  }
   if ((q == nullptr) != (scales == nullptr))
     return fail(ZERO_ERR_INVALID, "q and scales come together");
   if (q != nullptr) {

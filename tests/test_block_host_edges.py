@@ -5,7 +5,7 @@ import itertools
 import pytest
 import torch
 
-from test_block_host import P, attention, refused, z  # noqa: F401
+from test_block_host import P, attention, norm, refused, z  # noqa: F401
 
 # batch 2, 10 queries of 4 heads, 12 keys of 2 heads, head_dim 64, in bytes
 NQ, NK = 2 * 10 * 256 * 2, 2 * 12 * 128 * 2
@@ -84,3 +84,13 @@ def test_attention_outputs_side_by_side(z):  # noqa: F811
     part = dict(q=P, k=P + 512, v=P + 768, dq=P + 1024, dk=P + 1536, dv=P + 1792)
     accepted(z, *backward(z, rows, **part))
     refused(z, *backward(z, rows, **{**part, "dv": P + 2048 - 128}))
+
+
+def test_norm_outputs_in_place(z):  # noqa: F811
+    call = z.zero_rmsnorm_forward
+    accepted(z, call, norm(z), P, 0, 2 * P, 0, P, 0, 0, 0, 0)
+    accepted(z, call, norm(z), P, 3 * P, 2 * P, P, 3 * P, 0, 0, 0, 0)
+    refused(z, call, norm(z), P, 3 * P, 2 * P, 4 * P, 4 * P, 0, 0, 0, 0)  # the sum would be lost
+    refused(z, call, norm(z), P, 3 * P, 2 * P, P, P, 0, 0, 0, 0)
+    refused(z, call, norm(z, x_stride=72), P, 0, 2 * P, 0, P, 0, 0, 0, 0)  # rows not yet read
+    refused(z, call, norm(z, residual_stride=72), P, 3 * P, 2 * P, 4 * P, 3 * P, 0, 0, 0, 0)

@@ -36,6 +36,24 @@ def qkv(g, B, Sq, Sk, H, K, D, dtype, dout=0.1):
 
 
 # ---------------------------------------------------------------------------
+# RMSNorm: outputs in the place of inputs
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,cols", [(50, 1024), (7, 33), (3000, 520), (300, 4100)])
+def test_norm_in_place(rows, cols):
+    g = gen(cols)
+    x, res, w = normal(g, rows, cols, dtype=BF16), normal(g, rows, cols, dtype=BF16), normal(g, cols, dtype=BF16)
+    y, s, rstd = block.rmsnorm_forward(x, w, residual=res)
+    a, b = x.clone(), res.clone()
+    got = block.rmsnorm_forward(a, w, residual=b, out=b, sum_out=a)
+    assert all(same_bits(p, q) for p, q in zip(got, (y, s, rstd)))
+    a = s.clone()
+    assert same_bits(block.rmsnorm_forward(a, w, out=a)[0], y)
+    with pytest.raises(abi.ZeroError):
+        block.rmsnorm_forward(x, w, residual=res, out=a, sum_out=a)
+
+
+# ---------------------------------------------------------------------------
 # Attention: infinities in q
 # ---------------------------------------------------------------------------
 
