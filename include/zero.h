@@ -684,7 +684,9 @@ int zero_act_unpack(const int8_t* q, const uint8_t* scales, int64_t rows, int64_
 
 /* Weight gradient of a linear layer y = x W^T from its packed input:
  * dw[n_out, n_in] = dy^T X, X = the packed activation (tokens x n_in) restored
- * in dy's type; fp32 sums, rounded once to dw_dtype.
+ * in dy's type; fp32 sums, rounded once to dw_dtype. (The tensor cores truncate
+ * where they add: to 16 bits by up to a fifth of that type's rounding, to fp32
+ * up to 2e-6 of the result, where all terms have one sign; far less otherwise.)
  *   dy          [tokens, n_out] ZERO_F16 or ZERO_BF16, dy_stride elements
  *               between rows (a multiple of 8).
  *   dw_dtype    ZERO_F32 or dy's type.

@@ -41,11 +41,18 @@ constexpr int kRedRows = 128;
 
 // Steps whose sums stay in one accumulator when dw is fp32. The tensor core
 // truncates each addition to the running sum, so its error grows with the
-// number of additions in a row: 6.6e-6 of the result after 512 of them (8192
-// tokens). After 16 steps (64 additions) the sums are moved to a second
-// accumulator with rounded additions, which keeps the error below 1e-6. A
-// 16-bit dw is rounded 1000 times more coarsely and skips this.
+// number of additions in a row, four a step: with terms all of one sign by up to
+// 9e-8 of the result each (2048 of them 1.8e-4, 8192 7.5e-4), on normal data by
+// less (6.6e-6 after 512). After 16 steps the sums are moved to a second
+// accumulator with rounded additions, which keeps the error of one sign at 1.4e-6
+// (fp16 dy; 3e-7 with bf16, whose products have fewer bits to lose).
 constexpr int kRun = 16;
+
+// A 16-bit dw does without (its tiles may be wider: 335 against 520 us at 4096 x
+// 8192 x 8192) until a block's own run of tokens is so long that truncations of one
+// sign come to a fifth (fp16) or a tenth (bf16) of the type's rounding: 9e-8 x 4 x
+// 256 = 9e-5 of 4.9e-4, 9e-8 x 4 x 1024 = 3.7e-4 of 3.9e-3.
+constexpr int64_t kLongRunF16 = 256, kLongRunBF16 = 1024;
 
 // ROUND: with the second accumulator, MT x BN columns further.
 template <int MT, int BN, bool ROUND>
@@ -557,8 +564,13 @@ cudaError_t run(const WgradArgs& a, int split, cudaStream_t s) {
 template <typename T>
 cudaError_t wgrad_t(const WgradArgs& a, int sms, cudaStream_t s) {
   // sums of up to kRun steps stay in one accumulator either way
-  const bool round = a.dw_dtype == kF32 && a.tokens > kRun * kStep;
-  const Plan p = wgrad_plan(a.tokens, a.n_out, a.n_in, round, sms);
+  bool round = a.dw_dtype == kF32 && a.tokens > kRun * kStep;
+  Plan p = wgrad_plan(a.tokens, a.n_out, a.n_in, round, sms);
+  const int64_t steps = (a.tokens + kStep - 1) / kStep;
+  if (!round && (steps + p.split - 1) / p.split > (a.dtype == kF16 ? kLongRunF16 : kLongRunBF16)) {
+    round = true;
+    p = wgrad_plan(a.tokens, a.n_out, a.n_in, round, sms);
+  }
   if (round) return p.mt == 2 ? run<T, 2, 128, true>(a, p.split, s) : run<T, 1, 128, true>(a, p.split, s);
   if (p.bn == 256) return run<T, 2, 256, false>(a, p.split, s);
   return p.mt == 2 ? run<T, 2, 128, false>(a, p.split, s) : run<T, 1, 128, false>(a, p.split, s);

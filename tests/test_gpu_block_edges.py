@@ -301,3 +301,26 @@ def test_weight_grad_of_the_widest_rows():
     want = float((dy[:, 0].double() * codes).sum())  # small whole numbers: exact
     assert bool((dw == want).all())
     block.check()
+
+
+@pytest.mark.parametrize("dtype,tokens", [(F16, 1 << 20), (F16, 1 << 18), (BF16, 1 << 20)])
+def test_weight_grad_of_many_tokens(dtype, tokens):
+    """16-bit results of very long sums of one sign, which are made in rounded runs:
+    the sums' own error stays below a sixteenth of the type's rounding. The mean
+    over the outputs, spread over a binade, averages the rounding away (as it does
+    for the exact sums)."""
+    g = gen(3)
+    n_out, n_in = 128, 128
+    spread = torch.exp2(torch.rand(n_out, generator=g, device="cuda")) * (256 / tokens)
+    dy = ((torch.rand(tokens, n_out, generator=g, device="cuda") + 0.5) * spread).to(dtype)
+    x = ((torch.rand(tokens, n_in, generator=g, device="cuda") + 0.5) *
+         torch.exp2(torch.rand(n_in, generator=g, device="cuda"))).to(dtype)
+    p = block.PackedActivation(tokens, n_in).save(x)
+    dw = block.weight_grad(dy, p)
+    want = dy.double().t() @ p.restore(dtype).double()
+    u, n = ref.U[dtype], want.numel()
+    rounded = (want.to(dtype).double() - want) / want
+    assert float(rounded.mean().abs()) < 6 * u / math.sqrt(3 * n)
+    rel = (dw.double() - want) / want
+    assert float(rel.mean().abs()) < u / 16 + 6 * u / math.sqrt(3 * n)
+    assert float(rel.abs().max()) < u + u / 16
