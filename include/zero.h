@@ -613,9 +613,10 @@ int zero_dist_update_buckets(zero_layout_t* layout, const void* allreduced, int 
 /* taken from them, and attention's training pair. They need no layout. All   */
 /* buffers are the caller's; calls only enqueue kernels on `stream` (no       */
 /* allocation, no host synchronisation), so they can be captured into a CUDA  */
-/* graph. Results do not depend on timing: no atomic adds of values, every    */
-/* sum has a fixed order for given sizes. Non-finite inputs propagate to the  */
-/* outputs that depend on them, so the step's overflow check sees them.       */
+/* graph. Results do not depend on timing: every sum has a fixed order for    */
+/* given sizes, no element is added to from two places in one call.           */
+/* Non-finite inputs propagate to the outputs that depend on them, so the     */
+/* step's overflow check sees them.                                           */
 /* ------------------------------------------------------------------------ */
 
 /* Rows of an RMSNorm call. Strides are in elements between the starts of two

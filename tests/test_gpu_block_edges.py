@@ -1,6 +1,7 @@
 """The block operators at their edges: the largest sizes they take, infinities in
 queries, fp16 gradients far from one, non-finite rows beside masked ones, every
 way out of the weight gradient, outputs in place of inputs, scratch sizes."""
+import ctypes
 import math
 
 import pytest
@@ -33,6 +34,19 @@ def same_bits(a, b):
 def qkv(g, B, Sq, Sk, H, K, D, dtype, dout=0.1):
     return (normal(g, B, Sq, H, D, dtype=dtype), normal(g, B, Sk, K, D, dtype=dtype, scale=1.5),
             normal(g, B, Sk, K, D, dtype=dtype), normal(g, B, Sq, H, D, dtype=dtype, scale=dout))
+
+
+class Guarded:
+    """A tensor of the given shape between two guard regions of a pattern."""
+
+    def __init__(self, shape, dtype):
+        n = math.prod(shape) * torch.empty(0, dtype=dtype).element_size()
+        self.raw = torch.full((8192 + (n + 15) // 16 * 16,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.n = n
+        self.t = self.raw[4096:4096 + n].view(dtype).view(shape)
+
+    def intact(self):
+        return bool((self.raw[:4096] == 0xA5).all()) and bool((self.raw[4096 + self.n:] == 0xA5).all())
 
 
 # ---------------------------------------------------------------------------
@@ -303,6 +317,56 @@ def test_weight_grad_of_the_widest_rows():
     block.check()
 
 
+# few and many tokens; outputs that fill the machine (a tile's sums leave by bulk
+# stores or additions) or do not (clusters); rows that are whole vectors or not;
+# above 1024 tokens fp32 sums are moved in rounded runs
+@pytest.mark.parametrize("tokens,n_out,n_in", [
+    (130, 5000, 4104), (1000, 4104, 5000), (1024, 8200, 2056), (1030, 3000, 4100), (1100, 4104, 5000), (2500, 5001, 4100),
+    (1100, 4100, 4105), (200, 3001, 4110), (3000, 300, 520), (700, 136, 521), (65, 40, 72), (1500, 20, 33)])
+def test_weight_grad_accumulates_every_way_out(tokens, n_out, n_in):
+    g = gen(tokens + n_out)
+    pad = (-n_out) % 8
+    def micro(seed):
+        dy = normal(gen(seed), tokens, n_out + pad, dtype=BF16)[:, :n_out]
+        return dy, block.PackedActivation(tokens, n_in).save(normal(gen(seed + 1), tokens, n_in, dtype=BF16, scale=2))
+    main = normal(g, n_out, n_in)
+    out = Guarded((n_out, n_in), F32)
+    out.t.copy_(main)
+    want, size = main.double(), main.double().abs()
+    total = main.clone()
+    for seed in (11, 21):  # two micro-batches in a row
+        dy, p = micro(seed)
+        one = block.weight_grad(dy, p, dtype=F32)
+        block.weight_grad(dy, p, out=out.t, accumulate=True)
+        total += one  # the addition to what is there is one fp32 rounding
+        assert same_bits(out.t, total) and out.intact()
+        x = p.restore(BF16).double()
+        want = want + dy.double().t() @ x
+        size = size + dy.double().abs().t() @ x.abs()
+    ref.close(out.t, want, (tokens / 8 + 32) * 2 * ref.E * size + 4 * ref.E * want.abs(), "dw")
+    plain = Guarded((n_out, n_in), F32)
+    block.weight_grad(dy, p, out=plain.t)
+    assert same_bits(plain.t, one) and plain.intact()
+    block.check()
+
+
+@pytest.mark.parametrize("tokens,n_out,n_in", [(8192, 264, 328), (8192, 4096, 4096), (40000, 64, 96)])
+def test_weight_grad_fp32_sums_are_rounded(tokens, n_out, n_in):
+    """Sums of one sign, where truncated additions would all err the same way. A run
+    of 64 additions is off by 64 truncations of at most 2^-24 of it (2^-18), the runs'
+    rounded sums by one rounding each in random directions (2^-24 sqrt(runs) in the
+    mean, six times that at the worst of all outputs)."""
+    g = gen(tokens)
+    dy = (torch.rand(tokens, n_out, generator=g, device="cuda") + 0.5).to(BF16)
+    x = (torch.rand(tokens, n_in, generator=g, device="cuda") + 0.5).to(BF16)
+    p = block.PackedActivation(tokens, n_in).save(x)
+    dw = block.weight_grad(dy, p, dtype=F32)
+    n = min(n_out, 256)  # columns are enough
+    want = dy[:, :n].double().t() @ p.restore(BF16).double()
+    rel = (dw[:n].double() - want) / want
+    assert float(rel.mean().abs()) < 1e-6 and float(rel.abs().max()) < 1e-6 + 6 * ref.E * math.sqrt(tokens / 1024)
+
+
 @pytest.mark.parametrize("dtype,tokens", [(F16, 1 << 20), (F16, 1 << 18), (BF16, 1 << 20)])
 def test_weight_grad_of_many_tokens(dtype, tokens):
     """16-bit results of very long sums of one sign, which are made in rounded runs:
@@ -324,3 +388,45 @@ def test_weight_grad_of_many_tokens(dtype, tokens):
     rel = (dw.double() - want) / want
     assert float(rel.mean().abs()) < u / 16 + 6 * u / math.sqrt(3 * n)
     assert float(rel.abs().max()) < u + u / 16
+
+
+# ---------------------------------------------------------------------------
+# Scratch of exactly the reported size
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,cols,pad", [(1, 8, 0), (33, 1024, 0), (700, 3000, 0), (2500, 2048, 0), (5000, 512, 8),
+                                           (65536, 128, 0), (40000, 256, 0), (777, 33, 0), (50, 72, 3), (3, 20000, 0)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_norm_backward_scratch_is_enough(rows, cols, pad, dtype):
+    g = gen(rows)
+    x, dy, dsum = (normal(g, rows, cols + pad, dtype=dtype)[:, :cols] for _ in range(3))
+    w = normal(g, cols, dtype=dtype)
+    rstd = x.float().square().mean(1).rsqrt()
+    code = block.DTYPE_CODE[dtype]
+    desc = abi.RMSNORM_DESC.pack(rows, cols, *[cols + pad if rows > 1 else cols] * 3, code, code, 0.0)
+    space = Guarded((abi.zero_rmsnorm_backward_workspace(desc),), torch.uint8)
+    for extra in (None, dsum):
+        dx, dw = torch.empty(rows, cols, dtype=dtype, device="cuda"), torch.empty(cols, device="cuda")
+        abi.zero_rmsnorm_backward(desc, dy.data_ptr(), x.data_ptr(), w.data_ptr(), rstd.data_ptr(),
+                                  None if extra is None else extra.data_ptr(), dx.data_ptr(), dw.data_ptr(), abi.ZERO_F32,
+                                  space.t.data_ptr(), space.n, torch.cuda.current_stream().cuda_stream)
+        want = block.rmsnorm_backward(dy, x, w, rstd, dsum=extra, dweight_dtype=F32)
+        assert same_bits(dx, want[0]) and same_bits(dw, want[1]) and space.intact()
+
+
+@pytest.mark.parametrize("B,Sq,Sk,H,K,D", [(1, 1, 1, 1, 1, 8), (2, 300, 200, 4, 2, 64), (3, 129, 700, 6, 1, 128),
+                                           (5, 100, 1000, 5, 5, 72), (40, 100, 130, 1, 1, 64)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_backward_scratch_is_enough(B, Sq, Sk, H, K, D, dtype):
+    q, k, v, do = qkv(gen(B), B, Sq, Sk, H, K, D, dtype)
+    o, lse = block.attention_forward(q, k, v, causal=True)
+    tensors = (q, k, v, o, do, q, k, v)
+    desc = abi.zero_attention_desc(B, Sq, Sk, H, K, D, block.DTYPE_CODE[dtype], 1, 0, 0, D ** -0.5,
+                                   *[(ctypes.c_int64 * 3)(*t.stride()[:3]) for t in tensors])
+    space = Guarded((abi.zero_attention_backward_workspace(desc),), torch.uint8)
+    out = [torch.empty_like(t) for t in (q, k, v)]
+    abi.zero_attention_backward(desc, do.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                None, *[t.data_ptr() for t in out], space.t.data_ptr(), space.n,
+                                torch.cuda.current_stream().cuda_stream)
+    want = block.attention_backward(do, q, k, v, o, lse, causal=True)
+    assert all(same_bits(a, b) for a, b in zip(out, want)) and space.intact()
