@@ -749,11 +749,18 @@ int zero_attention_backward(const zero_attention_desc* desc, const void* dout, c
                             const int32_t* key_lengths, void* dq, void* dk, void* dv,
                             void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Whether a bounded device wait gave up in one of these operators since the
- * last call: ZERO_ERR_TIMEOUT if so (the outputs of the calls since then are
- * not to be used), ZERO_OK otherwise. Clears the mark. Synchronises `stream`;
- * covers the current device. */
+/* Whether a bounded device wait gave up in one of these operators, on any stream
+ * of the current device, since this thread's last call (its first: since the
+ * start): ZERO_ERR_TIMEOUT if so (the outputs of the calls since then are not to
+ * be used), ZERO_OK otherwise. Every thread is told once. Synchronises `stream`;
+ * what other streams have still to do is not waited for. */
 int zero_operator_status(void* stream);
+
+/* Enqueues a kernel whose bounded wait gives up after spin_limit tries (1..2^22)
+ * and records it as a block operator's does: of RMSNorm (kernels 0), the weight
+ * gradient (1), attention forward (2) or backward (3). The next
+ * zero_operator_status then returns ZERO_ERR_TIMEOUT. */
+int zero_selftest_operator_timeout(int kernels, uint32_t spin_limit, void* stream);
 
 /* Message for the last failing call on this thread ("" if none). The pointer
  * stays valid until the next failing call on this thread. */

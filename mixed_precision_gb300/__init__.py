@@ -20,6 +20,7 @@ from ._abi import (ZERO_BF16, ZERO_MAX_ELEMS, ZERO_STATE_BLOB_BYTES, zero_accumu
                    zero_rmsnorm_backward_workspace, zero_act_layout, zero_act_pack, zero_act_unpack,
                    zero_act_weight_grad, zero_act_weight_grad_workspace, zero_attention_desc,
                    zero_attention_forward, zero_attention_backward,
-                   zero_attention_backward_workspace, zero_operator_status, lib)
+                   zero_attention_backward_workspace, zero_operator_status,
+                   zero_selftest_operator_timeout, lib)
 
 __all__ = [n for n in dir() if n.startswith("zero_") or n.startswith("ZERO_")] + ["ZeroError", "lib"]

@@ -159,6 +159,7 @@ def lib() -> ctypes.CDLL:
             "zero_attention_backward_workspace": [P, ctypes.POINTER(I64)],
             "zero_attention_backward": [P] * 12 + [I64, P],
             "zero_operator_status": [P],
+            "zero_selftest_operator_timeout": [I, ctypes.c_uint32, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -453,5 +454,9 @@ def zero_attention_backward(desc, dout: int, q: int, k: int, v: int, o: int,
 
 
 def zero_operator_status(stream: int) -> None:
-    """Raises ZeroError(ZERO_ERR_TIMEOUT) if a bounded wait gave up since the last call."""
+    """Raises ZeroError(ZERO_ERR_TIMEOUT) if a bounded wait gave up since this thread's last call."""
     _check(lib().zero_operator_status(stream or None))
+
+
+def zero_selftest_operator_timeout(kernels: int, spin_limit: int, stream: int) -> None:
+    _check(lib().zero_selftest_operator_timeout(kernels, spin_limit, stream or None))

@@ -402,5 +402,6 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
 
 def check(stream=None) -> None:
     """Raise ZeroError(ZERO_ERR_TIMEOUT) if a kernel of this module gave up a
-    bounded wait since the last check. Synchronises the stream."""
+    bounded wait, on any stream of the device, since this thread's last check.
+    Synchronises the stream."""
     abi.zero_operator_status((stream or torch.cuda.current_stream()).cuda_stream)

@@ -103,11 +103,14 @@ cudaError_t launch_attention_forward(const AttnArgs& a, int sms, cudaStream_t s)
 int64_t attention_backward_bytes(const AttnArgs& a);
 cudaError_t launch_attention_backward(const AttnArgs& a, int sms, cudaStream_t s);
 
-// The kernels' error words on the current device (bit kErrWaitTimeout): *value
-// |= the word, which is cleared. Each synchronises the stream.
-cudaError_t norm_error(unsigned* value, cudaStream_t s);
-cudaError_t wgrad_error(unsigned* value, cudaStream_t s);
-cudaError_t attn_fwd_error(unsigned* value, cudaStream_t s);
-cudaError_t attn_bwd_error(unsigned* value, cudaStream_t s);
+// Where the kernels' error words are on the current device: each counts the waits
+// that gave up, and is never cleared.
+cudaError_t norm_error(unsigned** at);
+cudaError_t wgrad_error(unsigned** at);
+cudaError_t attn_fwd_error(unsigned** at);
+cudaError_t attn_bwd_error(unsigned** at);
+
+// A kernel whose one wait gives up after `limit` tries (k_misc.cu).
+cudaError_t launch_wait_that_gives_up(unsigned* error, uint32_t limit, cudaStream_t s);
 
 }  // namespace zg

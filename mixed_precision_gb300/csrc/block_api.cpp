@@ -276,6 +276,9 @@ int attention_args(const zero_attention_desc* d, bool backward, AttnArgs& a) {
   return ZERO_OK;
 }
 
+constexpr int kErrorWords = 4;
+cudaError_t (*const kErrorWord[kErrorWords])(unsigned**) = {norm_error, wgrad_error, attn_fwd_error, attn_bwd_error};
+
 }  // namespace
 
 extern "C" {
@@ -594,16 +597,40 @@ int zero_attention_backward(const zero_attention_desc* desc, const void* dout, c
 
 int zero_operator_status(void* stream) {
   Range r("zero_operator_status");
-  unsigned error = 0;
-  cudaError_t (*const words[])(unsigned*, cudaStream_t) = {norm_error, wgrad_error,
-                                                            attn_fwd_error, attn_bwd_error};
-  for (auto word : words) {
-    cudaError_t e = word(&error, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e, "operator status");
+  constexpr int kDevices = 64;
+  // What the thread last saw. Device counts are never cleared, so no thread takes
+  // a time-out from another, and none is lost between a read and a write.
+  static thread_local unsigned seen[kDevices][kErrorWords];
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int dev = 0;
+  unsigned now[kErrorWords];
+  cudaError_t e = cudaGetDevice(&dev);
+  for (int i = 0; i < kErrorWords && e == cudaSuccess; ++i) {
+    unsigned* at = nullptr;
+    e = kErrorWord[i](&at);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(&now[i], at, sizeof(unsigned), cudaMemcpyDeviceToHost, s);
   }
-  if (error != 0)
-    return fail(ZERO_ERR_TIMEOUT, "a bounded wait gave up in a block operator");
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return cuda_fail(e, "operator status");
+  if (dev >= kDevices) return fail(ZERO_ERR_INVALID, "device %d", dev);
+  bool late = false;
+  for (int i = 0; i < kErrorWords; ++i) {
+    late = late || now[i] != seen[dev][i];
+    seen[dev][i] = now[i];
+  }
+  if (late) return fail(ZERO_ERR_TIMEOUT, "a bounded wait gave up in a block operator");
   return ZERO_OK;
+}
+
+int zero_selftest_operator_timeout(int kernels, uint32_t spin_limit, void* stream) {
+  Range r("zero_selftest_operator_timeout");
+  if (kernels < 0 || kernels >= kErrorWords)
+    return fail(ZERO_ERR_INVALID, "kernels %d outside 0..%d", kernels, kErrorWords - 1);
+  if (spin_limit < 1 || spin_limit > kSpinLimit) return fail(ZERO_ERR_INVALID, "spin_limit outside 1..2^22");
+  unsigned* at = nullptr;
+  cudaError_t e = kErrorWord[kernels](&at);
+  if (e == cudaSuccess) e = launch_wait_that_gives_up(at, spin_limit, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "operator self-test");
 }
 
 }  // extern "C"

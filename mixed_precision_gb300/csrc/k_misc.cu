@@ -1,6 +1,7 @@
-// Gradient accumulation into fp32 main gradients, and the self-test of the
-// bounded-wait path.
-#include "bulk.cuh"
+// Gradient accumulation into fp32 main gradients, and the self-tests of the
+// bounded-wait paths.
+#include "block.h"
+#include "tc.cuh"
 #include "vec.cuh"
 #include "zero.h"
 
@@ -70,6 +71,24 @@ __global__ void k_selftest_wait(uint32_t limit, unsigned* err) {
     g_selftest_error = code;
     if (err != nullptr && code != 0u) atomicOr(err, code);
   }
+}
+
+// A block operator's wait on a barrier that nothing arrives at.
+__global__ void k_wait_that_gives_up(unsigned* error, uint32_t limit) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ uint32_t abort_word;
+  if (threadIdx.x == 0) {
+    abort_word = 0;
+    mbar_init(&bar, 1);
+    mbar_init_fence();
+    const Waiter wait{&abort_word, error, limit};
+    wait(&bar, 0);
+  }
+}
+
+cudaError_t launch_wait_that_gives_up(unsigned* error, uint32_t limit, cudaStream_t s) {
+  k_wait_that_gives_up<<<1, 32, 0, s>>>(error, limit);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_selftest_wait(uint32_t limit, unsigned* err, cudaStream_t s) {

@@ -215,7 +215,7 @@ struct RowStream {
     if (row >= rows) return false;
     const bool late = !mbar_wait(&full[s], parity);
     if (!team_any(late, team, id)) return true;
-    if (late) atomicOr(&g_norm_error, kErrWaitTimeout);
+    if (late) atomicAdd(&g_norm_error, 1u);
     for (int i = 0; i < kStages && row + i * step < rows; ++i)
       mbar_wait(&full[(s + i) % kStages], parity ^ (s + i >= kStages), kSpinLimit >> 10);
     return false;

@@ -21,19 +21,20 @@ namespace zg {
 // ---- bounded waits -----------------------------------------------------------
 
 // Waits of one block. The first that gives up marks the block's `abort` word
-// and the device's error word; every other wait of the block then ends within a
-// few tries, so the block runs to its end without hanging.
+// and counts in the device's error word; every other wait of the block then ends
+// within a few tries, so the block runs to its end without hanging.
 struct Waiter {
   volatile uint32_t* abort;  // shared memory, zero at the start
   unsigned* error;           // device error word
+  uint32_t limit = kSpinLimit;
 
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    for (uint32_t i = 0; i < limit; ++i) {
       if (mbar_try_wait(bar, parity)) return true;
       if ((i & 7) == 7 && *abort != 0) return false;
     }
     *abort = 1;
-    atomicOr(error, kErrWaitTimeout);
+    atomicAdd(error, 1u);
     return false;
   }
   // Whether a wait of the block has given up. Asked after a barrier behind the
@@ -42,19 +43,9 @@ struct Waiter {
   __device__ __forceinline__ bool gave_up() const { return *abort != 0; }
 };
 
-// A translation unit's error word, read and cleared (host): *value |= the word.
-// Synchronises the stream.
-#define ZG_ERROR_WORD(name, word)                                                                          \
-  cudaError_t name(unsigned* value, cudaStream_t s) {                                                      \
-    unsigned now = 0;                                                                                      \
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&now, word, sizeof(now), 0, cudaMemcpyDeviceToHost, s);      \
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);                                                    \
-    if (e != cudaSuccess || now == 0) return e;                                                            \
-    *value |= now;                                                                                         \
-    const unsigned zero = 0;                                                                               \
-    e = cudaMemcpyToSymbolAsync(word, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);                  \
-    return e == cudaSuccess ? cudaStreamSynchronize(s) : e;                                                \
-  }
+// Where a translation unit's error word is on the current device (host).
+#define ZG_ERROR_WORD(name, word) \
+  cudaError_t name(unsigned** at) { return cudaGetSymbolAddress(reinterpret_cast<void**>(at), word); }
 
 // ---- TMEM --------------------------------------------------------------------
 

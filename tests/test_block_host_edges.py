@@ -94,3 +94,8 @@ def test_norm_outputs_in_place(z):  # noqa: F811
     refused(z, call, norm(z), P, 3 * P, 2 * P, P, P, 0, 0, 0, 0)
     refused(z, call, norm(z, x_stride=72), P, 0, 2 * P, 0, P, 0, 0, 0, 0)  # rows not yet read
     refused(z, call, norm(z, residual_stride=72), P, 3 * P, 2 * P, 4 * P, 3 * P, 0, 0, 0, 0)
+
+
+def test_operator_timeout_arguments(z):  # noqa: F811
+    for kernels, limit in ((-1, 100), (4, 100), (0, 0), (0, (1 << 22) + 1)):
+        refused(z, z.zero_selftest_operator_timeout, kernels, limit, 0)

@@ -3,6 +3,7 @@ queries, fp16 gradients far from one, non-finite rows beside masked ones, every
 way out of the weight gradient, outputs in place of inputs, scratch sizes."""
 import ctypes
 import math
+import threading
 
 import pytest
 import torch
@@ -430,3 +431,42 @@ def test_attention_backward_scratch_is_enough(B, Sq, Sk, H, K, D, dtype):
                                 torch.cuda.current_stream().cuda_stream)
     want = block.attention_backward(do, q, k, v, o, lse, causal=True)
     assert all(same_bits(a, b) for a, b in zip(out, want)) and space.intact()
+
+
+# ---------------------------------------------------------------------------
+# Waits that give up
+# ---------------------------------------------------------------------------
+
+def timed_out():
+    try:
+        block.check()
+    except abi.ZeroError as e:
+        assert e.code == abi.ZERO_ERR_TIMEOUT
+        return True
+    return False
+
+
+@pytest.mark.parametrize("kernels", range(4))
+def test_a_wait_that_gives_up_is_reported(kernels):
+    """Once, to every thread, from whichever stream; the operators run on."""
+    timed_out()  # what other tests may have left to this thread
+    assert not timed_out()
+    side = torch.cuda.Stream()
+    told = []
+
+    def other():
+        told.append(timed_out())  # a thread's first call tells it of all since the start
+        told.append(timed_out())
+        abi.zero_selftest_operator_timeout(kernels, 1000, side.cuda_stream)
+        side.synchronize()
+        told.append(timed_out())
+        told.append(timed_out())
+
+    t = threading.Thread(target=other)
+    t.start()
+    t.join()
+    assert told[1:] == [False, True, False]
+    assert timed_out() and not timed_out()
+    x, w = normal(gen(1), 4, 64), torch.ones(64, device="cuda")
+    y, _, _ = block.rmsnorm_forward(x, w)
+    assert bool(y.isfinite().all()) and not timed_out()
