@@ -692,7 +692,8 @@ int zero_act_unpack(const int8_t* q, const uint8_t* scales, int64_t rows, int64_
  *               between rows (a multiple of 8).
  *   dw_dtype    ZERO_F32 or dy's type.
  *   accumulate  1: dw += (ZERO_F32 only; fp32 main gradients), 0: dw =.
- *   workspace   zero_act_weight_grad_workspace bytes (NULL when that is 0). */
+ *   workspace   of zero_act_weight_grad_workspace bytes, which are 0 at every
+ *               size: not used, may be NULL. */
 int zero_act_weight_grad_workspace(int64_t tokens, int64_t n_out, int64_t n_in, int64_t* bytes);
 int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const int8_t* q,
                          const uint8_t* scales, int64_t tokens, int64_t n_out, int64_t n_in,

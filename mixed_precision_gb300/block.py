@@ -8,6 +8,10 @@ one, outputs and scratch are allocated on it and the inputs are marked as used
 on it, so the caching allocator reuses none of them too early; ordering the
 streams' work stays the caller's job, as with any torch operation.
 
+Nothing is recorded for autograd: the results carry no graph, also where an
+input requires a gradient, and the gradients come from the backward functions
+(called by hand, or in a torch.autograd.Function of the caller's).
+
 Wrong shapes, types, devices or layouts raise ValueError here, or ZeroError
 (ZERO_ERR_INVALID) from the library; nothing is enqueued then.
 
