@@ -747,8 +747,13 @@ cudaError_t run(const AttnArgs& a, int sms, cudaStream_t s) {
   e = allow_smem(k_attn_dkv<T, DP>, Dkv<DP>::kSmem, asked_dkv);
   if (e != cudaSuccess) return e;
   const int q_tiles = (int)tiles(a.q_len);
-  // Shares for dq also where attn_grid would take single blocks: with 6 x 1021,
-  // 12/4 heads of 64 and random lengths dq, dk and dv take 38 us, else 40.
+  // Shares for dq also where attn_grid would take single blocks (lengths, less than
+  // four pieces a multiprocessor): a block's next loads then start early, and there
+  // are heads x batch pieces of each size to even out. dq, dk and dv with random
+  // lengths, dq in shares against single blocks, 12/4 heads, window 256, 6 x 1021:
+  // of 64 38.5, 40.5 us, of 128 64.8, 67.6; 16/8 heads, causal: 8 x 512 of 64 39.0,
+  // 40.8, 4 x 512 of 128 35.2, 35.6, 3 x 1024 of 128 56.0, 56.9; no mask, 4 x 1024 82.0,
+  // 82.1. With lengths, dk and dv are the other way round (attn_grid).
   // Each kernel's blocks start while the last of the one before run, and wait for
   // it where they need its results.
   cudaLaunchConfig_t cfg{};
