@@ -717,7 +717,7 @@ int zero_act_weight_grad(const void* dy, int64_t dy_stride, int dtype, const int
  *   no gradient; a key that no query sees has dk = dv = 0. (A NaN or inf in a
  *   row of q, k, v or dout may also reach rows that see something but that the
  *   causal mask or the window keeps from it: a weight of 0 times it.)
- *   scale       of the products q.k; > 0. */
+ *   scale       of the products q.k; > 0, < 1e37. */
 typedef struct {
   int64_t batch, q_len, k_len; /* lengths up to 2^28 */
   int32_t q_heads, kv_heads, head_dim;

@@ -224,8 +224,8 @@ int attention_args(const zero_attention_desc* d, bool backward, AttnArgs& a) {
     return fail(ZERO_ERR_INVALID, "head_dim %d: multiples of 8 up to 128", d->head_dim);
   if (!half_dtype(d->dtype)) return fail(ZERO_ERR_INVALID, "dtype %d: fp16 or bf16", d->dtype);
   if (d->window < 0) return fail(ZERO_ERR_INVALID, "window %lld < 0", (long long)d->window);
-  if (!(d->scale > 0.0) || !std::isfinite(d->scale))
-    return fail(ZERO_ERR_INVALID, "scale %g is not a finite number > 0", d->scale);
+  if (!(d->scale > 0.0) || !(d->scale < 1e37))  // in powers of two, times log2 e, still an fp32 number
+    return fail(ZERO_ERR_INVALID, "scale %g is not between 0 and 1e37", d->scale);
   // row counts and tile counts stay inside the kernels' index types
   if ((double)d->batch * d->q_heads * ((double)d->q_len + 128) > 2e11 ||
       (double)d->batch * d->kv_heads * ((double)d->k_len + 128) > 2e11)

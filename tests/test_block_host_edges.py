@@ -99,3 +99,9 @@ def test_norm_outputs_in_place(z):  # noqa: F811
 def test_operator_timeout_arguments(z):  # noqa: F811
     for kernels, limit in ((-1, 100), (4, 100), (0, 0), (0, (1 << 22) + 1)):
         refused(z, z.zero_selftest_operator_timeout, kernels, limit, 0)
+
+
+@pytest.mark.parametrize("scale", [1e37, 1e39, 1e300, float("inf")])
+def test_attention_scale_beyond_fp32(z, scale):  # noqa: F811
+    refused(z, *forward(z, attention(z, scale=scale)))
+    accepted(z, *forward(z, attention(z, scale=9e36)))
