@@ -596,7 +596,8 @@ constexpr int kSmemPerSm = 220 * 1024;
 // direct against through shared memory, bf16 with dsum:
 //   16384 x 1024   33.1, 28.7     4096 x 8192   74.6, 56.8    1024 x 1024   7.7, 6.9
 //   16384 x 2048   69.0, 49.1     1024 x 4096   19.7, 15.2     512 x 4096   9.6, 13.0
-// Short rows do better directly (65536 x 256: 27.6, 31.8; x 128: 16.4, 31.0),
+// Short rows do better directly than with a bulk copy a row and tensor (65536 x
+// 256: 27.6, 31.8; x 128: 16.4, 31.0; several rows a copy were not tried),
 // and so does fp32, whose loads are twice as long (16384 x 1024: 47 us,
 // 5.7 TB/s). Forward has the registers: through shared memory it took 48 us
 // where it takes 23 (16384 x 1024).
