@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int64_t bc = p.b * (int64_t)a.kv_heads + p.c;
         if (round == 0) griddep_wait();  // for max |v|; nothing has been written before
         const uint32_t v_top =
-            __reduce_max_sync(0xFFFFFFFFu, lane < a.v_parts ? a.v_top[bc * kBoundParts + lane] : 0u);
+            __reduce_max_sync(0xFFFFFFFFu, lane < a.v_parts ? __ldcg(&a.v_top[bc * kBoundParts + lane]) : 0u);
         size = __uint_as_float(sizes[0][row] << 16) + __uint_as_float(sizes[1][row] << 16);
         const uint32_t bound = __float_as_uint(fmaf(size, __uint_as_float(v_top), fabsf(minus_delta)));
         lift = ds_lift(bound);
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       int hi = a.window > 0 ? min((int)a.q_len, key - off + (int)a.window) : (int)a.q_len;
       if (key >= p.keys) hi = lo = 0;
       // p is 2^kLiftP times itself: what is missing to the lift of ds
-      const int lift = kNarrow<T> ? ds_lift(a.ds_top[p.b * (int64_t)a.kv_heads + p.c]) : 0;
+      const int lift = kNarrow<T> ? ds_lift(__ldcg(&a.ds_top[p.b * (int64_t)a.kv_heads + p.c])) : 0;
       const float rest = kNarrow<T> ? power_of_two(lift - kLiftP) : 1.0f;
       const uint64_t rest_pair = pair(rest, rest);
 #pragma unroll 1

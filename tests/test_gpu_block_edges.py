@@ -222,6 +222,31 @@ def test_attention_fp16_weak_weights_in_dv():
     assert float((weak - want).abs().max()) <= want * (2 * ref.U[F16] + 2 ** -14) + 2 ** -25
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_fp16_repeats_and_replays(D):
+    """The bounds are collected by maxima, the same in any order; captured, the three
+    kernels are ordered as in a stream."""
+    q, k, v, do = qkv(gen(D), 2, 700, 900, 8, 2, D, F16)
+    lengths = torch.tensor([900, 611], dtype=torch.int32, device="cuda")
+    mask = dict(causal=True, key_lengths=lengths)
+    o, lse = block.attention_forward(q, k, v, **mask)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = block.attention_backward(do, q, k, v, o, lse, **mask)
+    for scale in (1.0, 2.0 ** -9, 300.0):
+        do.copy_(normal(gen(D + 1), *do.shape, scale=scale))
+        v.copy_(normal(gen(D + 2), *v.shape, scale=1 / scale))
+        a = block.attention_forward(q, k, v, **mask)
+        o.copy_(a[0])
+        lse.copy_(a[1])
+        want = block.attention_backward(do, q, k, v, o, lse, **mask)
+        for _ in range(3):
+            graph.replay()
+            again = block.attention_backward(do, q, k, v, o, lse, **mask)
+            assert all(same_bits(x, y) and same_bits(x, z) for x, y, z in zip(want, held, again))
+        assert all(bool(x.isfinite().all()) for x in want)
+
+
 # ---------------------------------------------------------------------------
 # Attention: non-finite rows beside rows and keys that are masked
 # ---------------------------------------------------------------------------
