@@ -750,7 +750,145 @@ int zero_attention_backward(const zero_attention_desc* desc, const void* dout, c
                             const int32_t* key_lengths, void* dq, void* dk, void* dv,
                             void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Whether a bounded device wait gave up in one of these operators, on any stream
+/* ------------------------------------------------------------------------ */
+/* Operators of an expert layer, and products in 8-bit floating point          */
+/*                                                                            */
+/* Routing (the choice of experts, the rows' order by expert, the way there   */
+/* and back), the experts' products over ragged runs of rows, and products of */
+/* e4m3 matrices with block scales. The conventions are the block operators'  */
+/* above: the caller's buffers and stream, nothing allocated, fixed orders.   */
+/* What a device array says (offsets, places, choices) cannot be checked on   */
+/* the host; the kernels read and write inside the buffers whatever it holds. */
+/* No output may overlap an input or another output. Buffers start on 16 bytes; */
+/* logits and the products' outputs (y, dx, dw, out) on an element.            */
+/* ------------------------------------------------------------------------ */
+
+/* The routing of tokens to k of `experts` experts by their logits
+ * [tokens, experts] (row stride logits_stride, any dtype). Each token takes its
+ * k largest logits, the lower expert first where they are equal; a logit of
+ * -inf is never taken, so a row of nothing else (padding) goes nowhere. A NaN
+ * counts as the largest and gives its row NaN weights, as +inf does. -0 equals +0.
+ *   weights  fp32 [tokens, k], in the order taken: the softmax over the taken
+ *            logits (normalize) or over all of the row; 0 where none was taken.
+ *   chosen   int32 [tokens, k]: the experts; -1 where none was taken.
+ *   offsets  int32 [experts + 1]: expert e has the rows offsets[e] to
+ *            offsets[e + 1] - 1 of the order, by (token, position in chosen).
+ *   source   int32 [tokens * k]: row r of the order is slot source[r] =
+ *            token * k + position; -1 behind the last.
+ *   place    int32 [tokens, k]: the row of each slot, -1 where none was taken.
+ *   workspace  zero_route_workspace bytes.
+ * 1 <= experts <= 1024, 1 <= k <= min(experts, 32), tokens * k < 2^31. */
+int zero_route_workspace(int64_t tokens, int experts, int k, int64_t* bytes);
+int zero_route(const void* logits, int64_t logits_stride, int64_t tokens, int experts, int k,
+               int dtype, int normalize, float* weights, int32_t* chosen, int32_t* offsets,
+               int32_t* source, int32_t* place, void* workspace, int64_t workspace_bytes,
+               void* stream);
+
+/* dlogits [tokens, experts] (rows without gaps, the logits' dtype) of dweights
+ * fp32 [tokens, k]: with s = sum over the taken of weight * dweight,
+ *   normalize  weight * (dweight - s) where taken, 0 elsewhere;
+ *   else       weight * dweight where taken, less p * s everywhere, p the
+ *              softmax of the row's logits (0 for a row of -inf).
+ *   logits     read without normalize only; else it may be NULL. */
+int zero_route_backward(const float* dweights, const float* weights, const int32_t* chosen,
+                        const void* logits, int64_t logits_stride, int64_t tokens, int experts,
+                        int k, int dtype, int normalize, void* dlogits, void* stream);
+
+/* Rows to their experts and back. hidden elements a row, row strides free; out
+ * of the calls come rows without gaps. When hidden and the strides are multiples
+ * of 8, rows move as 16-byte vectors.
+ *   gather    rows[place[t, j]] = x[t]; a row that no slot fills is zero.
+ *   combine   out[t] = sum over j of weights[t, j] * y[place[t, j]], fp32 sums
+ *             in the order of j; slots with place -1 add nothing. weights NULL:
+ *             all 1 (the gradient of gather).
+ *   combine_backward  dy[place[t, j]] = weights[t, j] * dout[t], zero in rows
+ *             that no slot fills; dweights[t, j] = dout[t] . y[place[t, j]] in
+ *             fp32, 0 where place is -1.
+ *   source    says which rows no slot fills (-1). */
+int zero_experts_gather(const void* x, int64_t x_stride, int64_t tokens, int k, int64_t hidden,
+                        int dtype, const int32_t* place, const int32_t* source, void* rows,
+                        void* stream);
+int zero_experts_combine(const void* y, int64_t y_stride, int64_t tokens, int k, int64_t hidden,
+                         int dtype, const int32_t* place, const float* weights, void* out,
+                         void* stream);
+int zero_experts_combine_backward(const void* dout, int64_t dout_stride, const void* y,
+                                  int64_t y_stride, int64_t tokens, int k, int64_t hidden,
+                                  int dtype, const int32_t* place, const int32_t* source,
+                                  const float* weights, void* dy, float* dweights, void* stream);
+
+/* The experts' products: row r of expert e, offsets[e] <= r < offsets[e + 1].
+ *   offsets   int32 [experts + 1], device, not decreasing, within 0..rows.
+ *   weights   [experts][n_out][n_in] of dtype (fp16 or bf16), rows contiguous;
+ *             w_row_stride between rows, w_stride between experts' matrices.
+ *   x, dx     [rows, n_in], row stride x_stride; y, dy [rows, n_out], y_stride.
+ * Strides are in elements; of inputs they are multiples of 8 (dw's, y's and
+ * dx's are free). Sums are fp32.
+ *   forward      y[r] = x[r] W_e^T.
+ *   input_grad   dx[r] = dy[r] W_e.
+ *   weight_grad  dW_e = sum over its rows of dy[r]^T x[r]; an expert without rows
+ *                has zero. dw_dtype: fp32 or dtype; accumulate (fp32 only) adds
+ *                each element once to what is there.
+ * Rows of no expert come out as zero, and no row reaches another expert's
+ * results, whatever it holds. */
+typedef struct {
+  int64_t rows;          /* 0..2^31 - 1 */
+  int64_t n_out, n_in;   /* 1..2^24 */
+  int64_t x_stride, y_stride;
+  int64_t w_stride, w_row_stride;
+  int32_t experts;       /* 1..1024 */
+  int32_t dtype;
+} zero_experts_desc;
+
+int zero_experts_forward(const zero_experts_desc* desc, const void* x, const void* weights,
+                         const int32_t* offsets, void* y, void* stream);
+int zero_experts_input_grad(const zero_experts_desc* desc, const void* dy, const void* weights,
+                            const int32_t* offsets, void* dx, void* stream);
+int zero_experts_weight_grad(const zero_experts_desc* desc, const void* dy, const void* x,
+                             const int32_t* offsets, void* dw, int dw_dtype, int accumulate,
+                             void* stream);
+
+/* Scaled matrices: e4m3 codes with one power-of-two scale for each block of 128
+ * elements along the row, which is the contraction of a product.
+ *   q       [rows, pitch] bytes, pitch = cols rounded up to 128; codes of the
+ *           padding are 0.
+ *   scales  uint8 [rows, scale_pitch], scale_pitch = pitch / 128 rounded up to 4:
+ *           b stands for 2^(b - 127), 255 for NaN; the padding's are 127.
+ * pack: b - 127 is the least power, -127 at least, with max |finite x| of the
+ * block <= 448 * 2^(b - 127); code = x / 2^(b - 127) rounded to nearest even, NaN
+ * for an inf or a NaN. unpack: code * 2^(b - 127) rounded to the output type.
+ *   x       [batch][rows, cols], strides in elements between matrices and rows;
+ *           cols up to 65535 * 128.
+ *   q, scales      the matrices' packed form, [batch * rows, ..]; or both NULL.
+ *   qt, scales_t   that of the transposes, [batch * cols, ..], blocks of 128
+ *           rows of x; or both NULL. One read of x makes both forms. */
+int zero_scaled_layout(int64_t rows, int64_t cols, int64_t* pitch, int64_t* scale_pitch);
+int zero_scaled_pack(const void* x, int64_t batch_stride, int64_t x_stride, int64_t batch,
+                     int64_t rows, int64_t cols, int dtype, void* q, uint8_t* scales, void* qt,
+                     uint8_t* scales_t, void* stream);
+int zero_scaled_unpack(const void* q, const uint8_t* scales, int64_t rows, int64_t cols, void* out,
+                       int64_t out_stride, int dtype, void* stream);
+
+/* out[i, j] = sum over k of a[i, k] * b[j, k] of scaled matrices, fp32 sums.
+ *   experts 0   b [n, k] is one matrix, offsets NULL.
+ *   experts >0  b [experts * n, k]: rows offsets[e] to offsets[e + 1] - 1 of a
+ *               meet expert e's n rows; rows of no expert come out as zero.
+ *   out         [rows, n] of out_dtype, row stride out_stride; accumulate (fp32
+ *               only) adds each element once to what is there. */
+typedef struct {
+  int64_t rows;        /* 0..2^31 - 1 */
+  int64_t n, k;        /* 1..2^24 */
+  int64_t out_stride;
+  int32_t experts;     /* 0..1024 */
+  int32_t out_dtype;
+  int32_t accumulate;
+  int32_t reserved;    /* 0 */
+} zero_scaled_desc;
+
+int zero_scaled_matmul(const zero_scaled_desc* desc, const void* a, const uint8_t* a_scales,
+                       const void* b, const uint8_t* b_scales, const int32_t* offsets, void* out,
+                       void* stream);
+
+/* Whether a bounded device wait gave up in one of the operators above, on any stream
  * of the current device, since this thread's last call (its first: since the
  * start): ZERO_ERR_TIMEOUT if so (the outputs of the calls since then are not to
  * be used), ZERO_OK otherwise. Every thread is told once. Synchronises `stream`;

@@ -82,10 +82,25 @@ class zero_attention_desc(ctypes.Structure):
             "dk_strides", "dv_strides")]
 
 
+class zero_experts_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "rows", "n_out", "n_in", "x_stride", "y_stride", "w_stride", "w_row_stride")] + \
+        [("experts", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class zero_scaled_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "n", "k", "out_stride")] + \
+        [(n, ctypes.c_int32) for n in ("experts", "out_dtype", "accumulate", "reserved")]
+
+
 # The same descriptors as packed bytes (several times quicker to fill from
 # Python than a Structure): the calls below take either.
 RMSNORM_DESC = struct.Struct("=5q2id")
 ATTENTION_DESC = struct.Struct("=3q6iqd24q")
+EXPERTS_DESC = struct.Struct("=7q2i")
+SCALED_DESC = struct.Struct("=4q4i")
+assert EXPERTS_DESC.size == ctypes.sizeof(zero_experts_desc)
+assert SCALED_DESC.size == ctypes.sizeof(zero_scaled_desc)
 assert RMSNORM_DESC.size == ctypes.sizeof(zero_rmsnorm_desc)
 assert ATTENTION_DESC.size == ctypes.sizeof(zero_attention_desc)
 
@@ -158,6 +173,19 @@ def lib() -> ctypes.CDLL:
             "zero_attention_forward": [P] * 8,
             "zero_attention_backward_workspace": [P, ctypes.POINTER(I64)],
             "zero_attention_backward": [P] * 12 + [I64, P],
+            "zero_route_workspace": [I64, I, I, ctypes.POINTER(I64)],
+            "zero_route": [P, I64, I64, I, I, I, I, P, P, P, P, P, P, I64, P],
+            "zero_route_backward": [P, P, P, P, I64, I64, I, I, I, I, P, P],
+            "zero_experts_gather": [P, I64, I64, I, I64, I, P, P, P, P],
+            "zero_experts_combine": [P, I64, I64, I, I64, I, P, P, P, P],
+            "zero_experts_combine_backward": [P, I64, P, I64, I64, I, I64, I, P, P, P, P, P, P],
+            "zero_experts_forward": [P] * 6,
+            "zero_experts_input_grad": [P] * 6,
+            "zero_experts_weight_grad": [P] * 5 + [I, I, P],
+            "zero_scaled_layout": [I64, I64, ctypes.POINTER(I64), ctypes.POINTER(I64)],
+            "zero_scaled_pack": [P, I64, I64, I64, I64, I64, I, P, P, P, P, P],
+            "zero_scaled_unpack": [P, P, I64, I64, P, I64, I, P],
+            "zero_scaled_matmul": [P] * 8,
             "zero_operator_status": [P],
             "zero_selftest_operator_timeout": [I, ctypes.c_uint32, P],
         }
@@ -460,3 +488,79 @@ def zero_operator_status(stream: int) -> None:
 
 def zero_selftest_operator_timeout(kernels: int, spin_limit: int, stream: int) -> None:
     _check(lib().zero_selftest_operator_timeout(kernels, spin_limit, stream or None))
+
+
+# ---------------------------------------------------------------------------
+# The expert layer's operators and the products of scaled matrices
+# ---------------------------------------------------------------------------
+
+def zero_route_workspace(tokens: int, experts: int, k: int) -> int:
+    n = ctypes.c_int64()
+    _check(lib().zero_route_workspace(tokens, experts, k, n))
+    return n.value
+
+
+def zero_route(logits: int, logits_stride: int, tokens: int, experts: int, k: int, dtype: int, normalize: int,
+               weights: int, chosen: int, offsets: int, source: int, place: int, workspace: int,
+               workspace_bytes: int, stream: int) -> None:
+    _check(lib().zero_route(logits, logits_stride, tokens, experts, k, dtype, normalize, weights, chosen, offsets,
+                            source, place, workspace, workspace_bytes, stream))
+
+
+def zero_route_backward(dweights: int, weights: int, chosen: int, logits: int, logits_stride: int, tokens: int,
+                        experts: int, k: int, dtype: int, normalize: int, dlogits: int, stream: int) -> None:
+    _check(lib().zero_route_backward(dweights, weights, chosen, logits, logits_stride, tokens, experts, k, dtype,
+                                     normalize, dlogits, stream))
+
+
+def zero_experts_gather(x: int, x_stride: int, tokens: int, k: int, hidden: int, dtype: int, place: int,
+                        source: int, rows: int, stream: int) -> None:
+    _check(lib().zero_experts_gather(x, x_stride, tokens, k, hidden, dtype, place, source, rows, stream))
+
+
+def zero_experts_combine(y: int, y_stride: int, tokens: int, k: int, hidden: int, dtype: int, place: int,
+                         weights: int, out: int, stream: int) -> None:
+    _check(lib().zero_experts_combine(y, y_stride, tokens, k, hidden, dtype, place, weights, out, stream))
+
+
+def zero_experts_combine_backward(dout: int, dout_stride: int, y: int, y_stride: int, tokens: int, k: int,
+                                  hidden: int, dtype: int, place: int, source: int, weights: int, dy: int,
+                                  dweights: int, stream: int) -> None:
+    _check(lib().zero_experts_combine_backward(dout, dout_stride, y, y_stride, tokens, k, hidden, dtype, place,
+                                               source, weights, dy, dweights, stream))
+
+
+def zero_experts_forward(desc, x: int, weights: int, offsets: int, y: int, stream: int) -> None:
+    _check(lib().zero_experts_forward(_desc(desc), x, weights, offsets, y, stream))
+
+
+def zero_experts_input_grad(desc, dy: int, weights: int, offsets: int, dx: int, stream: int) -> None:
+    _check(lib().zero_experts_input_grad(_desc(desc), dy, weights, offsets, dx, stream))
+
+
+def zero_experts_weight_grad(desc, dy: int, x: int, offsets: int, dw: int, dw_dtype: int, accumulate: int,
+                             stream: int) -> None:
+    _check(lib().zero_experts_weight_grad(_desc(desc), dy, x, offsets, dw, dw_dtype, accumulate, stream))
+
+
+def zero_scaled_layout(rows: int, cols: int):
+    """(pitch, scale_pitch)"""
+    a, b = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().zero_scaled_layout(rows, cols, a, b))
+    return a.value, b.value
+
+
+def zero_scaled_pack(x: int, batch_stride: int, x_stride: int, batch: int, rows: int, cols: int, dtype: int,
+                     q: int, scales: int, qt: int, scales_t: int, stream: int) -> None:
+    _check(lib().zero_scaled_pack(x, batch_stride, x_stride, batch, rows, cols, dtype, q, scales, qt, scales_t,
+                                  stream))
+
+
+def zero_scaled_unpack(q: int, scales: int, rows: int, cols: int, out: int, out_stride: int, dtype: int,
+                       stream: int) -> None:
+    _check(lib().zero_scaled_unpack(q, scales, rows, cols, out, out_stride, dtype, stream))
+
+
+def zero_scaled_matmul(desc, a: int, a_scales: int, b: int, b_scales: int, offsets: int, out: int,
+                       stream: int) -> None:
+    _check(lib().zero_scaled_matmul(_desc(desc), a, a_scales, b, b_scales, offsets, out, stream))

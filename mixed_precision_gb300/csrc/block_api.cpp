@@ -3,96 +3,19 @@
 #include "zero.h"
 
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
 #include <cuda_runtime.h>
 
 #include "block.h"
-
-#ifndef ZERO_NO_NVTX
-#include <nvtx3/nvToolsExt.h>
-#endif
+#include "checks.h"
+#include "experts.h"
 
 using namespace zg;
 
 namespace {
 
-struct Range {
-#ifndef ZERO_NO_NVTX
-  explicit Range(const char* name) { nvtxRangePushA(name); }
-  ~Range() { nvtxRangePop(); }
-#else
-  explicit Range(const char*) {}
-#endif
-  Range(const Range&) = delete;
-  Range& operator=(const Range&) = delete;
-};
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  return zero_internal_fail(code, buf);
-}
-
-int cuda_fail(cudaError_t e, const char* what) {
-  return fail(ZERO_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool valid_dtype(int d) { return d == ZERO_F32 || d == ZERO_F16 || d == ZERO_BF16; }
-bool half_dtype(int d) { return d == ZERO_F16 || d == ZERO_BF16; }
-
-// A required device buffer: not NULL, 16-byte aligned.
-int need(const void* p, const char* name) {
-  if (p == nullptr) return fail(ZERO_ERR_INVALID, "%s is NULL", name);
-  if (!aligned16(p)) return fail(ZERO_ERR_INVALID, "%s is not 16-byte aligned", name);
-  return ZERO_OK;
-}
-#define NEED(p)                        \
-  do {                                 \
-    if (int rc_ = need(p, #p)) return rc_; \
-  } while (0)
-#define ALIGNED(p)                                                          \
-  do {                                                                      \
-    if (!aligned16(p)) return fail(ZERO_ERR_INVALID, "%s is not 16-byte aligned", #p); \
-  } while (0)
-
-// The current device's SM count, looked up once per device and process.
-int device_sms(int* sms) {
-  constexpr int kDevices = 64;
-  static int cached[kDevices];  // 0: not looked up; racing threads write the same value
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (dev < kDevices && (*sms = __atomic_load_n(&cached[dev], __ATOMIC_RELAXED)) > 0) return ZERO_OK;
-  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-  if (dev < kDevices) __atomic_store_n(&cached[dev], *sms, __ATOMIC_RELAXED);
-  return ZERO_OK;
-}
-
-constexpr int64_t kMaxRows = int64_t(1) << 31;
-constexpr int64_t kMaxStride = int64_t(1) << 38;  // in bytes below the tensor maps' 2^40
 constexpr int kMaxNormCols = 65536;
 constexpr int64_t kMaxLen = int64_t(1) << 28;
-
-int check_rows(int64_t rows, int64_t cols, int64_t max_cols) {
-  if (rows < 0 || rows > kMaxRows || cols < 1 || cols > max_cols)
-    return fail(ZERO_ERR_INVALID, "%lld rows x %lld cols out of range (cols 1..%lld)",
-                (long long)rows, (long long)cols, (long long)max_cols);
-  return ZERO_OK;
-}
-
-int check_stride(int64_t stride, int64_t cols, const char* name) {
-  if (stride < cols || stride > kMaxStride)
-    return fail(ZERO_ERR_INVALID, "%s %lld is out of range (cols %lld)", name, (long long)stride,
-                (long long)cols);
-  return ZERO_OK;
-}
 
 int check_norm(const zero_rmsnorm_desc* d) {
   if (d == nullptr) return fail(ZERO_ERR_INVALID, "desc is NULL");
@@ -276,8 +199,9 @@ int attention_args(const zero_attention_desc* d, bool backward, AttnArgs& a) {
   return ZERO_OK;
 }
 
-constexpr int kErrorWords = 4;
-cudaError_t (*const kErrorWord[kErrorWords])(unsigned**) = {norm_error, wgrad_error, attn_fwd_error, attn_bwd_error};
+constexpr int kErrorWords = 5, kBlockErrorWords = 4;  // of the block operators and of the experts' products
+cudaError_t (*const kErrorWord[kErrorWords])(unsigned**) = {norm_error, wgrad_error, attn_fwd_error, attn_bwd_error,
+                                                           product_error};
 
 }  // namespace
 
@@ -618,8 +542,8 @@ int zero_operator_status(void* stream) {
 
 int zero_selftest_operator_timeout(int kernels, uint32_t spin_limit, void* stream) {
   Range r("zero_selftest_operator_timeout");
-  if (kernels < 0 || kernels >= kErrorWords)
-    return fail(ZERO_ERR_INVALID, "kernels %d outside 0..%d", kernels, kErrorWords - 1);
+  if (kernels < 0 || kernels >= kBlockErrorWords)
+    return fail(ZERO_ERR_INVALID, "kernels %d outside 0..%d", kernels, kBlockErrorWords - 1);
   if (spin_limit < 1 || spin_limit > kSpinLimit) return fail(ZERO_ERR_INVALID, "spin_limit outside 1..2^22");
   unsigned* at = nullptr;
   cudaError_t e = kErrorWord[kernels](&at);
