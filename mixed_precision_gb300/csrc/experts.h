@@ -81,7 +81,7 @@ struct ProductArgs {
   const uint8_t *a_scales, *b_scales;  // kE4M3
   int64_t scale_pitch;
 };
-cudaError_t launch_product(const ProductArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_product(const ProductArgs& a, cudaStream_t s);
 cudaError_t product_error(unsigned** at);
 
 }  // namespace zg

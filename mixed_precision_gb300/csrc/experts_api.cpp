@@ -117,9 +117,7 @@ Buffer expert_matrices(const void* p, const zero_experts_desc* d, int64_t bytes,
 }
 
 int launch(const ProductArgs& a, const char* what, void* stream) {
-  int sms;
-  if (int rc = device_sms(&sms)) return rc;
-  cudaError_t e = launch_product(a, sms, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_product(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, what);
 }
 

@@ -1,9 +1,27 @@
-// The experts' products and the products of scaled e4m3 matrices: one thread an
-// output element, fp32 sums.
-#include <cuda_fp8.h>
+// The experts' products and the products of scaled e4m3 matrices, on the tensor
+// cores: out[n][m] = sum over k of a(m, k) b(n, k), a the weights (or the rows
+// whose columns are contiguous in out), b the rows.
+//
+// A pair of blocks (two SMs) makes tiles of 256 along M x up to 256 along N (224
+// with scales, which need TMEM too): each block holds half of either operand, so
+// an element that comes from L2 meets 256 others. The ragged side is N (rows in
+// runs by expert) or K (a weight gradient's rows). How long the runs are is known
+// on the device only: every block reads the offsets and takes each pairs-th tile
+// of the list that they make. Tiles of a run are equally wide, so its rows fill
+// them to within 32; rows of the next run that a tile also reads end in columns
+// that nobody stores. Along K the rows behind a run's end are cleared in shared
+// memory, in both operands.
+//
+// Twelve warps: one loads by TMA, one issues MMAs, one brings scales (words of four
+// exponents, which the tensor core applies itself), eight take the sums. The sums
+// leave TMEM after every kRun steps and are added up in registers, rounded: the
+// tensor core truncates where it adds, which over thousands of steps would cost an
+// fp32 result its last bits. TMEM holds two tiles' sums, so the MMAs go on meanwhile.
+#include <type_traits>
 
 #include "block.h"
 #include "experts.h"
+#include "tc.cuh"
 #include "vec.cuh"
 
 namespace zg {
@@ -11,86 +29,563 @@ namespace {
 
 __device__ unsigned g_product_error;
 
-struct E4M3 {
-  uint8_t bits;
+constexpr int kTileM = 256;                 // of a pair
+constexpr int kStepBytes = 128;             // along the contraction: 64 elements, of e4m3 128
+constexpr int kABytes = 128 * kStepBytes;   // of one block
+constexpr int kMnRows = 64;                 // rows of a step whose operands are contiguous along M and N
+constexpr int kMnChunk = kMnRows * 128;     // bytes of 64 columns of them
+constexpr int kRun = 16;                    // steps whose sums stay in the tensor core
+constexpr int kMaxStages = 12;
+constexpr int kStageBytes = 196608;         // of all stages
+constexpr int kScaleSteps = 4;              // steps that a word of scales lasts
+constexpr int kScaleSlots = 4;
+constexpr int kScaleSlot = 3 * 512;         // of 128 rows of a, 256 of b
+constexpr int kEpilogue = 8;                // warps
+constexpr int kThreadsHere = (4 + kEpilogue) * 32;
+struct ProductPlan {
+  int tile_n;    // widest tile, a multiple of 32
+  int stages;
+  int b_bytes;   // of a stage and block
+  int pairs;
+};
+
+template <bool A_MN, bool B_MN, bool SCALED>
+struct Form {
+  static constexpr bool kRaggedK = B_MN;
+  static constexpr int kStepK = SCALED ? 128 : 64;  // elements
+  static constexpr int kMaxN = SCALED ? 224 : 256;
+  static constexpr int kScaleCols = 2 * kMaxN;      // where the scales' TMEM starts
+  static constexpr int kSmem = kStageBytes + 1024 + (SCALED ? kScaleSlots * kScaleSlot : 0);
+};
+
+struct Runs {  // shared memory: the runs of rows, with those of no expert at the end
+  int64_t first[kMaxExperts + 2];  // a run's first row
+  int start[kMaxExperts + 3];      // tiles along N of the runs before
+  int low, high;                   // the rows that runs reach
+};
+
+struct Tile {
+  int g;
+  int64_t m0;          // of the pair
+  int64_t n0;          // first row of b and out (ragged K: of an expert's matrix)
+  int width, padded;   // rows of it; up to 32
+  int64_t k0, k1;
+  int steps;
+};
+
+// A block's way through the tiles.
+template <typename F>
+struct Walk {
+  const ProductArgs& a;
+  const ProductPlan& p;
+  const Runs& runs;
+  int64_t m_tiles, n_tiles, i, total;
+  int g = 0;
+
+  __device__ __forceinline__ Walk(const ProductArgs& a_, const ProductPlan& p_, const Runs& r_, int pair)
+      : a(a_), p(p_), runs(r_), m_tiles((a_.m + kTileM - 1) / kTileM), n_tiles(0), i(pair) {
+    if (F::kRaggedK) {
+      n_tiles = (a.n + p.tile_n - 1) / p.tile_n;
+      total = a.groups * m_tiles * n_tiles;
+    } else {
+      total = runs.start[a.groups + 2] * m_tiles;
+    }
+  }
+  __device__ __forceinline__ bool next(Tile& t) {
+    if (i >= total) return false;
+    int64_t local, rows, across;
+    if (F::kRaggedK) {
+      const int64_t each = m_tiles * n_tiles;
+      g = static_cast<int>(i / each);
+      local = i - g * each;
+      rows = a.n;
+      across = n_tiles;
+      t.k0 = runs.first[g];
+      t.k1 = runs.first[g + 1];
+    } else {
+      while (runs.start[g + 1] * m_tiles <= i) ++g;
+      local = i - runs.start[g] * m_tiles;
+      across = runs.start[g + 1] - runs.start[g];
+      t.k0 = 0;
+      t.k1 = g < a.groups ? a.k : 0;  // rows of no expert
+      rows = g < a.groups ? bound(a, g + 1) - runs.first[g] : g == a.groups ? a.n - runs.high : runs.low;
+    }
+    // bands of 8 tiles along M: the rows' tiles come round while a band's weights stay in L2
+    const int64_t band = local / (8 * across), in = local - band * 8 * across;
+    const int64_t wide = min((int64_t)8, m_tiles - band * 8), n = in / wide;
+    t.m0 = (band * 8 + in - n * wide) * kTileM;
+    const int each = static_cast<int>((rows + across - 1) / across + 31) / 32 * 32;
+    const int64_t at = n * each;
+    t.g = g;
+    t.n0 = (F::kRaggedK ? 0 : runs.first[g]) + at;
+    t.width = static_cast<int>(max((int64_t)0, min((int64_t)each, rows - at)));
+    t.padded = (t.width + 31) / 32 * 32;
+    t.steps = t.width > 0 && t.k1 > t.k0 ? static_cast<int>((t.k1 - t.k0 + F::kStepK - 1) / F::kStepK) : 0;
+    i += p.pairs;
+    return true;
+  }
+  static __device__ __forceinline__ int64_t bound(const ProductArgs& a, int g) {
+    const int64_t rows = F::kRaggedK ? a.k : a.n;
+    if (a.offsets == nullptr) return g == 0 ? 0 : rows;
+    const int64_t o = a.offsets[g];
+    return o < 0 ? 0 : o < rows ? o : rows;
+  }
+};
+
+// Fill `runs` (all threads of the block).
+template <typename F>
+__device__ void read_runs(const ProductArgs& a, const ProductPlan& p, Runs& runs) {
+  using W = Walk<F>;
+  if (F::kRaggedK) {
+    for (int g = threadIdx.x; g <= a.groups; g += kThreadsHere) runs.first[g] = W::bound(a, g);
+    __syncthreads();
+    return;
+  }
+  if (threadIdx.x == 0) {
+    runs.low = static_cast<int>(a.n);
+    runs.high = 0;
+  }
+  __syncthreads();
+  for (int g = threadIdx.x; g < a.groups; g += kThreadsHere) {
+    const int64_t from = W::bound(a, g), to = W::bound(a, g + 1);
+    const bool some = to > from;
+    runs.first[g] = from;
+    runs.start[g] = some ? static_cast<int>((to - from + p.tile_n - 1) / p.tile_n) : 0;
+    if (some) {
+      atomicMin(&runs.low, static_cast<int>(from));
+      atomicMax(&runs.high, static_cast<int>(to));
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    // rows before the first run and behind the last belong to nobody (all, when there is no run)
+    if (threadIdx.x == 0) {
+      runs.low = min(runs.low, runs.high);
+      runs.first[a.groups] = runs.high;
+      runs.first[a.groups + 1] = 0;
+      runs.start[a.groups] = static_cast<int>((a.n - runs.high + p.tile_n - 1) / p.tile_n);
+      runs.start[a.groups + 1] = (runs.low + p.tile_n - 1) / p.tile_n;
+    }
+    __syncwarp();
+    int sum = 0;
+    for (int at = 0; at < a.groups + 2; at += 32) {
+      const int g = at + threadIdx.x, own = g < a.groups + 2 ? runs.start[g] : 0;
+      int v = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (static_cast<int>(threadIdx.x) >= o) v += u;
+      }
+      if (g < a.groups + 2) runs.start[g] = sum + v - own;
+      sum += __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    if (threadIdx.x == 0) runs.start[a.groups + 2] = sum;
+  }
+  __syncthreads();
+}
+
+// A place in a ring of n.
+struct Ring {
+  int n, at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ explicit Ring(int n_) : n(n_) {}
+  __device__ __forceinline__ void step() {
+    if (++at == n) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
 };
 
 template <typename T>
-__device__ __forceinline__ float value(const ProductArgs&, const void* p, const uint8_t*, int64_t, int64_t, int64_t at) {
-  return DT<T>::to_f32(static_cast<const T*>(p)[at]);
-}
-template <>
-__device__ __forceinline__ float value<E4M3>(const ProductArgs& a, const void* p, const uint8_t* scales, int64_t row,
-                                             int64_t k, int64_t at) {
-  const uint32_t byte = scales[row * a.scale_pitch + k / kScaledBlock];
-  const float s = __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7FC00000u : byte << 23);
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(p)[at], __NV_E4M3))) * s;
+__device__ __forceinline__ uint32_t pair_of(float lo, float hi) {
+  const T a = DT<T>::from_f32(lo), b = DT<T>::from_f32(hi);
+  return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&a)) |
+         static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&b)) << 16;
 }
 
-__device__ __forceinline__ int64_t bound(const ProductArgs& a, int g, int64_t rows) {
-  if (a.offsets == nullptr) return g == 0 ? 0 : rows;
-  const int64_t o = a.offsets[g];
-  return o < 0 ? 0 : o < rows ? o : rows;
-}
-
-template <typename T, typename Out>
-__global__ void __launch_bounds__(256) k_product_plain(const ProductArgs a) {
-  const int64_t m = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-  const int64_t rows = a.ragged_k ? a.n * a.groups : a.n;
-  if (m >= a.m) return;
-  for (int64_t r = (int64_t)blockIdx.y * 8 + threadIdx.x / 32; r < rows; r += (int64_t)gridDim.y * 8) {
-    int g;
-    int64_t n = r, k0 = 0, k1 = a.k;
-    if (a.ragged_k) {
-      g = (int)(r / a.n);
-      n = r - g * a.n;
-      k0 = bound(a, g, a.k);
-      k1 = bound(a, g + 1, a.k);
-    } else {
-      for (g = 0; g < a.groups; ++g)
-        if (bound(a, g, a.n) <= r && r < bound(a, g + 1, a.n)) break;
+// The thread's column m of `rows` rows of out, from element `at` (row stride
+// out_row). A warp holds 32 neighbouring columns.
+template <typename T>
+__device__ __forceinline__ void store_columns(const ProductArgs& a, const float (&acc)[128], int64_t at, int rows,
+                                              bool in, bool pairs) {
+  T* out = static_cast<T*>(a.out) + at;
+  if (sizeof(T) == 2 && pairs) {
+    // two rows at once: the lanes of a pair of columns swap sums and store one row each
+    const int odd = threadIdx.x & 1;
+    out += odd ? a.out_row - 1 : 0;
+#pragma unroll
+    for (int j = 0; j < 128; j += 2) {
+      if (j % 8 == 0 && j >= rows) return;
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? acc[j] : acc[j + 1], 1);
+      const uint32_t two = odd ? pair_of<T>(got, acc[j + 1]) : pair_of<T>(acc[j], got);
+      if (in && j + odd < rows) *reinterpret_cast<uint32_t*>(out) = two;
+      out += 2 * a.out_row;
+      asm volatile("" : "+l"(out));  // one address that moves on, not 64 held beside the sums
     }
-    float sum = 0.0f;
-    if (g < a.groups)
-      for (int64_t k = k0; k < k1; ++k) {
-        const int64_t at_a = a.a_mn ? k * a.a_row + m : m * a.a_row + k;
-        const int64_t at_b = a.b_mn ? k * a.b_row + n : n * a.b_row + k;
-        const int64_t group = a.ragged_k ? 0 : g;
-        sum += value<T>(a, a.a, a.a_scales, group * a.m + m, k, group * a.a_group + at_a) *
-               value<T>(a, a.b, a.b_scales, n, k, at_b);
+    return;
+  }
+  if (!in) return;
+#pragma unroll
+  for (int c = 0; c < 128; c += 8) {
+    if (c >= rows) return;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = acc[c + j];
+    if (sizeof(T) == 4 && a.accumulate) {
+      const T* old = out;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (c + j < rows) v[j] += DT<T>::to_f32(*old);
+        old += a.out_row;
+        asm volatile("" : "+l"(old));
       }
-    Out* out = static_cast<Out*>(a.out) + (a.ragged_k ? g * a.out_group : 0) + n * a.out_row + m;
-    if (sizeof(Out) == 4 && a.accumulate)
-      *out = DT<Out>::from_f32(DT<Out>::to_f32(*out) + sum);
-    else
-      *out = DT<Out>::from_f32(sum);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (c + j < rows) *out = DT<T>::from_f32(v[j]);
+      out += a.out_row;
+      asm volatile("" : "+l"(out));
+    }
   }
 }
 
-template <typename T>
+template <bool A_MN, bool B_MN, bool SCALED>
+__global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
+    k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+              const __grid_constant__ ProductArgs a, const __grid_constant__ ProductPlan p) {
+  using F = Form<A_MN, B_MN, SCALED>;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], sums_full[2], sums_empty[2], last,
+      scales_full[kScaleSlots], scales_empty[kScaleSlots];
+  __shared__ uint32_t tmem_slot, abort_word;
+  __shared__ Runs runs;
+  // the swizzle is a function of address bits: tiles start on 1024 bytes, the same in both blocks
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const uint32_t base = smem_u32(smem), stage_bytes = kABytes + p.b_bytes;
+  uint8_t* scales = smem + kStageBytes;
+  const int warp = warp_number(), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 2);   // both blocks' loads; rank 0's barrier counts
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sums_full[s], 1);
+      mbar_init(&sums_empty[s], 2 * kEpilogue);
+    }
+    for (int s = 0; s < kScaleSlots; ++s) {
+      mbar_init(&scales_full[s], 2);
+      mbar_init(&scales_empty[s], 1);
+    }
+    mbar_init(&last, 1);
+    abort_word = 0;
+    mbar_init_fence();
+    tma_prefetch(&map_a);
+    tma_prefetch(&map_b);
+  }
+  if (warp == 3) tmem_alloc_pair(&tmem_slot, 512);
+  read_runs<F>(a, p, runs);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const PairWaiter wait{&abort_word, cluster_map(smem_u32(&abort_word), rank ^ 1), &g_product_error};
+  Walk<F> walk(a, p, runs, static_cast<int>(blockIdx.x / 2));
+  Tile t;
+
+  if (warp == 0) {
+    // ---- loads: each block its half of both operands
+    const uint32_t one = elect_one();
+    const uint32_t full0 = cluster_map(smem_u32(&full[0]), 0);
+    Ring ring(p.stages);
+    uint32_t tails = 0;
+    bool go = true;
+    while (go && walk.next(t)) {
+      const int half = t.padded / 2;
+      const int m = static_cast<int>(t.m0) + rank * 128, n = static_cast<int>(t.n0) + rank * half;
+      const int b_chunks = B_MN ? (half + 63) / 64 : 1;
+      const uint32_t bytes = kABytes + (B_MN ? b_chunks * kMnChunk : p.b_bytes);
+#pragma unroll 1
+      for (int step = 0; step < t.steps; ++step) {
+        const int s = ring.at;
+        if (!(go = wait(&empty[s], ring.phase ^ 1))) break;
+        const int k = static_cast<int>(t.k0) + step * F::kStepK;
+        const int left = static_cast<int>(min((int64_t)kMnRows, t.k1 - k));  // ragged K
+        const bool tail = F::kRaggedK && left < kMnRows;
+        const uint32_t to = base + s * stage_bytes;
+        if (one) {
+          uint32_t bar = full0 + s * 8;
+          if (tail) {
+            mbar_arrive_expect_tx(&last, bytes);
+            bar = cluster_map(smem_u32(&last), rank);
+          } else {
+            mbar_arrive_expect_tx_mapped(bar, bytes);
+          }
+          if (A_MN) {
+            tma_load3_pair(to, &map_a, m, k, F::kRaggedK ? 0 : t.g, bar);
+            tma_load3_pair(to + kMnChunk, &map_a, m + 64, k, F::kRaggedK ? 0 : t.g, bar);
+          } else {
+            tma_load3_pair(to, &map_a, k, m, t.g, bar);
+          }
+          if (B_MN) {
+            for (int c = 0; c < b_chunks; ++c) tma_load3_pair(to + kABytes + c * kMnChunk, &map_b, n + c * 64, k, 0, bar);
+          } else {
+            tma_load3_pair(to + kABytes, &map_b, k, n, 0, bar);
+          }
+        }
+        __syncwarp();
+        if (tail) {
+          // rows behind the run's end, up to the last MMA's: zero in both operands
+          if (!(go = wait(&last, tails++ & 1))) break;
+          const int clear = ((left + 15) / 16 * 16 - left) * 8, pieces = clear * (2 + b_chunks);
+          for (int i = lane; i < pieces; i += 32)
+            *reinterpret_cast<uint4*>(smem + s * stage_bytes + i / clear * kMnChunk + left * 128 + i % clear * 16) =
+                make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+          __syncwarp();
+          if (one) mbar_arrive_mapped(full0 + s * 8);
+        }
+        ring.step();
+      }
+    }
+    if (go) {  // every stage has been read
+      for (int s = 0; s < p.stages && go; ++s) {
+        go = wait(&empty[ring.at], ring.phase ^ 1);
+        ring.step();
+      }
+    }
+    if (!go)  // leave the copies in flight time to land
+      for (int i = 0; i < 64; ++i) __nanosleep(1000);
+  } else if (warp == 1 && rank == 0) {
+    // ---- the tensor cores of both blocks
+    const uint32_t one = elect_one();
+    const uint64_t a_desc = smem_desc(base, A_MN ? kMnChunk : 0, 1024);
+    const uint64_t b_desc = smem_desc(base + kABytes, B_MN ? kMnChunk : 0, 1024);
+    Ring ring(p.stages), slots(kScaleSlots), sums(2);
+    uint32_t sa = 0;
+    bool go = true;
+    while (go && walk.next(t)) {
+      const uint32_t idesc = SCALED ? 0 : mma_desc(a.dtype == kBF16, kTileM, t.padded, A_MN, B_MN);
+      uint32_t d = 0;
+#pragma unroll 1
+      for (int step = 0; step < t.steps; ++step) {
+        if (step % kRun == 0) {
+          if (!(go = wait(&sums_empty[sums.at], sums.phase ^ 1))) break;
+          tc_fence_after();
+          d = tmem + sums.at * F::kMaxN;
+        }
+        if (SCALED && step % kScaleSteps == 0) {
+          if (!(go = wait(&scales_full[slots.at], slots.phase))) break;
+          tc_fence_after();
+          const uint32_t from = smem_u32(scales) + slots.at * kScaleSlot;
+          sa = tmem + F::kScaleCols + (slots.at & 1) * 16;
+          tmem_copy_scales_pair(sa, from, one);
+          tmem_copy_scales_pair(sa + 4, from + 512, one);
+          tmem_copy_scales_pair(sa + 8, from + 1024, one);
+          mma_commit_pair(&scales_empty[slots.at], one);
+          slots.step();
+        }
+        const int s = ring.at;
+        if (!(go = wait(&full[s], ring.phase))) break;
+        tc_fence_after();
+        const uint32_t at = s * (stage_bytes / 16);  // in the descriptors' units of 16 bytes
+        const bool more = step % kRun > 0;
+        if constexpr (SCALED) {
+          const uint32_t scaled = mma_desc_scaled(kTileM, t.padded, step % kScaleSteps);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_scaled_pair(d, a_desc + at + k * 2, b_desc + at + k * 2, scaled, sa, sa + 4, more || k > 0, one);
+        } else if constexpr (F::kRaggedK) {
+          const int parts = static_cast<int>(min((int64_t)4, (t.k1 - t.k0 - (int64_t)step * kMnRows + 15) / 16));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < parts) mma_ss_pair(d, a_desc + at + k * 128, b_desc + at + k * 128, idesc, more || k > 0, one);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss_pair(d, a_desc + at + k * (A_MN ? 128 : 2), b_desc + at + k * 2, idesc, more || k > 0, one);
+        }
+        mma_commit_pair(&empty[s], one);
+        ring.step();
+        if (step % kRun == kRun - 1 || step + 1 == t.steps) {
+          mma_commit_pair(&sums_full[sums.at], one);
+          sums.step();
+        }
+      }
+    }
+    if (!go)  // leave the MMAs in flight time to end
+      for (int i = 0; i < 64; ++i) __nanosleep(1000);
+  } else if (SCALED && warp == 2) {
+    // ---- scales: a word (four blocks of 128) of every row of the tile
+    const uint32_t full0 = cluster_map(smem_u32(&scales_full[0]), 0);
+    Ring slots(kScaleSlots);
+    bool go = true;
+    while (go && walk.next(t)) {
+      const uint8_t* pa[4];
+      const uint8_t* pb[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        pa[i] = a.a_scales + (t.g * a.m + min(t.m0 + rank * 128 + lane + i * 32, a.m - 1)) * a.scale_pitch;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pb[i] = a.b_scales + min(t.n0 + lane + i * 32, a.n - 1) * a.scale_pitch;
+      const int words = (t.steps + kScaleSteps - 1) / kScaleSteps;
+      uint4 va, vb, vc;
+      auto fetch = [&](int w) {
+        if (w >= words) return;
+        auto word = [&](const uint8_t* q) { return *reinterpret_cast<const uint32_t*>(q + w * 4); };
+        va = make_uint4(word(pa[0]), word(pa[1]), word(pa[2]), word(pa[3]));
+        vb = make_uint4(word(pb[0]), word(pb[1]), word(pb[2]), word(pb[3]));
+        vc = make_uint4(word(pb[4]), word(pb[5]), word(pb[6]), word(pb[7]));
+      };
+      fetch(0);
+#pragma unroll 1
+      for (int w = 0; w < words; ++w) {
+        if (!(go = wait(&scales_empty[slots.at], slots.phase ^ 1))) break;
+        uint8_t* to = scales + slots.at * kScaleSlot + lane * 16;
+        *reinterpret_cast<uint4*>(to) = va;
+        *reinterpret_cast<uint4*>(to + 512) = vb;
+        *reinterpret_cast<uint4*>(to + 1024) = vc;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_mapped(full0 + slots.at * 8);
+        slots.step();
+        fetch(w + 1);
+      }
+    }
+    if (go)
+      for (int s = 0; s < kScaleSlots && go; ++s) {
+        go = wait(&scales_empty[slots.at], slots.phase ^ 1);
+        slots.step();
+      }
+  } else if (warp >= 4) {
+    // ---- sums: a thread has one column of out (lane of TMEM) in half of the tile's rows
+    const uint32_t empty0 = cluster_map(smem_u32(&sums_empty[0]), 0);
+    const int part = (warp - 4) / 4, row = (warp & 3) * 32 + lane;
+    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's lanes
+    const bool pairs = a.out_dtype != kF32 && a.m % 2 == 0 && a.out_row % 2 == 0 && a.out_group % 2 == 0 &&
+                       reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
+    Ring sums(2);
+    bool go = true;
+    while (go && walk.next(t)) {
+      const int half = t.padded / 2;  // rows of this warp
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+#pragma unroll 1
+      for (int step = 0; step < t.steps; step += kRun) {
+        if (!(go = wait(&sums_full[sums.at], sums.phase))) break;
+        tc_fence_after();
+        const uint32_t from = mine + sums.at * F::kMaxN + part * half;
+#pragma unroll
+        for (int c = 0; c < 128; c += 16)
+          if (c < half) {
+            uint32_t r[16];
+            tmem_ld16(from + c, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(r[j]);
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_mapped(empty0 + sums.at * 8);
+        sums.step();
+      }
+      if (!go || (a.accumulate && t.steps == 0)) continue;
+      const int64_t m = t.m0 + rank * 128 + row, n = t.n0 + part * half;
+      const int64_t at = (F::kRaggedK ? t.g * a.out_group : 0) + n * a.out_row + m;
+      const int rows = min(half, t.width - part * half);
+      if (a.out_dtype == kF32)
+        store_columns<float>(a, acc, at, rows, m < a.m, false);
+      else if (a.out_dtype == kF16)
+        store_columns<__half>(a, acc, at, rows, m < a.m, pairs);
+      else
+        store_columns<__nv_bfloat16>(a, acc, at, rows, m < a.m, pairs);
+    }
+  }
+  // No block leaves while the other may still reach its memory or arrive at its barriers.
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_free_pair(tmem, 512);
+  }
+}
+
+template <bool A_MN, bool B_MN, bool SCALED>
 cudaError_t run(const ProductArgs& a, cudaStream_t s) {
-  const int64_t rows = a.ragged_k ? a.n * a.groups : a.n;
-  const int64_t down = (rows + 7) / 8;
-  const dim3 grid((unsigned)((a.m + 31) / 32), (unsigned)(down < 65535 ? down : 65535));
-  if (a.out_dtype == kF32)
-    k_product_plain<T, float><<<grid, 256, 0, s>>>(a);
-  else if (a.out_dtype == kF16)
-    k_product_plain<T, __half><<<grid, 256, 0, s>>>(a);
-  else
-    k_product_plain<T, __nv_bfloat16><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  using F = Form<A_MN, B_MN, SCALED>;
+  constexpr uint64_t elem = SCALED ? 1 : 2;
+  auto kernel = k_product<A_MN, B_MN, SCALED>;
+  ProductPlan p{};
+  if (F::kRaggedK) {
+    const int64_t across = (a.n + F::kMaxN - 1) / F::kMaxN;
+    p.tile_n = static_cast<int>((a.n + across - 1) / across + 31) / 32 * 32;
+    p.b_bytes = (p.tile_n / 2 + 63) / 64 * kMnChunk;
+  } else {
+    const int64_t mean = (a.n + a.groups - 1) / a.groups;
+    p.tile_n = mean <= 48 ? 64 : mean <= 112 ? 128 : F::kMaxN;
+    p.b_bytes = p.tile_n / 2 * kStepBytes;
+  }
+  const int stage = kABytes + p.b_bytes;
+  p.stages = kStageBytes / stage < kMaxStages ? kStageBytes / stage : kMaxStages;
+
+  // a: along M and K (in either order) by group; b: its rows, all groups' together
+  const uint64_t groups = F::kRaggedK ? 1 : a.groups;
+  const uint64_t a_extent[3] = {(uint64_t)(A_MN ? a.m : a.k), (uint64_t)(A_MN ? a.k : a.m), groups};
+  const uint64_t a_strides[2] = {(uint64_t)a.a_row * elem, (uint64_t)(groups > 1 ? a.a_group : a.a_row) * elem};
+  const uint64_t b_extent[3] = {(uint64_t)(B_MN ? a.n : a.k), (uint64_t)(B_MN ? a.k : a.n), 1};
+  const uint64_t b_strides[2] = {(uint64_t)a.b_row * elem, (uint64_t)a.b_row * elem};
+  CUtensorMap map_a, map_b;
+  if (!make_tensor_map(&map_a, a.a, a.dtype, 3, a_extent, a_strides, A_MN ? kMnRows : 128) ||
+      !make_tensor_map(&map_b, a.b, a.dtype, 3, b_extent, b_strides, B_MN ? kMnRows : p.tile_n / 2))
+    return cudaErrorInvalidValue;
+
+  static std::atomic<uint64_t> asked{0};
+  cudaError_t e = allow_smem(kernel, F::kSmem, asked);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(kThreadsHere);
+  cfg.dynamicSmemBytes = F::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // As many pairs as run at once (fewer than half the SMs: a pair lies within one
+  // cluster of SMs); asked once per kernel and device.
+  constexpr int kDevices = 64;
+  static std::atomic<int> found[kDevices];
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  int pairs = dev < kDevices ? found[dev].load(std::memory_order_relaxed) : 0;
+  if (pairs == 0) {
+    cfg.gridDim = dim3(2);
+    if ((e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg)) != cudaSuccess) return e;
+    if (pairs < 1) return cudaErrorLaunchOutOfResources;
+    if (dev < kDevices) found[dev].store(pairs, std::memory_order_relaxed);
+  }
+  const int64_t m_tiles = (a.m + kTileM - 1) / kTileM, n_tiles = (a.n + p.tile_n - 1) / p.tile_n;
+  const int64_t most = m_tiles * (F::kRaggedK ? n_tiles * a.groups : n_tiles + a.groups + 2);
+  p.pairs = static_cast<int>(most < pairs ? most : pairs);
+  cfg.gridDim = dim3(2 * p.pairs);
+  return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, a, p);
 }
 
 }  // namespace
 
-cudaError_t product_error(unsigned** at) {
-  return cudaGetSymbolAddress(reinterpret_cast<void**>(at), g_product_error);
-}
+ZG_ERROR_WORD(product_error, g_product_error)
 
-cudaError_t launch_product(const ProductArgs& a, int sms, cudaStream_t s) {
-  (void)sms;
-  if (a.dtype == kE4M3) return run<E4M3>(a, s);
-  return a.dtype == kF16 ? run<__half>(a, s) : run<__nv_bfloat16>(a, s);
+cudaError_t launch_product(const ProductArgs& a, cudaStream_t s) {
+  if (a.dtype == kE4M3) return run<false, false, true>(a, s);
+  if (a.ragged_k) return run<true, true, false>(a, s);
+  return a.a_mn ? run<true, false, false>(a, s) : run<false, false, false>(a, s);
 }
 
 }  // namespace zg

@@ -226,6 +226,115 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// ---- pairs of blocks -----------------------------------------------------------
+//
+// Two blocks of a cluster (ranks 0 and 1) make one tile of 256 rows: each holds
+// its half of a's rows, of b's rows and of the sums' rows, at the same addresses.
+// Rank 0 issues the MMAs for both. The barriers that it waits on are its own; the
+// other block arrives there through `mapped` addresses (cluster_map).
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// The Waiter of a pair: who gives up tells the other block too.
+struct PairWaiter {
+  volatile uint32_t* abort;
+  uint32_t abort_there;  // the other block's, mapped
+  unsigned* error;
+
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+      if (mbar_try_wait_cluster(bar, parity)) return true;
+      if ((i & 7) == 7 && *abort != 0) return false;
+    }
+    *abort = 1;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(abort_there), "r"(1u) : "memory");
+    atomicAdd(error, 1u);
+    return false;
+  }
+};
+__device__ __forceinline__ void mbar_arrive_mapped(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect_tx_mapped(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+// Into this block's shared memory, counted on a mapped barrier of either block.
+__device__ __forceinline__ void tma_load3_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// One warp of each block.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free_pair(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void mma_ss_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(one)
+      : "memory");
+}
+// Instruction descriptor of e4m3 operands, both K-major, with power-of-two scales
+// for 32 elements each, which are byte `sf` of the scales' words.
+__device__ __forceinline__ uint32_t mma_desc_scaled(int m, int n, uint32_t sf) {
+  return sf << 4 | static_cast<uint32_t>(n / 8) << 17 | 1u << 23 | static_cast<uint32_t>(m / 16) << 24 | sf << 29;
+}
+// d = a b [+ d], one step of 32 along the contraction. sa, sb: TMEM, a word a row,
+// row r at lane r % 32 of each quarter of the lanes, column r / 32.
+__device__ __forceinline__ void mma_scaled_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+                                                uint32_t sb, bool add, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+          "r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(static_cast<uint32_t>(add)), "r"(one)
+      : "memory");
+}
+// 32 rows of 16 bytes (512 contiguous bytes) of both blocks' shared memory to 4
+// columns of their TMEM, once into each quarter of the lanes. MMAs issued later
+// by the same thread read it.
+__device__ __forceinline__ void tmem_copy_scales_pair(uint32_t to, uint32_t from, uint32_t one) {
+  const uint64_t desc = static_cast<uint64_t>((from >> 4) & 0x3FFF) | static_cast<uint64_t>(128 >> 4) << 32 | 1ull << 46;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(to),
+      "l"(desc), "r"(one)
+      : "memory");
+}
+// Arrive on bar of both blocks once all of the lane's earlier MMAs and copies are done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t one) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(one), "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
 // ---- launches (host) ---------------------------------------------------------
 
 // Allow a kernel `bytes` of dynamic shared memory on the current device: asked
@@ -245,8 +354,8 @@ inline cudaError_t allow_smem(Kernel* kernel, int bytes, std::atomic<uint64_t>& 
 
 // ---- tensor maps (host) --------------------------------------------------------
 
-// A map of up to 4 dimensions of elements of `dtype`, boxes of 128 bytes x rows
-// (x 1 x 1) with the 128-byte swizzle; out-of-range elements read as zero.
+// A map of up to 4 dimensions of elements of `dtype` (kF32, kF16, kBF16 or a byte
+// type), boxes of 128 bytes x rows (x 1 x 1) with the 128-byte swizzle; out-of-range elements read as zero.
 // strides: bytes, of dimensions 1 and up. False if the driver refuses it.
 bool make_tensor_map(CUtensorMap* map, const void* base, int dtype, int dims, const uint64_t* extent,
                      const uint64_t* strides, uint32_t box_rows);

@@ -1,4 +1,4 @@
-// Tensor maps for the tiled TMA loads of the block operators' kernels.
+// Tensor maps for the tiled TMA loads and stores of the operators' kernels.
 #include <atomic>
 
 #include <cuda.h>
@@ -34,8 +34,9 @@ bool make_tensor_map(CUtensorMap* map, const void* base, int dtype, int dims, co
   if (encode == nullptr) return false;
   const CUtensorMapDataType type = dtype == kF32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : dtype == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  const cuuint32_t box[4] = {dtype == kF32 ? 32u : 64u, box_rows, 1, 1}, step[4] = {1, 1, 1, 1};
+                                   : dtype == kF16  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                    : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const cuuint32_t box[4] = {dtype == kF32 ? 32u : dtype == kBF16 || dtype == kF16 ? 64u : 128u, box_rows, 1, 1}, step[4] = {1, 1, 1, 1};
   cuuint64_t n[4], s[3];
   for (int i = 0; i < dims; ++i) n[i] = extent[i];
   for (int i = 0; i + 1 < dims; ++i) s[i] = strides[i];
