@@ -59,117 +59,105 @@ struct Form {
 };
 
 struct Runs {  // shared memory: the runs of rows, with those of no expert at the end
-  int64_t first[kMaxExperts + 2];  // a run's first row
-  int start[kMaxExperts + 3];      // tiles along N of the runs before
-  int low, high;                   // the rows that runs reach
+  int first[kMaxExperts + 2];  // a run's first row
+  int rows[kMaxExperts + 2];
+  int start[kMaxExperts + 3];  // tiles along N of the runs before
+  int low, high;               // the rows that runs reach
 };
 
 struct Tile {
   int g;
-  int64_t m0;          // of the pair
-  int64_t n0;          // first row of b and out (ragged K: of an expert's matrix)
-  int width, padded;   // rows of it; up to 32
-  int64_t k0, k1;
+  int m0;             // of the pair
+  int n0;             // first row of b and out (ragged K: of an expert's matrix)
+  int width, padded;  // rows of it; up to 32
+  int k0, rows_k;     // the first row along K, how many (ragged K)
   int steps;
 };
 
-// A block's way through the tiles.
+// A block's way through the tiles: 32-bit numbers, which the host has checked.
 template <typename F>
 struct Walk {
   const ProductArgs& a;
   const ProductPlan& p;
   const Runs& runs;
-  int64_t m_tiles, n_tiles, i, total;
+  uint32_t m_tiles, n_tiles, i, total;
   int g = 0;
 
   __device__ __forceinline__ Walk(const ProductArgs& a_, const ProductPlan& p_, const Runs& r_, int pair)
-      : a(a_), p(p_), runs(r_), m_tiles((a_.m + kTileM - 1) / kTileM), n_tiles(0), i(pair) {
-    if (F::kRaggedK) {
-      n_tiles = (a.n + p.tile_n - 1) / p.tile_n;
-      total = a.groups * m_tiles * n_tiles;
-    } else {
-      total = runs.start[a.groups + 2] * m_tiles;
-    }
+      : a(a_), p(p_), runs(r_), m_tiles((static_cast<uint32_t>(a_.m) + kTileM - 1) / kTileM), i(pair) {
+    n_tiles = F::kRaggedK ? (static_cast<uint32_t>(a.n) + p.tile_n - 1) / p.tile_n : 0;
+    total = (F::kRaggedK ? a.groups * n_tiles : runs.start[a.groups + 2]) * m_tiles;
   }
   __device__ __forceinline__ bool next(Tile& t) {
     if (i >= total) return false;
-    int64_t local, rows, across;
+    uint32_t local, rows, across;
     if (F::kRaggedK) {
-      const int64_t each = m_tiles * n_tiles;
+      const uint32_t each = m_tiles * n_tiles;
       g = static_cast<int>(i / each);
       local = i - g * each;
-      rows = a.n;
+      rows = static_cast<uint32_t>(a.n);
       across = n_tiles;
       t.k0 = runs.first[g];
-      t.k1 = runs.first[g + 1];
+      t.rows_k = runs.rows[g];
+      t.steps = (t.rows_k + kMnRows - 1) / kMnRows;
     } else {
       while (runs.start[g + 1] * m_tiles <= i) ++g;
       local = i - runs.start[g] * m_tiles;
+      rows = runs.rows[g];
       across = runs.start[g + 1] - runs.start[g];
       t.k0 = 0;
-      t.k1 = g < a.groups ? a.k : 0;  // rows of no expert
-      rows = g < a.groups ? bound(a, g + 1) - runs.first[g] : g == a.groups ? a.n - runs.high : runs.low;
+      t.steps = g < a.groups ? (static_cast<int>(a.k) + F::kStepK - 1) / F::kStepK : 0;  // else rows of no expert
     }
     // bands of 8 tiles along M: the rows' tiles come round while a band's weights stay in L2
-    const int64_t band = local / (8 * across), in = local - band * 8 * across;
-    const int64_t wide = min((int64_t)8, m_tiles - band * 8), n = in / wide;
-    t.m0 = (band * 8 + in - n * wide) * kTileM;
-    const int each = static_cast<int>((rows + across - 1) / across + 31) / 32 * 32;
-    const int64_t at = n * each;
+    const uint32_t band = local / (8 * across), in = local - band * 8 * across;
+    const uint32_t wide = min(8u, m_tiles - band * 8), n = in / wide;
+    t.m0 = static_cast<int>((band * 8 + in - n * wide) * kTileM);
+    const uint32_t each = ((rows + across - 1) / across + 31) / 32 * 32, at = n * each;
     t.g = g;
-    t.n0 = (F::kRaggedK ? 0 : runs.first[g]) + at;
-    t.width = static_cast<int>(max((int64_t)0, min((int64_t)each, rows - at)));
+    t.n0 = static_cast<int>((F::kRaggedK ? 0 : runs.first[g]) + at);
+    t.width = static_cast<int>(min(each, rows - at));
     t.padded = (t.width + 31) / 32 * 32;
-    t.steps = t.width > 0 && t.k1 > t.k0 ? static_cast<int>((t.k1 - t.k0 + F::kStepK - 1) / F::kStepK) : 0;
     i += p.pairs;
     return true;
   }
-  static __device__ __forceinline__ int64_t bound(const ProductArgs& a, int g) {
-    const int64_t rows = F::kRaggedK ? a.k : a.n;
+  static __device__ __forceinline__ int bound(const ProductArgs& a, int g) {
+    const int rows = static_cast<int>(F::kRaggedK ? a.k : a.n);
     if (a.offsets == nullptr) return g == 0 ? 0 : rows;
-    const int64_t o = a.offsets[g];
-    return o < 0 ? 0 : o < rows ? o : rows;
+    return max(0, min(a.offsets[g], rows));
   }
 };
 
 // Fill `runs` (all threads of the block).
 template <typename F>
 __device__ void read_runs(const ProductArgs& a, const ProductPlan& p, Runs& runs) {
-  using W = Walk<F>;
-  if (F::kRaggedK) {
-    for (int g = threadIdx.x; g <= a.groups; g += kThreadsHere) runs.first[g] = W::bound(a, g);
-    __syncthreads();
-    return;
-  }
   if (threadIdx.x == 0) {
     runs.low = static_cast<int>(a.n);
     runs.high = 0;
   }
   __syncthreads();
   for (int g = threadIdx.x; g < a.groups; g += kThreadsHere) {
-    const int64_t from = W::bound(a, g), to = W::bound(a, g + 1);
-    const bool some = to > from;
+    const int from = Walk<F>::bound(a, g), to = Walk<F>::bound(a, g + 1);
     runs.first[g] = from;
-    runs.start[g] = some ? static_cast<int>((to - from + p.tile_n - 1) / p.tile_n) : 0;
-    if (some) {
-      atomicMin(&runs.low, static_cast<int>(from));
-      atomicMax(&runs.high, static_cast<int>(to));
+    runs.rows[g] = max(0, to - from);
+    if (!F::kRaggedK && to > from) {
+      atomicMin(&runs.low, from);
+      atomicMax(&runs.high, to);
     }
   }
   __syncthreads();
-  if (threadIdx.x < 32) {
-    // rows before the first run and behind the last belong to nobody (all, when there is no run)
+  if (!F::kRaggedK && threadIdx.x < 32) {
     if (threadIdx.x == 0) {
-      runs.low = min(runs.low, runs.high);
+      // rows before the first run and behind the last belong to nobody (all, when there is no run)
       runs.first[a.groups] = runs.high;
+      runs.rows[a.groups] = static_cast<int>(a.n) - runs.high;
       runs.first[a.groups + 1] = 0;
-      runs.start[a.groups] = static_cast<int>((a.n - runs.high + p.tile_n - 1) / p.tile_n);
-      runs.start[a.groups + 1] = (runs.low + p.tile_n - 1) / p.tile_n;
+      runs.rows[a.groups + 1] = min(runs.low, runs.high);
     }
     __syncwarp();
     int sum = 0;
     for (int at = 0; at < a.groups + 2; at += 32) {
-      const int g = at + threadIdx.x, own = g < a.groups + 2 ? runs.start[g] : 0;
+      const int g = at + threadIdx.x;
+      const int own = g < a.groups + 2 ? static_cast<int>((static_cast<uint32_t>(runs.rows[g]) + p.tile_n - 1) / p.tile_n) : 0;
       int v = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -195,6 +183,7 @@ struct Ring {
       phase ^= 1;
     }
   }
+  __device__ __forceinline__ int after(int steps) const { return (at + steps) % n; }
 };
 
 template <typename T>
@@ -256,8 +245,8 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
               const __grid_constant__ ProductArgs a, const __grid_constant__ ProductPlan p) {
   using F = Form<A_MN, B_MN, SCALED>;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], sums_full[2], sums_empty[2], last,
-      scales_full[kScaleSlots], scales_empty[kScaleSlots];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], sums_full[2], sums_empty[2],
+      tail[kMaxStages], scales_full[kScaleSlots], scales_empty[kScaleSlots];
   __shared__ uint32_t tmem_slot, abort_word;
   __shared__ Runs runs;
   // the swizzle is a function of address bits: tiles start on 1024 bytes, the same in both blocks
@@ -271,6 +260,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 2);   // both blocks' loads; rank 0's barrier counts
       mbar_init(&empty[s], 1);
+      mbar_init(&tail[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sums_full[s], 1);
@@ -280,7 +270,6 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
       mbar_init(&scales_full[s], 2);
       mbar_init(&scales_empty[s], 1);
     }
-    mbar_init(&last, 1);
     abort_word = 0;
     mbar_init_fence();
     tma_prefetch(&map_a);
@@ -302,26 +291,22 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     const uint32_t one = elect_one();
     const uint32_t full0 = cluster_map(smem_u32(&full[0]), 0);
     Ring ring(p.stages);
-    uint32_t tails = 0;
     bool go = true;
     while (go && walk.next(t)) {
-      const int half = t.padded / 2;
-      const int m = static_cast<int>(t.m0) + rank * 128, n = static_cast<int>(t.n0) + rank * half;
+      const int half = t.padded / 2, m = t.m0 + rank * 128, n = t.n0 + rank * half;
       const int b_chunks = B_MN ? (half + 63) / 64 : 1;
       const uint32_t bytes = kABytes + (B_MN ? b_chunks * kMnChunk : p.b_bytes);
 #pragma unroll 1
       for (int step = 0; step < t.steps; ++step) {
         const int s = ring.at;
         if (!(go = wait(&empty[s], ring.phase ^ 1))) break;
-        const int k = static_cast<int>(t.k0) + step * F::kStepK;
-        const int left = static_cast<int>(min((int64_t)kMnRows, t.k1 - k));  // ragged K
-        const bool tail = F::kRaggedK && left < kMnRows;
+        const int k = t.k0 + step * F::kStepK;
         const uint32_t to = base + s * stage_bytes;
         if (one) {
           uint32_t bar = full0 + s * 8;
-          if (tail) {
-            mbar_arrive_expect_tx(&last, bytes);
-            bar = cluster_map(smem_u32(&last), rank);
+          if (F::kRaggedK && (step + 1) * kMnRows > t.rows_k) {  // warp 2 passes it on
+            mbar_arrive_expect_tx(&tail[s], bytes);
+            bar = cluster_map(smem_u32(&tail[s]), rank);
           } else {
             mbar_arrive_expect_tx_mapped(bar, bytes);
           }
@@ -338,17 +323,6 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
           }
         }
         __syncwarp();
-        if (tail) {
-          // rows behind the run's end, up to the last MMA's: zero in both operands
-          if (!(go = wait(&last, tails++ & 1))) break;
-          const int clear = ((left + 15) / 16 * 16 - left) * 8, pieces = clear * (2 + b_chunks);
-          for (int i = lane; i < pieces; i += 32)
-            *reinterpret_cast<uint4*>(smem + s * stage_bytes + i / clear * kMnChunk + left * 128 + i % clear * 16) =
-                make_uint4(0, 0, 0, 0);
-          fence_async_smem();
-          __syncwarp();
-          if (one) mbar_arrive_mapped(full0 + s * 8);
-        }
         ring.step();
       }
     }
@@ -400,7 +374,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
           for (int k = 0; k < 4; ++k)
             mma_scaled_pair(d, a_desc + at + k * 2, b_desc + at + k * 2, scaled, sa, sa + 4, more || k > 0, one);
         } else if constexpr (F::kRaggedK) {
-          const int parts = static_cast<int>(min((int64_t)4, (t.k1 - t.k0 - (int64_t)step * kMnRows + 15) / 16));
+          const int parts = min(4, (t.rows_k - step * kMnRows + 15) / 16);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (k < parts) mma_ss_pair(d, a_desc + at + k * 128, b_desc + at + k * 128, idesc, more || k > 0, one);
@@ -419,6 +393,27 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     }
     if (!go)  // leave the MMAs in flight time to end
       for (int i = 0; i < 64; ++i) __nanosleep(1000);
+  } else if (F::kRaggedK && warp == 2) {
+    // ---- a run's last step, if it is not full: the rows behind its end, up to the
+    // last MMA's, are cleared in both operands before the step counts as loaded
+    const uint32_t full0 = cluster_map(smem_u32(&full[0]), 0);
+    Ring ring(p.stages);
+    uint32_t phases = 0;
+    while (walk.next(t)) {
+      if (t.steps == 0) continue;
+      const int s = ring.after(t.steps - 1), left = t.rows_k - (t.steps - 1) * kMnRows;
+      ring.at = ring.after(t.steps);
+      if (left == kMnRows) continue;
+      if (!wait(&tail[s], phases >> s & 1)) break;
+      phases ^= 1u << s;
+      const int clear = ((left + 15) / 16 * 16 - left) * 8, pieces = clear * (2 + (t.padded / 2 + 63) / 64);
+      for (int i = lane; i < pieces; i += 32)
+        *reinterpret_cast<uint4*>(smem + s * stage_bytes + i / clear * kMnChunk + left * 128 + i % clear * 16) =
+            make_uint4(0, 0, 0, 0);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_release_mapped(full0 + s * 8);
+    }
   } else if (SCALED && warp == 2) {
     // ---- scales: a word (four blocks of 128) of every row of the tile
     const uint32_t full0 = cluster_map(smem_u32(&scales_full[0]), 0);
@@ -429,9 +424,9 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
       const uint8_t* pb[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        pa[i] = a.a_scales + (t.g * a.m + min(t.m0 + rank * 128 + lane + i * 32, a.m - 1)) * a.scale_pitch;
+        pa[i] = a.a_scales + (t.g * a.m + min(t.m0 + (int64_t)rank * 128 + lane + i * 32, a.m - 1)) * a.scale_pitch;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) pb[i] = a.b_scales + min(t.n0 + lane + i * 32, a.n - 1) * a.scale_pitch;
+      for (int i = 0; i < 8; ++i) pb[i] = a.b_scales + min((int64_t)t.n0 + lane + i * 32, a.n - 1) * a.scale_pitch;
       const int words = (t.steps + kScaleSteps - 1) / kScaleSteps;
       uint4 va, vb, vc;
       auto fetch = [&](int w) {
@@ -451,7 +446,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
         *reinterpret_cast<uint4*>(to + 1024) = vc;
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_mapped(full0 + slots.at * 8);
+        if (lane == 0) mbar_arrive_release_mapped(full0 + slots.at * 8);
         slots.step();
         fetch(w + 1);
       }
@@ -495,7 +490,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
         sums.step();
       }
       if (!go || (a.accumulate && t.steps == 0)) continue;
-      const int64_t m = t.m0 + rank * 128 + row, n = t.n0 + part * half;
+      const int64_t m = t.m0 + (int64_t)rank * 128 + row, n = (int64_t)t.n0 + part * half;
       const int64_t at = (F::kRaggedK ? t.g * a.out_group : 0) + n * a.out_row + m;
       const int rows = min(half, t.width - part * half);
       if (a.out_dtype == kF32)
@@ -573,6 +568,7 @@ cudaError_t run(const ProductArgs& a, cudaStream_t s) {
   }
   const int64_t m_tiles = (a.m + kTileM - 1) / kTileM, n_tiles = (a.n + p.tile_n - 1) / p.tile_n;
   const int64_t most = m_tiles * (F::kRaggedK ? n_tiles * a.groups : n_tiles + a.groups + 2);
+  if (most > (int64_t)0x7FFFFFFF || a.n > 0x7FFFFFFF || a.k > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   p.pairs = static_cast<int>(most < pairs ? most : pairs);
   cfg.gridDim = dim3(2 * p.pairs);
   return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, a, p);

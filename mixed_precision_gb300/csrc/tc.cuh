@@ -239,17 +239,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // Rank 0 issues the MMAs for both. The barriers that it waits on are its own; the
 // other block arrives there through `mapped` addresses (cluster_map).
 
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // The Waiter of a pair: who gives up tells the other block too.
 struct PairWaiter {
   volatile uint32_t* abort;
@@ -258,7 +247,7 @@ struct PairWaiter {
 
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
     for (uint32_t i = 0; i < kSpinLimit; ++i) {
-      if (mbar_try_wait_cluster(bar, parity)) return true;
+      if (mbar_try_wait(bar, parity)) return true;
       if ((i & 7) == 7 && *abort != 0) return false;
     }
     *abort = 1;
@@ -267,11 +256,18 @@ struct PairWaiter {
     return false;
   }
 };
+// With the thread's writes to its own block's shared memory before it. (Release at
+// the cluster's scope is a fence of 1300 cycles, and who reads these writes is the
+// block's own tensor core.)
+__device__ __forceinline__ void mbar_arrive_release_mapped(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Without them: what it reports is ordered by other means (TMA's count, tcgen05's fences).
 __device__ __forceinline__ void mbar_arrive_mapped(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx_mapped(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
 // Into this block's shared memory, counted on a mapped barrier of either block.
