@@ -17,6 +17,10 @@
 // leave TMEM after every kRun steps and are added up in registers, rounded: the
 // tensor core truncates where it adds, which over thousands of steps would cost an
 // fp32 result its last bits. TMEM holds two tiles' sums, so the MMAs go on meanwhile.
+// A tile leaves through shared memory: 8 x 8 matrices are turned on the way in, so
+// that a row of out lies there as it does in memory, and TMA stores take 32 rows (16
+// of fp32) from there while the next are made. Rows behind the last whole 32 of a
+// run, and outs whose rows do not start on 16 bytes, go by ordinary stores.
 #include <type_traits>
 
 #include "block.h"
@@ -36,7 +40,9 @@ constexpr int kMnRows = 64;                 // rows of a step whose operands are
 constexpr int kMnChunk = kMnRows * 128;     // bytes of 64 columns of them
 constexpr int kRun = 16;                    // steps whose sums stay in the tensor core
 constexpr int kMaxStages = 12;
-constexpr int kStageBytes = 196608;         // of all stages
+constexpr int kStoreBytes = 8192;           // a buffer: 32 rows of 128 16-bit columns, 16 of fp32
+constexpr int kStoreSpace = 4 * kStoreBytes;  // two for each half of the epilogue's warps
+constexpr int kMostSmem = 232448 - 1024;    // dynamic shared memory; the rest is for the barriers
 constexpr int kScaleSteps = 4;              // steps that a word of scales lasts
 constexpr int kScaleSlots = 4;
 constexpr int kScaleSlot = 3 * 512;         // of 128 rows of a, 256 of b
@@ -47,6 +53,8 @@ struct ProductPlan {
   int stages;
   int b_bytes;   // of a stage and block
   int pairs;
+  int store_at, scales_at, runs_at;  // in shared memory, behind the stages
+  int tiles_out;                     // out can be written by TMA
 };
 
 template <bool A_MN, bool B_MN, bool SCALED>
@@ -55,14 +63,16 @@ struct Form {
   static constexpr int kStepK = SCALED ? 128 : 64;  // elements
   static constexpr int kMaxN = SCALED ? 224 : 256;
   static constexpr int kScaleCols = 2 * kMaxN;      // where the scales' TMEM starts
-  static constexpr int kSmem = kStageBytes + 1024 + (SCALED ? kScaleSlots * kScaleSlot : 0);
 };
 
-struct Runs {  // shared memory: the runs of rows, with those of no expert at the end
-  int first[kMaxExperts + 2];  // a run's first row
-  int rows[kMaxExperts + 2];
-  int start[kMaxExperts + 3];  // tiles along N of the runs before
-  int low, high;               // the rows that runs reach
+// The runs of rows, in shared memory, with those of no expert at the end.
+struct Runs {
+  int *first, *rows;  // a run's first row, how many; [groups + 2]
+  int* start;         // tiles along N of the runs before; [groups + 3]
+  int* reach;         // the lowest and the highest row that runs reach
+  __host__ __device__ static constexpr int bytes(int groups) { return (3 * (groups + 3) + 2) * 4; }
+  __device__ __forceinline__ Runs(void* at, int groups)
+      : first(static_cast<int*>(at)), rows(first + groups + 3), start(rows + groups + 3), reach(start + groups + 3) {}
 };
 
 struct Tile {
@@ -129,10 +139,10 @@ struct Walk {
 
 // Fill `runs` (all threads of the block).
 template <typename F>
-__device__ void read_runs(const ProductArgs& a, const ProductPlan& p, Runs& runs) {
+__device__ void read_runs(const ProductArgs& a, const ProductPlan& p, const Runs& runs) {
   if (threadIdx.x == 0) {
-    runs.low = static_cast<int>(a.n);
-    runs.high = 0;
+    runs.reach[0] = static_cast<int>(a.n);
+    runs.reach[1] = 0;
   }
   __syncthreads();
   for (int g = threadIdx.x; g < a.groups; g += kThreadsHere) {
@@ -140,18 +150,18 @@ __device__ void read_runs(const ProductArgs& a, const ProductPlan& p, Runs& runs
     runs.first[g] = from;
     runs.rows[g] = max(0, to - from);
     if (!F::kRaggedK && to > from) {
-      atomicMin(&runs.low, from);
-      atomicMax(&runs.high, to);
+      atomicMin(&runs.reach[0], from);
+      atomicMax(&runs.reach[1], to);
     }
   }
   __syncthreads();
   if (!F::kRaggedK && threadIdx.x < 32) {
     if (threadIdx.x == 0) {
       // rows before the first run and behind the last belong to nobody (all, when there is no run)
-      runs.first[a.groups] = runs.high;
-      runs.rows[a.groups] = static_cast<int>(a.n) - runs.high;
+      runs.first[a.groups] = runs.reach[1];
+      runs.rows[a.groups] = static_cast<int>(a.n) - runs.reach[1];
       runs.first[a.groups + 1] = 0;
-      runs.rows[a.groups + 1] = min(runs.low, runs.high);
+      runs.rows[a.groups + 1] = min(runs.reach[0], runs.reach[1]);
     }
     __syncwarp();
     int sum = 0;
@@ -187,72 +197,135 @@ struct Ring {
 };
 
 template <typename T>
-__device__ __forceinline__ uint32_t pair_of(float lo, float hi) {
-  const T a = DT<T>::from_f32(lo), b = DT<T>::from_f32(hi);
-  return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&a)) |
-         static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&b)) << 16;
+__device__ __forceinline__ uint32_t pair_of(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pair_of<__half>(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pair_of<__nv_bfloat16>(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The thread's column m of `rows` rows of out, from element `at` (row stride
-// out_row). A warp holds 32 neighbouring columns.
+// A buffer of the epilogue: [128 bytes of columns][row][16-byte piece ^ row], as TMA
+// takes it; 128 columns of kStoreRows rows.
 template <typename T>
-__device__ __forceinline__ void store_columns(const ProductArgs& a, const float (&acc)[128], int64_t at, int rows,
-                                              bool in, bool pairs) {
-  T* out = static_cast<T*>(a.out) + at;
-  if (sizeof(T) == 2 && pairs) {
-    // two rows at once: the lanes of a pair of columns swap sums and store one row each
-    const int odd = threadIdx.x & 1;
-    out += odd ? a.out_row - 1 : 0;
-#pragma unroll
-    for (int j = 0; j < 128; j += 2) {
-      if (j % 8 == 0 && j >= rows) return;
-      const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? acc[j] : acc[j + 1], 1);
-      const uint32_t two = odd ? pair_of<T>(got, acc[j + 1]) : pair_of<T>(acc[j], got);
-      if (in && j + odd < rows) *reinterpret_cast<uint32_t*>(out) = two;
-      out += 2 * a.out_row;
-      asm volatile("" : "+l"(out));  // one address that moves on, not 64 held beside the sums
+constexpr int kStoreRows = kStoreBytes / (128 * sizeof(T));
+
+// Its first `rows` rows to `out` (its first element) by ordinary stores; four warps.
+template <typename T>
+__device__ __noinline__ void store_rows(const ProductArgs& a, const uint8_t* buf, T* out, int64_t m, int rows, int warp,
+                                        int lane, bool aligned) {
+  constexpr int kElems = 16 / sizeof(T), kPieces = 128 / kElems, kAtOnce = 32 / kPieces;
+  const int piece = lane % kPieces;
+  const int columns = static_cast<int>(min((int64_t)kElems, a.m - m - piece * kElems));
+  for (int r = warp * kAtOnce + lane / kPieces; r < rows; r += 4 * kAtOnce) {
+    T e[kElems];
+    *reinterpret_cast<uint4*>(e) =
+        *reinterpret_cast<const uint4*>(buf + piece / 8 * (kStoreRows<T> * 128) + r * 128 + (piece % 8 ^ (r & 7)) * 16);
+    T* to = out + r * a.out_row + piece * kElems;
+    if (aligned && columns == kElems && !(sizeof(T) == 4 && a.accumulate)) {
+      *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(e);
+      continue;
     }
-    return;
+#pragma unroll
+    for (int j = 0; j < kElems; ++j) {
+      if (j >= columns) break;
+      if constexpr (sizeof(T) == 4) {
+        if (a.accumulate) e[j] += to[j];
+      }
+      to[j] = e[j];
+    }
   }
-  if (!in) return;
+}
+
+// A tile's sums out, as T, from TMEM at `from` (zeros). Four warps (`quarter`: 32
+// columns of out each) have columns [m, m + 128) of `rows` rows from row n of matrix
+// g; they share two buffers at `space`, which they take in turn, and barrier `id`. The
+// loop is not unrolled: unrolled it is more code than the instruction caches hold, and
+// took twice the time.
+template <typename T, bool CLIPS>
+__device__ __forceinline__ void store_tile(const ProductArgs& a, const CUtensorMap* map, bool tiles, uint32_t from,
+                                           bool zero, int64_t m, int64_t n, int g, int rows, int quarter, int lane,
+                                           uint8_t* space, uint32_t& turn, int id) {
+  constexpr int kRows = kStoreRows<T>, kBoxes = sizeof(T), kWide = 128 / (int)sizeof(T);
+  const bool issues = quarter == 0 && elect_one() != 0;
+  const int boxes = static_cast<int>(min((int64_t)kBoxes, (a.m - m + kWide - 1) / kWide));
+#pragma unroll 1
+  for (int row0 = 0; row0 < rows; row0 += kRows) {
+    uint8_t* buf = space + (turn++ & 1) * kStoreBytes;
+    uint32_t v[2][kRows / 2];  // [half of the columns][8 rows, as fragments]
 #pragma unroll
-  for (int c = 0; c < 128; c += 8) {
-    if (c >= rows) return;
-    float v[8];
+    for (int h = 0; h < 2; ++h) {
+      if (zero) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = acc[c + j];
-    if (sizeof(T) == 4 && a.accumulate) {
-      const T* old = out;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (c + j < rows) v[j] += DT<T>::to_f32(*old);
-        old += a.out_row;
-        asm volatile("" : "+l"(old));
+        for (int j = 0; j < kRows / 2; ++j) v[h][j] = 0;
+      } else if constexpr (kRows == 32) {
+        tmem_ld_16x32(from + ((uint32_t)h << 20) + row0, v[h]);
+      } else {
+        tmem_ld_16x16(from + ((uint32_t)h << 20) + row0, v[h]);
       }
     }
+    if (issues) tma_store_read<1>();  // the store before last has been read
+    some_sync(id, 128);
+    tmem_wait_ld();
+    tmem_loaded(v[0]);
+    tmem_loaded(v[1]);
+    auto sum = [&](int h, int k, int i) { return __uint_as_float(v[h][k * 4 + i]); };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (c + j < rows) *out = DT<T>::from_f32(v[j]);
-      out += a.out_row;
-      asm volatile("" : "+l"(out));
+    for (int k = 0; k < kRows / 8; ++k) {
+      if constexpr (sizeof(T) == 2) {
+        const int r = k * 8 + lane % 8;
+        store_turned4(smem_u32(buf) + quarter / 2 * (kRows * 128) + r * 128 + (((quarter & 1) * 4 + lane / 8) ^ (r & 7)) * 16,
+                      pair_of<T>(sum(0, k, 0), sum(0, k, 1)), pair_of<T>(sum(0, k, 2), sum(0, k, 3)),
+                      pair_of<T>(sum(1, k, 0), sum(1, k, 1)), pair_of<T>(sum(1, k, 2), sum(1, k, 3)));
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = k * 8 + 2 * (lane & 3) + (i & 1), at = h * 16 + i / 2 * 8 + lane / 4;
+            *reinterpret_cast<float*>(buf + quarter * (kRows * 128) + r * 128 + (at / 4 ^ (r & 7)) * 16 + at % 4 * 4) =
+                sum(h, k, i);
+          }
+      }
     }
+    fence_async_smem();
+    some_sync(id, 128);
+    const int left = rows - row0;
+    if (tiles && (CLIPS || left >= kRows)) {  // (CLIPS: rows behind these are behind the matrix's end, and dropped)
+      if (issues)
+        for (int c = 0; c < boxes; ++c) {
+          const uint32_t src = smem_u32(buf) + c * (kRows * 128);
+          if (sizeof(T) == 4 && a.accumulate)
+            tma_add3(map, src, (int)m + c * kWide, (int)n + row0, g);
+          else
+            tma_store3(map, src, (int)m + c * kWide, (int)n + row0, g);
+        }
+    } else {
+      store_rows(a, buf, static_cast<T*>(a.out) + g * a.out_group + (n + row0) * a.out_row + m, m, min(left, kRows),
+                 quarter, lane, tiles);
+    }
+    if (issues) tma_store_commit();
   }
 }
 
 template <bool A_MN, bool B_MN, bool SCALED>
 __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-              const __grid_constant__ ProductArgs a, const __grid_constant__ ProductPlan p) {
+              const __grid_constant__ CUtensorMap map_out, const __grid_constant__ ProductArgs a, const __grid_constant__ ProductPlan p) {
   using F = Form<A_MN, B_MN, SCALED>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], sums_full[2], sums_empty[2],
       tail[kMaxStages], scales_full[kScaleSlots], scales_empty[kScaleSlots];
   __shared__ uint32_t tmem_slot, abort_word;
-  __shared__ Runs runs;
   // the swizzle is a function of address bits: tiles start on 1024 bytes, the same in both blocks
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem), stage_bytes = kABytes + p.b_bytes;
-  uint8_t* scales = smem + kStageBytes;
+  uint8_t* scales = smem + p.scales_at;
+  const Runs runs(smem + p.runs_at, a.groups);
   const int warp = warp_number(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
 
@@ -274,6 +347,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     mbar_init_fence();
     tma_prefetch(&map_a);
     tma_prefetch(&map_b);
+    if (p.tiles_out) tma_prefetch(&map_out);
   }
   if (warp == 3) tmem_alloc_pair(&tmem_slot, 512);
   read_runs<F>(a, p, runs);
@@ -457,49 +531,81 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
         slots.step();
       }
   } else if (warp >= 4) {
-    // ---- sums: a thread has one column of out (lane of TMEM) in half of the tile's rows
+    // ---- sums: four warps have the tile's columns of out (lanes of TMEM), each 32, in half of its rows
     const uint32_t empty0 = cluster_map(smem_u32(&sums_empty[0]), 0);
-    const int part = (warp - 4) / 4, row = (warp & 3) * 32 + lane;
-    const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's lanes
-    const bool pairs = a.out_dtype != kF32 && a.m % 2 == 0 && a.out_row % 2 == 0 && a.out_group % 2 == 0 &&
-                       reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
+    const int part = (warp - 4) / 4, quarter = warp & 3;
+    const uint32_t mine = tmem + ((uint32_t)quarter << 21);  // the warp's lanes
+    uint32_t turn = 0;
     Ring sums(2);
     bool go = true;
-    while (go && walk.next(t)) {
-      const int half = t.padded / 2;  // rows of this warp
-      float acc[128];
-#pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+    while (walk.next(t)) {
+      // the first four warps have the first half of the rows, in whole 32s
+      const int first = part == 0 ? 0 : (t.padded / 2 + 31) / 32 * 32;
+      const int half = part == 0 ? min((t.padded / 2 + 31) / 32 * 32, t.padded) : t.padded - first;
+      uint32_t from = 0;
+      // Of a run that is not the only one the sums go to registers, of the last one back.
+      uint32_t acc[8][16];
 #pragma unroll 1
       for (int step = 0; step < t.steps; step += kRun) {
         if (!(go = wait(&sums_full[sums.at], sums.phase))) break;
         tc_fence_after();
-        const uint32_t from = mine + sums.at * F::kMaxN + part * half;
+        from = mine + sums.at * F::kMaxN + first;
+        const bool end = step + kRun >= t.steps;
+        if (step == 0 && end) break;
+        // (up to 128 rows, whatever the tile's width)
+        if (step == 0) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 16)
-          if (c < half) {
+          for (int i = 0; i < 8; ++i) tmem_ld_16x32(from + ((uint32_t)(i % 2) << 20) + i / 2 * 32, acc[i]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) tmem_loaded(acc[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
             uint32_t r[16];
-            tmem_ld16(from + c, r);
+            tmem_ld_16x32(from + ((uint32_t)(i % 2) << 20) + i / 2 * 32, r);
             tmem_wait_ld();
+            tmem_loaded(r);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(r[j]);
+            for (int j = 0; j < 16; ++j) acc[i][j] = __float_as_uint(__uint_as_float(acc[i][j]) + __uint_as_float(r[j]));
           }
+        }
+        if (end) break;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_mapped(empty0 + sums.at * 8);
         sums.step();
       }
-      if (!go || (a.accumulate && t.steps == 0)) continue;
-      const int64_t m = t.m0 + (int64_t)rank * 128 + row, n = (int64_t)t.n0 + part * half;
-      const int64_t at = (F::kRaggedK ? t.g * a.out_group : 0) + n * a.out_row + m;
-      const int rows = min(half, t.width - part * half);
-      if (a.out_dtype == kF32)
-        store_columns<float>(a, acc, at, rows, m < a.m, false);
-      else if (a.out_dtype == kF16)
-        store_columns<__half>(a, acc, at, rows, m < a.m, pairs);
-      else
-        store_columns<__nv_bfloat16>(a, acc, at, rows, m < a.m, pairs);
+      // the four go on together or not at all
+      if (!(go = some_sync_and(1 + part, 128, go))) break;
+      if (t.steps > kRun) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i / 2 * 32 < half) tmem_st_16x32(from + ((uint32_t)(i % 2) << 20) + i / 2 * 32, acc[i]);
+        tmem_wait_st();
+      }
+      if (!(a.accumulate && t.steps == 0)) {
+        uint8_t* space = smem + p.store_at + part * (2 * kStoreBytes);
+        auto store = [&](auto type) {
+          store_tile<decltype(type), F::kRaggedK>(a, &map_out, p.tiles_out != 0, from, t.steps == 0,
+                                                  t.m0 + (int64_t)rank * 128, t.n0 + (int64_t)first, F::kRaggedK ? t.g : 0,
+                                                  min(half, t.width - first), quarter, lane, space, turn, 1 + part);
+        };
+        if (a.out_dtype == kF32)
+          store(float());
+        else if (a.out_dtype == kF16)
+          store(__half());
+        else
+          store(__nv_bfloat16());
+      }
+      if (t.steps > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_mapped(empty0 + sums.at * 8);
+        sums.step();
+      }
     }
+    tma_store_read<0>();
   }
   // No block leaves while the other may still reach its memory or arrive at its barriers.
   __syncwarp();
@@ -526,8 +632,11 @@ cudaError_t run(const ProductArgs& a, cudaStream_t s) {
     p.tile_n = mean <= 48 ? 64 : mean <= 112 ? 128 : F::kMaxN;
     p.b_bytes = p.tile_n / 2 * kStepBytes;
   }
-  const int stage = kABytes + p.b_bytes;
-  p.stages = kStageBytes / stage < kMaxStages ? kStageBytes / stage : kMaxStages;
+  const int stage = kABytes + p.b_bytes, behind = kStoreSpace + (SCALED ? kScaleSlots * kScaleSlot : 0) + Runs::bytes(a.groups);
+  p.stages = min((kMostSmem - 1024 - behind) / stage, kMaxStages);
+  p.store_at = p.stages * stage;
+  p.scales_at = p.store_at + kStoreSpace;
+  p.runs_at = p.scales_at + (SCALED ? kScaleSlots * kScaleSlot : 0);
 
   // a: along M and K (in either order) by group; b: its rows, all groups' together
   const uint64_t groups = F::kRaggedK ? 1 : a.groups;
@@ -535,17 +644,24 @@ cudaError_t run(const ProductArgs& a, cudaStream_t s) {
   const uint64_t a_strides[2] = {(uint64_t)a.a_row * elem, (uint64_t)(groups > 1 ? a.a_group : a.a_row) * elem};
   const uint64_t b_extent[3] = {(uint64_t)(B_MN ? a.n : a.k), (uint64_t)(B_MN ? a.k : a.n), 1};
   const uint64_t b_strides[2] = {(uint64_t)a.b_row * elem, (uint64_t)a.b_row * elem};
-  CUtensorMap map_a, map_b;
+  const int64_t size = a.out_dtype == kF32 ? 4 : 2;
+  const uint64_t out_groups = F::kRaggedK ? a.groups : 1;
+  const uint64_t out_extent[3] = {(uint64_t)a.m, (uint64_t)a.n, out_groups};
+  const uint64_t out_strides[2] = {(uint64_t)(a.out_row * size), (uint64_t)((out_groups > 1 ? a.out_group : a.out_row) * size)};
+  p.tiles_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && out_strides[0] % 16 == 0 && out_strides[1] % 16 == 0;
+  CUtensorMap map_a, map_b, map_out{};
   if (!make_tensor_map(&map_a, a.a, a.dtype, 3, a_extent, a_strides, A_MN ? kMnRows : 128) ||
-      !make_tensor_map(&map_b, a.b, a.dtype, 3, b_extent, b_strides, B_MN ? kMnRows : p.tile_n / 2))
+      !make_tensor_map(&map_b, a.b, a.dtype, 3, b_extent, b_strides, B_MN ? kMnRows : p.tile_n / 2) ||
+      (p.tiles_out && !make_tensor_map(&map_out, a.out, a.out_dtype, 3, out_extent, out_strides,
+                                       size == 4 ? kStoreRows<float> : kStoreRows<__half>)))
     return cudaErrorInvalidValue;
 
   static std::atomic<uint64_t> asked{0};
-  cudaError_t e = allow_smem(kernel, F::kSmem, asked);
+  cudaError_t e = allow_smem(kernel, kMostSmem, asked);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kThreadsHere);
-  cfg.dynamicSmemBytes = F::kSmem;
+  cfg.dynamicSmemBytes = kMostSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -571,7 +687,7 @@ cudaError_t run(const ProductArgs& a, cudaStream_t s) {
   if (most > (int64_t)0x7FFFFFFF || a.n > 0x7FFFFFFF || a.k > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   p.pairs = static_cast<int>(most < pairs ? most : pairs);
   cfg.gridDim = dim3(2 * p.pairs);
-  return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, a, p);
+  return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, map_out, a, p);
 }
 
 }  // namespace
