@@ -84,4 +84,23 @@ struct ProductArgs {
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t s);
 cudaError_t product_error(unsigned** at);
 
+#ifdef __CUDACC__
+// A launch that may begin while the kernel ahead of it in the stream still runs: the
+// kernel calls griddep_wait() before its first access to memory.
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 }  // namespace zg

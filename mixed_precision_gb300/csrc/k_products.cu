@@ -21,6 +21,8 @@
 // that a row of out lies there as it does in memory, and TMA stores take 32 rows (16
 // of fp32) from there while the next are made. Rows behind the last whole 32 of a
 // run, and outs whose rows do not start on 16 bytes, go by ordinary stores.
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "block.h"
@@ -350,9 +352,10 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     if (p.tiles_out) tma_prefetch(&map_out);
   }
   if (warp == 3) tmem_alloc_pair(&tmem_slot, 512);
+  griddep_wait();
+  griddep_trigger();
   read_runs<F>(a, p, runs);
   tc_fence_before();
-  __syncthreads();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
@@ -617,19 +620,75 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
   }
 }
 
+// The width of tiles with the least estimated time, in cycles: a step of 64 (e4m3: 128)
+// along K takes 2 for each row of the tile, 200 at least and what its bytes need at 96
+// a cycle; a tile's sums leave at 16 a row (fp32 30), and 3000 more lie around it. Wide
+// tiles win but where they leave most of a round empty. 2048 x 2048 x 4096 in e4m3
+// takes 25 us with tiles of 128, 27 with 224; 8192 x 2048 x 1024 27 and 23; 16384 x
+// 2048 x 2048 in bf16 by 16 experts 99 us with tiles of 128, 83 with 256.
+int choose_width(const ProductArgs& a, bool ragged_k, int step_k, int most, int pairs) {
+  const double m_tiles = std::ceil(a.m / (double)kTileM), mean = (ragged_k ? a.k : a.n) / (double)a.groups;
+  const double steps = std::ceil((ragged_k ? mean : (double)a.k) / step_k);
+  const bool known = ragged_k || a.offsets == nullptr;  // how many tiles there are
+  int best = most;
+  double least = 1e300;
+  for (int w = a.n <= 32 ? 32 : 64; w <= most; w += 32) {
+    const double across = known ? std::ceil(a.n / (double)w) : std::max(1.0, mean / w + 0.5);
+    const double tiles = m_tiles * across * (ragged_k || !known ? a.groups : 1);
+    const double rounds = known ? std::ceil(tiles / pairs) : std::max(1.0, tiles / pairs + 0.5);
+    const double width = std::min((double)w, std::ceil((known ? a.n / across : mean) / 32) * 32);
+    const double step = std::max({2 * width, 200.0, (kABytes + 64.0 * w) / 96});
+    const double time = rounds * (std::max(steps * step, (a.out_dtype == kF32 ? 30 : 16) * width) + 3000);
+    if (time <= least) {
+      least = time;
+      best = w;
+    }
+    if (w >= a.n) break;
+  }
+  return best;
+}
+
 template <bool A_MN, bool B_MN, bool SCALED>
 cudaError_t run(const ProductArgs& a, cudaStream_t s) {
   using F = Form<A_MN, B_MN, SCALED>;
   constexpr uint64_t elem = SCALED ? 1 : 2;
   auto kernel = k_product<A_MN, B_MN, SCALED>;
+  static std::atomic<uint64_t> asked{0};
+  cudaError_t e = allow_smem(kernel, kMostSmem, asked);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(kThreadsHere);
+  cfg.dynamicSmemBytes = kMostSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // As many pairs as run at once; asked once per kernel and device.
+  constexpr int kDevices = 64;
+  static std::atomic<int> found[kDevices];
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  int pairs = dev < kDevices ? found[dev].load(std::memory_order_relaxed) : 0;
+  if (pairs == 0) {
+    cfg.gridDim = dim3(2);
+    if ((e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg)) != cudaSuccess) return e;
+    if (pairs < 1) return cudaErrorLaunchOutOfResources;
+    if (dev < kDevices) found[dev].store(pairs, std::memory_order_relaxed);
+  }
+
   ProductPlan p{};
-  if (F::kRaggedK) {
-    const int64_t across = (a.n + F::kMaxN - 1) / F::kMaxN;
+  const int width = choose_width(a, F::kRaggedK, F::kStepK, F::kMaxN, pairs);
+  const int64_t across = (a.n + width - 1) / width;
+  if (F::kRaggedK) {  // every expert's tiles are the same: as narrow as they can be
     p.tile_n = static_cast<int>((a.n + across - 1) / across + 31) / 32 * 32;
     p.b_bytes = (p.tile_n / 2 + 63) / 64 * kMnChunk;
   } else {
-    const int64_t mean = (a.n + a.groups - 1) / a.groups;
-    p.tile_n = mean <= 48 ? 64 : mean <= 112 ? 128 : F::kMaxN;
+    p.tile_n = width;
     p.b_bytes = p.tile_n / 2 * kStepBytes;
   }
   const int stage = kABytes + p.b_bytes, behind = kStoreSpace + (SCALED ? kScaleSlots * kScaleSlot : 0) + Runs::bytes(a.groups);
@@ -656,37 +715,12 @@ cudaError_t run(const ProductArgs& a, cudaStream_t s) {
                                        size == 4 ? kStoreRows<float> : kStoreRows<__half>)))
     return cudaErrorInvalidValue;
 
-  static std::atomic<uint64_t> asked{0};
-  cudaError_t e = allow_smem(kernel, kMostSmem, asked);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(kThreadsHere);
-  cfg.dynamicSmemBytes = kMostSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  // As many pairs as run at once (fewer than half the SMs: a pair lies within one
-  // cluster of SMs); asked once per kernel and device.
-  constexpr int kDevices = 64;
-  static std::atomic<int> found[kDevices];
-  int dev = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  int pairs = dev < kDevices ? found[dev].load(std::memory_order_relaxed) : 0;
-  if (pairs == 0) {
-    cfg.gridDim = dim3(2);
-    if ((e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg)) != cudaSuccess) return e;
-    if (pairs < 1) return cudaErrorLaunchOutOfResources;
-    if (dev < kDevices) found[dev].store(pairs, std::memory_order_relaxed);
-  }
   const int64_t m_tiles = (a.m + kTileM - 1) / kTileM, n_tiles = (a.n + p.tile_n - 1) / p.tile_n;
   const int64_t most = m_tiles * (F::kRaggedK ? n_tiles * a.groups : n_tiles + a.groups + 2);
   if (most > (int64_t)0x7FFFFFFF || a.n > 0x7FFFFFFF || a.k > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   p.pairs = static_cast<int>(most < pairs ? most : pairs);
   cfg.gridDim = dim3(2 * p.pairs);
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, map_out, a, p);
 }
 

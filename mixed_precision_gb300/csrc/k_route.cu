@@ -9,6 +9,7 @@
 // what the blocks before it have taken of each expert and places its own slots
 // in order (k_order): a stable counting sort, no order left to atomics.
 #include "block.h"
+#include "bulk.cuh"
 #include "experts.h"
 #include "vec.cuh"
 
@@ -37,6 +38,8 @@ __device__ __forceinline__ float warp_sum(float x) {
 // PER: experts a lane.
 template <typename T, int PER>
 __global__ void __launch_bounds__(kRouteThreads) k_choose(const RouteArgs a, int per_block) {
+  griddep_wait();
+  griddep_trigger();
   extern __shared__ int32_t count[];  // [experts]
   for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) count[e] = 0;
   __syncthreads();
@@ -124,6 +127,8 @@ __device__ int block_prefix(int32_t* x, int n, int32_t* warps) {
 }
 
 __global__ void __launch_bounds__(kRouteThreads) k_order(const RouteArgs a, int per_block, int blocks) {
+  griddep_wait();
+  griddep_trigger();
   extern __shared__ int32_t shared[];
   __shared__ int32_t warps[kRouteWarps];
   int32_t *total = shared, *next = shared + a.experts;  // next: rows of the expert in blocks before, then the block's own
@@ -179,11 +184,15 @@ __global__ void __launch_bounds__(kRouteThreads) k_order(const RouteArgs a, int 
 }
 
 __global__ void __launch_bounds__(kRouteThreads) k_no_tokens(int32_t* offsets, int n) {
+  griddep_wait();
+  griddep_trigger();
   for (int i = threadIdx.x; i < n; i += kRouteThreads) offsets[i] = 0;
 }
 
 template <typename T, int PER>
 __global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a) {
+  griddep_wait();
+  griddep_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   if (t >= a.tokens) return;
@@ -243,13 +252,11 @@ int tokens_per_block(int64_t tokens) {
 
 template <typename T, int PER>
 cudaError_t choose(const RouteArgs& a, int per_block, int blocks, cudaStream_t s) {
-  k_choose<T, PER><<<blocks, kRouteThreads, a.experts * 4, s>>>(a, per_block);
-  return cudaGetLastError();
+  return launch_next(k_choose<T, PER>, dim3(blocks), kRouteThreads, a.experts * 4, s, a, per_block);
 }
 template <typename T, int PER>
 cudaError_t backward(const RouteArgs& a, cudaStream_t s) {
-  k_route_backward<T, PER><<<(unsigned)((a.tokens + 7) / 8), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_next(k_route_backward<T, PER>, dim3((unsigned)((a.tokens + 7) / 8)), 256, 0, s, a);
 }
 
 #define ZG_BY_EXPERTS(T, call, ...)                                                \
@@ -273,15 +280,13 @@ int64_t route_workspace_bytes(int64_t tokens, int experts, int k) {
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
   if (a.tokens == 0) {
-    k_no_tokens<<<1, kRouteThreads, 0, s>>>(a.offsets, a.experts + 1);
-    return cudaGetLastError();
+    return launch_next(k_no_tokens, dim3(1), kRouteThreads, 0, s, a.offsets, a.experts + 1);
   }
   const int per = tokens_per_block(a.tokens);
   const int blocks = (int)((a.tokens + per - 1) / per);
   cudaError_t e = ZG_BY_TYPE(choose, a, per, blocks, s);
   if (e != cudaSuccess) return e;
-  k_order<<<blocks, kRouteThreads, a.experts * 8, s>>>(a, per, blocks);
-  return cudaGetLastError();
+  return launch_next(k_order, dim3(blocks), kRouteThreads, a.experts * 8, s, a, per, blocks);
 }
 
 cudaError_t launch_route_backward(const RouteArgs& a, cudaStream_t s) { return ZG_BY_TYPE(backward, a, s); }

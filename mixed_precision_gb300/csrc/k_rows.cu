@@ -5,6 +5,7 @@
 // order are read or written. The places come from the device; a place outside
 // the order is passed by. Rows that no slot fills are made zero by the warp of
 // their number. Bound by HBM: each row moves once.
+#include "bulk.cuh"
 #include "experts.h"
 #include "vec.cuh"
 
@@ -63,6 +64,8 @@ __device__ __forceinline__ int load_place(const RowsArgs& a, int64_t t, int lane
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kRowThreads) k_gather(const RowsArgs a) {
+  griddep_wait();
+  griddep_trigger();
   using P = Piece<T, VEC>;
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32;
@@ -93,6 +96,8 @@ __global__ void __launch_bounds__(kRowThreads) k_gather(const RowsArgs a) {
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kRowThreads) k_combine(const RowsArgs a) {
+  griddep_wait();
+  griddep_trigger();
   using P = Piece<T, VEC>;
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32;
@@ -134,6 +139,8 @@ __global__ void __launch_bounds__(kRowThreads) k_combine(const RowsArgs a) {
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kRowThreads) k_combine_backward(const RowsArgs a) {
+  griddep_wait();
+  griddep_trigger();
   using P = Piece<T, VEC>;
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32;
@@ -187,19 +194,13 @@ bool whole_vectors(const RowsArgs& a) {
   return a.hidden % 8 == 0 && a.x_stride % 8 == 0 && a.y_stride % 8 == 0;
 }
 
-#define ZG_ROWS(kernel)                                                                       \
-  const unsigned blocks = (unsigned)((a.tokens + kRowThreads / 32 - 1) / (kRowThreads / 32)); \
-  const bool vec = whole_vectors(a);                                                          \
-  if (a.dtype == kF32)                                                                        \
-    vec ? kernel<float, true><<<blocks, kRowThreads, 0, s>>>(a)                               \
-        : kernel<float, false><<<blocks, kRowThreads, 0, s>>>(a);                             \
-  else if (a.dtype == kF16)                                                                   \
-    vec ? kernel<__half, true><<<blocks, kRowThreads, 0, s>>>(a)                              \
-        : kernel<__half, false><<<blocks, kRowThreads, 0, s>>>(a);                            \
-  else                                                                                        \
-    vec ? kernel<__nv_bfloat16, true><<<blocks, kRowThreads, 0, s>>>(a)                       \
-        : kernel<__nv_bfloat16, false><<<blocks, kRowThreads, 0, s>>>(a);                     \
-  return cudaGetLastError()
+#define ZG_ROWS(kernel)                                                                             \
+  const unsigned blocks = (unsigned)((a.tokens + kRowThreads / 32 - 1) / (kRowThreads / 32));       \
+  const bool vec = whole_vectors(a);                                                                \
+  auto go = [&](auto* k) { return launch_next(k, dim3(blocks), kRowThreads, 0, s, a); };            \
+  if (a.dtype == kF32) return vec ? go(kernel<float, true>) : go(kernel<float, false>);             \
+  if (a.dtype == kF16) return vec ? go(kernel<__half, true>) : go(kernel<__half, false>);           \
+  return vec ? go(kernel<__nv_bfloat16, true>) : go(kernel<__nv_bfloat16, false>)
 
 }  // namespace
 

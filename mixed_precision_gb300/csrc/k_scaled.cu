@@ -11,6 +11,7 @@
 
 #include <cuda_fp8.h>
 
+#include "bulk.cuh"
 #include "experts.h"
 #include "vec.cuh"
 
@@ -143,6 +144,8 @@ struct Place {
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kPackThreads, sizeof(T) == 2 ? 5 : 3) k_scaled_pack_rows(const ScaledArgs a, int wide) {
+  griddep_wait();
+  griddep_trigger();
   const Place at(wide);
   const int64_t z = blockIdx.z, c = at.block * kScaledBlock + (threadIdx.x & 7) * 8;
   const T* x = static_cast<const T*>(a.x) + z * a.batch_stride + c;
@@ -253,6 +256,8 @@ __device__ __forceinline__ void pack_tile(const ScaledArgs& a, const Pack8<T> (&
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kTileThreads, 2) k_scaled_pack(const ScaledArgs a) {
+  griddep_wait();
+  griddep_trigger();
   __shared__ __align__(16) uint32_t turned[kTile * 32];  // [column][rows as 32 words], word w at w ^ (column / 8 * 2)
   __shared__ float tops[kTileWarps][kTile];
   const int64_t r0 = (int64_t)blockIdx.x * kTile, c0 = (int64_t)blockIdx.y * kTile, z = blockIdx.z;
@@ -285,6 +290,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_scaled_pack(const ScaledArg
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kPackThreads) k_scaled_unpack(const ScaledArgs a, int wide) {
+  griddep_wait();
+  griddep_trigger();
   const Place at(wide);
   const int64_t c = at.block * kScaledBlock + (threadIdx.x & 7) * 8;
   if (at.block >= a.pitch / kScaledBlock) return;
@@ -343,18 +350,15 @@ cudaError_t pack(const ScaledArgs& a, cudaStream_t s) {
   const int64_t across = a.pitch / kTile, down = (a.rows + kTile - 1) / kTile;
   if (a.qt == nullptr) {
     const RowGrid g(a.rows, across, a.batch);
-    k_scaled_pack_rows<T, VEC><<<g.grid, kPackThreads, 0, s>>>(a, g.wide);
-  } else {
-    k_scaled_pack<T, VEC><<<dim3((unsigned)down, (unsigned)across, (unsigned)a.batch), kTileThreads, 0, s>>>(a);
+    return launch_next(k_scaled_pack_rows<T, VEC>, g.grid, kPackThreads, 0, s, a, g.wide);
   }
-  return cudaGetLastError();
+  return launch_next(k_scaled_pack<T, VEC>, dim3((unsigned)down, (unsigned)across, (unsigned)a.batch), kTileThreads, 0, s, a);
 }
 
 template <typename T, bool VEC>
 cudaError_t unpack(const ScaledArgs& a, cudaStream_t s) {
   const RowGrid g(a.rows, a.pitch / kScaledBlock, 1);
-  k_scaled_unpack<T, VEC><<<g.grid, kPackThreads, 0, s>>>(a, g.wide);
-  return cudaGetLastError();
+  return launch_next(k_scaled_unpack<T, VEC>, g.grid, kPackThreads, 0, s, a, g.wide);
 }
 
 }  // namespace
