@@ -7,7 +7,8 @@
 // ones are struck out and the next round follows. Blocks hold neighbouring
 // tokens and count their choices by expert (k_choose); then every block adds up
 // what the blocks before it have taken of each expert and places its own slots
-// in order (k_order): a stable counting sort, no order left to atomics.
+// in order (k_order): a stable counting sort, no order left to atomics. Of few
+// tokens one block does both.
 #include "block.h"
 #include "bulk.cuh"
 #include "experts.h"
@@ -35,13 +36,77 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// PER: experts a lane.
-template <typename T, int PER>
+// Exclusive prefix over x[0..n) in shared memory, by the whole block; returns the sum.
+__device__ int block_prefix(int32_t* x, int n, int32_t* warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  int carry = 0;
+  for (int at = 0; at < n; at += kRouteThreads) {
+    const int i = at + threadIdx.x;
+    const int v = i < n ? x[i] : 0;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+      if (lane >= o) s += u;
+    }
+    if (lane == 31) warps[warp] = s;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < kRouteWarps; ++w) {
+      if (w < warp) before += warps[w];
+      all += warps[w];
+    }
+    if (i < n) x[i] = carry + before + s - v;
+    carry += all;
+    __syncthreads();
+  }
+  return carry;
+}
+
+// The slots [s0, s1) to their rows and the offsets: total[e] choices of each expert in
+// all, before[e] of them in blocks before (shared memory; both are overwritten).
+__device__ void place_slots(const RouteArgs& a, int64_t s0, int64_t s1, int blocks, int32_t* total, int32_t* before,
+                            int32_t* warps) {
+  const int E = a.experts;
+  const int taken = block_prefix(total, E, warps);
+  int32_t* next = before;  // the next row of each expert
+  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+    if (blockIdx.x == 0) a.offsets[e] = total[e];
+    next[e] += total[e];
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[E] = taken;
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  for (int64_t at = s0; at < s1; at += kRouteThreads) {
+    const int64_t slot = at + threadIdx.x;
+    const int e = slot < s1 ? a.chosen[slot] : -1;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+    const int rank = __popc(same & ((1u << lane) - 1));
+    int row = -1;
+    // the warps with slots take their rows one after the other
+    const int turns = (int)min((int64_t)kRouteWarps, (s1 - at + 31) / 32);
+    for (int w = 0; w < turns; ++w) {
+      if (w == warp && e >= 0) row = next[e] + rank;
+      __syncwarp();
+      if (w == warp && e >= 0 && rank == 0) next[e] += __popc(same);
+      __syncthreads();
+    }
+    if (slot < s1) a.place[slot] = row;
+    if (row >= 0) a.source[row] = (int32_t)slot;
+  }
+  // behind the last row; every block takes a share
+  for (int64_t r = taken + (int64_t)blockIdx.x * kRouteThreads + threadIdx.x; r < a.tokens * a.k;
+       r += (int64_t)blocks * kRouteThreads)
+    a.source[r] = -1;
+}
+
+// PER: experts a lane. ALONE: the only block, which places its slots too.
+template <typename T, int PER, bool ALONE>
 __global__ void __launch_bounds__(kRouteThreads) k_choose(const RouteArgs a, int per_block) {
   griddep_wait();
   griddep_trigger();
-  extern __shared__ int32_t count[];  // [experts]
-  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) count[e] = 0;
+  extern __shared__ int32_t count[];  // [experts], twice if ALONE
+  for (int e = threadIdx.x; e < (ALONE ? 2 : 1) * a.experts; e += kRouteThreads) count[e] = 0;
   __syncthreads();
   const int lane = threadIdx.x & 31;
   const int64_t t0 = (int64_t)blockIdx.x * per_block, t1 = min(t0 + per_block, a.tokens);
@@ -95,35 +160,13 @@ __global__ void __launch_bounds__(kRouteThreads) k_choose(const RouteArgs a, int
     }
   }
   __syncthreads();
-  int32_t* out = a.counts + (int64_t)blockIdx.x * a.experts;
-  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) out[e] = count[e];
-}
-
-// Exclusive prefix over x[0..n) in shared memory, by the whole block; returns the sum.
-__device__ int block_prefix(int32_t* x, int n, int32_t* warps) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  int carry = 0;
-  for (int at = 0; at < n; at += kRouteThreads) {
-    const int i = at + threadIdx.x;
-    const int v = i < n ? x[i] : 0;
-    int s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-      if (lane >= o) s += u;
-    }
-    if (lane == 31) warps[warp] = s;
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < kRouteWarps; ++w) {
-      if (w < warp) before += warps[w];
-      all += warps[w];
-    }
-    if (i < n) x[i] = carry + before + s - v;
-    carry += all;
-    __syncthreads();
+  if constexpr (ALONE) {
+    __shared__ int32_t warps[kRouteWarps];
+    place_slots(a, 0, a.tokens * a.k, 1, count, count + a.experts, warps);
+  } else {
+    int32_t* out = a.counts + (int64_t)blockIdx.x * a.experts;
+    for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) out[e] = count[e];
   }
-  return carry;
 }
 
 __global__ void __launch_bounds__(kRouteThreads) k_order(const RouteArgs a, int per_block, int blocks) {
@@ -131,7 +174,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_order(const RouteArgs a, int 
   griddep_trigger();
   extern __shared__ int32_t shared[];
   __shared__ int32_t warps[kRouteWarps];
-  int32_t *total = shared, *next = shared + a.experts;  // next: rows of the expert in blocks before, then the block's own
+  int32_t *total = shared, *before = shared + a.experts;
   const int E = a.experts;
   for (int e = threadIdx.x; e < 2 * E; e += kRouteThreads) shared[e] = 0;
   __syncthreads();
@@ -139,48 +182,19 @@ __global__ void __launch_bounds__(kRouteThreads) k_order(const RouteArgs a, int 
   const int parts = max(1, kRouteThreads / E);
   for (int i = threadIdx.x; i < E * parts; i += kRouteThreads) {
     const int e = i % E, p = i / E;
-    int all = 0, before = 0;
+    int all = 0, earlier = 0;
 #pragma unroll 8
     for (int b = p; b < blocks; b += parts) {
       const int c = a.counts[(int64_t)b * E + e];
       all += c;
-      before += b < (int)blockIdx.x ? c : 0;
+      earlier += b < (int)blockIdx.x ? c : 0;
     }
     atomicAdd(&total[e], all);
-    atomicAdd(&next[e], before);
+    atomicAdd(&before[e], earlier);
   }
   __syncthreads();
-  const int taken = block_prefix(total, E, warps);
-  for (int e = threadIdx.x; e < E; e += kRouteThreads) {
-    if (blockIdx.x == 0) a.offsets[e] = total[e];
-    next[e] += total[e];
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[E] = taken;
-  __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   const int64_t s0 = (int64_t)blockIdx.x * per_block * a.k;
-  const int64_t s1 = min(s0 + (int64_t)per_block * a.k, a.tokens * a.k);
-  for (int64_t at = s0; at < s1; at += kRouteThreads) {
-    const int64_t slot = at + threadIdx.x;
-    const int e = slot < s1 ? a.chosen[slot] : -1;
-    const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-    const int rank = __popc(same & ((1u << lane) - 1));
-    int row = -1;
-    // the warps with slots take their rows one after the other
-    const int turns = (int)min((int64_t)kRouteWarps, (s1 - at + 31) / 32);
-    for (int w = 0; w < turns; ++w) {
-      if (w == warp && e >= 0) row = next[e] + rank;
-      __syncwarp();
-      if (w == warp && e >= 0 && rank == 0) next[e] += __popc(same);
-      __syncthreads();
-    }
-    if (slot < s1) a.place[slot] = row;
-    if (row >= 0) a.source[row] = (int32_t)slot;
-  }
-  // behind the last row; every block takes a share
-  for (int64_t r = taken + (int64_t)blockIdx.x * kRouteThreads + threadIdx.x; r < a.tokens * a.k;
-       r += (int64_t)blocks * kRouteThreads)
-    a.source[r] = -1;
+  place_slots(a, s0, min(s0 + (int64_t)per_block * a.k, a.tokens * a.k), blocks, total, before, warps);
 }
 
 __global__ void __launch_bounds__(kRouteThreads) k_no_tokens(int32_t* offsets, int n) {
@@ -243,16 +257,21 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteArgs a) {
     if (i * 32 + lane < a.experts) out[i * 32 + lane] = DT<T>::from_f32(d[i]);
 }
 
+// Up to so many tokens take one block, which saves a launch.
+constexpr int64_t kFewTokens = 128;
+
 // Tokens a block: a warp's one at least, 152 blocks at most (an SM's one each:
 // k_order reads the counts of all of them).
 int tokens_per_block(int64_t tokens) {
+  if (tokens <= kFewTokens) return (int)tokens;
   const int64_t per = (tokens + 151) / 152;
   return (int)((per + kRouteWarps - 1) / kRouteWarps * kRouteWarps);
 }
 
 template <typename T, int PER>
 cudaError_t choose(const RouteArgs& a, int per_block, int blocks, cudaStream_t s) {
-  return launch_next(k_choose<T, PER>, dim3(blocks), kRouteThreads, a.experts * 4, s, a, per_block);
+  return blocks == 1 ? launch_next(k_choose<T, PER, true>, dim3(1), kRouteThreads, a.experts * 8, s, a, per_block)
+                     : launch_next(k_choose<T, PER, false>, dim3(blocks), kRouteThreads, a.experts * 4, s, a, per_block);
 }
 template <typename T, int PER>
 cudaError_t backward(const RouteArgs& a, cudaStream_t s) {
@@ -285,7 +304,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
   const int per = tokens_per_block(a.tokens);
   const int blocks = (int)((a.tokens + per - 1) / per);
   cudaError_t e = ZG_BY_TYPE(choose, a, per, blocks, s);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || blocks == 1) return e;
   return launch_next(k_order, dim3(blocks), kRouteThreads, a.experts * 8, s, a, per, blocks);
 }
 

@@ -27,6 +27,7 @@ __all__ = ["Routing", "route", "route_backward", "gather", "combine", "combine_b
            "weight_grad", "check"]
 
 _I32 = torch.int32
+_new_routing = object.__new__
 _experts_desc = abi.EXPERTS_DESC.pack
 
 
@@ -77,19 +78,25 @@ def route(logits: torch.Tensor, k: int, normalize: bool = True, stream=None) -> 
     tokens, num_experts = logits.shape
     handle, side = _stream(stream, (logits,))
     device = logits.device
+    # one allocation: four arrays of tokens * k, the offsets, the scratch, each from a 16-byte boundary
     nbytes = _route_scratch(tokens, num_experts, k)
-    weights = _new(side, (tokens, k), _F32, device)
-    experts = _new(side, (tokens, k), _I32, device)
-    place = _new(side, (tokens, k), _I32, device)
-    source = _new(side, tokens * k, _I32, device)
-    offsets = _new(side, num_experts + 1, _I32, device)
-    space = _new(side, nbytes, torch.uint8, device)
-    rc = _library().zero_route(logits.data_ptr(), step, tokens, num_experts, k, code, normalize, weights.data_ptr(),
-                               experts.data_ptr(), offsets.data_ptr(), source.data_ptr(), place.data_ptr(),
-                               space.data_ptr(), nbytes, handle)
+    slots = tokens * k
+    each, ends = (slots + 3) // 4 * 4, (num_experts + 4) // 4 * 4
+    space = _new(side, 4 * each + ends + nbytes // 4, _I32, logits.device)
+    at = space.data_ptr()
+    rc = _library().zero_route(logits.data_ptr(), step, tokens, num_experts, k, code, normalize, at, at + 4 * each,
+                               at + 16 * each, at + 8 * each, at + 12 * each, at + 16 * each + 4 * ends, nbytes, handle)
     if rc:
         abi._check(rc)
-    return Routing(num_experts, normalize, weights, experts, offsets, source, place)
+    r = _new_routing(Routing)
+    r.num_experts, r.normalize, r.tokens, r.k = num_experts, bool(normalize), tokens, k
+    shape, steps = (tokens, k), (k, 1)
+    r.weights = space.view(_F32).as_strided(shape, steps)
+    r.experts = space.as_strided(shape, steps, each)
+    r.source = space.as_strided((slots,), (1,), 2 * each)
+    r.place = space.as_strided(shape, steps, 3 * each)
+    r.offsets = space.as_strided((num_experts + 1,), (1,), 4 * each)
+    return r
 
 
 def route_backward(dweights: torch.Tensor, logits: torch.Tensor, routing: Routing, out=None,
