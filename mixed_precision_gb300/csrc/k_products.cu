@@ -314,6 +314,41 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const CUtensorM
   }
 }
 
+// fp32 sums go out from registers: the thread's column (`in`: one of out's) of `rows`
+// rows from `out` on, a warp 128 bytes of a row.
+__device__ __forceinline__ void store_sums(const ProductArgs& a, uint32_t from, bool zero, float* out, int rows, bool in) {
+#pragma unroll 1
+  for (int row0 = 0; row0 < rows; row0 += 16) {
+    uint32_t r[16];
+    if (zero) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) r[j] = 0;
+    } else {
+      tmem_ld16(from + row0, r);
+      tmem_wait_ld();
+      tmem_loaded(r);
+    }
+    if (!in) continue;
+    const int left = rows - row0;
+    float* to = out + row0 * a.out_row;
+    if (a.accumulate) {
+      const float* old = to;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        if (j < left) r[j] = __float_as_uint(__uint_as_float(r[j]) + *old);
+        old += a.out_row;
+        asm volatile("" : "+l"(old));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (j < left) *to = __uint_as_float(r[j]);
+      to += a.out_row;
+      asm volatile("" : "+l"(to));  // one address that moves on, not all at once
+    }
+  }
+}
+
 template <bool A_MN, bool B_MN, bool SCALED>
 __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     k_product(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -505,27 +540,36 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) pb[i] = a.b_scales + min((int64_t)t.n0 + lane + i * 32, a.n - 1) * a.scale_pitch;
       const int words = (t.steps + kScaleSteps - 1) / kScaleSteps;
-      uint4 va, vb, vc;
-      auto fetch = [&](int w) {
+      struct Words {
+        uint4 a, b, c;
+      } even, odd;  // two words are under way
+      auto fetch = [&](int w, Words& v) {
         if (w >= words) return;
         auto word = [&](const uint8_t* q) { return *reinterpret_cast<const uint32_t*>(q + w * 4); };
-        va = make_uint4(word(pa[0]), word(pa[1]), word(pa[2]), word(pa[3]));
-        vb = make_uint4(word(pb[0]), word(pb[1]), word(pb[2]), word(pb[3]));
-        vc = make_uint4(word(pb[4]), word(pb[5]), word(pb[6]), word(pb[7]));
+        v.a = make_uint4(word(pa[0]), word(pa[1]), word(pa[2]), word(pa[3]));
+        v.b = make_uint4(word(pb[0]), word(pb[1]), word(pb[2]), word(pb[3]));
+        v.c = make_uint4(word(pb[4]), word(pb[5]), word(pb[6]), word(pb[7]));
       };
-      fetch(0);
-#pragma unroll 1
-      for (int w = 0; w < words; ++w) {
-        if (!(go = wait(&scales_empty[slots.at], slots.phase ^ 1))) break;
+      auto put = [&](const Words& v) {
+        if (!(go = wait(&scales_empty[slots.at], slots.phase ^ 1))) return;
         uint8_t* to = scales + slots.at * kScaleSlot + lane * 16;
-        *reinterpret_cast<uint4*>(to) = va;
-        *reinterpret_cast<uint4*>(to + 512) = vb;
-        *reinterpret_cast<uint4*>(to + 1024) = vc;
+        *reinterpret_cast<uint4*>(to) = v.a;
+        *reinterpret_cast<uint4*>(to + 512) = v.b;
+        *reinterpret_cast<uint4*>(to + 1024) = v.c;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_release_mapped(full0 + slots.at * 8);
         slots.step();
-        fetch(w + 1);
+      };
+      fetch(0, even);
+      fetch(1, odd);
+#pragma unroll 1
+      for (int w = 0; w < words && go; w += 2) {
+        put(even);
+        fetch(w + 2, even);
+        if (!go || w + 1 >= words) break;
+        put(odd);
+        fetch(w + 3, odd);
       }
     }
     if (go)
@@ -565,12 +609,18 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            uint32_t r[16];
-            tmem_ld_16x32(from + ((uint32_t)(i % 2) << 20) + i / 2 * 32, r);
-            tmem_wait_ld();
-            tmem_loaded(r);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[i][j] = __float_as_uint(__uint_as_float(acc[i][j]) + __uint_as_float(r[j]));
+            for (int k = 0; k < 2; ++k) {
+              uint32_t r[8];
+              tmem_ld_16x16(from + ((uint32_t)(i % 2) << 20) + i / 2 * 32 + k * 16, r);
+              tmem_wait_ld();
+              tmem_loaded(r);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                uint32_t& to = acc[i][k * 8 + j];
+                to = __float_as_uint(__uint_as_float(to) + __uint_as_float(r[j]));
+              }
+            }
           }
         }
         if (end) break;
@@ -594,9 +644,12 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
                                                   t.m0 + (int64_t)rank * 128, t.n0 + (int64_t)first, F::kRaggedK ? t.g : 0,
                                                   min(half, t.width - first), quarter, lane, space, turn, 1 + part);
         };
-        if (a.out_dtype == kF32)
-          store(float());
-        else if (a.out_dtype == kF16)
+        if (a.out_dtype == kF32) {
+          const int64_t m = t.m0 + (int64_t)rank * 128 + quarter * 32 + lane;
+          store_sums(a, from, t.steps == 0,
+                     static_cast<float*>(a.out) + (F::kRaggedK ? t.g * a.out_group : 0) + (t.n0 + (int64_t)first) * a.out_row + m,
+                     min(half, t.width - first), m < a.m);
+        } else if (a.out_dtype == kF16)
           store(__half());
         else
           store(__nv_bfloat16());
