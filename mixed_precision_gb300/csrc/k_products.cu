@@ -13,14 +13,28 @@
 // memory, in both operands.
 //
 // Twelve warps: one loads by TMA, one issues MMAs, one brings scales (words of four
-// exponents, which the tensor core applies itself), eight take the sums. The sums
-// leave TMEM after every kRun steps and are added up in registers, rounded: the
-// tensor core truncates where it adds, which over thousands of steps would cost an
-// fp32 result its last bits. TMEM holds two tiles' sums, so the MMAs go on meanwhile.
-// A tile leaves through shared memory: 8 x 8 matrices are turned on the way in, so
-// that a row of out lies there as it does in memory, and TMA stores take 32 rows (16
-// of fp32) from there while the next are made. Rows behind the last whole 32 of a
-// run, and outs whose rows do not start on 16 bytes, go by ordinary stores.
+// exponents, which the tensor core applies itself) or clears rows, eight take the
+// sums. These leave TMEM after a run of steps and are added up in registers,
+// rounded: the tensor core truncates where it adds, which over thousands of steps
+// would cost an fp32 result its last bits. TMEM holds two tiles' sums, so the MMAs go
+// on meanwhile.
+//
+// An SM's stores leave at 32 bytes a cycle at most, whatever way they take (measured
+// alone and on all SMs at once: by TMA, from registers, by 64 to 512 bytes of a row).
+// fp32 sums go straight from registers, a warp 128 bytes of a row. 16-bit ones go
+// through shared memory: 8 x 8 matrices are turned on the way in, so that a row of out
+// lies there as it does in memory, and TMA stores take 32 rows from there while the
+// next are made. From registers, 64 bytes of a row each, they were as fast, but not
+// where rows start inside a sector (520 x 1000 weights: 47 us, so 29). Rows behind the
+// last whole 32 of a run, and outs whose rows do not start on 16 bytes, go by ordinary
+// stores.
+//
+// Measured (with the L2 flushed before): 16384 x 2048 x 2048 in bf16 by 16 even
+// experts 83 us forward (1660 TFLOP/s), 105 for the weights' gradient in fp32; 8192 x
+// 8192 x 8192 599 us (1840, 0.93 of the library's product); 8192 x 8192 x 4096 in e4m3
+// 156 us (3530 TFLOP/s); 74 rows x 2048 x 1024 by 16 experts 17 us. Bound by the tensor
+// cores, long under load by the power limit: the clock falls from 1.9 to 1.5 GHz, and
+// the forward products take 91 us, the library's batched product 86.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -40,10 +54,12 @@ constexpr int kStepBytes = 128;             // along the contraction: 64 element
 constexpr int kABytes = 128 * kStepBytes;   // of one block
 constexpr int kMnRows = 64;                 // rows of a step whose operands are contiguous along M and N
 constexpr int kMnChunk = kMnRows * 128;     // bytes of 64 columns of them
-constexpr int kRun = 16;                    // steps whose sums stay in the tensor core
+// Steps whose sums stay in the tensor core (powers of two). Each of four truncated
+// additions a step costs up to 9e-8 of the result where all terms have one sign: 3e-6
+// after 8 steps, of a 16-bit result's rounding (4e-4 and up) 2e-5 after 64. On the
+// inputs of a layer fp32 results are off by 4e-7 with 8 (9e-7 with 16) in norm.
+constexpr int kRunF32 = 8, kRunHalf = 64;
 constexpr int kMaxStages = 12;
-constexpr int kStoreBytes = 8192;           // a buffer: 32 rows of 128 16-bit columns, 16 of fp32
-constexpr int kStoreSpace = 4 * kStoreBytes;  // two for each half of the epilogue's warps
 constexpr int kMostSmem = 232448 - 1024;    // dynamic shared memory; the rest is for the barriers
 constexpr int kScaleSteps = 4;              // steps that a word of scales lasts
 constexpr int kScaleSlots = 4;
@@ -53,10 +69,11 @@ constexpr int kThreadsHere = (4 + kEpilogue) * 32;
 struct ProductPlan {
   int tile_n;    // widest tile, a multiple of 32
   int stages;
+  int run;       // steps whose sums stay in the tensor core, a power of two
   int b_bytes;   // of a stage and block
   int pairs;
   int store_at, scales_at, runs_at;  // in shared memory, behind the stages
-  int tiles_out;                     // out can be written by TMA
+  int tiles_out;                     // out is of 16 bits and can be written by TMA
 };
 
 template <bool A_MN, bool B_MN, bool SCALED>
@@ -211,40 +228,35 @@ __device__ __forceinline__ uint32_t pair_of<__nv_bfloat16>(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// A buffer of the epilogue: [128 bytes of columns][row][16-byte piece ^ row], as TMA
-// takes it; 128 columns of kStoreRows rows.
-template <typename T>
-constexpr int kStoreRows = kStoreBytes / (128 * sizeof(T));
+// A buffer of 16-bit results: [64 columns][row][16-byte piece ^ row], as TMA takes
+// it; 128 columns of kStoreRows rows.
+constexpr int kStoreRows = 32, kStoreBytes = kStoreRows * 128 * 2;
+constexpr int kStoreSpace = 4 * kStoreBytes;  // two for each half of the epilogue's warps
 
 // Its first `rows` rows to `out` (its first element) by ordinary stores; four warps.
-template <typename T>
-__device__ __noinline__ void store_rows(const ProductArgs& a, const uint8_t* buf, T* out, int64_t m, int rows, int warp,
-                                        int lane, bool aligned) {
-  constexpr int kElems = 16 / sizeof(T), kPieces = 128 / kElems, kAtOnce = 32 / kPieces;
-  const int piece = lane % kPieces;
-  const int columns = static_cast<int>(min((int64_t)kElems, a.m - m - piece * kElems));
-  for (int r = warp * kAtOnce + lane / kPieces; r < rows; r += 4 * kAtOnce) {
-    T e[kElems];
+__device__ __noinline__ void store_rows(const ProductArgs& a, const uint8_t* buf, uint16_t* out, int64_t m, int rows,
+                                        int warp, int lane, bool aligned) {
+  const int piece = lane % 16;
+  const int columns = static_cast<int>(min((int64_t)8, a.m - m - piece * 8));
+  for (int r = warp * 2 + lane / 16; r < rows; r += 8) {
+    uint16_t e[8];
     *reinterpret_cast<uint4*>(e) =
-        *reinterpret_cast<const uint4*>(buf + piece / 8 * (kStoreRows<T> * 128) + r * 128 + (piece % 8 ^ (r & 7)) * 16);
-    T* to = out + r * a.out_row + piece * kElems;
-    if (aligned && columns == kElems && !(sizeof(T) == 4 && a.accumulate)) {
+        *reinterpret_cast<const uint4*>(buf + piece / 8 * (kStoreRows * 128) + r * 128 + (piece % 8 ^ (r & 7)) * 16);
+    uint16_t* to = out + r * a.out_row + piece * 8;
+    if (aligned && columns == 8) {
       *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(e);
       continue;
     }
 #pragma unroll
-    for (int j = 0; j < kElems; ++j) {
+    for (int j = 0; j < 8; ++j) {
       if (j >= columns) break;
-      if constexpr (sizeof(T) == 4) {
-        if (a.accumulate) e[j] += to[j];
-      }
       to[j] = e[j];
     }
   }
 }
 
-// A tile's sums out, as T, from TMEM at `from` (zeros). Four warps (`quarter`: 32
-// columns of out each) have columns [m, m + 128) of `rows` rows from row n of matrix
+// A tile's sums out, as T (16 bits), from TMEM at `from` (zeros). Four warps (`quarter`:
+// 32 columns of out each) have columns [m, m + 128) of `rows` rows from row n of matrix
 // g; they share two buffers at `space`, which they take in turn, and barrier `id`. The
 // loop is not unrolled: unrolled it is more code than the instruction caches hold, and
 // took twice the time.
@@ -252,22 +264,19 @@ template <typename T, bool CLIPS>
 __device__ __forceinline__ void store_tile(const ProductArgs& a, const CUtensorMap* map, bool tiles, uint32_t from,
                                            bool zero, int64_t m, int64_t n, int g, int rows, int quarter, int lane,
                                            uint8_t* space, uint32_t& turn, int id) {
-  constexpr int kRows = kStoreRows<T>, kBoxes = sizeof(T), kWide = 128 / (int)sizeof(T);
   const bool issues = quarter == 0 && elect_one() != 0;
-  const int boxes = static_cast<int>(min((int64_t)kBoxes, (a.m - m + kWide - 1) / kWide));
+  const int boxes = a.m - m > 64 ? 2 : 1;
 #pragma unroll 1
-  for (int row0 = 0; row0 < rows; row0 += kRows) {
+  for (int row0 = 0; row0 < rows; row0 += kStoreRows) {
     uint8_t* buf = space + (turn++ & 1) * kStoreBytes;
-    uint32_t v[2][kRows / 2];  // [half of the columns][8 rows, as fragments]
+    uint32_t v[2][16];  // [half of the columns][8 rows, as fragments]
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (zero) {
 #pragma unroll
-        for (int j = 0; j < kRows / 2; ++j) v[h][j] = 0;
-      } else if constexpr (kRows == 32) {
-        tmem_ld_16x32(from + ((uint32_t)h << 20) + row0, v[h]);
+        for (int j = 0; j < 16; ++j) v[h][j] = 0;
       } else {
-        tmem_ld_16x16(from + ((uint32_t)h << 20) + row0, v[h]);
+        tmem_ld_16x32(from + ((uint32_t)h << 20) + row0, v[h]);
       }
     }
     if (issues) tma_store_read<1>();  // the store before last has been read
@@ -275,40 +284,23 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const CUtensorM
     tmem_wait_ld();
     tmem_loaded(v[0]);
     tmem_loaded(v[1]);
-    auto sum = [&](int h, int k, int i) { return __uint_as_float(v[h][k * 4 + i]); };
+    auto pair = [&](int h, int j) { return pair_of<T>(__uint_as_float(v[h][j]), __uint_as_float(v[h][j + 1])); };
 #pragma unroll
-    for (int k = 0; k < kRows / 8; ++k) {
-      if constexpr (sizeof(T) == 2) {
-        const int r = k * 8 + lane % 8;
-        store_turned4(smem_u32(buf) + quarter / 2 * (kRows * 128) + r * 128 + (((quarter & 1) * 4 + lane / 8) ^ (r & 7)) * 16,
-                      pair_of<T>(sum(0, k, 0), sum(0, k, 1)), pair_of<T>(sum(0, k, 2), sum(0, k, 3)),
-                      pair_of<T>(sum(1, k, 0), sum(1, k, 1)), pair_of<T>(sum(1, k, 2), sum(1, k, 3)));
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = k * 8 + 2 * (lane & 3) + (i & 1), at = h * 16 + i / 2 * 8 + lane / 4;
-            *reinterpret_cast<float*>(buf + quarter * (kRows * 128) + r * 128 + (at / 4 ^ (r & 7)) * 16 + at % 4 * 4) =
-                sum(h, k, i);
-          }
-      }
+    for (int k = 0; k < 4; ++k) {
+      const int r = k * 8 + lane % 8;
+      store_turned4(smem_u32(buf) + quarter / 2 * (kStoreRows * 128) + r * 128 + (((quarter & 1) * 4 + lane / 8) ^ (r & 7)) * 16,
+                    pair(0, k * 4), pair(0, k * 4 + 2), pair(1, k * 4), pair(1, k * 4 + 2));
     }
     fence_async_smem();
     some_sync(id, 128);
     const int left = rows - row0;
-    if (tiles && (CLIPS || left >= kRows)) {  // (CLIPS: rows behind these are behind the matrix's end, and dropped)
+    if (tiles && (CLIPS || left >= kStoreRows)) {  // (CLIPS: rows behind these are behind the matrix's end, and dropped)
       if (issues)
-        for (int c = 0; c < boxes; ++c) {
-          const uint32_t src = smem_u32(buf) + c * (kRows * 128);
-          if (sizeof(T) == 4 && a.accumulate)
-            tma_add3(map, src, (int)m + c * kWide, (int)n + row0, g);
-          else
-            tma_store3(map, src, (int)m + c * kWide, (int)n + row0, g);
-        }
+        for (int c = 0; c < boxes; ++c)
+          tma_store3(map, smem_u32(buf) + c * (kStoreRows * 128), (int)m + c * 64, (int)n + row0, g);
     } else {
-      store_rows(a, buf, static_cast<T*>(a.out) + g * a.out_group + (n + row0) * a.out_row + m, m, min(left, kRows),
-                 quarter, lane, tiles);
+      store_rows(a, buf, static_cast<uint16_t*>(a.out) + g * a.out_group + (n + row0) * a.out_row + m, m,
+                 min(left, kStoreRows), quarter, lane, tiles);
     }
     if (issues) tma_store_commit();
   }
@@ -459,7 +451,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
       uint32_t d = 0;
 #pragma unroll 1
       for (int step = 0; step < t.steps; ++step) {
-        if (step % kRun == 0) {
+        if ((step & (p.run - 1)) == 0) {
           if (!(go = wait(&sums_empty[sums.at], sums.phase ^ 1))) break;
           tc_fence_after();
           d = tmem + sums.at * F::kMaxN;
@@ -479,7 +471,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
         if (!(go = wait(&full[s], ring.phase))) break;
         tc_fence_after();
         const uint32_t at = s * (stage_bytes / 16);  // in the descriptors' units of 16 bytes
-        const bool more = step % kRun > 0;
+        const bool more = (step & (p.run - 1)) != 0;
         if constexpr (SCALED) {
           const uint32_t scaled = mma_desc_scaled(kTileM, t.padded, step % kScaleSteps);
 #pragma unroll
@@ -497,7 +489,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
         }
         mma_commit_pair(&empty[s], one);
         ring.step();
-        if (step % kRun == kRun - 1 || step + 1 == t.steps) {
+        if (((step + 1) & (p.run - 1)) == 0 || step + 1 == t.steps) {
           mma_commit_pair(&sums_full[sums.at], one);
           sums.step();
         }
@@ -593,11 +585,11 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
       // Of a run that is not the only one the sums go to registers, of the last one back.
       uint32_t acc[8][16];
 #pragma unroll 1
-      for (int step = 0; step < t.steps; step += kRun) {
+      for (int step = 0; step < t.steps; step += p.run) {
         if (!(go = wait(&sums_full[sums.at], sums.phase))) break;
         tc_fence_after();
         from = mine + sums.at * F::kMaxN + first;
-        const bool end = step + kRun >= t.steps;
+        const bool end = step + p.run >= t.steps;
         if (step == 0 && end) break;
         // (up to 128 rows, whatever the tile's width)
         if (step == 0) {
@@ -631,28 +623,26 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
       }
       // the four go on together or not at all
       if (!(go = some_sync_and(1 + part, 128, go))) break;
-      if (t.steps > kRun) {
+      if (t.steps > p.run) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (i / 2 * 32 < half) tmem_st_16x32(from + ((uint32_t)(i % 2) << 20) + i / 2 * 32, acc[i]);
         tmem_wait_st();
       }
       if (!(a.accumulate && t.steps == 0)) {
+        const int64_t m = t.m0 + (int64_t)rank * 128, n = t.n0 + (int64_t)first;
+        const int g = F::kRaggedK ? t.g : 0, rows = min(half, t.width - first);
         uint8_t* space = smem + p.store_at + part * (2 * kStoreBytes);
-        auto store = [&](auto type) {
-          store_tile<decltype(type), F::kRaggedK>(a, &map_out, p.tiles_out != 0, from, t.steps == 0,
-                                                  t.m0 + (int64_t)rank * 128, t.n0 + (int64_t)first, F::kRaggedK ? t.g : 0,
-                                                  min(half, t.width - first), quarter, lane, space, turn, 1 + part);
-        };
-        if (a.out_dtype == kF32) {
-          const int64_t m = t.m0 + (int64_t)rank * 128 + quarter * 32 + lane;
-          store_sums(a, from, t.steps == 0,
-                     static_cast<float*>(a.out) + (F::kRaggedK ? t.g * a.out_group : 0) + (t.n0 + (int64_t)first) * a.out_row + m,
-                     min(half, t.width - first), m < a.m);
-        } else if (a.out_dtype == kF16)
-          store(__half());
+        const int64_t column = m + quarter * 32 + lane;
+        if (a.out_dtype == kF32)
+          store_sums(a, from, t.steps == 0, static_cast<float*>(a.out) + g * a.out_group + n * a.out_row + column, rows,
+                     column < a.m);
+        else if (a.out_dtype == kF16)
+          store_tile<__half, F::kRaggedK>(a, &map_out, p.tiles_out != 0, from, t.steps == 0, m, n, g, rows, quarter, lane,
+                                          space, turn, 1 + part);
         else
-          store(__nv_bfloat16());
+          store_tile<__nv_bfloat16, F::kRaggedK>(a, &map_out, p.tiles_out != 0, from, t.steps == 0, m, n, g, rows, quarter,
+                                                 lane, space, turn, 1 + part);
       }
       if (t.steps > 0) {
         tc_fence_before();
@@ -735,6 +725,7 @@ cudaError_t run(const ProductArgs& a, cudaStream_t s) {
   }
 
   ProductPlan p{};
+  p.run = a.out_dtype == kF32 ? kRunF32 : kRunHalf;
   const int width = choose_width(a, F::kRaggedK, F::kStepK, F::kMaxN, pairs);
   const int64_t across = (a.n + width - 1) / width;
   if (F::kRaggedK) {  // every expert's tiles are the same: as narrow as they can be
@@ -756,16 +747,15 @@ cudaError_t run(const ProductArgs& a, cudaStream_t s) {
   const uint64_t a_strides[2] = {(uint64_t)a.a_row * elem, (uint64_t)(groups > 1 ? a.a_group : a.a_row) * elem};
   const uint64_t b_extent[3] = {(uint64_t)(B_MN ? a.n : a.k), (uint64_t)(B_MN ? a.k : a.n), 1};
   const uint64_t b_strides[2] = {(uint64_t)a.b_row * elem, (uint64_t)a.b_row * elem};
-  const int64_t size = a.out_dtype == kF32 ? 4 : 2;
   const uint64_t out_groups = F::kRaggedK ? a.groups : 1;
   const uint64_t out_extent[3] = {(uint64_t)a.m, (uint64_t)a.n, out_groups};
-  const uint64_t out_strides[2] = {(uint64_t)(a.out_row * size), (uint64_t)((out_groups > 1 ? a.out_group : a.out_row) * size)};
-  p.tiles_out = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && out_strides[0] % 16 == 0 && out_strides[1] % 16 == 0;
+  const uint64_t out_strides[2] = {(uint64_t)a.out_row * 2, (uint64_t)(out_groups > 1 ? a.out_group : a.out_row) * 2};
+  p.tiles_out = a.out_dtype != kF32 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && out_strides[0] % 16 == 0 &&
+                out_strides[1] % 16 == 0;
   CUtensorMap map_a, map_b, map_out{};
   if (!make_tensor_map(&map_a, a.a, a.dtype, 3, a_extent, a_strides, A_MN ? kMnRows : 128) ||
       !make_tensor_map(&map_b, a.b, a.dtype, 3, b_extent, b_strides, B_MN ? kMnRows : p.tile_n / 2) ||
-      (p.tiles_out && !make_tensor_map(&map_out, a.out, a.out_dtype, 3, out_extent, out_strides,
-                                       size == 4 ? kStoreRows<float> : kStoreRows<__half>)))
+      (p.tiles_out && !make_tensor_map(&map_out, a.out, a.out_dtype, 3, out_extent, out_strides, kStoreRows)))
     return cudaErrorInvalidValue;
 
   const int64_t m_tiles = (a.m + kTileM - 1) / kTileM, n_tiles = (a.n + p.tile_n - 1) / p.tile_n;
