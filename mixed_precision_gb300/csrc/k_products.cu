@@ -663,6 +663,22 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
   }
 }
 
+// out of no rows along K: zero.
+__global__ void __launch_bounds__(256) k_product_zero(const ProductArgs a) {
+  griddep_wait();
+  griddep_trigger();
+  const int64_t rows = a.n * a.groups;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int64_t at = r / a.n * a.out_group + r % a.n * a.out_row;
+    for (int64_t m = threadIdx.x; m < a.m; m += 256) {
+      if (a.out_dtype == kF32)
+        static_cast<float*>(a.out)[at + m] = 0.0f;
+      else
+        static_cast<uint16_t*>(a.out)[at + m] = 0;
+    }
+  }
+}
+
 // The width of tiles with the least estimated time, in cycles: a step of 64 (e4m3: 128)
 // along K takes 2 for each row of the tile, 200 at least and what its bytes need at 96
 // a cycle; a tile's sums leave at 16 a row (fp32 30), and 3000 more lie around it. Wide
@@ -773,6 +789,10 @@ ZG_ERROR_WORD(product_error, g_product_error)
 
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t s) {
   if (a.dtype == kE4M3) return run<false, false, true>(a, s);
+  if (a.ragged_k && a.k == 0) {
+    if (a.accumulate) return cudaSuccess;
+    return launch_next(k_product_zero, dim3((unsigned)std::min<int64_t>(a.n * a.groups, 4096)), 256, 0, s, a);
+  }
   if (a.ragged_k) return run<true, true, false>(a, s);
   return a.a_mn ? run<true, false, false>(a, s) : run<false, false, false>(a, s);
 }

@@ -499,3 +499,167 @@ def test_python_refusals():
         with pytest.raises((ValueError, RuntimeError)):
             bad()
     assert block.check is experts.check
+
+
+# ---------------------------------------------------------------------------
+# What the tensor-core products add: tiles, runs, ways out, kernels that overlap
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("tokens", [127, 128, 129, 256])
+@pytest.mark.parametrize("n,k", [(8, 3), (1000, 32)])
+def test_route_at_one_blocks_border(tokens, n, k):
+    g = gen(tokens + n)
+    logits = normal(g, tokens, n, scale=2)
+    logits[::9] = -math.inf
+    check_route(logits, k, True)
+    check_route(logits.round() + 0.0, k, False)
+
+
+def test_routing_arrays_start_on_16_bytes_and_are_apart():
+    """The arrays of a routing are parts of one allocation: each passes the checks that a user's own would."""
+    for tokens, n, k in ((1, 1, 1), (3, 5, 3), (129, 7, 5)):
+        r = experts.route(normal(gen(tokens), tokens, n), k)
+        again = experts.Routing(n, True, r.weights, r.experts, r.offsets, r.source, r.place)
+        x = normal(gen(1), tokens, 40, dtype=BF16)
+        assert torch.equal(experts.gather(x, r), experts.gather(x, again))
+        before = [t.clone() for t in (r.weights, r.experts, r.offsets, r.source, r.place)]
+        r.weights.fill_(7.0), r.offsets.fill_(3)
+        assert torch.equal(r.experts, before[1]) and torch.equal(r.source, before[3]) and torch.equal(r.place, before[4])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_weight_grad_of_no_rows(dtype):
+    off = torch.zeros(4, dtype=I32, device="cuda")
+    x, dy = torch.empty(0, 72, dtype=dtype, device="cuda"), torch.empty(0, 33, dtype=dtype, device="cuda")
+    for out in (dtype, F32):
+        dw = torch.full((3, 33, 80), 5.0, dtype=out, device="cuda")
+        experts.weight_grad(dy, x, off, out=dw[:, :, :72])
+        assert not bool(dw[:, :, :72].any()) and bool((dw[:, :, 72:] == 5).all())
+    dw = torch.full((3, 33, 72), 5.0, device="cuda")
+    experts.weight_grad(dy, x, off, out=dw, accumulate=True)
+    assert bool((dw == 5).all())
+
+
+@pytest.mark.parametrize("counts", [[1] * 1024, [0] * 1023 + [5], [3, 0] * 512])
+def test_products_of_a_thousand_experts(counts):
+    check_products(counts, 40, 72, BF16)
+
+
+# run lengths around the tiles' widths (32 to 256) and the steps' rows (64), outs that leave by
+# whole tiles, by ragged ends and element by element
+@pytest.mark.parametrize("counts", [[255, 257, 223, 225], [31, 32, 33, 511, 513], [2049]])
+@pytest.mark.parametrize("n_out,n_in", [(128, 136), (257, 264), (255, 520), (1, 8), (2, 1), (511, 72)])
+def test_products_around_the_tiles(counts, n_out, n_in):
+    check_products(counts, n_out, n_in, BF16)
+
+
+@pytest.mark.parametrize("shift", [0, 1, 2, 4, 8])
+@pytest.mark.parametrize("pad", [0, 1, 2, 8])
+def test_outputs_at_any_alignment(shift, pad):
+    """y, dx and dw that start on any element, rows any elements apart: the same bits, and nothing beside them."""
+    g = gen(11)
+    off = offsets_of([90, 40, 0, 133])
+    x, w, dy = normal(g, 263, 136, dtype=F16), normal(g, 4, 264, 136, dtype=F16), normal(g, 263, 264, dtype=F16)
+
+    def placed(want, call):
+        shape = want.shape
+        row = shape[-1] + pad
+        each = shape[-2] * row
+        count = each * (shape[0] if want.dim() == 3 else 1)
+        flat = torch.full((count + 32,), 5.0, dtype=want.dtype, device="cuda")
+        out = flat.as_strided(shape, (each, row, 1) if want.dim() == 3 else (row, 1), shift)
+        call(out)
+        assert torch.equal(out, want)
+        out.fill_(5.0)
+        assert bool((flat == 5).all())
+
+    placed(experts.forward(x, w, off), lambda o: experts.forward(x, w, off, out=o))
+    placed(experts.input_grad(dy, w, off), lambda o: experts.input_grad(dy, w, off, out=o))
+    for out in (F16, F32):
+        placed(experts.weight_grad(dy, x, off, dtype=out), lambda o: experts.weight_grad(dy, x, off, out=o))
+
+
+def test_sums_of_many_runs():
+    """K beyond the steps that stay in the tensor core: 8 of 64 for fp32 results, 64 for 16-bit ones."""
+    for k in (511, 512, 513, 4095, 4097, 9000):
+        g = gen(k)
+        off = offsets_of([70, 0, 190])
+        x, w = normal(g, 260, (k + 7) // 8 * 8, dtype=BF16)[:, :k], normal(g, 3, 72, (k + 7) // 8 * 8, dtype=BF16)[:, :, :k]
+        want, size = ref.forward(x, w, off.tolist())
+        close(experts.forward(x, w, off), want, ref.product_tol(k, size, want, BF16, BF16, run=4096), f"y {k}")
+        off = offsets_of([k, 3])
+        x, dy = normal(g, k + 3, 136, dtype=F16).abs(), normal(g, k + 3, 264, dtype=F16).abs()
+        want, size = ref.weight_grad(dy, x, off.tolist())
+        close(experts.weight_grad(dy, x, off, dtype=F32), want, ref.product_tol(k, size, want, F16, F32, run=512), f"dw {k}")
+
+
+def test_calls_one_behind_the_other():
+    """Kernels of neighbouring calls overlap: buffers that are read by one call and overwritten by the next,
+    in every order, hold what they hold when each call is waited for."""
+    logits, x, w_up, w_down, dout = layer_inputs(5, tokens=700)
+
+    def passes(wait):
+        g, kept = gen(77), []
+        rows = h = y = None
+        for i in range(12):
+            r = experts.route(logits + 0.1 * i, 2)
+            wait()
+            rows = experts.gather(x, r, out=rows)
+            wait()
+            h = experts.forward(rows, w_up, r.offsets, out=h)
+            wait()
+            y = experts.forward(h, w_down, r.offsets, out=y)
+            wait()
+            out = experts.combine(y, r)
+            wait()
+            dw = experts.weight_grad(y, h, r.offsets, dtype=F32)
+            wait()
+            experts.input_grad(y, w_down, r.offsets, out=h)
+            wait()
+            experts.weight_grad(y, h, r.offsets, out=dw, accumulate=True)
+            wait()
+            kept.append((r.place, out, dw, h.clone()))
+        return kept
+
+    want = passes(torch.cuda.synchronize)
+    for _ in range(3):
+        got = passes(lambda: None)
+        assert all(torch.equal(a, b) for p, q in zip(got, want) for a, b in zip(p, q))
+    experts.check()
+
+
+def test_products_on_two_streams_at_once():
+    g = gen(8)
+    off = offsets_of([500, 0, 900, 600])
+    x, w = normal(g, 2000, 520, dtype=BF16), normal(g, 4, 776, 520, dtype=BF16)
+    want = experts.forward(x, w, off)
+    dw = experts.weight_grad(want, x, off, dtype=F32)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(6):
+        outs.append((experts.forward(x, w, off, stream=sides[0]), experts.weight_grad(want, x, off, dtype=F32, stream=sides[1])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, want) and torch.equal(b, dw) for a, b in outs)
+
+
+def test_products_of_two_graphs():
+    """Captured calls hold no workspace: two graphs of the same products replayed at once."""
+    g = gen(9)
+    off = offsets_of([300, 10, 90])
+    x, w = normal(g, 400, 264, dtype=F16), normal(g, 3, 136, 264, dtype=F16)
+    want = experts.forward(x, w, off)
+    sides, graphs, outs = [torch.cuda.Stream() for _ in range(2)], [], []
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            outs.append(experts.forward(x, w, off))
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, graph in zip(sides, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)

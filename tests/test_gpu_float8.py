@@ -264,3 +264,43 @@ def test_refusals():
             bad()
     assert float8.pack(x[:0])[0].restore().shape == (0, 64)
 
+
+@pytest.mark.parametrize("rows", [1, 31, 33, 113, 223, 225, 449])
+@pytest.mark.parametrize("n", [1, 127, 129, 255, 257])
+def test_matmul_around_the_tiles(rows, n):
+    check_matmul(rows, n, 520, F32, gen(rows + n))
+    check_matmul(rows, n, 520, F16, gen(rows + n))
+
+
+@pytest.mark.parametrize("k", [1, 511, 512, 513, 1023, 1025, 2047, 4097, 9000])
+def test_matmul_of_many_steps(k):
+    """Words of four scales, runs of 8 steps of 128 (fp32) and of 64."""
+    g = gen(k)
+    x, w = normal(g, 70, k).abs(), normal(g, 300, k).abs()
+    a, b = float8.pack(x)[0], float8.pack(w)[0]
+    ra, rb = a.restore(F32).double(), b.restore(F32).double()
+    want, size = ra @ rb.t(), ra.abs() @ rb.abs().t()
+    for out, run in ((F32, 1024), (BF16, 8192)):
+        close(float8.matmul(a, b, dtype=out), want, ref.product_tol(k, size, want, None, out, per_mma=32, run=run), f"{out}")
+
+
+def test_matmul_reads_nothing_behind_the_columns():
+    """The codes and scales of the padding belong to the caller: what they hold does not matter."""
+    g = gen(4)
+    a, b = float8.pack(normal(g, 40, 300))[0], float8.pack(normal(g, 50, 300))[0]
+    want = float8.matmul(a, b, dtype=F32)
+    for m in (a, b):
+        m.q.view(torch.uint8)[:, 300:] = 0x7F  # NaN
+        m.scales[:, 3:] = 255
+    assert torch.equal(float8.matmul(a, b, dtype=F32), want)
+
+
+def test_experts_matmul_of_a_thousand():
+    g = gen(6)
+    counts = [1, 0] * 512
+    x, w = normal(g, 512, 264), normal(g, 1024, 33, 264)
+    a, b = float8.pack(x)[0], float8.pack(w)[0]
+    y = float8.matmul(a, b, offsets_of(counts), dtype=F32)
+    ra, rb = a.restore(F32).double(), b.restore(F32).double()[::2]
+    want, size = torch.einsum("rk,rnk->rn", ra, rb), torch.einsum("rk,rnk->rn", ra.abs(), rb.abs())
+    close(y, want, ref.product_tol(264, size, want, None, F32, per_mma=32, run=1024), "y")
