@@ -306,37 +306,27 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const CUtensorM
   }
 }
 
-// fp32 sums go out from registers: the thread's column (`in`: one of out's) of `rows`
-// rows from `out` on, a warp 128 bytes of a row.
-__device__ __forceinline__ void store_sums(const ProductArgs& a, uint32_t from, bool zero, float* out, int rows, bool in) {
-#pragma unroll 1
-  for (int row0 = 0; row0 < rows; row0 += 16) {
-    uint32_t r[16];
-    if (zero) {
+// fp32 sums go out from registers: the thread's column of `rows` rows from `out` on, a
+// warp 128 bytes of a row.
+__device__ __forceinline__ void store_sums(const ProductArgs& a, uint32_t (&acc)[8][16], float* out, int rows) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) r[j] = 0;
-    } else {
-      tmem_ld16(from + row0, r);
-      tmem_wait_ld();
-      tmem_loaded(r);
-    }
-    if (!in) continue;
-    const int left = rows - row0;
-    float* to = out + row0 * a.out_row;
+  for (int i = 0; i < 8; ++i) {
+    if (i * 16 >= rows) return;
+    const int left = rows - i * 16;
     if (a.accumulate) {
-      const float* old = to;
+      const float* old = out;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        if (j < left) r[j] = __float_as_uint(__uint_as_float(r[j]) + *old);
+        if (j < left) acc[i][j] = __float_as_uint(__uint_as_float(acc[i][j]) + *old);
         old += a.out_row;
-        asm volatile("" : "+l"(old));
+        asm volatile("" : "+l"(old));  // one address that moves on, not all at once
       }
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      if (j < left) *to = __uint_as_float(r[j]);
-      to += a.out_row;
-      asm volatile("" : "+l"(to));  // one address that moves on, not all at once
+      if (j < left) *out = __uint_as_float(acc[i][j]);
+      out += a.out_row;
+      asm volatile("" : "+l"(out));
     }
   }
 }
@@ -574,6 +564,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     const uint32_t empty0 = cluster_map(smem_u32(&sums_empty[0]), 0);
     const int part = (warp - 4) / 4, quarter = warp & 3;
     const uint32_t mine = tmem + ((uint32_t)quarter << 21);  // the warp's lanes
+    const bool f32 = a.out_dtype == kF32;
     uint32_t turn = 0;
     Ring sums(2);
     bool go = true;
@@ -582,7 +573,14 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
       const int first = part == 0 ? 0 : (t.padded / 2 + 31) / 32 * 32;
       const int half = part == 0 ? min((t.padded / 2 + 31) / 32 * 32, t.padded) : t.padded - first;
       uint32_t from = 0;
-      // Of a run that is not the only one the sums go to registers, of the last one back.
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_mapped(empty0 + sums.at * 8);
+        sums.step();
+      };
+      // fp32 sums go to registers, and their TMEM is free at once; 16-bit results' only
+      // where there are several runs, and back after the last. (Of 128 rows, whatever the tile's width.)
       uint32_t acc[8][16];
 #pragma unroll 1
       for (int step = 0; step < t.steps; step += p.run) {
@@ -590,66 +588,58 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
         tc_fence_after();
         from = mine + sums.at * F::kMaxN + first;
         const bool end = step + p.run >= t.steps;
-        if (step == 0 && end) break;
-        // (up to 128 rows, whatever the tile's width)
+        if (step == 0 && end && !f32) break;
         if (step == 0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) tmem_ld_16x32(from + ((uint32_t)(i % 2) << 20) + i / 2 * 32, acc[i]);
+          for (int i = 0; i < 8; ++i) tmem_ld16(from + i * 16, acc[i]);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 8; ++i) tmem_loaded(acc[i]);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 16; ++i) {
+            uint32_t r[8];
+            tmem_ld8(from + i * 8, r);
+            tmem_wait_ld();
+            tmem_loaded(r);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t r[8];
-              tmem_ld_16x16(from + ((uint32_t)(i % 2) << 20) + i / 2 * 32 + k * 16, r);
-              tmem_wait_ld();
-              tmem_loaded(r);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                uint32_t& to = acc[i][k * 8 + j];
-                to = __float_as_uint(__uint_as_float(to) + __uint_as_float(r[j]));
-              }
+            for (int j = 0; j < 8; ++j) {
+              uint32_t& to = acc[i / 2][i % 2 * 8 + j];
+              to = __float_as_uint(__uint_as_float(to) + __uint_as_float(r[j]));
             }
           }
         }
-        if (end) break;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_mapped(empty0 + sums.at * 8);
-        sums.step();
+        if (end && !f32) break;
+        release();
       }
       // the four go on together or not at all
       if (!(go = some_sync_and(1 + part, 128, go))) break;
-      if (t.steps > p.run) {
+      if (!f32 && t.steps > p.run) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (i / 2 * 32 < half) tmem_st_16x32(from + ((uint32_t)(i % 2) << 20) + i / 2 * 32, acc[i]);
+          if (i * 16 < half) tmem_st16(from + i * 16, acc[i]);
         tmem_wait_st();
+      }
+      if (f32 && t.steps == 0) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) acc[j / 16][j % 16] = 0;
       }
       if (!(a.accumulate && t.steps == 0)) {
         const int64_t m = t.m0 + (int64_t)rank * 128, n = t.n0 + (int64_t)first;
         const int g = F::kRaggedK ? t.g : 0, rows = min(half, t.width - first);
         uint8_t* space = smem + p.store_at + part * (2 * kStoreBytes);
         const int64_t column = m + quarter * 32 + lane;
-        if (a.out_dtype == kF32)
-          store_sums(a, from, t.steps == 0, static_cast<float*>(a.out) + g * a.out_group + n * a.out_row + column, rows,
-                     column < a.m);
-        else if (a.out_dtype == kF16)
+        if (f32) {
+          if (column < a.m)
+            store_sums(a, acc, static_cast<float*>(a.out) + g * a.out_group + n * a.out_row + column, rows);
+        } else if (a.out_dtype == kF16)
           store_tile<__half, F::kRaggedK>(a, &map_out, p.tiles_out != 0, from, t.steps == 0, m, n, g, rows, quarter, lane,
                                           space, turn, 1 + part);
         else
           store_tile<__nv_bfloat16, F::kRaggedK>(a, &map_out, p.tiles_out != 0, from, t.steps == 0, m, n, g, rows, quarter,
                                                  lane, space, turn, 1 + part);
       }
-      if (t.steps > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_mapped(empty0 + sums.at * 8);
-        sums.step();
-      }
+      if (!f32 && t.steps > 0) release();
     }
     tma_store_read<0>();
   }
