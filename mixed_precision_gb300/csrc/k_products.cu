@@ -31,10 +31,14 @@
 //
 // Measured (with the L2 flushed before): 16384 x 2048 x 2048 in bf16 by 16 even
 // experts 83 us forward (1660 TFLOP/s), 105 for the weights' gradient in fp32; 8192 x
-// 8192 x 8192 599 us (1840, 0.93 of the library's product); 8192 x 8192 x 4096 in e4m3
-// 156 us (3530 TFLOP/s); 74 rows x 2048 x 1024 by 16 experts 17 us. Bound by the tensor
-// cores, long under load by the power limit: the clock falls from 1.9 to 1.5 GHz, and
-// the forward products take 91 us, the library's batched product 86.
+// 8192 x 8192 599 us (1840, 0.93 of the library's burst rate); 8192 x 8192 x 4096 in
+// e4m3 157 us (3500 TFLOP/s); 74 rows x 2048 x 1024 by 16 experts 10 us captured (5.9
+// TB/s of weights). Large ones are bound by the tensor cores (75 to 85 % of the cycles;
+// the rest is a pair's last tile, which others do not have, and each kernel's start and
+// end), long under load by the power limit: the clock falls from 1.9 to 1.5 GHz, and the
+// forward products take 91 us, the library's batched product 86. fp32 weight gradients:
+// 268 MB of sums beside them. Many small experts: a tile's way out (4500 cycles for 128 x
+// 192 sums of a block) is longer than its products.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -505,7 +505,7 @@ def test_python_refusals():
 # What the tensor-core products add: tiles, runs, ways out, kernels that overlap
 # ---------------------------------------------------------------------------
 
-@pytest.mark.parametrize("tokens", [127, 128, 129, 256])
+@pytest.mark.parametrize("tokens", [63, 64, 65, 127, 128, 129, 256])
 @pytest.mark.parametrize("n,k", [(8, 3), (1000, 32)])
 def test_route_at_one_blocks_border(tokens, n, k):
     g = gen(tokens + n)
