@@ -269,7 +269,7 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, const CUtensorM
                                            bool zero, int64_t m, int64_t n, int g, int rows, int quarter, int lane,
                                            uint8_t* space, uint32_t& turn, int id) {
   const bool issues = quarter == 0 && elect_one() != 0;
-  const int boxes = a.m - m > 64 ? 2 : 1;
+  const int boxes = m >= a.m ? 0 : a.m - m > 64 ? 2 : 1;
 #pragma unroll 1
   for (int row0 = 0; row0 < rows; row0 += kStoreRows) {
     uint8_t* buf = space + (turn++ & 1) * kStoreBytes;
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
       }
       if (!f32 && t.steps > 0) release();
     }
-    tma_store_read<0>();
+    tma_store_written();
   }
   // No block leaves while the other may still reach its memory or arrive at its barriers.
   __syncwarp();

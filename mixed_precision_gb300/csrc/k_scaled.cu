@@ -3,10 +3,9 @@
 // bits of the largest magnitude, without a logarithm; infinities and NaN, which have
 // no part in it, are looked for in the maxima, and only where there is one is each
 // element asked. What counts is that a thread's loads are all under way before it needs
-// the first. bf16 8192 x 4096: packed in 18 us (5.7 TB/s; 12 instructions an element fill
-// 54 % of the issue slots), restored in 14 (7.3); the transpose of 4097 x 2048 in 11
-// (2.3 TB/s, 28 % of the issue slots: a block's three barriers and its 528 blocks' 1.7
-// rounds).
+// the first. bf16 8192 x 4096, captured: packed in 15.7 us (6.4 TB/s), the transpose in
+// 24, both in 36 (a thread's 32 elements cost it some 450 instructions, and 304 blocks
+// at a time their barriers); from cold caches the first takes 18 and restoring 14.
 //
 // Along rows alone, eight lanes hold a scale block (16 elements each). With the
 // transpose, a block of threads takes 128 x 128 elements, so it has whole scale

@@ -240,6 +240,8 @@ template <int LATER>
 __device__ __forceinline__ void tma_store_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LATER) : "memory");
 }
+// Until all of the thread's groups are in memory.
+__device__ __forceinline__ void tma_store_written() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // End the group, and wait until its shared memory has been read.
 __device__ __forceinline__ void tma_store_done() {
   asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group.read 0;" ::: "memory");

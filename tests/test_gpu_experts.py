@@ -2,6 +2,9 @@
 routing, rows to the experts and back, the experts' products. Sizes, types,
 strides and masks where they can go wrong, with the tolerances of _experts_ref."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -663,3 +666,31 @@ def test_products_of_two_graphs():
                 graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+def test_first_calls_captured():
+    """A process whose first calls of all are recorded into a graph."""
+    code = """
+import torch
+from mixed_precision_gb300 import experts, float8
+x = torch.randn(300, 136, device='cuda').bfloat16()
+w = torch.randn(4, 264, 136, device='cuda').bfloat16()
+off = torch.tensor([0, 100, 100, 250, 300], dtype=torch.int32, device='cuda')
+logits = torch.randn(300, 4, device='cuda')
+torch.cuda.synchronize()
+def calls():
+    y = experts.forward(x, w, off)
+    r = experts.route(logits, 2)
+    return (y, experts.input_grad(y, w, off), experts.weight_grad(y, x, off, dtype=torch.float32), experts.gather(x, r),
+            float8.matmul(float8.pack(x)[0], float8.pack(x)[0], dtype=torch.float32))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+experts.check()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
