@@ -77,6 +77,7 @@ struct ProductPlan {
   int b_bytes;   // of a stage and block
   int pairs;
   int store_at, scales_at, runs_at;  // in shared memory, behind the stages
+  Divide by_expert, by_band;         // ragged K: by an expert's tiles, by those of 8 along M
   int tiles_out;                     // out is of 16 bits and can be written by TMA
 };
 
@@ -126,7 +127,7 @@ struct Walk {
     uint32_t local, rows, across;
     if (F::kRaggedK) {
       const uint32_t each = m_tiles * n_tiles;
-      g = static_cast<int>(i / each);
+      g = static_cast<int>(p.by_expert(i));
       local = i - g * each;
       rows = static_cast<uint32_t>(a.n);
       across = n_tiles;
@@ -142,10 +143,10 @@ struct Walk {
       t.steps = g < a.groups ? (static_cast<int>(a.k) + F::kStepK - 1) / F::kStepK : 0;  // else rows of no expert
     }
     // bands of 8 tiles along M: the rows' tiles come round while a band's weights stay in L2
-    const uint32_t band = local / (8 * across), in = local - band * 8 * across;
-    const uint32_t wide = min(8u, m_tiles - band * 8), n = in / wide;
+    const uint32_t band = F::kRaggedK ? p.by_band(local) : local / (8 * across), in = local - band * 8 * across;
+    const uint32_t wide = min(8u, m_tiles - band * 8), n = wide == 8 ? in / 8 : in / wide;
     t.m0 = static_cast<int>((band * 8 + in - n * wide) * kTileM);
-    const uint32_t each = ((rows + across - 1) / across + 31) / 32 * 32, at = n * each;
+    const uint32_t each = F::kRaggedK ? p.tile_n : ((rows + across - 1) / across + 31) / 32 * 32, at = n * each;
     t.g = g;
     t.n0 = static_cast<int>((F::kRaggedK ? 0 : runs.first[g]) + at);
     t.width = static_cast<int>(min(each, rows - at));
@@ -771,6 +772,10 @@ cudaError_t run(const ProductArgs& a, cudaStream_t s) {
   const int64_t m_tiles = (a.m + kTileM - 1) / kTileM, n_tiles = (a.n + p.tile_n - 1) / p.tile_n;
   const int64_t most = m_tiles * (F::kRaggedK ? n_tiles * a.groups : n_tiles + a.groups + 2);
   if (most > (int64_t)0x7FFFFFFF || a.n > 0x7FFFFFFF || a.k > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  if (F::kRaggedK) {
+    p.by_expert = Divide(static_cast<uint32_t>(m_tiles * n_tiles));
+    p.by_band = Divide(static_cast<uint32_t>(8 * n_tiles));
+  }
   p.pairs = static_cast<int>(most < pairs ? most : pairs);
   cfg.gridDim = dim3(2 * p.pairs);
   cfg.numAttrs = 2;
