@@ -824,7 +824,7 @@ int zero_experts_combine_backward(const void* dout, int64_t dout_stride, const v
  * Strides are in elements; of inputs they are multiples of 8 (dw's, y's and
  * dx's are free; rows that start on 16 bytes leave faster). Sums are fp32: the
  * tensor cores truncate where they add, so an fp32 dw's are moved on with a
- * rounding after 512 rows, a 16-bit result's after 4096 terms.
+ * rounding after 512 rows, a 16-bit result's after 1024 terms.
  *   forward      y[r] = x[r] W_e^T.
  *   input_grad   dx[r] = dy[r] W_e.
  *   weight_grad  dW_e = sum over its rows of dy[r]^T x[r]; an expert without rows

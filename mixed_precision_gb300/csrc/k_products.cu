@@ -59,10 +59,14 @@ constexpr int kABytes = 128 * kStepBytes;   // of one block
 constexpr int kMnRows = 64;                 // rows of a step whose operands are contiguous along M and N
 constexpr int kMnChunk = kMnRows * 128;     // bytes of 64 columns of them
 // Steps whose sums stay in the tensor core (powers of two). Each of four truncated
-// additions a step costs up to 9e-8 of the result where all terms have one sign: 3e-6
-// after 8 steps, of a 16-bit result's rounding (4e-4 and up) 2e-5 after 64. On the
-// inputs of a layer fp32 results are off by 4e-7 with 8 (9e-7 with 16) in norm.
-constexpr int kRunF32 = 8, kRunHalf = 64;
+// additions a step may cost 2^-23 of the sum: 4e-6 after 8 steps, 8e-6 after 16, of a
+// 16-bit result's rounding (4e-4 and up). On the inputs of a layer fp32 results are off
+// by 4e-7 with 8 (9e-7 with 16) in norm. 16-bit results of 16384 x 2048 x 2048 in bf16
+// differ from rounded fp32 sums by 1.1e-4 in norm with 64, 7e-5 with 16 in the same 82 us,
+// 6e-5 with 8 in 84; of 8192 x 8192 x 8192 16 costs 0.8 %. e4m3's steps are of twice as
+// many products for each addition: 5e-5 with 64; 16 would take 8 % of a product of 128 x
+// 4096 x 4096.
+constexpr int kRunF32 = 8, kRunHalf = 16, kRunScaledHalf = 64;
 constexpr int kMaxStages = 12;
 constexpr int kMostSmem = 232448 - 1024;    // dynamic shared memory; the rest is for the barriers
 constexpr int kScaleSteps = 4;              // steps that a word of scales lasts
@@ -736,7 +740,7 @@ cudaError_t run(const ProductArgs& a, cudaStream_t s) {
   }
 
   ProductPlan p{};
-  p.run = a.out_dtype == kF32 ? kRunF32 : kRunHalf;
+  p.run = a.out_dtype == kF32 ? kRunF32 : SCALED ? kRunScaledHalf : kRunHalf;
   const int width = choose_width(a, F::kRaggedK, F::kStepK, F::kMaxN, pairs);
   const int64_t across = (a.n + width - 1) / width;
   if (F::kRaggedK) {  // every expert's tiles are the same: as narrow as they can be
