@@ -112,7 +112,8 @@ struct Tile {
   int steps;
 };
 
-// A block's way through the tiles: 32-bit numbers, which the host has checked.
+// A block's way through the tiles: 32-bit numbers, which the host has checked. (A run
+// along K may have 2^31 - 1 rows: its last step's end is not an int.)
 template <typename F>
 struct Walk {
   const ProductArgs& a;
@@ -137,7 +138,7 @@ struct Walk {
       across = n_tiles;
       t.k0 = runs.first[g];
       t.rows_k = runs.rows[g];
-      t.steps = (t.rows_k + kMnRows - 1) / kMnRows;
+      t.steps = static_cast<int>((static_cast<uint32_t>(t.rows_k) + kMnRows - 1) / kMnRows);
     } else {
       while (runs.start[g + 1] * m_tiles <= i) ++g;
       local = i - runs.start[g] * m_tiles;
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
         const uint32_t to = base + s * stage_bytes;
         if (one) {
           uint32_t bar = full0 + s * 8;
-          if (F::kRaggedK && (step + 1) * kMnRows > t.rows_k) {  // warp 2 passes it on
+          if (F::kRaggedK && t.rows_k - step * kMnRows < kMnRows) {  // warp 2 passes it on
             mbar_arrive_expect_tx(&tail[s], bytes);
             bar = cluster_map(smem_u32(&tail[s]), rank);
           } else {
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
           for (int k = 0; k < 4; ++k)
             mma_scaled_pair(d, a_desc + at + k * 2, b_desc + at + k * 2, scaled, sa, sa + 4, more || k > 0, one);
         } else if constexpr (F::kRaggedK) {
-          const int parts = min(4, (t.rows_k - step * kMnRows + 15) / 16);
+          const int parts = (min(kMnRows, t.rows_k - step * kMnRows) + 15) / 16;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (k < parts) mma_ss_pair(d, a_desc + at + k * 128, b_desc + at + k * 128, idesc, more || k > 0, one);

@@ -37,3 +37,29 @@ def test_small_terms_behind_a_large_one(product, dtype):
     else:
         got = experts.weight_grad(left.t().contiguous(), right.t().contiguous(), offsets_of([k]))[0]
     close(got, want, tol, product)
+
+
+# ---------------------------------------------------------------------------
+# Sizes
+# ---------------------------------------------------------------------------
+
+def test_products_of_the_most_rows():
+    """Runs of 2^31 - 6 and 5 rows, whose steps of 64 end behind the largest int. A few rows are not zero."""
+    rows = 2 ** 31 - 1
+    x = torch.zeros(rows, 8, dtype=BF16, device="cuda")
+    at = torch.tensor([0, 63, 64, 2 ** 30 + 7, rows - 70, rows - 65, rows - 64, rows - 6, rows - 5, rows - 1], device="cuda")
+    some = torch.randint(-8, 9, (len(at), 8), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(BF16)
+    x[at] = some
+    dw = experts.weight_grad(x, x, offsets_of([rows - 5, 5]), dtype=F32)
+    some = some.float()
+    assert torch.equal(dw[0], some[:-2].t() @ some[:-2])
+    assert torch.equal(dw[1], some[-2:].t() @ some[-2:])
+    # forward: the last tile's other half starts behind the largest int
+    w = torch.randint(-8, 9, (2, 8, 8), device="cuda", generator=torch.Generator("cuda").manual_seed(2)).to(BF16)
+    y = experts.forward(x, w, offsets_of([rows - 5, 5]))
+    assert torch.equal(y[at[:-2]].float(), (some[:-2] @ w[0].float().t()).to(BF16).float())
+    assert torch.equal(y[at[-2:]].float(), (some[-2:] @ w[1].float().t()).to(BF16).float())
+    assert int(y[:2 ** 30].count_nonzero()) + int(y[2 ** 30:].count_nonzero()) == int(y[at].count_nonzero())
+    experts.check()
+    del x, y
+    torch.cuda.empty_cache()
