@@ -817,7 +817,9 @@ int zero_experts_combine_backward(const void* dout, int64_t dout_stride, const v
                                   const float* weights, void* dy, float* dweights, void* stream);
 
 /* The experts' products: row r of expert e, offsets[e] <= r < offsets[e + 1].
- *   offsets   int32 [experts + 1], device, not decreasing, within 0..rows.
+ *   offsets   int32 [experts + 1], device, not decreasing, within 0..rows (one
+ *             that decreases counts as the largest before it, one outside as the
+ *             nearest inside).
  *   weights   [experts][n_out][n_in] of dtype (fp16 or bf16), rows contiguous;
  *             w_row_stride between rows, w_stride between experts' matrices.
  *   x, dx     [rows, n_in], row stride x_stride; y, dy [rows, n_out], y_stride.

@@ -174,8 +174,10 @@ __device__ void read_runs(const ProductArgs& a, const ProductPlan& p, const Runs
     runs.reach[1] = 0;
   }
   __syncthreads();
+  bool falls = false;
   for (int g = threadIdx.x; g < a.groups; g += kThreadsHere) {
     const int from = Walk<F>::bound(a, g), to = Walk<F>::bound(a, g + 1);
+    falls = falls || to < from;
     runs.first[g] = from;
     runs.rows[g] = max(0, to - from);
     if (!F::kRaggedK && to > from) {
@@ -183,7 +185,23 @@ __device__ void read_runs(const ProductArgs& a, const ProductPlan& p, const Runs
       atomicMax(&runs.reach[1], to);
     }
   }
-  __syncthreads();
+  // An offset that decreases, which no routing makes, counts as the largest before it: runs
+  // stay apart, so a row has one writer and there are no more tiles than the host has counted.
+  if (__syncthreads_or(falls)) {
+    if (threadIdx.x == 0) {
+      const int start = Walk<F>::bound(a, 0);
+      int end = start;
+      for (int g = 0; g < a.groups; ++g) {
+        const int to = max(end, Walk<F>::bound(a, g + 1));
+        runs.first[g] = end;
+        runs.rows[g] = to - end;
+        end = to;
+      }
+      runs.reach[0] = end > start ? start : static_cast<int>(a.n);
+      runs.reach[1] = end > start ? end : 0;
+    }
+    __syncthreads();
+  }
   if (!F::kRaggedK && threadIdx.x < 32) {
     if (threadIdx.x == 0) {
       // rows before the first run and behind the last belong to nobody (all, when there is no run)

@@ -6,8 +6,8 @@ import torch
 
 import _experts_ref as ref
 from _block_ref import U, close
-from mixed_precision_gb300 import experts
-from test_gpu_experts import offsets_of
+from mixed_precision_gb300 import experts, float8
+from test_gpu_experts import gen, normal, offsets_of
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +63,29 @@ def test_products_of_the_most_rows():
     experts.check()
     del x, y
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------------------
+# Offsets that no routing makes
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("offsets,as_if", [([0, 300, 100, 400], [0, 300, 300, 400]), ([500, 100, 200, 300], [500] * 4),
+                                           ([20, 10, 400, 390], [20, 20, 400, 400]), ([0, 450, 0, 450], [0, 450, 450, 450]),
+                                           ([70, 900, -5, 460], [70, 500, 500, 500])])
+def test_offsets_that_decrease(offsets, as_if):
+    """Each counts as the largest before it: no row belongs to two experts, and none is left unwritten."""
+    g = gen(21)
+    rows, n_out, n_in = 500, 136, 264
+    x, dy, w = normal(g, rows, n_in, dtype=BF16), normal(g, rows, n_out, dtype=BF16), normal(g, 3, n_out, n_in, dtype=BF16)
+    x8, w8 = float8.pack(x)[0], float8.pack(w)[0]
+
+    def calls(off):
+        off = torch.tensor(off, dtype=torch.int32, device="cuda")
+        y, dx = (torch.full((rows, n), 5.0, dtype=BF16, device="cuda") for n in (n_out, n_in))
+        y8 = torch.full((rows, n_out), 5.0, device="cuda")
+        return (experts.forward(x, w, off, out=y), experts.input_grad(dy, w, off, out=dx),
+                experts.weight_grad(dy, x, off, dtype=F32), float8.matmul(x8, w8, off, out=y8))
+
+    for a, b in zip(calls(offsets), calls(as_if)):
+        assert torch.equal(a, b)
+    experts.check()
