@@ -9,12 +9,11 @@
 // on the device only: every block reads the offsets and takes each pairs-th tile
 // of the list that they make. Tiles of a run are equally wide, so its rows fill
 // them to within 32; rows of the next run that a tile also reads end in columns
-// that nobody stores. Along K the rows behind a run's end are cleared in shared
-// memory, in both operands.
+// that nobody stores. Along K a run's last rows are loaded behind rows of zeros: TMA
+// counts rows from the step's first (Form), and from a negative start it fills zeros.
 //
 // Twelve warps: one loads by TMA, one issues MMAs, one brings scales (words of four
-// exponents, which the tensor core applies itself) or clears rows, eight take the
-// sums. These leave TMEM after a run of steps and are added up in registers,
+// exponents, which the tensor core applies itself), eight take the sums. These leave TMEM after a run of steps and are added up in registers,
 // rounded: the tensor core truncates where it adds, which over thousands of steps
 // would cost an fp32 result its last bits. TMEM holds two tiles' sums, so the MMAs go
 // on meanwhile.
@@ -91,6 +90,9 @@ struct Form {
   static constexpr int kStepK = SCALED ? 128 : 64;  // elements
   static constexpr int kMaxN = SCALED ? 224 : 256;
   static constexpr int kScaleCols = 2 * kMaxN;      // where the scales' TMEM starts
+  // The operands' tensor maps: contiguous side, the other, groups; with a ragged K
+  // (both contiguous along M and N): columns, a step's rows, the step's first row, so
+  // that rows in front of the first are outside of the tensor.
 };
 
 // The runs of rows, in shared memory, with those of no expert at the end.
@@ -240,7 +242,6 @@ struct Ring {
       phase ^= 1;
     }
   }
-  __device__ __forceinline__ int after(int steps) const { return (at + steps) % n; }
 };
 
 template <typename T>
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
   using F = Form<A_MN, B_MN, SCALED>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], sums_full[2], sums_empty[2],
-      tail[kMaxStages], scales_full[kScaleSlots], scales_empty[kScaleSlots];
+      scales_full[kScaleSlots], scales_empty[kScaleSlots];
   __shared__ uint32_t tmem_slot, abort_word;
   // the swizzle is a function of address bits: tiles start on 1024 bytes, the same in both blocks
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -380,7 +381,6 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&full[s], 2);   // both blocks' loads; rank 0's barrier counts
       mbar_init(&empty[s], 1);
-      mbar_init(&tail[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sums_full[s], 1);
@@ -425,21 +425,23 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
         const int k = t.k0 + step * F::kStepK;
         const uint32_t to = base + s * stage_bytes;
         if (one) {
-          uint32_t bar = full0 + s * 8;
-          if (F::kRaggedK && t.rows_k - step * kMnRows < kMnRows) {  // warp 2 passes it on
-            mbar_arrive_expect_tx(&tail[s], bytes);
-            bar = cluster_map(smem_u32(&tail[s]), rank);
-          } else {
-            mbar_arrive_expect_tx_mapped(bar, bytes);
-          }
-          if (A_MN) {
-            tma_load3_pair(to, &map_a, m, k, F::kRaggedK ? 0 : t.g, bar);
-            tma_load3_pair(to + kMnChunk, &map_a, m + 64, k, F::kRaggedK ? 0 : t.g, bar);
+          const uint32_t bar = full0 + s * 8;
+          mbar_arrive_expect_tx_mapped(bar, bytes);
+          // ragged K: `from` rows before the step's first, which read as zeros, so that
+          // the stage ends with the run's last row
+          const int from = F::kRaggedK ? min(0, t.rows_k - step * kMnRows - kMnRows) : 0;
+          if (F::kRaggedK) {
+            tma_load3_pair(to, &map_a, m, from, k, bar);
+            tma_load3_pair(to + kMnChunk, &map_a, m + 64, from, k, bar);
+          } else if (A_MN) {
+            tma_load3_pair(to, &map_a, m, k, t.g, bar);
+            tma_load3_pair(to + kMnChunk, &map_a, m + 64, k, t.g, bar);
           } else {
             tma_load3_pair(to, &map_a, k, m, t.g, bar);
           }
           if (B_MN) {
-            for (int c = 0; c < b_chunks; ++c) tma_load3_pair(to + kABytes + c * kMnChunk, &map_b, n + c * 64, k, 0, bar);
+            for (int c = 0; c < b_chunks; ++c)
+              tma_load3_pair(to + kABytes + c * kMnChunk, &map_b, n + c * 64, from, k, bar);
           } else {
             tma_load3_pair(to + kABytes, &map_b, k, n, 0, bar);
           }
@@ -496,10 +498,10 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
           for (int k = 0; k < 4; ++k)
             mma_scaled_pair(d, a_desc + at + k * 2, b_desc + at + k * 2, scaled, sa, sa + 4, more || k > 0, one);
         } else if constexpr (F::kRaggedK) {
-          const int parts = (min(kMnRows, t.rows_k - step * kMnRows) + 15) / 16;
+          const int first = (kMnRows - min(kMnRows, t.rows_k - step * kMnRows)) / 16;  // 16s of zeros are left out
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (k < parts) mma_ss_pair(d, a_desc + at + k * 128, b_desc + at + k * 128, idesc, more || k > 0, one);
+            if (k >= first) mma_ss_pair(d, a_desc + at + k * 128, b_desc + at + k * 128, idesc, more || k > first, one);
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -515,27 +517,6 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     }
     if (!go)  // leave the MMAs in flight time to end
       for (int i = 0; i < 64; ++i) __nanosleep(1000);
-  } else if (F::kRaggedK && warp == 2) {
-    // ---- a run's last step, if it is not full: the rows behind its end, up to the
-    // last MMA's, are cleared in both operands before the step counts as loaded
-    const uint32_t full0 = cluster_map(smem_u32(&full[0]), 0);
-    Ring ring(p.stages);
-    uint32_t phases = 0;
-    while (walk.next(t)) {
-      if (t.steps == 0) continue;
-      const int s = ring.after(t.steps - 1), left = t.rows_k - (t.steps - 1) * kMnRows;
-      ring.at = ring.after(t.steps);
-      if (left == kMnRows) continue;
-      if (!wait(&tail[s], phases >> s & 1)) break;
-      phases ^= 1u << s;
-      const int clear = ((left + 15) / 16 * 16 - left) * 8, pieces = clear * (2 + (t.padded / 2 + 63) / 64);
-      for (int i = lane; i < pieces; i += 32)
-        *reinterpret_cast<uint4*>(smem + s * stage_bytes + i / clear * kMnChunk + left * 128 + i % clear * 16) =
-            make_uint4(0, 0, 0, 0);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_release_mapped(full0 + s * 8);
-    }
   } else if (SCALED && warp == 2) {
     // ---- scales: a word (four blocks of 128) of every row of the tile
     const uint32_t full0 = cluster_map(smem_u32(&scales_full[0]), 0);
@@ -776,10 +757,11 @@ cudaError_t run(const ProductArgs& a, cudaStream_t s) {
   p.runs_at = p.scales_at + (SCALED ? kScaleSlots * kScaleSlot : 0);
 
   // a: along M and K (in either order) by group; b: its rows, all groups' together
-  const uint64_t groups = F::kRaggedK ? 1 : a.groups;
-  const uint64_t a_extent[3] = {(uint64_t)(A_MN ? a.m : a.k), (uint64_t)(A_MN ? a.k : a.m), groups};
+  const uint64_t groups = F::kRaggedK ? 1 : a.groups, rows = a.k;
+  const uint64_t a_extent[3] = {(uint64_t)(A_MN ? a.m : a.k), F::kRaggedK ? kMnRows : (uint64_t)(A_MN ? a.k : a.m),
+                                F::kRaggedK ? rows : groups};
   const uint64_t a_strides[2] = {(uint64_t)a.a_row * elem, (uint64_t)(groups > 1 ? a.a_group : a.a_row) * elem};
-  const uint64_t b_extent[3] = {(uint64_t)(B_MN ? a.n : a.k), (uint64_t)(B_MN ? a.k : a.n), 1};
+  const uint64_t b_extent[3] = {(uint64_t)(B_MN ? a.n : a.k), F::kRaggedK ? kMnRows : (uint64_t)a.n, F::kRaggedK ? rows : 1};
   const uint64_t b_strides[2] = {(uint64_t)a.b_row * elem, (uint64_t)a.b_row * elem};
   const uint64_t out_groups = F::kRaggedK ? a.groups : 1;
   const uint64_t out_extent[3] = {(uint64_t)a.m, (uint64_t)a.n, out_groups};

@@ -65,6 +65,30 @@ def test_products_of_the_most_rows():
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("n_out,n_in", [(8, 264), (300, 72), (33, 520)])
+def test_weight_grad_of_every_last_step(dtype, n_out, n_in):
+    """Runs of 0 to 66 rows and of 190 to 200, between runs of NaN and inf: each run's last step holds its rows
+    and nothing of its neighbours'."""
+    g = gen(n_out)
+    counts = [c for n in list(range(67)) + list(range(190, 201)) for c in (n, 1 + n % 3)] + [2]
+    off = offsets_of([3] + counts)
+    rows = sum(counts) + 3 + 5  # and rows of no expert at both ends
+    wide = [torch.zeros(rows, (n + 7) // 8 * 8, dtype=dtype, device="cuda") for n in (n_out, n_in)]
+    dy, x = wide[0][:, :n_out], wide[1][:, :n_in]
+    dy.copy_(normal(g, rows, n_out)), x.copy_(normal(g, rows, n_in))
+    o = off.tolist()
+    dy[:3], x[rows - 5:] = float("nan"), float("inf")
+    for e in range(2, len(o) - 1, 2):
+        x[o[e]:o[e + 1]], dy[o[e]:o[e + 1]] = float("nan"), float("inf")
+    want, size = ref.weight_grad(dy, x, o)
+    for out in (dtype, F32):
+        dw = experts.weight_grad(dy, x, off, dtype=out)
+        assert bool(dw[2::2].isnan().all())
+        close(dw[1::2], want[1::2], ref.product_tol(200, size[1::2], want[1::2], dtype, out), f"{out}")
+    experts.check()
+
+
 # ---------------------------------------------------------------------------
 # Offsets that no routing makes
 # ---------------------------------------------------------------------------
