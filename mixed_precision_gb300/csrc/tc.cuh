@@ -280,15 +280,44 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // Rank 0 issues the MMAs for both. The barriers that it waits on are its own; the
 // other block arrives there through `mapped` addresses (cluster_map).
 
+// The thread's writes, and those that it has been told of, before what it tells the
+// other block: some 1300 cycles, more while other warps of the block store.
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// mbar_try_wait, behind the writes of the other block before its arrivals.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // The Waiter of a pair: who gives up tells the other block too.
 struct PairWaiter {
   volatile uint32_t* abort;
   uint32_t abort_there;  // the other block's, mapped
   unsigned* error;
 
+  template <bool CLUSTER = false>
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
     for (uint32_t i = 0; i < kSpinLimit; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
+      if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
       if ((i & 7) == 7 && *abort != 0) return false;
     }
     *abort = 1;
@@ -296,14 +325,13 @@ struct PairWaiter {
     atomicAdd(error, 1u);
     return false;
   }
+  // For an arrival of the other block that tells of its threads' writes.
+  __device__ __forceinline__ bool cluster(uint64_t* bar, uint32_t parity) const {
+    return operator()<true>(bar, parity);
+  }
 };
-// With the thread's writes to its own block's shared memory before it. (Release at
-// the cluster's scope is a fence of 1300 cycles, and who reads these writes is the
-// block's own tensor core.)
-__device__ __forceinline__ void mbar_arrive_release_mapped(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Without them: what it reports is ordered by other means (TMA's count, tcgen05's fences).
+// Arrivals of either block, with no order of the thread's own writes: what they report
+// is ordered by other means (TMA's count, tcgen05's fences, fence_cluster).
 __device__ __forceinline__ void mbar_arrive_mapped(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }

@@ -113,3 +113,39 @@ def test_offsets_that_decrease(offsets, as_if):
     for a, b in zip(calls(offsets), calls(as_if)):
         assert torch.equal(a, b)
     experts.check()
+
+
+# ---------------------------------------------------------------------------
+# Scales on their way to the tensor cores
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("m,n,k", [(70, 300, 700), (300, 260, 4000), (600, 2049, 264)])
+def test_products_whose_scales_change(m, n, k):
+    """Products with other scales in every row and block, one behind the other beside another stream's traffic:
+    none takes a scale of the one before, in either half of a tile."""
+    g = gen(m)
+
+    def packed(rows):
+        scale = torch.exp2(torch.randint(-12, 12, (rows, (k + 127) // 128), generator=g, device="cuda").float())
+        return float8.pack(normal(g, rows, k) * scale.repeat_interleave(128, 1)[:, :k])[0]
+
+    sets = []
+    for _ in range(3):
+        a, b = packed(m), packed(n)
+        ra, rb = a.restore(F32).double(), b.restore(F32).double()
+        want, size = ra @ rb.t(), ra.abs() @ rb.abs().t()
+        out = float8.matmul(a, b, dtype=F32)
+        close(out, want, ref.product_tol(k, size, want, None, F32, per_mma=32, run=1024), "product")
+        sets.append((a, b, out))
+    side, other = torch.cuda.Stream(), torch.zeros(1 << 24, device="cuda")
+    side.wait_stream(torch.cuda.current_stream())
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(150):
+        if i % 10 == 0:
+            with torch.cuda.stream(side):
+                other.add_(1.0)
+        a, b, out = sets[i % 3]
+        differ += (float8.matmul(a, b, dtype=F32) != out).any()
+    torch.cuda.synchronize()
+    assert int(differ) == 0
+    float8.check()
