@@ -398,12 +398,12 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     if (p.tiles_out) tma_prefetch(&map_out);
   }
   if (warp == 3) tmem_alloc_pair(&tmem_slot, 512);
+  tc_fence_before();
+  cluster_sync();  // while the kernel ahead ends: 0.2 us of every product
+  tc_fence_after();
   griddep_wait();
   griddep_trigger();
   read_runs<F>(a, p, runs);
-  tc_fence_before();
-  cluster_sync();
-  tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const PairWaiter wait{&abort_word, cluster_map(smem_u32(&abort_word), rank ^ 1), &g_product_error};
   Walk<F> walk(a, p, runs, static_cast<int>(blockIdx.x / 2));
