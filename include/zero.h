@@ -907,6 +907,12 @@ int zero_operator_status(void* stream);
  * zero_operator_status then returns ZERO_ERR_TIMEOUT. */
 int zero_selftest_operator_timeout(int kernels, uint32_t spin_limit, void* stream);
 
+/* The same for the experts' and scaled products, whose blocks work in pairs: one
+ * block's wait gives up after spin_limit tries and is recorded, the other block's,
+ * which has no end of its own so soon, is told. ends (device int32 [2], by block): 1
+ * where a wait ran out, 2 where the block was told. block: 0 or 1 gives up. */
+int zero_selftest_pair_timeout(int block, uint32_t spin_limit, int32_t* ends, void* stream);
+
 /* Message for the last failing call on this thread ("" if none). The pointer
  * stays valid until the next failing call on this thread. */
 const char* zero_last_error(void);

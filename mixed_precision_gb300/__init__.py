@@ -21,7 +21,7 @@ from ._abi import (ZERO_BF16, ZERO_MAX_ELEMS, ZERO_STATE_BLOB_BYTES, zero_accumu
                    zero_act_weight_grad, zero_act_weight_grad_workspace, zero_attention_desc,
                    zero_attention_forward, zero_attention_backward,
                    zero_attention_backward_workspace, zero_operator_status,
-                   zero_selftest_operator_timeout, zero_route, zero_route_workspace, zero_route_backward,
+                   zero_selftest_operator_timeout, zero_selftest_pair_timeout, zero_route, zero_route_workspace, zero_route_backward,
                    zero_experts_gather, zero_experts_combine, zero_experts_combine_backward,
                    zero_experts_desc, zero_experts_forward, zero_experts_input_grad,
                    zero_experts_weight_grad, zero_scaled_desc, zero_scaled_layout, zero_scaled_pack,

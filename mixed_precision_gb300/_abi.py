@@ -188,6 +188,7 @@ def lib() -> ctypes.CDLL:
             "zero_scaled_matmul": [P] * 8,
             "zero_operator_status": [P],
             "zero_selftest_operator_timeout": [I, ctypes.c_uint32, P],
+            "zero_selftest_pair_timeout": [I, ctypes.c_uint32, P, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -488,6 +489,10 @@ def zero_operator_status(stream: int) -> None:
 
 def zero_selftest_operator_timeout(kernels: int, spin_limit: int, stream: int) -> None:
     _check(lib().zero_selftest_operator_timeout(kernels, spin_limit, stream or None))
+
+
+def zero_selftest_pair_timeout(block: int, spin_limit: int, ends: int, stream: int) -> None:
+    _check(lib().zero_selftest_pair_timeout(block, spin_limit, ends or None, stream or None))
 
 
 # ---------------------------------------------------------------------------

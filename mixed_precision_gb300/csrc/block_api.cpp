@@ -536,7 +536,7 @@ int zero_operator_status(void* stream) {
     late = late || now[i] != seen[dev][i];
     seen[dev][i] = now[i];
   }
-  if (late) return fail(ZERO_ERR_TIMEOUT, "a bounded wait gave up in a block operator");
+  if (late) return fail(ZERO_ERR_TIMEOUT, "a bounded wait gave up in an operator");
   return ZERO_OK;
 }
 
@@ -549,6 +549,16 @@ int zero_selftest_operator_timeout(int kernels, uint32_t spin_limit, void* strea
   cudaError_t e = kErrorWord[kernels](&at);
   if (e == cudaSuccess) e = launch_wait_that_gives_up(at, spin_limit, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "operator self-test");
+}
+
+int zero_selftest_pair_timeout(int block, uint32_t spin_limit, int32_t* ends, void* stream) {
+  Range r("zero_selftest_pair_timeout");
+  if (block < 0 || block > 1) return fail(ZERO_ERR_INVALID, "block %d: 0 or 1", block);
+  if (spin_limit < 1 || spin_limit > kSpinLimit) return fail(ZERO_ERR_INVALID, "spin_limit outside 1..2^22");
+  if (ends == nullptr || reinterpret_cast<uintptr_t>(ends) % 4 != 0)
+    return fail(ZERO_ERR_INVALID, "ends is NULL or not 4-byte aligned");
+  cudaError_t e = launch_pair_that_gives_up(block, spin_limit, ends, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ZERO_OK : cuda_fail(e, "pair self-test");
 }
 
 }  // extern "C"

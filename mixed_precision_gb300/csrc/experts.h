@@ -83,6 +83,7 @@ struct ProductArgs {
 };
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t s);
 cudaError_t product_error(unsigned** at);
+cudaError_t launch_pair_that_gives_up(int giver, uint32_t limit, int32_t* ends, cudaStream_t s);
 
 #ifdef __CUDACC__
 // A launch that may begin while the kernel ahead of it in the stream still runs: the

@@ -697,6 +697,35 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
   }
 }
 
+// A pair whose block `giver` waits `limit` times on a barrier that nothing arrives at,
+// the other block until it is told. ends[block]: 1 where the wait ran out, 2 where the
+// other block's did (0: neither). Four warps go on together, as the sums' do.
+__global__ void __launch_bounds__(128) __cluster_dims__(2, 1, 1) k_pair_that_gives_up(int giver, uint32_t limit, int32_t* ends) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ uint32_t abort_word;
+  __shared__ unsigned late;
+  const int rank = static_cast<int>(cluster_rank());
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    mbar_init_fence();
+    abort_word = 0;
+    late = 0;
+  }
+  __syncthreads();
+  cluster_sync();
+  const PairWaiter wait{&abort_word, cluster_map(smem_u32(&abort_word), rank ^ 1), &late, rank == giver ? limit : kSpinLimit};
+  bool go = true;
+  if (threadIdx.x < 32) go = wait(&bar, 0);
+  __syncwarp();
+  go = some_sync_and(1, 128, go);
+  if (threadIdx.x == 0) {
+    ends[rank] = go ? 0 : late != 0 ? 1 : 2;
+    if (late != 0) atomicAdd(&g_product_error, 1u);
+  }
+  __syncwarp();
+  cluster_sync();
+}
+
 // out of no rows along K: zero.
 __global__ void __launch_bounds__(256) k_product_zero(const ProductArgs a) {
   griddep_wait();
@@ -825,6 +854,11 @@ cudaError_t run(const ProductArgs& a, cudaStream_t s) {
 }  // namespace
 
 ZG_ERROR_WORD(product_error, g_product_error)
+
+cudaError_t launch_pair_that_gives_up(int giver, uint32_t limit, int32_t* ends, cudaStream_t s) {
+  k_pair_that_gives_up<<<2, 128, 0, s>>>(giver, limit, ends);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t s) {
   if (a.dtype == kE4M3) return run<false, false, true>(a, s);

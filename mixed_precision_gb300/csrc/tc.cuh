@@ -313,10 +313,11 @@ struct PairWaiter {
   volatile uint32_t* abort;
   uint32_t abort_there;  // the other block's, mapped
   unsigned* error;
+  uint32_t limit = kSpinLimit;
 
   template <bool CLUSTER = false>
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+    for (uint32_t i = 0; i < limit; ++i) {
       if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
       if ((i & 7) == 7 && *abort != 0) return false;
     }

@@ -6,6 +6,7 @@ import torch
 
 import _experts_ref as ref
 from _block_ref import U, close
+from mixed_precision_gb300 import _abi as abi
 from mixed_precision_gb300 import experts, float8
 from test_gpu_experts import gen, normal, offsets_of
 
@@ -149,3 +150,32 @@ def test_products_whose_scales_change(m, n, k):
     torch.cuda.synchronize()
     assert int(differ) == 0
     float8.check()
+
+
+# ---------------------------------------------------------------------------
+# A wait that gives up
+# ---------------------------------------------------------------------------
+
+def timed_out():
+    try:
+        experts.check()
+    except abi.ZeroError as e:
+        assert e.code == abi.ZERO_ERR_TIMEOUT
+        return True
+    return False
+
+
+@pytest.mark.parametrize("block", [0, 1])
+def test_a_pair_that_gives_up_is_reported(block):
+    """One block's wait runs out, the other's ends because it is told; both leave, the time-out is reported
+    once, and products run on."""
+    timed_out()  # what other tests may have left to this thread
+    ends = torch.full((2,), -1, dtype=torch.int32, device="cuda")
+    abi.zero_selftest_pair_timeout(block, 1000, ends.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert timed_out() and not timed_out()
+    assert ends.tolist() == [1 + block, 2 - block]
+    g = gen(5)
+    x, w = normal(g, 70, 264, dtype=BF16), normal(g, 1, 136, 264, dtype=BF16)
+    want, size = ref.forward(x, w, [0, 70])
+    close(experts.forward(x, w, offsets_of([70])), want, ref.product_tol(264, size, want, BF16, BF16), "y")
+    assert not timed_out()
