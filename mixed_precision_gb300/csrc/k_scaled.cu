@@ -292,47 +292,50 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_scaled_pack(const ScaledArg
   }
 }
 
+// The grid holds 65535 blocks across: wider matrices (the transposes of very many rows)
+// take several rounds.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kPackThreads) k_scaled_unpack(const ScaledArgs a, int wide) {
   griddep_wait();
   griddep_trigger();
   const Place at(wide);
-  const int64_t c = at.block * kScaledBlock + (threadIdx.x & 7) * 8;
-  if (at.block >= a.pitch / kScaledBlock) return;
-  uint2 q[kPasses][2];
-  uint32_t byte[kPasses];
+  for (int64_t block = at.block; block < a.pitch / kScaledBlock; block += (int64_t)gridDim.y << wide) {
+    const int64_t c = block * kScaledBlock + (threadIdx.x & 7) * 8;
+    uint2 q[kPasses][2];
+    uint32_t byte[kPasses];
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int64_t r = min(at.row + i * at.step, a.rows - 1);
+    for (int i = 0; i < kPasses; ++i) {
+      const int64_t r = min(at.row + i * at.step, a.rows - 1);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) q[i][h] = *reinterpret_cast<const uint2*>(a.q_in + r * a.pitch + c + h * 64);
-    byte[i] = a.scales_in[r * a.scale_pitch + at.block];
-  }
+      for (int h = 0; h < 2; ++h) q[i][h] = *reinterpret_cast<const uint2*>(a.q_in + r * a.pitch + c + h * 64);
+      byte[i] = a.scales_in[r * a.scale_pitch + block];
+    }
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int64_t r = at.row + i * at.step;
-    if (r >= a.rows) return;
-    // 2^-127 is a subnormal number; 255 stands for NaN
-    const float s = __uint_as_float(byte[i] == 0 ? 0x00400000u : byte[i] == 255 ? 0x7FC00000u : byte[i] << 23);
+    for (int i = 0; i < kPasses; ++i) {
+      const int64_t r = at.row + i * at.step;
+      if (r >= a.rows) break;
+      // 2^-127 is a subnormal number; 255 stands for NaN
+      const float s = __uint_as_float(byte[i] == 0 ? 0x00400000u : byte[i] == 255 ? 0x7FC00000u : byte[i] << 23);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      Pack8<T> out;
+      for (int h = 0; h < 2; ++h) {
+        Pack8<T> out;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t w = (p < 2 ? q[i][h].x : q[i][h].y) >> (p & 1) * 16 & 0xFFFFu;
-        const __half2_raw e = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
-        const float2 f = __half22float2(__half2(e));
-        out.e[2 * p] = DT<T>::from_f32(f.x * s);
-        out.e[2 * p + 1] = DT<T>::from_f32(f.y * s);
-      }
-      T* to = static_cast<T*>(a.out) + r * a.stride + c + h * 64;
-      const int64_t left = a.cols - c - h * 64;
-      if constexpr (VEC) {
-        if (left > 0) store8_raw(to, out);
-      } else {
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t w = (p < 2 ? q[i][h].x : q[i][h].y) >> (p & 1) * 16 & 0xFFFFu;
+          const __half2_raw e = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
+          const float2 f = __half22float2(__half2(e));
+          out.e[2 * p] = DT<T>::from_f32(f.x * s);
+          out.e[2 * p + 1] = DT<T>::from_f32(f.y * s);
+        }
+        T* to = static_cast<T*>(a.out) + r * a.stride + c + h * 64;
+        const int64_t left = a.cols - c - h * 64;
+        if constexpr (VEC) {
+          if (left > 0) store8_raw(to, out);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < left) to[j] = out.e[j];
+          for (int j = 0; j < 8; ++j)
+            if (j < left) to[j] = out.e[j];
+        }
       }
     }
   }
@@ -345,7 +348,8 @@ struct RowGrid {
   RowGrid(int64_t rows, int64_t blocks, int64_t batch) {
     while (wide < 5 && (1 << wide) < blocks) ++wide;
     const int64_t each = (32 >> wide) * kPasses;
-    grid = dim3((unsigned)((rows + each - 1) / each), (unsigned)((blocks + (1 << wide) - 1) >> wide), (unsigned)batch);
+    const int64_t across = (blocks + (1 << wide) - 1) >> wide;
+    grid = dim3((unsigned)((rows + each - 1) / each), (unsigned)(across < 65535 ? across : 65535), (unsigned)batch);
   }
 };
 

@@ -179,3 +179,24 @@ def test_a_pair_that_gives_up_is_reported(block):
     want, size = ref.forward(x, w, [0, 70])
     close(experts.forward(x, w, offsets_of([70])), want, ref.product_tol(264, size, want, BF16, BF16), "y")
     assert not timed_out()
+
+
+# ---------------------------------------------------------------------------
+# Wide scaled matrices
+# ---------------------------------------------------------------------------
+
+def test_restore_of_wide_rows():
+    """More columns than one grid takes (65535 x 32 scale blocks of 128): what packing makes of the transpose of
+    very many rows."""
+    cols = 65535 * 32 * 128 + 1000
+    x = torch.zeros(cols, 2, dtype=BF16, device="cuda")
+    at = torch.tensor([0, 127, 65535 * 32 * 128 - 1, 65535 * 32 * 128, cols - 500, cols - 1], device="cuda")
+    x[at] = torch.tensor([[1.0, -2.0], [3.0, 4.0], [5.0, 6.0], [-7.0, 8.0], [9.0, 10.0], [11.0, 12.0]], device="cuda").to(BF16)
+    _, xt = float8.pack(x, direct=False, transposed=True)
+    y = xt.restore(BF16)
+    assert torch.equal(y, x.t())
+    wide = torch.full((2, cols + 3), 5.0, dtype=F16, device="cuda")  # element by element
+    xt.restore(out=wide[:, :cols])
+    assert torch.equal(wide[:, :cols], x.t().to(F16)) and bool((wide[:, cols:] == 5).all())
+    del x, y, xt, wide
+    torch.cuda.empty_cache()
