@@ -1,14 +1,16 @@
 """The expert layer's operators and the scaled products at their edges: sums that
 would be lost in truncated additions, the largest sizes, offsets that no routing
 makes, the smallest choices."""
+import math
+
 import pytest
 import torch
 
 import _experts_ref as ref
-from _block_ref import U, close
+from _block_ref import E, TINY, U, close
 from mixed_precision_gb300 import _abi as abi
 from mixed_precision_gb300 import experts, float8
-from test_gpu_experts import gen, normal, offsets_of
+from test_gpu_experts import check_route, gen, normal, offsets_of
 
 pytestmark = pytest.mark.gpu
 
@@ -200,3 +202,101 @@ def test_restore_of_wide_rows():
     assert torch.equal(wide[:, :cols], x.t().to(F16)) and bool((wide[:, cols:] == 5).all())
     del x, y, xt, wide
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------------------
+# A lone choice
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("tokens,n", [(1, 1), (70, 1), (33, 16), (200, 2), (65, 128), (40, 300), (9, 1024)])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+def test_top_1(tokens, n, dtype):
+    """k = 1: normalised weights are 1 and pass nothing back, the softmax over all gives w dw (delta - p)."""
+    g = gen(tokens + n)
+    logits = normal(g, tokens, n, dtype=dtype)
+    logits[::5] = -math.inf
+    dw = normal(g, tokens, 1)
+    r, _ = check_route(logits, 1, True)
+    taken = r.experts >= 0
+    assert torch.equal(r.weights, taken.float())
+    assert not bool(experts.route_backward(dw, logits, r).any())
+
+    r, _ = check_route(logits, 1, False)
+    w = r.weights.double()
+    d = torch.where(taken, dw.double(), 0.0)
+    at = torch.where(taken, r.experts, n).long()
+    p = torch.nan_to_num(torch.softmax(logits.double(), 1), nan=0.0)
+    own = torch.zeros(tokens, n + 1, dtype=torch.float64, device="cuda").scatter(1, at, w * d)[:, :n]
+    want, size = own - p * (w * d), own.abs() + p * (w * d).abs()
+    # p as the weights (logits within 6 of zero, n / 32 additions and 5 shuffles), the product, one addition
+    rel = 8 * E + 2 * (12.0 * E + 4 * E) + (n / 32 + 8) * E
+    close(experts.route_backward(dw, logits, r), want, rel * size + U[dtype] * want.abs() + TINY[dtype], "dlogits")
+
+    y = normal(g, tokens, 72, dtype=dtype)
+    rows = experts.gather(y, r)
+    last = int(r.offsets[-1])
+    assert torch.equal(rows[:last], y[r.source[:last].long()]) and not bool(rows[last:].any())
+    out = experts.combine(rows, r)
+    assert torch.equal(out, torch.where(taken, (r.weights * y.float()).to(dtype), torch.zeros((), dtype=dtype, device="cuda")))
+    dy, dweights = experts.combine_backward(y, rows, r)
+    assert torch.equal(dy[:last], (r.weights.view(-1)[r.source[:last].long()][:, None] * y.float()[r.source[:last].long()]).to(dtype))
+    sq = torch.where(taken, (y.double() ** 2).sum(1, keepdim=True), 0.0)
+    close(dweights, sq, (72 / 32 + 16) * E * sq, "dweights")
+
+
+def test_top_1_gradient_by_differences():
+    g = gen(31)
+    logits, c = normal(g, 20, 12), normal(g, 20, 1)
+    r = experts.route(logits, 1, normalize=False)
+    got, at = experts.route_backward(c, logits, r).double(), r.experts.long()
+    h = 1e-5
+    for e in range(12):
+        step = torch.zeros(12, dtype=torch.float64, device="cuda")
+        step[e] = h
+        up, down = (torch.softmax(logits.double() + s * step, 1).gather(1, at) for s in (1, -1))
+        # differences: h^2 of the third derivative and 1e-16 / h; the kernel: fp32
+        assert float((got[:, e] - ((up - down) * c.double()).sum(1) / (2 * h)).abs().max()) < 1e-5
+
+
+# ---------------------------------------------------------------------------
+# fp32 sums by their runs: 512 rows of 16 bits, 1024 of 8
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("sign", [False, True])
+@pytest.mark.parametrize("counts,n_out,n_in", [([20000, 1500], 136, 72), ([2000, 1, 2096, 0], 512, 768), ([700] * 9, 1024, 512),
+                                               ([511, 513, 1025], 33, 264)])
+def test_weight_grad_by_runs(counts, n_out, n_in, dtype, sign):
+    g = gen(sum(counts) + n_out)
+    rows, off = sum(counts), offsets_of(counts)
+    dy = torch.zeros(rows, (n_out + 7) // 8 * 8, dtype=dtype, device="cuda")[:, :n_out]
+    x = normal(g, rows, n_in, dtype=dtype)
+    dy.copy_(normal(g, rows, n_out))
+    if sign:
+        dy, x = dy.abs_(), x.abs()
+    want, size = ref.weight_grad(dy, x, off.tolist())
+    tol = ref.product_tol(max(counts), size, want, dtype, F32, run=512)
+    close(experts.weight_grad(dy, x, off, dtype=F32), want, tol, "dw")
+    start = normal(g, *want.shape)
+    dw = start.clone()
+    experts.weight_grad(dy, x, off, out=dw, accumulate=True)
+    close(dw, want + start.double(), tol + E * (want + start.double()).abs(), "dw added")
+    close(experts.weight_grad(dy, x, off), want, ref.product_tol(max(counts), size, want, dtype, dtype, run=1024), "dw rounded")
+
+
+@pytest.mark.parametrize("sign", [False, True])
+@pytest.mark.parametrize("m,n,k", [(70, 40, 20000), (1025, 2049, 1100), (257, 300, 4097)])
+def test_scaled_products_by_runs(m, n, k, sign):
+    g = gen(m + k)
+    x, w = normal(g, m, k), normal(g, n, k)
+    if sign:
+        x, w = x.abs(), w.abs()
+    a, b = float8.pack(x)[0], float8.pack(w)[0]
+    ra, rb = a.restore(F32).double(), b.restore(F32).double()
+    want, size = ra @ rb.t(), ra.abs() @ rb.abs().t()
+    tol = ref.product_tol(k, size, want, None, F32, per_mma=32, run=1024)
+    close(float8.matmul(a, b, dtype=F32), want, tol, "product")
+    start = normal(g, m, n)
+    out = start.clone()
+    float8.matmul(a, b, out=out, accumulate=True)
+    close(out, want + start.double(), tol + E * (want + start.double()).abs(), "added")
