@@ -759,8 +759,10 @@ int zero_attention_backward(const zero_attention_desc* desc, const void* dout, c
 /* above: the caller's buffers and stream, nothing allocated, fixed orders.   */
 /* What a device array says (offsets, places, choices) cannot be checked on   */
 /* the host; the kernels read and write inside the buffers whatever it holds. */
-/* No output may overlap an input or another output. Buffers start on 16 bytes; */
-/* logits and the products' outputs (y, dx, dw, out) on an element.            */
+/* No output may overlap an input or another output, each taken from its      */
+/* first element to its last (columns of one buffer, side by side, overlap    */
+/* so). Buffers start on 16 bytes; logits and the products' outputs (y, dx,   */
+/* dw, out) on an element.                                                    */
 /* ------------------------------------------------------------------------ */
 
 /* The routing of tokens to k of `experts` experts by their logits

@@ -235,7 +235,11 @@ def forward(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, out=No
 
     x [rows, n_in] and weight [experts, n_out, n_in] are fp16 or bf16, their
     strides free multiples of 8 (of one projection, or of all experts' in a flat
-    parameter buffer). offsets: int32 [experts + 1], as ``route`` gives."""
+    parameter buffer). offsets: int32 [experts + 1], as ``route`` gives.
+
+    A new result has rows without gaps: with an n_out that is no multiple of 8 it
+    (and a dy of its shape) is no input of another product. `out` may be columns of
+    a wider buffer, ``buffer[:, :n_out]``, whose row stride is a multiple of 8."""
     each, w_step = _matrices(weight, "weight")
     experts, n_out, n_in = weight.shape
     dtype = weight.dtype
@@ -252,7 +256,9 @@ def forward(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, out=No
 
 
 def input_grad(dy: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, out=None, stream=None) -> torch.Tensor:
-    """dx [rows, n_in]: dx[r] = dy[r] W_e for each expert's rows; rows of no expert are zero."""
+    """dx [rows, n_in]: dx[r] = dy[r] W_e for each expert's rows; rows of no
+    expert are zero. dy's and weight's strides are multiples of 8 (``forward``
+    says how an odd n_out meets that)."""
     each, w_step = _matrices(weight, "weight")
     experts, n_out, n_in = weight.shape
     dtype = weight.dtype
@@ -273,8 +279,8 @@ def weight_grad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, out=No
     """dw [experts, n_out, n_in]: the sum over each expert's rows of dy[r]^T
     x[r]; zero for an expert without rows.
 
-    dw is fp32 or the inputs' type (`dtype`; default out's, or theirs), its
-    strides free: `out` may be all experts' gradients in a flat buffer.
+    dy's and x's row strides are multiples of 8. dw is fp32 or the inputs' type
+    (`dtype`; default out's, or theirs), its strides free: `out` may be all experts' gradients in a flat buffer.
     `accumulate` adds to an fp32 `out` (main gradients over micro-batches)."""
     rows, y_step = _rows(dy, "dy", None)
     x_rows, x_step = _rows(x, "x", None, dy.dtype)

@@ -300,3 +300,24 @@ def test_scaled_products_by_runs(m, n, k, sign):
     out = start.clone()
     float8.matmul(a, b, out=out, accumulate=True)
     close(out, want + start.double(), tol + E * (want + start.double()).abs(), "added")
+
+
+# ---------------------------------------------------------------------------
+# Odd widths from product to product
+# ---------------------------------------------------------------------------
+
+def test_products_of_an_odd_width_in_padded_rows():
+    """n_out = 33: a result without gaps is refused as an input, columns of a wider buffer are taken."""
+    g = gen(41)
+    off = offsets_of([50, 30])
+    x, w = normal(g, 80, 72, dtype=BF16), normal(g, 2, 33, 72, dtype=BF16)
+    tight = experts.forward(x, w, off)
+    for call in (lambda: experts.input_grad(tight, w, off), lambda: experts.weight_grad(tight, x, off)):
+        with pytest.raises(abi.ZeroError):
+            call()
+    y = experts.forward(x, w, off, out=torch.zeros(80, 40, dtype=BF16, device="cuda")[:, :33])
+    assert torch.equal(y, tight)
+    want, size = ref.input_grad(y, w, off.tolist())
+    close(experts.input_grad(y, w, off), want, ref.product_tol(33, size, want, BF16, BF16), "dx")
+    want, size = ref.weight_grad(y, x, off.tolist())
+    close(experts.weight_grad(y, x, off, dtype=F32), want, ref.product_tol(50, size, want, BF16, F32), "dw")
