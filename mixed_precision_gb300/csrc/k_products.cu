@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
   using F = Form<A_MN, B_MN, SCALED>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], sums_full[2], sums_empty[2],
-      scales_full[kScaleSlots], scales_passed[kScaleSlots], scales_empty[kScaleSlots];
+      scales_full[kScaleSlots], scales_empty[kScaleSlots];
   __shared__ uint32_t tmem_slot, abort_word;
   // the swizzle is a function of address bits: tiles start on 1024 bytes, the same in both blocks
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -388,7 +388,6 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     }
     for (int s = 0; s < kScaleSlots; ++s) {
       mbar_init(&scales_full[s], 2);  // both blocks' scales; rank 0's barrier counts
-      mbar_init(&scales_passed[s], 1);
       mbar_init(&scales_empty[s], 1);
     }
     abort_word = 0;
@@ -478,7 +477,7 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
           d = tmem + sums.at * F::kMaxN;
         }
         if (SCALED && step % kScaleSteps == 0) {
-          if (!(go = wait(&scales_full[slots.at], slots.phase))) break;
+          if (!(go = wait.written(&scales_full[slots.at], slots.phase))) break;
           tc_fence_after();
           const uint32_t from = smem_u32(scales) + slots.at * kScaleSlot;
           sa = tmem + F::kScaleCols + (slots.at & 1) * 16;
@@ -519,8 +518,10 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
     if (!go)  // leave the MMAs in flight time to end
       for (int i = 0; i < 64; ++i) __nanosleep(1000);
   } else if (SCALED && warp == 2) {
-    // ---- scales: a word (four blocks of 128) of every row of the tile
-    uint64_t* const done = rank == 0 ? scales_full : scales_passed;
+    // ---- scales: a word (four blocks of 128) of every row of the tile. Rank 0's MMAs learn
+    // of either block's by fences of shared memory, which cost nothing that shows (8192 x
+    // 2048 x 1024: 16.7 us; fences of all memory, in warps of their own, took 17.7).
+    const uint32_t full0 = cluster_map(smem_u32(&scales_full[0]), 0);
     Ring slots(kScaleSlots);
     bool go = true;
     while (go && walk.next(t)) {
@@ -550,7 +551,10 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
         *reinterpret_cast<uint4*>(to + 1024) = v.c;
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&done[slots.at]);
+        if (lane == 0) {
+          fence_release_shared();
+          mbar_arrive_mapped(full0 + slots.at * 8);
+        }
         slots.step();
       };
       fetch(0, even);
@@ -569,40 +573,6 @@ __global__ void __launch_bounds__(kThreadsHere, 1) __cluster_dims__(2, 1, 1)
         go = wait(&scales_empty[slots.at], slots.phase ^ 1);
         slots.step();
       }
-  } else if (SCALED && warp == 3) {
-    // ---- rank 1's scales are made known to rank 0, whose MMAs read them: a fence at the
-    // cluster's scope for all words that are there, then rank 0's warp tells its own
-    // block. Neither has loads of its own to wait for. (8192 x 8192 x 4096 takes 150 us;
-    // with the fence in the warp that loads 176, without an order that PTX grants 148. Rank
-    // 0 alone, writing to both blocks, 154; 2048 x 2048 x 4097 in fp32 23.7, so 21.7.)
-    const uint32_t there = cluster_map(smem_u32(&scales_passed[0]), 0);
-    Ring slots(kScaleSlots);
-    bool go = true;
-    while (go && walk.next(t)) {
-      int words = (t.steps + kScaleSteps - 1) / kScaleSteps;
-      while (words > 0) {
-        if (rank == 0) {
-          if (!(go = wait.cluster(&scales_passed[slots.at], slots.phase))) break;
-          if (lane == 0) mbar_arrive(&scales_full[slots.at]);
-          slots.step();
-          --words;
-          continue;
-        }
-        if (!(go = wait(&scales_passed[slots.at], slots.phase))) break;
-        const int first = slots.at;
-        int n = 0;
-        do {
-          slots.step();
-          ++n;
-        } while (n < min(words, kScaleSlots) && __all_sync(0xFFFFFFFFu, mbar_test(&scales_passed[slots.at], slots.phase)));
-        if (lane == 0) {
-          fence_cluster();
-          for (int i = 0; i < n; ++i) mbar_arrive_mapped(there + (first + i) % kScaleSlots * 8);
-        }
-        __syncwarp();
-        words -= n;
-      }
-    }
   } else if (warp >= 4) {
     // ---- sums: four warps have the tile's columns of out (lanes of TMEM), each 32, in half of its rows
     const uint32_t empty0 = cluster_map(smem_u32(&sums_empty[0]), 0);

@@ -280,27 +280,22 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // Rank 0 issues the MMAs for both. The barriers that it waits on are its own; the
 // other block arrives there through `mapped` addresses (cluster_map).
 
-// The thread's writes, and those that it has been told of, before what it tells the
-// other block: some 1300 cycles, more while other warps of the block store.
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
-// mbar_try_wait, behind the writes of the other block before its arrivals.
+// Of shared memory only, at the cluster's scope: the block's writes (the thread's and
+// those that it has been told of) before its next arrival on a mapped barrier ...
+__device__ __forceinline__ void fence_release_shared() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+// ... and behind a wait for such arrivals, what they tell of. (fence.acq_rel.cluster, of
+// all memory, takes 1300 cycles.)
+__device__ __forceinline__ void fence_acquire_shared() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+// mbar_try_wait for arrivals of either block, without an order (fence_acquire_shared).
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// Whether the phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -326,13 +321,15 @@ struct PairWaiter {
     atomicAdd(error, 1u);
     return false;
   }
-  // For an arrival of the other block that tells of its threads' writes.
-  __device__ __forceinline__ bool cluster(uint64_t* bar, uint32_t parity) const {
-    return operator()<true>(bar, parity);
+  // For arrivals of either block that tell of writes to its shared memory.
+  __device__ __forceinline__ bool written(uint64_t* bar, uint32_t parity) const {
+    const bool ok = operator()<true>(bar, parity);
+    fence_acquire_shared();
+    return ok;
   }
 };
 // Arrivals of either block, with no order of the thread's own writes: what they report
-// is ordered by other means (TMA's count, tcgen05's fences, fence_cluster).
+// is ordered by other means (TMA's count, tcgen05's fences, fence_release_shared).
 __device__ __forceinline__ void mbar_arrive_mapped(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
