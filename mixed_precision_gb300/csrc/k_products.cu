@@ -168,6 +168,22 @@ struct Walk {
   }
 };
 
+// The runs of offsets that decrease, by one thread. Out of line: in the way of every call
+// its code cost a kernel whose instructions are in no cache yet 3000 cycles.
+template <typename F>
+__device__ __noinline__ void join_runs(const ProductArgs& a, Runs runs) {
+  const int start = Walk<F>::bound(a, 0);
+  int end = start;
+  for (int g = 0; g < a.groups; ++g) {
+    const int to = max(end, Walk<F>::bound(a, g + 1));
+    runs.first[g] = end;
+    runs.rows[g] = to - end;
+    end = to;
+  }
+  runs.reach[0] = end > start ? start : static_cast<int>(a.n);
+  runs.reach[1] = end > start ? end : 0;
+}
+
 // Fill `runs` (all threads of the block).
 template <typename F>
 __device__ void read_runs(const ProductArgs& a, const ProductPlan& p, const Runs& runs) {
@@ -190,18 +206,7 @@ __device__ void read_runs(const ProductArgs& a, const ProductPlan& p, const Runs
   // An offset that decreases, which no routing makes, counts as the largest before it: runs
   // stay apart, so a row has one writer and there are no more tiles than the host has counted.
   if (__syncthreads_or(falls)) {
-    if (threadIdx.x == 0) {
-      const int start = Walk<F>::bound(a, 0);
-      int end = start;
-      for (int g = 0; g < a.groups; ++g) {
-        const int to = max(end, Walk<F>::bound(a, g + 1));
-        runs.first[g] = end;
-        runs.rows[g] = to - end;
-        end = to;
-      }
-      runs.reach[0] = end > start ? start : static_cast<int>(a.n);
-      runs.reach[1] = end > start ? end : 0;
-    }
+    if (threadIdx.x == 0) join_runs<F>(a, runs);
     __syncthreads();
   }
   if (!F::kRaggedK && threadIdx.x < 32) {
