@@ -13,10 +13,10 @@
 // counts rows from the step's first (Form), and from a negative start it fills zeros.
 //
 // Twelve warps: one loads by TMA, one issues MMAs, one brings scales (words of four
-// exponents, which the tensor core applies itself), eight take the sums. These leave TMEM after a run of steps and are added up in registers,
-// rounded: the tensor core truncates where it adds, which over thousands of steps
-// would cost an fp32 result its last bits. TMEM holds two tiles' sums, so the MMAs go
-// on meanwhile.
+// exponents, which the tensor core applies itself), eight take the sums. These leave TMEM
+// after a run of steps and are added up in registers, rounded: the tensor core truncates
+// where it adds, which over thousands of steps would cost an fp32 result its last bits.
+// TMEM holds two tiles' sums, so the MMAs go on meanwhile.
 //
 // An SM's stores leave at 32 bytes a cycle at most, whatever way they take (measured
 // alone and on all SMs at once: by TMA, from registers, by 64 to 512 bytes of a row).
@@ -24,20 +24,20 @@
 // through shared memory: 8 x 8 matrices are turned on the way in, so that a row of out
 // lies there as it does in memory, and TMA stores take 32 rows from there while the
 // next are made. From registers, 64 bytes of a row each, they were as fast, but not
-// where rows start inside a sector (520 x 1000 weights: 47 us, so 29). Rows behind the
+// where rows start inside a sector (520 x 1000 weights: 47 us, so 27). Rows behind the
 // last whole 32 of a run, and outs whose rows do not start on 16 bytes, go by ordinary
 // stores.
 //
-// Measured (with the L2 flushed before): 16384 x 2048 x 2048 in bf16 by 16 even
-// experts 83 us forward (1660 TFLOP/s), 105 for the weights' gradient in fp32; 8192 x
-// 8192 x 8192 599 us (1840, 0.93 of the library's burst rate); 8192 x 8192 x 4096 in
-// e4m3 157 us (3500 TFLOP/s); 74 rows x 2048 x 1024 by 16 experts 10 us captured (5.9
-// TB/s of weights). Large ones are bound by the tensor cores (75 to 85 % of the cycles;
-// the rest is a pair's last tile, which others do not have, and each kernel's start and
-// end), long under load by the power limit: the clock falls from 1.9 to 1.5 GHz, and the
-// forward products take 91 us, the library's batched product 86. fp32 weight gradients:
-// 268 MB of sums beside them. Many small experts: a tile's way out (4500 cycles for 128 x
-// 192 sums of a block) is longer than its products.
+// Measured (captured, one behind the other): 16384 x 2048 x 2048 in bf16 by 16 even
+// experts 78 us forward (1770 TFLOP/s), 98 for the weights' gradient in fp32; 8192 x 8192 x
+// 8192 570 us (1930, 0.98 of the library's burst rate); 8192 x 8192 x 4096 in e4m3 150 us
+// (3660 TFLOP/s); 74 rows x 2048 x 1024 by 16 experts 9.5 us (6.2 TB/s of weights). Large
+// ones are bound by the tensor cores (74 to 84 % of the cycles; the rest is a pair's last
+// tile, which others do not have, and each kernel's start and end), long under load by the
+// power limit: the clock falls from 1.9 to 1.5 GHz, and the forward products take 91 us, the
+// library's batched product 86. fp32 weight gradients: 268 MB of sums beside them (added to
+// what is there 479 us: reads that wait for each other). Many small experts: a tile's way
+// out (4500 cycles for 128 x 192 sums of a block) is longer than its products.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

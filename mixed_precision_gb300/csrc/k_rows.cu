@@ -5,8 +5,9 @@
 // order are read or written. The places come from the device; a place outside
 // the order is passed by. Rows that no slot fills are made zero by the warp of
 // their number. Bound by HBM: each row moves once. Gather of 8192 rows of 2048 in bf16
-// to two experts each takes 14 us (101 MB: 7.2 TB/s, part of it in the L2 when it ends),
-// combine's gradients of 8191 x 1024 in fp16 by 8 43 us (286 MB, 6.7 TB/s).
+// to two experts each takes 13 us (101 MB: 7.7 TB/s, part of it in the L2 when it ends),
+// combine back 25, combine's gradients of 8191 x 1024 in fp16 by 8 43 us (286 MB, 6.7
+// TB/s). Few tokens of wide rows leave most SMs idle: 512 of 4096, 8 each, combine in 31 us.
 #include "bulk.cuh"
 #include "experts.h"
 #include "vec.cuh"

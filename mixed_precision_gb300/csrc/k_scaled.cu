@@ -5,7 +5,7 @@
 // element asked. What counts is that a thread's loads are all under way before it needs
 // the first. bf16 8192 x 4096, captured: packed in 15.7 us (6.4 TB/s), the transpose in
 // 24, both in 36 (a thread's 32 elements cost it some 450 instructions, and 304 blocks
-// at a time their barriers); from cold caches the first takes 18 and restoring 14.
+// at a time their barriers); from cold caches the first takes 18 and restoring 14 (11 captured).
 //
 // Along rows alone, eight lanes hold a scale block (16 elements each). With the
 // transpose, a block of threads takes 128 x 128 elements, so it has whole scale
